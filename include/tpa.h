@@ -469,6 +469,177 @@ int tpa_lm_head_logprobs_entropy(const tpa_tree_view* tree, const void* hidden, 
                                  float* seq_logp, float* seq_entropy, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* Head norms and rotary positions: what a policy's attention layer does to
+ * the query and key heads between their projection and the attention.  For
+ * each row x (one token's head of d values) with weight w and position p
+ *   y = R(p) (x * rsqrt(mean(x^2) + eps) * w),
+ * R(p) turning the pair j of the first rot_dim values by the angle whose
+ * cosine and sine are table[p][j] and table[p][rot_dim / 2 + j]; the other
+ * d - rot_dim values are not turned.  Pair j is (x_j, x_{j + rot_dim/2}), or
+ * (x_2j, x_2j+1) with interleaved.  Without weights (both NULL) there is no
+ * norm, the rotation alone.  Computed in fp32, rounded to bf16 once.        */
+/* ------------------------------------------------------------------------ */
+
+enum { TPA_WEIGHT_F32 = 0, TPA_WEIGHT_BF16 = 1 };
+
+typedef struct {
+  const float* table;       /* [table_rows, rot_dim] fp32 cos | sin (device, 16-byte aligned); NULL: no rotation
+                               (tpa_paged_append only) */
+  int32_t table_rows;       /* positions must be below it */
+  int32_t rot_dim;          /* multiple of 16, <= d */
+  int32_t interleaved;      /* 0: halves, 1: neighbours */
+  int32_t weight_type;      /* TPA_WEIGHT_F32 or TPA_WEIGHT_BF16 */
+  const void* q_weight;     /* [d] device, 16-byte aligned; both weights or neither */
+  const void* k_weight;
+  float eps;                /* >= 0 */
+  int32_t reserved_;
+} tpa_rope_params;
+
+/*
+ * tpa_rope_table — write table[p][j] = scale * cos(p * f_j) and
+ * table[p][rot_dim/2 + j] = scale * sin(p * f_j) for p < n_positions, angles
+ * in fp64 and rounded to fp32 once.  f_j = inv_freq[j] (host array of
+ * rot_dim / 2 doubles, read during the call), or base^(-2j / rot_dim) when
+ * inv_freq is NULL.
+ *   n_positions >= 1, rot_dim a multiple of 16 in [16, 128], base > 0, scale
+ *   finite; table device, 16-byte aligned.
+ * Errors: TPA_ERR_INVALID_ARG, TPA_ERR_CUDA.
+ */
+int tpa_rope_table(float* table, int32_t n_positions, int32_t rot_dim, double base, const double* inv_freq,
+                   double scale, void* stream);
+
+/*
+ * tpa_qk_norm_rope_fwd
+ *   positions [n_rows] int32 (device).  A row with a negative position is
+ *     padding: its outputs are 0 and its inputs are not used.
+ *   n_tokens, t_pad: NULL and 0, or the arrays of a packed tree (positions =
+ *     view.depth, n_tokens = view.n_tokens): row r is also padding when
+ *     r % t_pad >= n_tokens[r / t_pad].
+ *   q [n_rows, Hq, d], k [n_rows, Hkv, d] bf16: heads contiguous, rows
+ *     q_stride / k_stride elements apart (multiples of 8, >= H * d), so both may
+ *     be slices of a fused projection's output; q_out, k_out likewise (written;
+ *     the same pointer and stride as the input is allowed).  16-byte aligned.
+ *   d in {64, 128}.
+ * A position >= table_rows gives rows of 0 and is reported by
+ * tpa_sync_status (TPA_ERR_INVALID_ARG).  One kernel on `stream`; n_rows = 0
+ * does nothing.  Errors: TPA_ERR_INVALID_ARG, TPA_ERR_CUDA.
+ */
+int tpa_qk_norm_rope_fwd(const int32_t* positions, const int32_t* n_tokens, int32_t t_pad, int64_t n_rows,
+                         const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                         const tpa_rope_params* rope, void* q_out, int64_t q_out_stride, void* k_out,
+                         int64_t k_out_stride, int32_t n_heads_q, int32_t n_heads_kv, int32_t head_dim,
+                         void* stream);
+
+/* Workspace bytes of tpa_qk_norm_rope_bwd (partial sums of the weights'
+ * gradients); 0 on an unsupported head_dim. */
+uint64_t tpa_qk_norm_rope_bwd_workspace_bytes(int32_t head_dim);
+
+/*
+ * tpa_qk_norm_rope_bwd — gradients of the call above: with h = x rsqrt(mean(x^2) + eps)
+ * and z = R(p)^T dy,
+ *   dw = sum over rows and heads of z * h,
+ *   dx = rsqrt(mean(x^2) + eps) (z w - h mean(z w h))   (z without norm).
+ *   dq_out, dk_out: gradients of q_out and k_out, of type grad_in (TPA_GRAD_F32
+ *     or TPA_GRAD_BF16), heads contiguous, row strides in elements
+ *   q, k: the inputs of the forward (not read without norm; may then be NULL)
+ *   dq, dk (written, of type grad_out; padding rows 0; may be dq_out / dk_out
+ *     themselves when type and stride agree)
+ *   dq_weight, dk_weight [d] fp32 (written; NULL without norm)
+ *   workspace: tpa_qk_norm_rope_bwd_workspace_bytes() bytes, 16-byte aligned (NULL without norm)
+ * Sums are fp32 in a fixed order: results are deterministic.  One kernel, and
+ * a second that adds the partial sums.  Errors: TPA_ERR_INVALID_ARG,
+ * TPA_ERR_BUFFER_TOO_SMALL, TPA_ERR_CUDA.
+ */
+int tpa_qk_norm_rope_bwd(const int32_t* positions, const int32_t* n_tokens, int32_t t_pad, int64_t n_rows,
+                         const void* dq_out, int64_t dq_out_stride, const void* dk_out, int64_t dk_out_stride,
+                         int32_t grad_in, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                         const tpa_rope_params* rope, void* dq, int64_t dq_stride, void* dk, int64_t dk_stride,
+                         int32_t grad_out, float* dq_weight, float* dk_weight, void* workspace,
+                         uint64_t workspace_bytes, int32_t n_heads_q, int32_t n_heads_kv, int32_t head_dim,
+                         void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Paged key/value cache: the policy's sampling side (the rollouts that are
+ * packed into trees, "概述" of the tree-training page).  Keys and values live
+ * in pages of page_size token slots,
+ *   k_cache, v_cache [n_pages, Hkv, page_size, d] bf16 (device, 16-byte aligned),
+ * page_size in {16, 32, 64, 128}, d in {64, 128}, n_pages * Hkv * page_size
+ * < 2^31.  Token t of sequence s is slot t % page_size of page
+ * pages[s][t / page_size]; sequences may share the pages of a common prefix.
+ * A batch is described by
+ *   pages [n_seqs, max_pages] int32, rows page_stride elements apart,
+ *   offsets [n_seqs + 1] int32, non-decreasing from 0: the new tokens of
+ *     sequence s are rows [offsets[s], offsets[s+1]) of the call's tensors
+ *     (a sequence may have none); rows from offsets[n_seqs] on are padding,
+ *     neither used nor written,
+ *   kv_lens [n_seqs] int32: tokens of sequence s in the cache, the new ones
+ *     (its last) included,
+ * all in device memory and read by the kernels, so a captured call can be
+ * replayed after they change.  Values out of range (a page outside
+ * [0, n_pages), more tokens than max_pages hold, an offset out of order or
+ * above the call's rows) are reported by tpa_sync_status
+ * (TPA_ERR_INVALID_ARG); nothing outside the tensors is read or written.    */
+/* ------------------------------------------------------------------------ */
+
+typedef struct {
+  void* k_cache;
+  void* v_cache;
+  const int32_t* pages;
+  const int32_t* offsets;
+  const int32_t* kv_lens;
+  int32_t n_pages, page_size, n_seqs, max_pages, page_stride;
+  int32_t n_heads_kv, head_dim;
+  int32_t n_rows;           /* rows of the call's q, k, v: >= offsets[n_seqs] */
+} tpa_paged_view;
+
+/*
+ * tpa_paged_append — norm and rotate the keys of the new tokens at their
+ * positions (kv_lens[s] minus the sequence's new tokens, and on) and write
+ * them and the values into the cache; with q, the queries are treated
+ * likewise and written to q_out.
+ *   k, v [n_rows, Hkv, d], q [n_rows, Hq, d] bf16 with row strides in elements
+ *     (multiples of 8); q and q_out NULL with n_heads_q = 0 for keys and values alone
+ *   rope: as above; table NULL for no rotation
+ * A token that is out of range (a negative position, a bad page, a position
+ * >= table_rows) is skipped and reported.  Two tokens of one call that share a
+ * slot leave either one's values in each 16-byte piece of it.  One kernel.
+ * Errors: TPA_ERR_INVALID_ARG, TPA_ERR_CUDA.
+ */
+int tpa_paged_append(const tpa_paged_view* cache, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                     const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride, int32_t n_heads_q,
+                     const tpa_rope_params* rope, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Drafted tokens (speculative sampling): the policy's probabilities decide
+ * how many of a sequence's drafted tokens stand, and the next one is drawn.  */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * tpa_verify_drafts — for each sequence, drafted token i = 0, 1, ... stands iff
+ *   u_accept[i] * q_i(x_i) < p_i(x_i)
+ * (the product formed exactly); the first that does not ends the run.  With a of n_drafts tokens standing, the
+ * next token is the lowest v with  sum_{w <= v} r(w) > u_next * sum_w r(w),
+ *   r = max(p_a - q_a, 0) when a < n_drafts (p_a where that leaves nothing),
+ *   r = p_a               when a = n_drafts,
+ * sums in fp64 (should rounding leave none, the last v with r(v) > 0; a row of zeros gives -1).
+ *   target [n_seqs, K+1, vocab] fp32: p_0 .. p_K; sequences target_stride and
+ *     rows vocab elements apart; need not be normalised (entries >= 0; a
+ *     negative or NaN entry counts as 0)
+ *   draft [n_seqs, K, vocab] fp32: q_0 .. q_{K-1}, or NULL: q_i is all on x_i
+ *   draft_tokens [n_seqs, K] int32; a token outside [0, vocab) does not stand and is reported
+ *   n_drafts [n_seqs] int32 in [0, K] (NULL: K; out of range: clamped and reported)
+ *   u_accept [n_seqs, K], u_next [n_seqs] fp32 in [0, 1)
+ *   tokens [n_seqs, K+1] int32 (written): the tokens that stand, the next one, then -1
+ *   n_accepted [n_seqs] int32 (written): a
+ *   K in [0, 1024]; with K = 0, draft_tokens and u_accept may be NULL.
+ * One kernel, one cluster of CTAs a sequence.  Errors: TPA_ERR_INVALID_ARG, TPA_ERR_CUDA.
+ */
+int tpa_verify_drafts(const float* target, int64_t target_stride, const float* draft, int64_t draft_stride,
+                      const int32_t* draft_tokens, const int32_t* n_drafts, const float* u_accept,
+                      const float* u_next, int32_t* tokens, int32_t* n_accepted, int32_t n_seqs, int32_t max_drafts,
+                      int32_t vocab, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Status                                                                    */
 /* ------------------------------------------------------------------------ */
 

@@ -15,6 +15,7 @@ STATUS = {
 BLOCK_SIZE = 128
 LOGITS_COMPACT, LOGITS_PADDED = 0, 1
 GRAD_F32, GRAD_BF16 = 0, 1
+WEIGHT_F32, WEIGHT_BF16 = 0, 1
 BALANCE_FFD, BALANCE_KK = 0, 1
 MASK_U8, MASK_BITS = 0, 1
 
@@ -61,6 +62,23 @@ class PackingMetrics(C.Structure):
     ]
 
 
+class RopeParams(C.Structure):
+    _fields_ = [
+        ("table", C.c_void_p), ("table_rows", C.c_int32), ("rot_dim", C.c_int32), ("interleaved", C.c_int32),
+        ("weight_type", C.c_int32), ("q_weight", C.c_void_p), ("k_weight", C.c_void_p), ("eps", C.c_float),
+        ("reserved_", C.c_int32),
+    ]
+
+
+class PagedView(C.Structure):
+    _fields_ = [
+        ("k_cache", C.c_void_p), ("v_cache", C.c_void_p), ("pages", C.c_void_p), ("offsets", C.c_void_p),
+        ("kv_lens", C.c_void_p), ("n_pages", C.c_int32), ("page_size", C.c_int32), ("n_seqs", C.c_int32),
+        ("max_pages", C.c_int32), ("page_stride", C.c_int32), ("n_heads_kv", C.c_int32), ("head_dim", C.c_int32),
+        ("n_rows", C.c_int32),
+    ]
+
+
 # name -> (restype, argtypes); every symbol declared in include/tpa.h
 PROTOTYPES = {
     "tpa_tree_pack": (C.c_int, [_i32p, _i64p, C.c_int32, C.c_int32, C.POINTER(C.c_void_p)]),
@@ -100,6 +118,22 @@ PROTOTYPES = {
     "tpa_lm_head_logprobs_entropy": (C.c_int, [C.POINTER(TreeView), C.c_void_p, C.c_void_p, C.c_int32, C.c_int32,
                                                C.c_void_p, C.c_uint64, C.c_void_p, C.c_void_p, C.c_void_p,
                                                C.c_void_p, C.c_void_p]),
+    "tpa_rope_table": (C.c_int, [C.c_void_p, C.c_int32, C.c_int32, C.c_double, C.POINTER(C.c_double), C.c_double,
+                                 C.c_void_p]),
+    "tpa_qk_norm_rope_fwd": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int32, C.c_int64, C.c_void_p, C.c_int64,
+                                       C.c_void_p, C.c_int64, C.POINTER(RopeParams), C.c_void_p, C.c_int64,
+                                       C.c_void_p, C.c_int64, C.c_int32, C.c_int32, C.c_int32, C.c_void_p]),
+    "tpa_qk_norm_rope_bwd_workspace_bytes": (C.c_uint64, [C.c_int32]),
+    "tpa_qk_norm_rope_bwd": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int32, C.c_int64, C.c_void_p, C.c_int64,
+                                       C.c_void_p, C.c_int64, C.c_int32, C.c_void_p, C.c_int64, C.c_void_p,
+                                       C.c_int64, C.POINTER(RopeParams), C.c_void_p, C.c_int64, C.c_void_p,
+                                       C.c_int64, C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p, C.c_uint64,
+                                       C.c_int32, C.c_int32, C.c_int32, C.c_void_p]),
+    "tpa_paged_append": (C.c_int, [C.POINTER(PagedView), C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p,
+                                   C.c_int64, C.c_void_p, C.c_int64, C.c_int32, C.POINTER(RopeParams), C.c_void_p]),
+    "tpa_verify_drafts": (C.c_int, [C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p,
+                                    C.c_void_p, C.c_void_p, C.c_void_p, C.c_int32, C.c_int32, C.c_int32,
+                                    C.c_void_p]),
     "tpa_sync_status": (C.c_int, [C.c_void_p]),
     "tpa_device_check": (C.c_int, []),
     "tpa_wait_probe": (C.c_int, [C.c_uint64, C.c_int32, C.c_void_p]),

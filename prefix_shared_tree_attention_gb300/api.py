@@ -10,7 +10,8 @@ import numpy as np
 import torch
 
 from ._abi import (BALANCE_FFD, BALANCE_KK, GRAD_BF16, GRAD_F32, LOGITS_COMPACT, LOGITS_PADDED, MASK_BITS,
-                   MASK_U8, BlockMaskView, PackingMetrics, TreeInfo, TreeView, check, lib)
+                   MASK_U8, WEIGHT_BF16, WEIGHT_F32, BlockMaskView, PackingMetrics, PagedView, RopeParams, TreeInfo,
+                   TreeView, check, lib)
 
 
 def _stream_ptr(stream) -> int:
@@ -359,6 +360,272 @@ def lm_head_logprobs_entropy(dtree: DeviceTree, hidden: torch.Tensor, weight: to
         workspace.numel() * workspace.element_size(), pl.data_ptr(), pe.data_ptr(), sl.data_ptr(), se.data_ptr(),
         _stream_ptr(stream)))
     return pl, pe, sl, se
+
+
+def _same_device(*tensors) -> torch.device:
+    """The one CUDA device of the tensors given (None is passed over), which
+    must be the current one: the library launches there."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("every tensor must be a CUDA tensor")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError("every tensor must be on one device")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {dev}, which is not the current device")
+    return dev
+
+
+def _head_rows(name: str, t: torch.Tensor, dtypes=(torch.bfloat16,)) -> tuple[int, int, int, int]:
+    """(rows, row stride, heads, d) of a tensor [..., H, d] whose heads are
+    contiguous and whose leading dimensions are evenly spaced rows."""
+    if t.dtype not in dtypes or t.dim() < 3:
+        raise ValueError(f"{name} must be [..., heads, d] of {' or '.join(str(x) for x in dtypes)}")
+    H, d = t.shape[-2:]
+    if t.stride(-1) != 1 or (H > 1 and t.stride(-2) != d):
+        raise ValueError(f"{name} must have its heads and their values contiguous")
+    rows, stride = t.shape[-3], t.stride(-3)
+    if rows == 1:
+        stride = H * d
+    for i in range(t.dim() - 4, -1, -1):
+        if t.shape[i] != 1:
+            if rows == 1:
+                stride = t.stride(i)
+            elif t.stride(i) != rows * stride:
+                raise ValueError(f"the leading dimensions of {name} must be evenly spaced rows")
+            rows *= t.shape[i]
+    return rows, stride, H, d
+
+
+def rope_table(n_positions: int, rot_dim: int, base: float = 10000.0, inv_freq: Sequence[float] | None = None,
+               scale: float = 1.0, device="cuda", out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Cosines and sines of the rotary positions (tpa_rope_table): fp32
+    [n_positions, rot_dim], cos | sin, made once for a model.  ``inv_freq``
+    gives the rot_dim / 2 frequencies in place of ``base`` ** (-2 j / rot_dim)."""
+    fr = None
+    if inv_freq is not None:
+        if len(inv_freq) != rot_dim // 2:
+            raise ValueError("inv_freq must hold rot_dim / 2 frequencies")
+        fr = (C.c_double * len(inv_freq))(*[float(f) for f in inv_freq])
+    if out is None:
+        out = torch.empty((n_positions, rot_dim), dtype=torch.float32, device=device)
+    if out.dtype != torch.float32 or not out.is_contiguous() or tuple(out.shape) != (n_positions, rot_dim):
+        raise ValueError("out must be a contiguous fp32 tensor [n_positions, rot_dim]")
+    _same_device(out)
+    check("tpa_rope_table", lib().tpa_rope_table(out.data_ptr(), int(n_positions), int(rot_dim), float(base), fr,
+                                                 float(scale), _stream_ptr(stream)))
+    return out
+
+
+def _rope_params(table, q_weight, k_weight, eps, interleaved, d) -> RopeParams:
+    p = RopeParams()
+    if table is not None:
+        if table.dtype != torch.float32 or table.dim() != 2 or not table.is_contiguous():
+            raise ValueError("table must be a contiguous fp32 tensor [positions, rot_dim]")
+        p.table, p.table_rows, p.rot_dim = table.data_ptr(), table.shape[0], table.shape[1]
+    if (q_weight is None) != (k_weight is None):
+        raise ValueError("give both norm weights or neither")
+    if q_weight is not None:
+        for w in (q_weight, k_weight):
+            if w.dtype not in _WEIGHT or w.dtype != q_weight.dtype or w.numel() != d or not w.is_contiguous():
+                raise ValueError("norm weights must be contiguous, of d values, both fp32 or both bf16")
+        p.weight_type = _WEIGHT[q_weight.dtype]
+        p.q_weight, p.k_weight = q_weight.data_ptr(), k_weight.data_ptr()
+    p.eps, p.interleaved = eps, 1 if interleaved else 0
+    return p
+
+
+_WEIGHT = {torch.float32: WEIGHT_F32, torch.bfloat16: WEIGHT_BF16}
+
+
+def _positions(positions, rows: int):
+    """(positions pointer, n_tokens pointer, t_pad, device) of an int32 tensor or a packed tree."""
+    if isinstance(positions, DeviceTree):
+        v = positions.view
+        if rows != v.n_trees * v.t_pad:
+            raise ValueError(f"q has {rows} rows; the tree has {v.n_trees} x {v.t_pad} positions")
+        return v.depth, v.n_tokens, v.t_pad, positions.buf
+    if positions.dtype != torch.int32 or not positions.is_contiguous() or positions.numel() != rows:
+        raise ValueError("positions must be a contiguous int32 tensor with one entry a row of q, or a DeviceTree")
+    return positions.data_ptr(), None, 0, positions
+
+
+def qk_norm_rope_fwd(positions: "torch.Tensor | DeviceTree", q: torch.Tensor, k: torch.Tensor, table: torch.Tensor,
+                     q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                     interleaved: bool = False, out: tuple | None = None, stream=None):
+    """RMS norm of every query and key head (with weights) and rotation by
+    position in one pass (tpa_qk_norm_rope_fwd): returns q and k, bf16.
+
+    q [..., Hq, d] and k [..., Hkv, d] bf16 may be slices of a fused
+    projection; ``positions`` is an int32 tensor of their rows (negative:
+    padding, which comes out 0) or a ``DeviceTree`` (token depths; q and k then
+    are [B, T_pad, H, d] and the results go to ``tree_attn_fwd``)."""
+    rows, sq, Hq, d = _head_rows("q", q)
+    rows_k, sk, Hkv, dk = _head_rows("k", k)
+    if rows_k != rows or dk != d:
+        raise ValueError("q and k must have the same rows and head_dim")
+    pos, n_tok, t_pad, pbuf = _positions(positions, rows)
+    rp = _rope_params(table, q_weight, k_weight, eps, interleaved, d)
+    qo, ko = out if out is not None else (torch.empty(q.shape, dtype=q.dtype, device=q.device),
+                                          torch.empty(k.shape, dtype=k.dtype, device=k.device))
+    _same_device(q, k, table, q_weight, k_weight, pbuf, qo, ko)
+    if qo.shape != q.shape or ko.shape != k.shape:
+        raise ValueError("out must be shaped like q and k")
+    _, so, _, _ = _head_rows("out[0]", qo)
+    _, sko, _, _ = _head_rows("out[1]", ko)
+    check("tpa_qk_norm_rope_fwd", lib().tpa_qk_norm_rope_fwd(
+        pos, n_tok, t_pad, rows, q.data_ptr(), sq, k.data_ptr(), sk, C.byref(rp), qo.data_ptr(), so, ko.data_ptr(),
+        sko, Hq, Hkv, d, _stream_ptr(stream)))
+    return qo, ko
+
+
+def qk_norm_rope_bwd(positions: "torch.Tensor | DeviceTree", dq_out: torch.Tensor, dk_out: torch.Tensor,
+                     q: torch.Tensor | None, k: torch.Tensor | None, table: torch.Tensor,
+                     q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                     interleaved: bool = False, grad_dtype: torch.dtype = torch.bfloat16, out: tuple | None = None,
+                     workspace: torch.Tensor | None = None, stream=None):
+    """Gradients of ``qk_norm_rope_fwd`` (tpa_qk_norm_rope_bwd): from those of
+    its outputs (fp32 or bf16, as ``tree_attn_bwd`` returns them) and its inputs
+    q, k (needed with weights only) returns dq, dk of ``grad_dtype`` and the
+    weights' gradients, fp32 (None without weights)."""
+    if grad_dtype not in _GRAD or dq_out.dtype != dk_out.dtype:
+        raise ValueError("gradients must be fp32 or bf16, dq_out and dk_out alike")
+    rows, sgq, Hq, d = _head_rows("dq_out", dq_out, _GRAD)
+    rows_k, sgk, Hkv, dk_ = _head_rows("dk_out", dk_out, _GRAD)
+    if rows_k != rows or dk_ != d:
+        raise ValueError("dq_out and dk_out must have the same rows and head_dim")
+    pos, n_tok, t_pad, pbuf = _positions(positions, rows)
+    rp = _rope_params(table, q_weight, k_weight, eps, interleaved, d)
+    norm = q_weight is not None
+    sq = sk = 0
+    if norm:
+        if q is None or k is None or q.shape != dq_out.shape or k.shape != dk_out.shape:
+            raise ValueError("q and k must be given with the weights, shaped like dq_out and dk_out")
+        sq, sk = _head_rows("q", q)[1], _head_rows("k", k)[1]
+    dev = dq_out.device
+    dq, dk = out if out is not None else (torch.empty(dq_out.shape, dtype=grad_dtype, device=dev),
+                                          torch.empty(dk_out.shape, dtype=grad_dtype, device=dev))
+    if dq.shape != dq_out.shape or dk.shape != dk_out.shape or dq.dtype != grad_dtype or dk.dtype != grad_dtype:
+        raise ValueError("out must be shaped like dq_out and dk_out and of grad_dtype")
+    so, sko = _head_rows("out[0]", dq, _GRAD)[1], _head_rows("out[1]", dk, _GRAD)[1]
+    dwq = dwk = None
+    if norm:
+        dwq, dwk = (torch.empty(d, dtype=torch.float32, device=dev) for _ in range(2))
+        if workspace is None:
+            workspace = torch.empty(int(lib().tpa_qk_norm_rope_bwd_workspace_bytes(d)), dtype=torch.uint8, device=dev)
+    _same_device(dq_out, dk_out, table, q_weight, k_weight, pbuf, dq, dk, workspace, *((q, k) if norm else ()))
+    check("tpa_qk_norm_rope_bwd", lib().tpa_qk_norm_rope_bwd(
+        pos, n_tok, t_pad, rows, dq_out.data_ptr(), sgq, dk_out.data_ptr(), sgk, _GRAD[dq_out.dtype],
+        q.data_ptr() if norm else None, sq, k.data_ptr() if norm else None, sk, C.byref(rp), dq.data_ptr(), so,
+        dk.data_ptr(), sko, _GRAD[grad_dtype], _ptr(dwq), _ptr(dwk), _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), Hq, Hkv, d, _stream_ptr(stream)))
+    return dq, dk, dwq, dwk
+
+
+def _paged_view(k_cache, v_cache, pages, offsets, kv_lens, n_rows: int, d: int) -> PagedView:
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if t.dtype != torch.bfloat16 or t.dim() != 4 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous bf16 tensor [n_pages, Hkv, page_size, d]")
+    if k_cache.shape != v_cache.shape or k_cache.shape[3] != d:
+        raise ValueError("k_cache and v_cache must match, and share head_dim with the new tokens")
+    if pages.dtype != torch.int32 or pages.dim() != 2 or pages.stride(1) != 1:
+        raise ValueError("pages must be an int32 tensor [n_seqs, max_pages] with unit column stride")
+    n = pages.shape[0]
+    for name, t, m in (("offsets", offsets, n + 1), ("kv_lens", kv_lens, n)):
+        if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != m or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 tensor of {m} entries")
+    v = PagedView()
+    v.k_cache, v.v_cache, v.pages = k_cache.data_ptr(), v_cache.data_ptr(), pages.data_ptr()
+    v.offsets, v.kv_lens = offsets.data_ptr(), kv_lens.data_ptr()
+    v.n_pages, v.n_heads_kv, v.page_size, v.head_dim = k_cache.shape
+    v.n_seqs, v.max_pages = pages.shape
+    v.page_stride = pages.stride(0) if n > 1 else max(pages.shape[1], 1)
+    v.n_rows = n_rows
+    return v
+
+
+def paged_append(k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Tensor, offsets: torch.Tensor,
+                 kv_lens: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q: torch.Tensor | None = None,
+                 table: torch.Tensor | None = None, q_weight: torch.Tensor | None = None,
+                 k_weight: torch.Tensor | None = None, eps: float = 1e-6, interleaved: bool = False,
+                 q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+    """Write the new tokens' keys (normed with weights, rotated with a table)
+    and values into a paged cache (tpa_paged_append); with ``q`` also returns
+    the queries, normed and rotated, for ``paged_attn_fwd``.
+
+    Caches are bf16 [n_pages, Hkv, page_size, d]; ``pages`` [n_seqs, max_pages],
+    ``offsets`` [n_seqs + 1] and ``kv_lens`` [n_seqs] (the new tokens included)
+    are int32 device tensors; q, k, v are [tokens, H, d], rows behind
+    offsets[n_seqs] padding (their rows of the result are not written)."""
+    rows, sk, Hkv, d = _head_rows("k", k)
+    if v.shape != k.shape:
+        raise ValueError("k and v must have the same shape")
+    sv = _head_rows("v", v)[1]
+    cache = _paged_view(k_cache, v_cache, pages, offsets, kv_lens, rows, d)
+    if Hkv != cache.n_heads_kv:
+        raise ValueError("k must have the cache's heads")
+    rp = _rope_params(table, q_weight, k_weight, eps, interleaved, d)
+    sq = so = Hq = 0
+    if q is not None:
+        rows_q, sq, Hq, dq = _head_rows("q", q)
+        if rows_q != rows or dq != d:
+            raise ValueError("q must have the rows and head_dim of k")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must be shaped like q")
+        so = _head_rows("q_out", q_out)[1]
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _same_device(k, v, q, q_out, k_cache, v_cache, pages, offsets, kv_lens, table, q_weight, k_weight)
+    check("tpa_paged_append", lib().tpa_paged_append(C.byref(cache), k.data_ptr(), sk, v.data_ptr(), sv, _ptr(q), sq,
+                                                     _ptr(q_out), so, Hq, C.byref(rp), _stream_ptr(stream)))
+    return q_out
+
+
+def verify_drafts(target_probs: torch.Tensor, draft_tokens: torch.Tensor, u_accept: torch.Tensor,
+                  u_next: torch.Tensor, draft_probs: torch.Tensor | None = None,
+                  n_drafts: torch.Tensor | None = None, out: tuple | None = None, stream=None):
+    """Accept or reject drafted tokens against the policy's probabilities and
+    draw the next token, from given uniform numbers (tpa_verify_drafts).
+
+    target_probs [S, K+1, V] and draft_probs [S, K, V] fp32 (None: drafts
+    without probabilities), draft_tokens [S, K] int32, n_drafts [S] int32 (None:
+    K each), u_accept [S, K] and u_next [S] fp32 in [0, 1).  Returns tokens
+    [S, K+1] int32 (the accepted drafts, the drawn token, then -1) and the
+    number accepted [S] int32."""
+    if target_probs.dim() != 3 or draft_tokens.dim() != 2:
+        raise ValueError("target_probs must be [S, K+1, V] and draft_tokens [S, K]")
+    S, K1, V = target_probs.shape
+    K = K1 - 1
+    for name, t, shape, dt in (("draft_tokens", draft_tokens, (S, K), torch.int32),
+                               ("u_accept", u_accept, (S, K), torch.float32), ("u_next", u_next, (S,), torch.float32),
+                               ("n_drafts", n_drafts, (S,), torch.int32)):
+        if t is not None and (t.dtype != dt or tuple(t.shape) != shape or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous {dt} tensor of shape {shape}")
+    for name, t, k in (("target_probs", target_probs, K1), ("draft_probs", draft_probs, K)):
+        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (S, k, V) or
+                              (V > 1 and t.stride(2) != 1) or (k > 1 and t.stride(1) != V)):
+            raise ValueError(f"{name} must be fp32 [{S}, {k}, {V}] with contiguous sequences")
+    if out is None:
+        out = (torch.empty((S, K1), dtype=torch.int32, device=target_probs.device),
+               torch.empty(S, dtype=torch.int32, device=target_probs.device))
+    tokens, n_accepted = out
+    if (tokens.dtype != torch.int32 or tuple(tokens.shape) != (S, K1) or not tokens.is_contiguous() or
+            n_accepted.dtype != torch.int32 or tuple(n_accepted.shape) != (S,) or not n_accepted.is_contiguous()):
+        raise ValueError("out must be contiguous int32 tensors [S, K+1] and [S]")
+    _same_device(target_probs, draft_tokens, u_accept, u_next, draft_probs, n_drafts, tokens, n_accepted)
+    ts = target_probs.stride(0) if S > 1 else K1 * V
+    ds = 0 if draft_probs is None else draft_probs.stride(0) if S > 1 else K * V
+    check("tpa_verify_drafts", lib().tpa_verify_drafts(
+        target_probs.data_ptr(), ts, _ptr(draft_probs) if K else None, ds, draft_tokens.data_ptr(), _ptr(n_drafts),
+        u_accept.data_ptr(), u_next.data_ptr(), tokens.data_ptr(), n_accepted.data_ptr(), S, K, V,
+        _stream_ptr(stream)))
+    return tokens, n_accepted
 
 
 def sync_status(stream=None) -> None:
