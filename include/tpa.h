@@ -609,6 +609,39 @@ int tpa_paged_append(const tpa_paged_view* cache, const void* k, int64_t k_strid
                      const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride, int32_t n_heads_q,
                      const tpa_rope_params* rope, void* stream);
 
+/* Workspace bytes of tpa_paged_attn_fwd (the parts of tiles whose keys are
+ * split over several CTAs; independent of the batch); 0 on invalid arguments. */
+uint64_t tpa_paged_attn_workspace_bytes(int32_t max_q_len, int32_t n_heads_q, int32_t n_heads_kv,
+                                        int32_t head_dim);
+
+/*
+ * tpa_paged_attn_fwd — attention of the new tokens over their sequences' pages
+ * (after tpa_paged_append has written theirs): with pos = kv_lens[s] - (new
+ * tokens of s) + i for the i-th of them and query head h on key/value head
+ * h / (Hq / Hkv),
+ *   O = sum_j softmax_j(scale q . k_j) v_j over the keys j <= pos, and
+ *   j > pos - window when window > 0;  LSE = log sum_j exp(scale q . k_j).
+ * A token that sees no key (pos < 0: more new tokens than cached ones) gets
+ * O = 0 and LSE = -inf.  Slots that no token of the batch sees may hold
+ * anything, NaN included, and pages that hold only such slots are not read
+ * (their table entries may be anything); the keys and values of seen slots
+ * must be finite.
+ *   q [n_rows, Hq, d] bf16, rows q_stride elements apart (a multiple of 8), 16-byte aligned
+ *   o [n_rows, Hq, d] bf16, lse [n_rows, Hq] fp32 (written, rows behind the last sequence not)
+ *   Hq / Hkv <= 32
+ *   max_q_len: the most new tokens of a sequence; larger ones stay right but the
+ *     kernel is chosen by it.  softmax_scale <= 0 selects 1/sqrt(d).
+ *   workspace: tpa_paged_attn_workspace_bytes() bytes, 256-byte aligned, of one
+ *     call at a time (two calls, or graphs, that may run together need two)
+ * fp32 sums and statistics; probabilities are bf16 operands of the second
+ * product.  Deterministic.  Two kernels on `stream`.  Errors:
+ * TPA_ERR_INVALID_ARG, TPA_ERR_BUFFER_TOO_SMALL, TPA_ERR_UNSUPPORTED_DEVICE,
+ * TPA_ERR_CUDA.
+ */
+int tpa_paged_attn_fwd(const tpa_paged_view* cache, const void* q, int64_t q_stride, void* o, float* lse,
+                       int32_t n_heads_q, int32_t max_q_len, float softmax_scale, int32_t window,
+                       void* workspace, uint64_t workspace_bytes, void* stream);
+
 /* ------------------------------------------------------------------------ */
 /* Drafted tokens (speculative sampling): the policy's probabilities decide
  * how many of a sequence's drafted tokens stand, and the next one is drawn.  */

@@ -20,7 +20,7 @@ the C names without the ``tpa_`` prefix:
 from ._abi import BLOCK_SIZE, LOGITS_COMPACT, LOGITS_PADDED, STATUS, TpaError, lib  # noqa: F401
 from .api import (  # noqa: F401
     BlockMask, DeviceTree, Tree, balance, block_classify, dense_mask, device_check, extract_sequences,
-    lm_head_logprobs_entropy, lm_head_workspace_bytes, packing_metrics, paged_append, qk_norm_rope_bwd,
-    qk_norm_rope_fwd, rope_table, sync_status, tree_attn_bwd, tree_pack_padded,
+    lm_head_logprobs_entropy, lm_head_workspace_bytes, packing_metrics, paged_append,
+    paged_attn_fwd, paged_attn_workspace_bytes, qk_norm_rope_bwd, qk_norm_rope_fwd, rope_table, sync_status, tree_attn_bwd, tree_pack_padded,
     tree_attn_bwd_workspace_bytes, tree_attn_fwd, tree_logprobs_entropy, tree_pack, verify_drafts, wait_probe,
 )

@@ -131,6 +131,9 @@ PROTOTYPES = {
                                        C.c_int32, C.c_int32, C.c_int32, C.c_void_p]),
     "tpa_paged_append": (C.c_int, [C.POINTER(PagedView), C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p,
                                    C.c_int64, C.c_void_p, C.c_int64, C.c_int32, C.POINTER(RopeParams), C.c_void_p]),
+    "tpa_paged_attn_workspace_bytes": (C.c_uint64, [C.c_int32, C.c_int32, C.c_int32, C.c_int32]),
+    "tpa_paged_attn_fwd": (C.c_int, [C.POINTER(PagedView), C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_int32,
+                                     C.c_int32, C.c_float, C.c_int32, C.c_void_p, C.c_uint64, C.c_void_p]),
     "tpa_verify_drafts": (C.c_int, [C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p,
                                     C.c_void_p, C.c_void_p, C.c_void_p, C.c_int32, C.c_int32, C.c_int32,
                                     C.c_void_p]),

@@ -587,6 +587,43 @@ def paged_append(k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Tens
     return q_out
 
 
+def paged_attn_workspace_bytes(max_q_len: int, n_heads_q: int, n_heads_kv: int, head_dim: int) -> int:
+    return int(lib().tpa_paged_attn_workspace_bytes(int(max_q_len), int(n_heads_q), int(n_heads_kv), int(head_dim)))
+
+
+def paged_attn_fwd(k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Tensor, offsets: torch.Tensor,
+                   kv_lens: torch.Tensor, q: torch.Tensor, max_q_len: int, softmax_scale: float | None = None,
+                   window: int = 0, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                   workspace: torch.Tensor | None = None, stream=None):
+    """Attention of each sequence's new tokens over its pages, causal at the
+    sequence's end (tpa_paged_attn_fwd): returns O [tokens, Hq, d] bf16 and LSE
+    [tokens, Hq] fp32.
+
+    The batch is described as for ``paged_append``, which is called first (its
+    result is ``q``); ``max_q_len`` is the most new tokens of any sequence and
+    ``window`` limits each token to that many keys (0: all)."""
+    rows, sq, Hq, d = _head_rows("q", q)
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, Hq, d]")
+    cache = _paged_view(k_cache, v_cache, pages, offsets, kv_lens, rows, d)
+    o = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else out
+    if lse is None:
+        lse = torch.empty((rows, Hq), dtype=torch.float32, device=q.device)
+    if o.shape != q.shape or o.dtype != q.dtype or not o.is_contiguous():
+        raise ValueError("out must be contiguous bf16 shaped like q")
+    if tuple(lse.shape) != (rows, Hq) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous fp32 tensor [tokens, Hq]")
+    if workspace is None:
+        workspace = torch.empty(paged_attn_workspace_bytes(max_q_len, Hq, cache.n_heads_kv, d), dtype=torch.uint8,
+                                device=q.device)
+    _same_device(q, o, lse, workspace, k_cache, v_cache, pages, offsets, kv_lens)
+    check("tpa_paged_attn_fwd", lib().tpa_paged_attn_fwd(
+        C.byref(cache), q.data_ptr(), sq, o.data_ptr(), lse.data_ptr(), Hq, int(max_q_len),
+        float(softmax_scale or 0.0), int(window), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _stream_ptr(stream)))
+    return o, lse
+
+
 def verify_drafts(target_probs: torch.Tensor, draft_tokens: torch.Tensor, u_accept: torch.Tensor,
                   u_next: torch.Tensor, draft_probs: torch.Tensor | None = None,
                   n_drafts: torch.Tensor | None = None, out: tuple | None = None, stream=None):

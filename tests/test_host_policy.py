@@ -119,6 +119,34 @@ def test_append_of_nothing(tpa):
     assert _append(tpa.lib(), _paged(n_rows=0)) == 0
 
 
+def _attend(L, view, q=P, sq=256, o=P, lse=P, hq=4, max_q=5, scale=0.0, window=0, ws=P, nbytes=1 << 30):
+    return L.tpa_paged_attn_fwd(C.byref(view), q, sq, o, lse, hq, max_q, scale, window, ws, nbytes, None)
+
+
+@pytest.mark.parametrize("kw", BAD_PAGED)
+def test_attend_view_refusals(tpa, kw):
+    assert _attend(tpa.lib(), _paged(**kw)) == BAD
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(q=None), BAD), (dict(o=None), BAD), (dict(lse=None), BAD), (dict(ws=None), BAD), (dict(q=P + 8), BAD),
+    (dict(o=P + 4), BAD), (dict(lse=P + 2), BAD), (dict(ws=P + 128), BAD), (dict(sq=128), BAD), (dict(sq=257), BAD),
+    (dict(hq=3), BAD), (dict(hq=0), BAD), (dict(max_q=0), BAD), (dict(window=-1), BAD),
+    (dict(scale=float("nan")), BAD), (dict(scale=float("inf")), BAD), (dict(nbytes=1000), -8)])
+def test_attend_refusals(tpa, kw, status):
+    assert _attend(tpa.lib(), _paged(), **kw) == status
+
+
+def test_attend_of_nothing(tpa):
+    assert _attend(tpa.lib(), _paged(n_rows=0)) == 0
+
+
+def test_attend_workspace_bytes(tpa):
+    f = tpa.paged_attn_workspace_bytes
+    assert 0 < f(1, 32, 8, 64) < f(1, 32, 8, 128) and f(1, 32, 8, 128) <= f(5, 32, 8, 128)
+    assert f(0, 8, 8, 128) == f(1, 6, 4, 128) == f(1, 8, 8, 96) == f(1, 0, 8, 64) == 0
+
+
 def _verify(L, target=P, ts=300, draft=None, ds=0, toks=P, nd=None, ua=P, un=P, out=P, acc=P, S=2, K=2, V=100):
     return L.tpa_verify_drafts(target, ts, draft, ds, toks, nd, ua, un, out, acc, S, K, V, None)
 
@@ -157,6 +185,11 @@ def test_python_refusals(tpa):
                 dict(kv_lens=i32(3)), dict(v=k[:2]), dict(q=q[:3]), dict(q_out=q), dict(k=k[:, :1], v=k[:, :1]), dict()):
         with pytest.raises(ValueError):
             tpa.paged_append(**{**good, **bad})
+    good = {x: good[x] for x in ("k_cache", "v_cache", "pages", "offsets", "kv_lens")} | dict(q=q, max_q_len=2)
+    for bad in (dict(q=q[None]), dict(q=q.float()), dict(out=q.float()), dict(out=q[:3]), dict(lse=torch.zeros(4)),
+                dict(lse=torch.zeros((4, 4), dtype=torch.float64)), dict(pages=i32(2, 3)[:, ::2]), dict()):
+        with pytest.raises(ValueError):
+            tpa.paged_attn_fwd(**{**good, **bad})
     p, x, u, n = torch.zeros((2, 3, 10)), i32(2, 2), torch.zeros((2, 2)), torch.zeros(2)
     for bad in (dict(target_probs=p.double()), dict(target_probs=p[:, :, ::2]), dict(draft_tokens=x.long()),
                 dict(u_accept=u[:, :1]), dict(u_next=u), dict(draft_probs=p), dict(n_drafts=i32(3)), dict()):
