@@ -34,6 +34,7 @@ int tpa_internal_status_lmh(bool clear);
 int tpa_internal_status_rope(bool clear);
 int tpa_internal_status_verify(bool clear);
 int tpa_internal_status_paged(bool clear);
+int tpa_internal_status_ptile(bool clear);
 
 // The per-sequence gather of the log-prob pass (logprobs.cu), shared with
 // the fused LM-head path: seq_entropy[t] = pos_entropy[position of token t],

@@ -25,21 +25,6 @@ __device__ unsigned int g_status_paged = 0;
 
 using namespace paged;
 
-constexpr uint32_t kSmemMax = 232448;  // 227 KB opt-in per CTA
-
-struct Params {
-  Batch b;
-  const __nv_bfloat16* q;
-  __nv_bfloat16* o;
-  float* lse;
-  float* part_o;    // [2 grid][R][D]: sums relative to the row's own maximum
-  float2* part_ml;  // [2 grid][R]: maximum (log2 units) and sum
-  Split* split;     // [grid]
-  int64_t q_stride;
-  int32_t hq, min_steps;
-  float scale_log2;
-};
-
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -57,25 +42,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// 2-D tiled load: 64 columns x 16 rows into a swizzled tile
-__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* m, uint64_t* bar, int c0, int c1) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
-          tc::smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(tc::smem_u32(bar)), "r"(c0), "r"(c1)
-      : "memory");
-}
-
-// Writes the record of the tile that this CTA's first segment is a part of.
-__device__ __forceinline__ void write_split(const Params& p, const Walk& w, long long total, int n_ctas) {
-  Split s = {};
-  if (w.begin > 0) {  // the tile began in an earlier CTA
-    const int c0 = cta_of(total, n_ctas, w.item), c1 = cta_of(total, n_ctas, w.item + w.t.steps - 1);
-    if (c0 + 1 == int(blockIdx.x)) s = Split{1, w.head, w.t.first, w.t.n, c0, c1, {0, 0}};
-  }
-  p.split[blockIdx.x] = s;
 }
 
 // ------------------------------------------------------------------ few rows
@@ -498,21 +464,12 @@ int num_sms() {
   return sms;
 }
 
-// Cache rows as a matrix [n_pages * Hkv * page_size, d]: boxes of 64 columns x `rows` rows.
-bool cache_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t d, uint32_t box_rows) {
-  tmap::EncodeTiledFn fn = tmap::encode_fn();
-  if (!fn) return false;
-  const cuuint64_t dims[2] = {d, rows};
-  const cuuint64_t strides[1] = {d * 2};
-  const cuuint32_t box[2] = {64, box_rows};
-  const cuuint32_t estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+// Rows of a tile: 16 or 32 (m16n8k16) while every sequence's queries fit in
+// them, else tcgen05 tiles of 128, or pairs of them when that leaves them full.
+int tile_rows(int64_t max_q, int group) {
+  const int64_t rows = max_q * group;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : 256;
 }
-
-// Rows of a tile: 16 while every sequence's queries fit in them, else 32.
-int tile_rows(int64_t max_q, int group) { return max_q * group <= 16 ? 16 : 32; }
 
 uint64_t part_bytes(int rows, int d) {
   return uint64_t(2) * kMaxGrid * rows * (uint64_t(d) * 4 + 8) + uint64_t(kMaxGrid) * sizeof(Split);
@@ -595,6 +552,7 @@ extern "C" int tpa_paged_attn_fwd(const tpa_paged_view* cache, const void* q, in
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
   p.hq = n_heads_q;
+  p.rows = R;
   p.scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf(float(d))) * kLog2e;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.part_o = reinterpret_cast<float*>(ws);
@@ -602,6 +560,11 @@ extern "C" int tpa_paged_attn_fwd(const tpa_paged_view* cache, const void* q, in
   p.split = reinterpret_cast<Split*>(ws + uint64_t(2) * kMaxGrid * R * (uint64_t(d) * 4 + 8));
   const int sms = num_sms(), grid = sms < kMaxGrid ? sms : kMaxGrid;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (R >= 128) {
+    const int rt = tpa_internal_paged_tile(cache, p, R, grid, st);
+    if (rt != TPA_OK) return rt;
+    return d == 128 ? launch_join<128>(p, grid, R, st) : launch_join<64>(p, grid, R, st);
+  }
   if (d == 128) return R == 16 ? launch_rows<128, 1>(cache, p, grid, st) : launch_rows<128, 2>(cache, p, grid, st);
   return R == 16 ? launch_rows<64, 1>(cache, p, grid, st) : launch_rows<64, 2>(cache, p, grid, st);
 }

@@ -11,16 +11,20 @@
 // lengths are read from device memory by every CTA (a scan over the
 // sequences), so nothing of the partition is computed on the host.
 #pragma once
+#include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
 
 #include "device_common.cuh"
 #include "tc.cuh"
+#include "tmap.h"
 
 namespace paged {
 
 constexpr int kStep = 128;     // keys of a step
+constexpr uint32_t kSmemMax = 232448;  // 227 KB opt-in per CTA
 constexpr int kMaxGrid = 160;  // CTAs of a launch, at most (one an SM)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -198,4 +202,53 @@ struct Split {
   int32_t valid, head, first, n, c0, c1, pad_[2];
 };
 
+struct Params {
+  Batch b;
+  const __nv_bfloat16* q;
+  __nv_bfloat16* o;
+  float* lse;
+  float* part_o;    // [2 grid][R][D]: sums relative to the row's own maximum
+  float2* part_ml;  // [2 grid][R]: maximum (log2 units) and sum
+  Split* split;     // [grid]
+  int64_t q_stride;
+  int32_t hq, min_steps, rows;  // rows: R, of a part
+  float scale_log2;
+};
+
+// 2-D tiled load: a box of 64 columns into 128-byte swizzled rows
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* m, uint64_t* bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+          tc::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(tc::smem_u32(bar)), "r"(c0), "r"(c1)
+      : "memory");
+}
+
+// Writes the record of the tile that this CTA's first segment is a part of.
+__device__ __forceinline__ void write_split(const Params& p, const Walk& w, long long total, int n_ctas) {
+  Split s = {};
+  if (w.begin > 0) {  // the tile began in an earlier CTA
+    const int c0 = cta_of(total, n_ctas, w.item), c1 = cta_of(total, n_ctas, w.item + w.t.steps - 1);
+    if (c0 + 1 == int(blockIdx.x)) s = Split{1, w.head, w.t.first, w.t.n, c0, c1, {0, 0}};
+  }
+  p.split[blockIdx.x] = s;
+}
+
+// Cache rows as a matrix [n_pages * Hkv * page_size, d]: boxes of 64 columns x `rows` rows.
+inline bool cache_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t d, uint32_t box_rows) {
+  tmap::EncodeTiledFn fn = tmap::encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {d, rows};
+  const cuuint64_t strides[1] = {d * 2};
+  const cuuint32_t box[2] = {64, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace paged
+
+// paged_tile.cu: launches the attention kernel for tiles of `rows` (128 or 256)
+// rows; the caller joins split tiles afterwards.
+int tpa_internal_paged_tile(const tpa_paged_view* cache, paged::Params& p, int rows, int grid, cudaStream_t stream);

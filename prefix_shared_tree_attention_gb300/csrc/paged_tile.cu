@@ -1,0 +1,522 @@
+// Paged attention for many rows (chunks of a prompt): tcgen05 tiles.
+//
+// A tile is NH sub-tiles of 128 rows, row r = token * group + head, so a K/V
+// tile of 128 keys is read once for NH * 128 / group tokens of all the group's
+// heads.  The roles and the softmax are those of the tree attention's forward:
+//   warpgroup h < NH  softmax of sub-tile h: thread r owns row r (TMEM lane r),
+//                     online in the log2 domain; P goes to TMEM over S as the
+//                     bf16 operand of the second MMA; O is rescaled in TMEM
+//                     only when a row's maximum has grown by 2^8
+//   warp 4 NH         one thread: walks this CTA's steps, hands each segment to
+//                     the other roles, loads Q, and the pages of K and V (a
+//                     page of 16 to 128 slots is a box; one of 128-byte rows
+//                     swizzled as the MMA descriptors want)
+//   warp 4 NH + 1     one thread issues the MMAs
+// Bound by the tensor and exponential pipes: 4 d operations and one exponential
+// for each (row, key).
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "device_common.cuh"
+#include "internal.h"
+#include "paged_common.cuh"
+#include "tc.cuh"
+#include "tmap.h"
+
+namespace {
+
+__device__ unsigned int g_status_ptile = 0;
+
+using namespace paged;
+using tc::add2;
+using tc::f2;
+using tc::fma2;
+using tc::unf2;
+
+constexpr uint32_t kChunk = 128 * 128;  // bytes of a 128-row x 64-column bf16 tile
+
+// One CTA's part of a tile, as the producer hands it to the other roles.
+struct Segment {
+  int32_t n_it;  // steps; -1: no more
+  int32_t head, first, n, pos0, lo, hi, key0, whole, slot;
+  int32_t pad_[2];
+};
+
+template <int D, int NH>
+struct TileCfg {
+  static constexpr int NCH = D / 64;
+  static constexpr uint32_t TILE = NCH * kChunk;  // 128 x D bf16
+  static constexpr int NS_FIT = int((kSmemMax - 1024 - 4096 - NH * TILE) / (2 * TILE));
+  static constexpr int NS = NS_FIT > 3 ? 3 : NS_FIT;  // K and V ring depth
+  static constexpr uint32_t OFF_Q = 0;
+  static constexpr uint32_t OFF_K = OFF_Q + NH * TILE;
+  static constexpr uint32_t OFF_V = OFF_K + NS * TILE;
+  static constexpr uint32_t OFF_SCAN = OFF_V + NS * TILE;
+  static constexpr uint32_t OFF_SEG = OFF_SCAN + 2112;
+  static constexpr uint32_t OFF_BAR = OFF_SEG + 128;
+  // q_full, q_empty, k_full[NS], k_empty[NS], v_full[NS], v_empty[NS], s_full[NH], p_full[NH], o_free[NH],
+  // o_final, drain, seg_full[2], seg_empty[2]
+  static constexpr int NBAR = 2 + 4 * NS + 3 * NH + 2 + 4;
+  static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr uint32_t BYTES = OFF_MISC + 16 + 1024;
+  // Two sub-tiles: registers move from the producer/issuer warpgroup to the
+  // softmax warpgroups, within what the CTA was launched with.
+  static constexpr int THREADS = NH == 2 ? 384 : 256;
+  static constexpr int REG_LAUNCH = 168, REG_LOW = 120, REG_HIGH = 184;
+  static_assert(NH != 2 || REG_HIGH * 256 + REG_LOW * 128 <= REG_LAUNCH * 384, "register split");
+  static constexpr uint32_t TMEM_COLS = NH == 2 ? 512 : 256;
+  static_assert(sizeof(Scan) <= 2112 && sizeof(Segment) * 2 <= 128 && NS >= 2, "layout");
+  static_assert(BYTES <= kSmemMax, "shared memory budget");
+};
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// O (+)= P V with P read from TMEM
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+template <int D, int NH>
+__global__ void __launch_bounds__(TileCfg<D, NH>::THREADS, 1)
+    paged_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const Params p) {
+  using C = TileCfg<D, NH>;
+  constexpr int NCH = C::NCH, NS = C::NS;
+  constexpr uint32_t TILE = C::TILE;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem + C::OFF_Q;
+  uint8_t* sK = smem + C::OFF_K;
+  uint8_t* sV = smem + C::OFF_V;
+  Scan* sc = reinterpret_cast<Scan*>(smem + C::OFF_SCAN);
+  volatile Segment* seg_ring = reinterpret_cast<volatile Segment*>(smem + C::OFF_SEG);
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* k_full = q_full + 2;
+  uint64_t* k_empty = k_full + NS;
+  uint64_t* v_full = k_empty + NS;
+  uint64_t* v_empty = v_full + NS;
+  uint64_t* s_full = v_empty + NS;
+  uint64_t* p_full = s_full + NH;
+  uint64_t* o_free = p_full + NH;
+  uint64_t* o_final = o_free + NH;
+  uint64_t* drain = o_final + 1;
+  uint64_t* seg_full = drain + 1;   // [2]
+  uint64_t* seg_empty = drain + 3;  // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+
+  const int warp = threadIdx.x >> 5;
+  constexpr int W_TMA = 4 * NH, W_MMA = 4 * NH + 1;
+  const int sub_tok = p.b.tile_tok / NH;  // tokens of a sub-tile
+
+  tc::grid_launch_dependents();  // the joining kernel waits for this one's end by itself
+  if (threadIdx.x == 0) {
+    tc::mbar_init(q_full, 1);
+    tc::mbar_init(q_empty, 1);
+    for (int s = 0; s < NS; ++s) {
+      tc::mbar_init(k_full + s, 1);
+      tc::mbar_init(k_empty + s, 1);
+      tc::mbar_init(v_full + s, 1);
+      tc::mbar_init(v_empty + s, 1);
+    }
+    for (int h = 0; h < NH; ++h) {
+      tc::mbar_init(s_full + h, 1);
+      tc::mbar_init(p_full + h, 128);
+      tc::mbar_init(o_free + h, 128);
+    }
+    tc::mbar_init(o_final, 1);
+    tc::mbar_init(drain, 1);
+    for (int s = 0; s < 2; ++s) {
+      tc::mbar_init(seg_full + s, 1);
+      tc::mbar_init(seg_empty + s, 1 + 128 * NH);
+    }
+    *abort_flag = 0;
+    tc::fence_mbar_init();
+  }
+  const long long per_head = scan_batch(p.b, sc, &g_status_ptile);
+  const long long total = per_head * p.b.hkv;
+  const int n_ctas = used_ctas(total, gridDim.x, p.min_steps);
+  if (int(blockIdx.x) >= n_ctas) {
+    if (threadIdx.x == 0) p.split[blockIdx.x].valid = 0;
+    return;
+  }
+  if (warp == W_MMA) tc::tmem_alloc(tmem_slot, C::TMEM_COLS);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp >= W_TMA) {
+    if constexpr (NH == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REG_LOW));
+    if (warp == W_TMA) {
+      // ---------------------------------------------------------- producer
+      if (tc::elect_one()) {
+        tc::tma_prefetch_desc(&tm_q);
+        tc::tma_prefetch_desc(&tm_k);
+        tc::tma_prefetch_desc(&tm_v);
+        auto wait1 = [&](uint64_t* b_, uint32_t par) { return tc::mbar_wait(b_, par, abort_flag, &g_status_ptile); };
+        const long long f0 = cta_begin(total, n_ctas, blockIdx.x), f1 = cta_begin(total, n_ctas, blockIdx.x + 1);
+        Walk w;
+        w.start(p.b, sc, per_head, f0, f1 - f0);
+        write_split(p, w, total, n_ctas);
+        const int per_step = kStep >> p.b.page_shift;       // pages of a step
+        const uint32_t page_bytes = uint32_t(128) << p.b.page_shift;  // of one 64-column piece
+        const uint32_t q_bytes = uint32_t(NH * NCH) * sub_tok * p.b.group * 128;
+        int kt = 0, vt = 0;
+        bool ok = true, more = w.end > w.begin;
+        for (int k = 0; ok; ++k) {
+          if (!(ok = wait1(seg_empty + (k & 1), ((k >> 1) & 1) ^ 1))) break;
+          volatile Segment* sg = seg_ring + (k & 1);
+          const int n_it = more ? w.end - w.begin : -1;
+          const int key0 = (w.t.step0 + w.begin) * kStep;
+          sg->n_it = n_it;
+          sg->head = w.head;
+          sg->first = w.t.first;
+          sg->n = w.t.n;
+          sg->pos0 = w.t.pos0;
+          sg->lo = w.t.lo;
+          sg->hi = w.t.hi;
+          sg->key0 = key0;
+          sg->whole = w.begin == 0 && w.end == w.t.steps;
+          sg->slot = blockIdx.x * 2 + (w.begin == 0 ? 1 : 0);
+          tc::mbar_arrive(seg_full + (k & 1));
+          if (!more) break;
+          if (!(ok = wait1(q_empty, (k & 1) ^ 1))) break;
+          tc::mbar_arrive_expect_tx(q_full, q_bytes);
+          for (int h = 0; h < NH; ++h)
+            for (int c = 0; c < NCH; ++c)
+              tc::tma_load_3d(sQ + h * TILE + c * kChunk, &tm_q, q_full, c * 64, w.head * p.b.group,
+                              w.t.first + h * sub_tok);
+          const int32_t* row = p.b.pages + int64_t(w.seq) * p.b.page_stride;
+          const int lo = w.t.lo, hi = w.t.hi, head = w.head;
+          // K runs ahead of V by one step: the MMAs need K(j+1) before V(j)
+          int kj = 0, vj = 0;
+          while (kj < n_it || vj < n_it) {
+            const bool do_k = kj < n_it && kj <= vj + 1;
+            const int j = do_k ? kj : vj;
+            const int key = key0 + j * kStep;
+            int pg[8], n_pg = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int ki = key + (i << p.b.page_shift);
+              const bool need = i < per_step && ki < hi && ki + p.b.page_size > lo;
+              pg[i] = need ? __ldg(row + (ki >> p.b.page_shift)) : -1;
+              if (need && (pg[i] < 0 || pg[i] >= p.b.n_pages)) {  // never followed: page 0 is read in its place
+                atomicOr(&g_status_ptile, TPA_DEV_BAD_INPUT);
+                pg[i] = 0;
+              }
+              n_pg += need;
+            }
+            const int gx = (do_k ? kt : vt) + j, s = gx % NS;
+            if (!(ok = wait1((do_k ? k_empty : v_empty) + s, ((gx / NS) & 1) ^ 1))) break;
+            uint64_t* fb = (do_k ? k_full : v_full) + s;
+            uint8_t* dst = (do_k ? sK : sV) + s * TILE;
+            tc::mbar_arrive_expect_tx(fb, n_pg * NCH * page_bytes);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if (pg[i] < 0) continue;
+              const int r0 = (pg[i] * p.b.hkv + head) << p.b.page_shift;
+#pragma unroll
+              for (int c = 0; c < NCH; ++c)
+                tma_load_2d(dst + c * kChunk + i * page_bytes, do_k ? &tm_k : &tm_v, fb, c * 64, r0);
+            }
+            if (do_k) ++kj; else ++vj;
+          }
+          kt += kj;
+          vt += vj;
+          if (ok) more = w.next(p.b);
+        }
+        if (*abort_flag) {  // let the copies already issued land before the CTA exits
+          volatile int never = 0;
+          for (int j = (kt > NS ? kt - NS : 0); j < kt; ++j)
+            tc::mbar_wait(k_full + (j % NS), (j / NS) & 1, &never, &g_status_ptile, 100000000ull);
+          for (int j = (vt > NS ? vt - NS : 0); j < vt; ++j)
+            tc::mbar_wait(v_full + (j % NS), (j / NS) & 1, &never, &g_status_ptile, 100000000ull);
+        }
+      }
+      __syncwarp();
+    } else if (warp == W_MMA) {
+      // ---------------------------------------------------------- MMA issuer
+      constexpr uint32_t idesc_qk = tc::idesc_bf16(128, 128, false, false);
+      constexpr uint32_t idesc_pv = tc::idesc_bf16(128, D, false, true);
+      const uint64_t dQ = tc::smem_desc(tc::smem_u32(sQ), 16, 1024);
+      const uint64_t dK = tc::smem_desc(tc::smem_u32(sK), 16, 1024);
+      const uint64_t dV = tc::smem_desc(tc::smem_u32(sV), kChunk, 1024);
+      auto issue_s = [&](int h, int s) {  // S_h = Q_h K(s)^T
+        const uint64_t qa = dQ + ((h * TILE) >> 4), kb_ = dK + ((s * TILE) >> 4);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = ((k >> 2) * kChunk + (k & 3) * 32) >> 4;
+          tc::mma_ss(tmem + h * 128, qa + off, kb_ + off, idesc_qk, k > 0);
+        }
+        tc::mma_commit(s_full + h);
+      };
+      auto issue_pv = [&](int h, int s, bool first) {  // O_h (+)= P_h V(s)
+        const uint64_t vb = dV + ((s * TILE) >> 4);
+#pragma unroll
+        for (int k = 0; k < kStep / 16; ++k)
+          mma_ts(tmem + 128 * NH + h * 128, tmem + h * 128 + k * 8, vb + ((k * 2048) >> 4), idesc_pv,
+                 (!first || k > 0) ? 1u : 0u);
+      };
+      auto wait1 = [&](uint64_t* b_, uint32_t par) { return tc::mbar_wait(b_, par, abort_flag, &g_status_ptile); };
+      if (tc::elect_one()) {
+        int t = 0;  // steps so far
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+          if (!(ok = wait1(seg_full + (k & 1), (k >> 1) & 1))) break;
+          const int n_it = seg_ring[k & 1].n_it;
+          tc::mbar_arrive(seg_empty + (k & 1));
+          if (n_it < 0) break;
+          if (!(ok = wait1(q_full, k & 1) && wait1(k_full + t % NS, (t / NS) & 1))) break;
+          tc::tc_fence_after();
+          for (int h = 0; h < NH; ++h) issue_s(h, t % NS);
+          tc::mma_commit(k_empty + t % NS);
+          if (n_it == 1) tc::mma_commit(q_empty);
+          for (int j = 0; ok && j < n_it; ++j) {
+            const int g = t + j, sv = g % NS, s1 = (g + 1) % NS;
+            const bool more = j + 1 < n_it;
+            if (!(ok = wait1(v_full + sv, (g / NS) & 1))) break;
+            for (int h = 0; h < NH && ok; ++h) {
+              if (!(ok = wait1(p_full + h, g & 1))) break;
+              if (j == 0 && k > 0 && !(ok = wait1(o_free + h, (k - 1) & 1))) break;
+              tc::tc_fence_after();
+              issue_pv(h, sv, j == 0);
+              if (more) {
+                if (h == 0 && !(ok = wait1(k_full + s1, ((g + 1) / NS) & 1))) break;
+                tc::tc_fence_after();
+                issue_s(h, s1);
+              }
+            }
+            if (!ok) break;
+            tc::mma_commit(v_empty + sv);
+            if (more) {
+              tc::mma_commit(k_empty + s1);
+              if (j + 2 == n_it) tc::mma_commit(q_empty);  // the segment's last S was just issued
+            }
+          }
+          if (ok) tc::mma_commit(o_final);
+          t += n_it;
+        }
+        if (*abort_flag) {  // let issued MMAs finish before TMEM is released
+          volatile int never = 0;
+          tc::mma_commit(drain);
+          tc::mbar_wait(drain, 0, &never, &g_status_ptile, 100000000ull);
+        }
+      }
+      __syncwarp();
+    }
+  } else if (warp < 4 * NH) {
+    if constexpr (NH == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REG_HIGH));
+    // ------------------------------------------------------------ softmax (sub-tile h)
+    const int h = warp >> 2;
+    const int r = threadIdx.x & 127;  // row of the sub-tile = TMEM lane
+    const int tok = h * sub_tok + r / p.b.group, gh = r % p.b.group;
+    const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_base + h * 128;
+    const uint32_t tO = tmem + lane_base + 128 * NH + h * 128;
+    const uint64_t sl2 = f2(p.scale_log2, p.scale_log2);
+    auto wait_all = [&](uint64_t* b_, uint32_t par) {
+      return __all_sync(0xffffffffu, tc::mbar_wait(b_, par, abort_flag, &g_status_ptile));
+    };
+    int tb = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      if (!wait_all(seg_full + (k & 1), (k >> 1) & 1)) break;
+      const volatile Segment* sg = seg_ring + (k & 1);
+      const int n_it = sg->n_it, first = sg->first, n_tok = sg->n, lo = sg->lo, hi = sg->hi, key_first = sg->key0;
+      const int slot = sg->whole ? -1 : sg->slot, head = sg->head * p.b.group + gh, pos_first = sg->pos0;
+      tc::mbar_arrive(seg_empty + (k & 1));
+      if (n_it < 0) break;
+      const bool live = r < sub_tok * p.b.group && tok < n_tok;
+      const int pos = live ? pos_first + tok : -1;
+      // every live row of the sub-tile sees the keys in [all_lo, all_hi)
+      const int all_hi = pos_first + h * sub_tok + 1;
+      const int all_lo = p.b.window > 0 ? pos_first + min((h + 1) * sub_tok, n_tok) - p.b.window : 0;
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int j = 0; j < n_it; ++j) {
+        const int key0 = key_first + j * kStep;
+        if (key0 < lo || key0 + kStep > hi) {
+          // slots that no row sees may hold anything: zero their values, so that 0 x NaN does not come in
+          const int g = tb + j, sv_ = g % NS;
+          if (!wait_all(v_full + sv_, (g / NS) & 1)) { ok = false; break; }
+          if (key0 + r < lo || key0 + r >= hi) {
+#pragma unroll
+            for (int c = 0; c < NCH; ++c)
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<uint4*>(sV + sv_ * TILE + c * kChunk + r * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+          }
+          tc::fence_proxy_async_smem();
+        }
+        if (!wait_all(s_full + h, (tb + j) & 1)) { ok = false; break; }
+        tc::tc_fence_after();
+        uint32_t sv[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tc::tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sv + c * 32));
+        tc::tmem_ld_wait();
+        if (key0 + kStep > all_hi || key0 < all_lo) {
+          const int last = pos - key0, before = p.b.window > 0 ? last - p.b.window : -1;
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c > last || c <= before) sv[c] = 0xff800000u;  // -inf
+        }
+        // row max: 8 independent chains, then a short tree
+        float mxs[8];
+#pragma unroll
+        for (int t = 0; t < 8; ++t) mxs[t] = fmaxf(__uint_as_float(sv[2 * t]), __uint_as_float(sv[2 * t + 1]));
+#pragma unroll
+        for (int c = 16; c < 128; c += 16)
+#pragma unroll
+          for (int t = 0; t < 8; ++t)
+            mxs[t] = max3(mxs[t], __uint_as_float(sv[c + 2 * t]), __uint_as_float(sv[c + 2 * t + 1]));
+        const float mx = fmaxf(max3(mxs[0], mxs[1], mxs[2]), max3(mxs[3], mxs[4], max3(mxs[5], mxs[6], mxs[7])));
+        const float m_new = fmaxf(m_run, mx * p.scale_log2);
+        const bool resc = m_new > m_run + kRescale;
+        float alpha = 1.f;
+        if (resc) {
+          alpha = tc::ex2(m_run - m_new);
+          m_run = m_new;
+        }
+        const float m_use = (m_run == -INFINITY) ? 0.f : m_run;
+        const uint64_t negm = f2(-m_use, -m_use);
+        uint64_t sum2[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};  // 4 chains
+        uint32_t pk[64];
+#pragma unroll
+        for (int c = 0; c < 64; ++c) {
+          float a, bb;
+          unf2(fma2(f2(__uint_as_float(sv[2 * c]), __uint_as_float(sv[2 * c + 1])), sl2, negm), a, bb);
+          const float p0 = tc::ex2(a), p1 = tc::ex2(bb);
+          sum2[c & 3] = add2(sum2[c & 3], f2(p0, p1));
+          pk[c] = tc::pack_bf16(p0, p1);
+        }
+        float s_lo, s_hi;
+        unf2(add2(add2(sum2[0], sum2[1]), add2(sum2[2], sum2[3])), s_lo, s_hi);
+        l_run = l_run * alpha + (s_lo + s_hi);
+        // O holds the result of the step before: s_full was committed after it
+        if (j >= 1 && __any_sync(0xffffffffu, resc)) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t ov[32];
+            tc::tmem_ld32(tO + c * 32, ov);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int u = 0; u < 32; ++u) ov[u] = __float_as_uint(__uint_as_float(ov[u]) * alpha);
+            tc::tmem_st32(tO + c * 32, ov);
+          }
+        }
+        tc::tmem_st32(tS, *reinterpret_cast<const uint32_t(*)[32]>(pk));  // P over the first 64 columns of S
+        tc::tmem_st32(tS + 32, *reinterpret_cast<const uint32_t(*)[32]>(pk + 32));
+        tc::tmem_st_wait();
+        tc::tc_fence_before();
+        tc::mbar_arrive(p_full + h);
+      }
+      if (!ok || !wait_all(o_final, k & 1)) { ok = false; break; }
+      tc::tc_fence_after();
+      const float inv = slot < 0 ? (l_run > 0.f ? 1.f / l_run : 0.f) : 1.f;
+      const int64_t row = int64_t(first + tok) * p.hq + head;
+      const int64_t prow = int64_t(slot) * p.rows + tok * p.b.group + gh;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t ov[32];
+        tc::tmem_ld32(tO + c * 32, ov);
+        tc::tmem_ld_wait();
+        if (c == D / 32 - 1) {
+          tc::tc_fence_before();
+          tc::mbar_arrive(o_free + h);  // O may be overwritten by the next segment
+        }
+        if (live) {
+          if (slot < 0) {
+            uint4* dst = reinterpret_cast<uint4*>(p.o + row * D + c * 32);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              uint32_t w[4];
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                w[x] = tc::pack_bf16(__uint_as_float(ov[8 * u + 2 * x]) * inv, __uint_as_float(ov[8 * u + 2 * x + 1]) * inv);
+              dst[u] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(p.part_o + prow * D + c * 32);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) dst[u] = make_uint4(ov[4 * u], ov[4 * u + 1], ov[4 * u + 2], ov[4 * u + 3]);
+          }
+        }
+      }
+      if (live) {
+        if (slot < 0)
+          p.lse[row] = l_run > 0.f ? (m_run + __log2f(l_run)) * kLn2 : -INFINITY;
+        else
+          p.part_ml[prow] = make_float2(m_run, l_run);
+      }
+      tb += n_it;
+    }
+  }
+
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  if (warp == W_MMA) tc::tmem_dealloc(tmem, C::TMEM_COLS);
+}
+
+// launch_tile<D, 2> returns this (not a library status) when the kernel was not
+// compiled to the register count that its setmaxnreg split assumes
+constexpr int kRegsMismatch = 1;
+
+// Queries [n_rows, Hq, d]: boxes of 64 columns x the group's heads x a sub-tile's tokens.
+bool query_map(CUtensorMap* m, const tpa_paged_view* c, const Params& p, int sub_tok) {
+  tmap::EncodeTiledFn fn = tmap::encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {cuuint64_t(c->head_dim), cuuint64_t(p.hq), cuuint64_t(c->n_rows)};
+  const cuuint64_t strides[2] = {cuuint64_t(c->head_dim) * 2, cuuint64_t(p.q_stride) * 2};
+  const cuuint32_t box[3] = {64, cuuint32_t(p.b.group), cuuint32_t(sub_tok)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16*>(p.q), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int NH>
+int launch_tile(const tpa_paged_view* c, Params& p, int grid, cudaStream_t st) {
+  using C = TileCfg<D, NH>;
+  const int sub_tok = 128 / p.b.group;
+  CUtensorMap tq, tk, tv;
+  const uint64_t rows = uint64_t(c->n_pages) * c->n_heads_kv * c->page_size;
+  if (!query_map(&tq, c, p, sub_tok) || !cache_map(&tk, c->k_cache, rows, D, c->page_size) ||
+      !cache_map(&tv, c->v_cache, rows, D, c->page_size))
+    return TPA_ERR_CUDA;
+  p.b.tile_tok = NH * sub_tok;
+  p.min_steps = 2;
+  TPA_CUDA_TRY(cudaFuncSetAttribute(paged_tile_kernel<D, NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES));
+  if constexpr (NH == 2) {
+    cudaFuncAttributes fa;
+    TPA_CUDA_TRY(cudaFuncGetAttributes(&fa, paged_tile_kernel<D, NH>));
+    if (fa.numRegs != C::REG_LAUNCH) return kRegsMismatch;
+  }
+  paged_tile_kernel<D, NH><<<grid, C::THREADS, C::BYTES, st>>>(tq, tk, tv, p);
+  TPA_CUDA_TRY(cudaGetLastError());
+  return TPA_OK;
+}
+
+}  // namespace
+
+TPA_DEFINE_STATUS_READER(tpa_internal_status_ptile, g_status_ptile)
+
+int tpa_internal_paged_tile(const tpa_paged_view* c, Params& p, int rows, int grid, cudaStream_t st) {
+  if (rows == 256) {
+    const int rc = c->head_dim == 128 ? launch_tile<128, 2>(c, p, grid, st) : launch_tile<64, 2>(c, p, grid, st);
+    if (rc != kRegsMismatch) return rc;
+  }
+  return c->head_dim == 128 ? launch_tile<128, 1>(c, p, grid, st) : launch_tile<64, 1>(c, p, grid, st);
+}
