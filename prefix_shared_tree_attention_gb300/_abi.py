@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 from . import build as _build
 
@@ -79,6 +80,11 @@ class PagedView(C.Structure):
     ]
 
 
+# The two structures above as bytes: what the bindings of short calls pass in their place.
+ROPE_PARAMS = struct.Struct("@PiiiiPPfi")
+PAGED_VIEW = struct.Struct("@PPPPPiiiiiiii")
+assert ROPE_PARAMS.size == C.sizeof(RopeParams) and PAGED_VIEW.size == C.sizeof(PagedView)
+
 # name -> (restype, argtypes); every symbol declared in include/tpa.h
 PROTOTYPES = {
     "tpa_tree_pack": (C.c_int, [_i32p, _i64p, C.c_int32, C.c_int32, C.POINTER(C.c_void_p)]),
@@ -121,18 +127,18 @@ PROTOTYPES = {
     "tpa_rope_table": (C.c_int, [C.c_void_p, C.c_int32, C.c_int32, C.c_double, C.POINTER(C.c_double), C.c_double,
                                  C.c_void_p]),
     "tpa_qk_norm_rope_fwd": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int32, C.c_int64, C.c_void_p, C.c_int64,
-                                       C.c_void_p, C.c_int64, C.POINTER(RopeParams), C.c_void_p, C.c_int64,
+                                       C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_int64,
                                        C.c_void_p, C.c_int64, C.c_int32, C.c_int32, C.c_int32, C.c_void_p]),
     "tpa_qk_norm_rope_bwd_workspace_bytes": (C.c_uint64, [C.c_int32]),
     "tpa_qk_norm_rope_bwd": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int32, C.c_int64, C.c_void_p, C.c_int64,
                                        C.c_void_p, C.c_int64, C.c_int32, C.c_void_p, C.c_int64, C.c_void_p,
-                                       C.c_int64, C.POINTER(RopeParams), C.c_void_p, C.c_int64, C.c_void_p,
+                                       C.c_int64, C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p,
                                        C.c_int64, C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p, C.c_uint64,
                                        C.c_int32, C.c_int32, C.c_int32, C.c_void_p]),
-    "tpa_paged_append": (C.c_int, [C.POINTER(PagedView), C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p,
-                                   C.c_int64, C.c_void_p, C.c_int64, C.c_int32, C.POINTER(RopeParams), C.c_void_p]),
+    "tpa_paged_append": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p,
+                                   C.c_int64, C.c_void_p, C.c_int64, C.c_int32, C.c_void_p, C.c_void_p]),
     "tpa_paged_attn_workspace_bytes": (C.c_uint64, [C.c_int32, C.c_int32, C.c_int32, C.c_int32]),
-    "tpa_paged_attn_fwd": (C.c_int, [C.POINTER(PagedView), C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_int32,
+    "tpa_paged_attn_fwd": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_int32,
                                      C.c_int32, C.c_float, C.c_int32, C.c_void_p, C.c_uint64, C.c_void_p]),
     "tpa_verify_drafts": (C.c_int, [C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p,
                                     C.c_void_p, C.c_void_p, C.c_void_p, C.c_int32, C.c_int32, C.c_int32,

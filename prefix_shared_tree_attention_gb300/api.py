@@ -10,7 +10,7 @@ import numpy as np
 import torch
 
 from ._abi import (BALANCE_FFD, BALANCE_KK, GRAD_BF16, GRAD_F32, LOGITS_COMPACT, LOGITS_PADDED, MASK_BITS,
-                   MASK_U8, WEIGHT_BF16, WEIGHT_F32, BlockMaskView, PackingMetrics, PagedView, RopeParams, TreeInfo,
+                   MASK_U8, PAGED_VIEW, ROPE_PARAMS, WEIGHT_BF16, WEIGHT_F32, BlockMaskView, PackingMetrics, TreeInfo,
                    TreeView, check, lib)
 
 
@@ -362,27 +362,27 @@ def lm_head_logprobs_entropy(dtree: DeviceTree, hidden: torch.Tensor, weight: to
     return pl, pe, sl, se
 
 
-def _same_device(*tensors) -> torch.device:
-    """The one CUDA device of the tensors given (None is passed over), which
-    must be the current one: the library launches there."""
-    dev = None
+def _launch_stream(stream, first: torch.Tensor, *tensors) -> int:
+    """The stream of a call, after a check that its tensors (None is passed
+    over) are on the one CUDA device that is current: the library launches there."""
+    dev = first.get_device()
     for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("every tensor must be a CUDA tensor")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError("every tensor must be on one device")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {dev}, which is not the current device")
-    return dev
+        if t is not None and t.get_device() != dev:
+            raise ValueError("every tensor must be a CUDA tensor, all on one device")
+    if dev < 0:
+        raise ValueError("every tensor must be a CUDA tensor")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on cuda:{dev}, which is not the current device")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_ptr(stream)
 
 
 def _head_rows(name: str, t: torch.Tensor, dtypes=(torch.bfloat16,)) -> tuple[int, int, int, int]:
     """(rows, row stride, heads, d) of a tensor [..., H, d] whose heads are
     contiguous and whose leading dimensions are evenly spaced rows."""
+    if t.dim() == 3 and t.dtype in dtypes:
+        (n, H, d), (row, head, one) = t.shape, t.stride()
+        if one == 1 and (head == d or H == 1):
+            return n, (row if n > 1 else H * d), H, d
     if t.dtype not in dtypes or t.dim() < 3:
         raise ValueError(f"{name} must be [..., heads, d] of {' or '.join(str(x) for x in dtypes)}")
     H, d = t.shape[-2:]
@@ -415,28 +415,29 @@ def rope_table(n_positions: int, rot_dim: int, base: float = 10000.0, inv_freq: 
         out = torch.empty((n_positions, rot_dim), dtype=torch.float32, device=device)
     if out.dtype != torch.float32 or not out.is_contiguous() or tuple(out.shape) != (n_positions, rot_dim):
         raise ValueError("out must be a contiguous fp32 tensor [n_positions, rot_dim]")
-    _same_device(out)
+    st = _launch_stream(stream, out)
     check("tpa_rope_table", lib().tpa_rope_table(out.data_ptr(), int(n_positions), int(rot_dim), float(base), fr,
-                                                 float(scale), _stream_ptr(stream)))
+                                                 float(scale), st))
     return out
 
 
-def _rope_params(table, q_weight, k_weight, eps, interleaved, d) -> RopeParams:
-    p = RopeParams()
+def _rope_params(table, q_weight, k_weight, eps, interleaved, d) -> bytes:
+    """A tpa_rope_params as bytes (a ctypes structure takes longer to fill than the kernel to launch)."""
+    at = rows = rot = wt = wq = wk = 0
     if table is not None:
         if table.dtype != torch.float32 or table.dim() != 2 or not table.is_contiguous():
             raise ValueError("table must be a contiguous fp32 tensor [positions, rot_dim]")
-        p.table, p.table_rows, p.rot_dim = table.data_ptr(), table.shape[0], table.shape[1]
+        at = table.data_ptr()
+        rows, rot = table.shape
     if (q_weight is None) != (k_weight is None):
         raise ValueError("give both norm weights or neither")
     if q_weight is not None:
-        for w in (q_weight, k_weight):
-            if w.dtype not in _WEIGHT or w.dtype != q_weight.dtype or w.numel() != d or not w.is_contiguous():
-                raise ValueError("norm weights must be contiguous, of d values, both fp32 or both bf16")
-        p.weight_type = _WEIGHT[q_weight.dtype]
-        p.q_weight, p.k_weight = q_weight.data_ptr(), k_weight.data_ptr()
-    p.eps, p.interleaved = eps, 1 if interleaved else 0
-    return p
+        dt = q_weight.dtype
+        if (dt not in _WEIGHT or k_weight.dtype != dt or q_weight.numel() != d or k_weight.numel() != d or
+                not q_weight.is_contiguous() or not k_weight.is_contiguous()):
+            raise ValueError("norm weights must be contiguous, of d values, both fp32 or both bf16")
+        wt, wq, wk = _WEIGHT[dt], q_weight.data_ptr(), k_weight.data_ptr()
+    return ROPE_PARAMS.pack(at, rows, rot, 1 if interleaved else 0, wt, wq, wk, eps, 0)
 
 
 _WEIGHT = {torch.float32: WEIGHT_F32, torch.bfloat16: WEIGHT_BF16}
@@ -472,14 +473,14 @@ def qk_norm_rope_fwd(positions: "torch.Tensor | DeviceTree", q: torch.Tensor, k:
     rp = _rope_params(table, q_weight, k_weight, eps, interleaved, d)
     qo, ko = out if out is not None else (torch.empty(q.shape, dtype=q.dtype, device=q.device),
                                           torch.empty(k.shape, dtype=k.dtype, device=k.device))
-    _same_device(q, k, table, q_weight, k_weight, pbuf, qo, ko)
+    st = _launch_stream(stream, q, k, table, q_weight, k_weight, pbuf, qo, ko)
     if qo.shape != q.shape or ko.shape != k.shape:
         raise ValueError("out must be shaped like q and k")
     _, so, _, _ = _head_rows("out[0]", qo)
     _, sko, _, _ = _head_rows("out[1]", ko)
     check("tpa_qk_norm_rope_fwd", lib().tpa_qk_norm_rope_fwd(
-        pos, n_tok, t_pad, rows, q.data_ptr(), sq, k.data_ptr(), sk, C.byref(rp), qo.data_ptr(), so, ko.data_ptr(),
-        sko, Hq, Hkv, d, _stream_ptr(stream)))
+        pos, n_tok, t_pad, rows, q.data_ptr(), sq, k.data_ptr(), sk, rp, qo.data_ptr(), so, ko.data_ptr(), sko, Hq,
+        Hkv, d, st))
     return qo, ko
 
 
@@ -517,35 +518,34 @@ def qk_norm_rope_bwd(positions: "torch.Tensor | DeviceTree", dq_out: torch.Tenso
         dwq, dwk = (torch.empty(d, dtype=torch.float32, device=dev) for _ in range(2))
         if workspace is None:
             workspace = torch.empty(int(lib().tpa_qk_norm_rope_bwd_workspace_bytes(d)), dtype=torch.uint8, device=dev)
-    _same_device(dq_out, dk_out, table, q_weight, k_weight, pbuf, dq, dk, workspace, *((q, k) if norm else ()))
+    st = _launch_stream(stream, dq_out, dk_out, table, q_weight, k_weight, pbuf, dq, dk, workspace, *((q, k) if norm else ()))
     check("tpa_qk_norm_rope_bwd", lib().tpa_qk_norm_rope_bwd(
         pos, n_tok, t_pad, rows, dq_out.data_ptr(), sgq, dk_out.data_ptr(), sgk, _GRAD[dq_out.dtype],
-        q.data_ptr() if norm else None, sq, k.data_ptr() if norm else None, sk, C.byref(rp), dq.data_ptr(), so,
+        q.data_ptr() if norm else None, sq, k.data_ptr() if norm else None, sk, rp, dq.data_ptr(), so,
         dk.data_ptr(), sko, _GRAD[grad_dtype], _ptr(dwq), _ptr(dwk), _ptr(workspace),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), Hq, Hkv, d, _stream_ptr(stream)))
+        0 if workspace is None else workspace.numel() * workspace.element_size(), Hq, Hkv, d, st))
     return dq, dk, dwq, dwk
 
 
-def _paged_view(k_cache, v_cache, pages, offsets, kv_lens, n_rows: int, d: int) -> PagedView:
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if t.dtype != torch.bfloat16 or t.dim() != 4 or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous bf16 tensor [n_pages, Hkv, page_size, d]")
-    if k_cache.shape != v_cache.shape or k_cache.shape[3] != d:
-        raise ValueError("k_cache and v_cache must match, and share head_dim with the new tokens")
-    if pages.dtype != torch.int32 or pages.dim() != 2 or pages.stride(1) != 1:
+def _paged_view(k_cache, v_cache, pages, offsets, kv_lens, n_rows: int, n_heads_kv: int | None, d: int):
+    """A tpa_paged_view as bytes, and the cache's key/value heads."""
+    bf16, i32 = torch.bfloat16, torch.int32
+    shape = k_cache.shape
+    if (k_cache.dtype != bf16 or v_cache.dtype != bf16 or len(shape) != 4 or not k_cache.is_contiguous() or
+            not v_cache.is_contiguous()):
+        raise ValueError("k_cache and v_cache must be contiguous bf16 tensors [n_pages, Hkv, page_size, d]")
+    n_pages, hkv, page, dc = shape
+    if v_cache.shape != shape or dc != d or (n_heads_kv is not None and n_heads_kv != hkv):
+        raise ValueError("k_cache and v_cache must match, and have the head_dim and key/value heads of the new tokens")
+    if pages.dtype != i32 or pages.dim() != 2 or pages.stride(1) != 1:
         raise ValueError("pages must be an int32 tensor [n_seqs, max_pages] with unit column stride")
-    n = pages.shape[0]
-    for name, t, m in (("offsets", offsets, n + 1), ("kv_lens", kv_lens, n)):
-        if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != m or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int32 tensor of {m} entries")
-    v = PagedView()
-    v.k_cache, v.v_cache, v.pages = k_cache.data_ptr(), v_cache.data_ptr(), pages.data_ptr()
-    v.offsets, v.kv_lens = offsets.data_ptr(), kv_lens.data_ptr()
-    v.n_pages, v.n_heads_kv, v.page_size, v.head_dim = k_cache.shape
-    v.n_seqs, v.max_pages = pages.shape
-    v.page_stride = pages.stride(0) if n > 1 else max(pages.shape[1], 1)
-    v.n_rows = n_rows
-    return v
+    n, width = pages.shape
+    if (offsets.dtype != i32 or kv_lens.dtype != i32 or offsets.shape != (n + 1,) or kv_lens.shape != (n,) or
+            not offsets.is_contiguous() or not kv_lens.is_contiguous()):
+        raise ValueError("offsets [n_seqs + 1] and kv_lens [n_seqs] must be contiguous int32 tensors")
+    return PAGED_VIEW.pack(k_cache.data_ptr(), v_cache.data_ptr(), pages.data_ptr(), offsets.data_ptr(),
+                           kv_lens.data_ptr(), n_pages, page, n, width, pages.stride(0) if n > 1 else max(width, 1),
+                           hkv, d, n_rows), hkv
 
 
 def paged_append(k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Tensor, offsets: torch.Tensor,
@@ -565,9 +565,7 @@ def paged_append(k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Tens
     if v.shape != k.shape:
         raise ValueError("k and v must have the same shape")
     sv = _head_rows("v", v)[1]
-    cache = _paged_view(k_cache, v_cache, pages, offsets, kv_lens, rows, d)
-    if Hkv != cache.n_heads_kv:
-        raise ValueError("k must have the cache's heads")
+    cache, _ = _paged_view(k_cache, v_cache, pages, offsets, kv_lens, rows, Hkv, d)
     rp = _rope_params(table, q_weight, k_weight, eps, interleaved, d)
     sq = so = Hq = 0
     if q is not None:
@@ -581,9 +579,9 @@ def paged_append(k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Tens
         so = _head_rows("q_out", q_out)[1]
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _same_device(k, v, q, q_out, k_cache, v_cache, pages, offsets, kv_lens, table, q_weight, k_weight)
-    check("tpa_paged_append", lib().tpa_paged_append(C.byref(cache), k.data_ptr(), sk, v.data_ptr(), sv, _ptr(q), sq,
-                                                     _ptr(q_out), so, Hq, C.byref(rp), _stream_ptr(stream)))
+    st = _launch_stream(stream, k, v, q, q_out, k_cache, v_cache, pages, offsets, kv_lens, table, q_weight, k_weight)
+    check("tpa_paged_append", lib().tpa_paged_append(cache, k.data_ptr(), sk, v.data_ptr(), sv, _ptr(q), sq,
+                                                     _ptr(q_out), so, Hq, rp, st))
     return q_out
 
 
@@ -605,22 +603,21 @@ def paged_attn_fwd(k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Te
     rows, sq, Hq, d = _head_rows("q", q)
     if q.dim() != 3:
         raise ValueError("q must be [tokens, Hq, d]")
-    cache = _paged_view(k_cache, v_cache, pages, offsets, kv_lens, rows, d)
+    cache, hkv = _paged_view(k_cache, v_cache, pages, offsets, kv_lens, rows, None, d)
     o = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else out
     if lse is None:
         lse = torch.empty((rows, Hq), dtype=torch.float32, device=q.device)
     if o.shape != q.shape or o.dtype != q.dtype or not o.is_contiguous():
         raise ValueError("out must be contiguous bf16 shaped like q")
-    if tuple(lse.shape) != (rows, Hq) or lse.dtype != torch.float32 or not lse.is_contiguous():
+    if lse.shape != (rows, Hq) or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous fp32 tensor [tokens, Hq]")
     if workspace is None:
-        workspace = torch.empty(paged_attn_workspace_bytes(max_q_len, Hq, cache.n_heads_kv, d), dtype=torch.uint8,
-                                device=q.device)
-    _same_device(q, o, lse, workspace, k_cache, v_cache, pages, offsets, kv_lens)
+        workspace = torch.empty(paged_attn_workspace_bytes(max_q_len, Hq, hkv, d), dtype=torch.uint8, device=q.device)
+    st = _launch_stream(stream, q, o, lse, workspace, k_cache, v_cache, pages, offsets, kv_lens)
     check("tpa_paged_attn_fwd", lib().tpa_paged_attn_fwd(
-        C.byref(cache), q.data_ptr(), sq, o.data_ptr(), lse.data_ptr(), Hq, int(max_q_len),
+        cache, q.data_ptr(), sq, o.data_ptr(), lse.data_ptr(), Hq, int(max_q_len),
         float(softmax_scale or 0.0), int(window), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-        _stream_ptr(stream)))
+        st))
     return o, lse
 
 
@@ -639,29 +636,37 @@ def verify_drafts(target_probs: torch.Tensor, draft_tokens: torch.Tensor, u_acce
         raise ValueError("target_probs must be [S, K+1, V] and draft_tokens [S, K]")
     S, K1, V = target_probs.shape
     K = K1 - 1
-    for name, t, shape, dt in (("draft_tokens", draft_tokens, (S, K), torch.int32),
-                               ("u_accept", u_accept, (S, K), torch.float32), ("u_next", u_next, (S,), torch.float32),
-                               ("n_drafts", n_drafts, (S,), torch.int32)):
-        if t is not None and (t.dtype != dt or tuple(t.shape) != shape or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous {dt} tensor of shape {shape}")
-    for name, t, k in (("target_probs", target_probs, K1), ("draft_probs", draft_probs, K)):
-        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (S, k, V) or
-                              (V > 1 and t.stride(2) != 1) or (k > 1 and t.stride(1) != V)):
-            raise ValueError(f"{name} must be fp32 [{S}, {k}, {V}] with contiguous sequences")
+    i32, f32 = torch.int32, torch.float32
+    if draft_tokens.dtype != i32 or draft_tokens.shape != (S, K) or not draft_tokens.is_contiguous():
+        raise ValueError("draft_tokens must be a contiguous int32 tensor [S, K]")
+    if (u_accept.dtype != f32 or u_accept.shape != (S, K) or not u_accept.is_contiguous() or u_next.dtype != f32 or
+            u_next.shape != (S,) or not u_next.is_contiguous()):
+        raise ValueError("u_accept [S, K] and u_next [S] must be contiguous fp32 tensors")
+    if n_drafts is not None and (n_drafts.dtype != i32 or n_drafts.shape != (S,) or not n_drafts.is_contiguous()):
+        raise ValueError("n_drafts must be a contiguous int32 tensor [S]")
+    ts, tr, t1 = target_probs.stride()
+    if target_probs.dtype != f32 or (V > 1 and t1 != 1) or (K > 0 and tr != V):
+        raise ValueError("target_probs must be fp32 with contiguous sequences")
+    ds = 0
+    if draft_probs is not None:
+        if draft_probs.dtype != f32 or draft_probs.shape != (S, K, V):
+            raise ValueError("draft_probs must be fp32 [S, K, V]")
+        ds, dr, d1 = draft_probs.stride()
+        if (V > 1 and d1 != 1) or (K > 1 and dr != V):
+            raise ValueError("draft_probs must have contiguous sequences")
     if out is None:
-        out = (torch.empty((S, K1), dtype=torch.int32, device=target_probs.device),
-               torch.empty(S, dtype=torch.int32, device=target_probs.device))
+        out = (torch.empty((S, K1), dtype=i32, device=target_probs.device),
+               torch.empty(S, dtype=i32, device=target_probs.device))
     tokens, n_accepted = out
-    if (tokens.dtype != torch.int32 or tuple(tokens.shape) != (S, K1) or not tokens.is_contiguous() or
-            n_accepted.dtype != torch.int32 or tuple(n_accepted.shape) != (S,) or not n_accepted.is_contiguous()):
+    if (tokens.dtype != i32 or tokens.shape != (S, K1) or not tokens.is_contiguous() or
+            n_accepted.dtype != i32 or n_accepted.shape != (S,) or not n_accepted.is_contiguous()):
         raise ValueError("out must be contiguous int32 tensors [S, K+1] and [S]")
-    _same_device(target_probs, draft_tokens, u_accept, u_next, draft_probs, n_drafts, tokens, n_accepted)
-    ts = target_probs.stride(0) if S > 1 else K1 * V
-    ds = 0 if draft_probs is None else draft_probs.stride(0) if S > 1 else K * V
+    st = _launch_stream(stream, target_probs, draft_tokens, u_accept, u_next, draft_probs, n_drafts, tokens, n_accepted)
+    if S == 1:
+        ts, ds = K1 * V, K * V
     check("tpa_verify_drafts", lib().tpa_verify_drafts(
         target_probs.data_ptr(), ts, _ptr(draft_probs) if K else None, ds, draft_tokens.data_ptr(), _ptr(n_drafts),
-        u_accept.data_ptr(), u_next.data_ptr(), tokens.data_ptr(), n_accepted.data_ptr(), S, K, V,
-        _stream_ptr(stream)))
+        u_accept.data_ptr(), u_next.data_ptr(), tokens.data_ptr(), n_accepted.data_ptr(), S, K, V, st))
     return tokens, n_accepted
 
 
