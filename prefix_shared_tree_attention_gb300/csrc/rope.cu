@@ -5,13 +5,23 @@
 //   z = R(p)^T dy,  h = x r:   dw = sum z h,  dx = r (z w - h mean(z w h))
 //
 // Bound by HBM: 2 bytes in and 2 out for each value, the cos | sin row of a
-// token read once for all its heads.  A row of d values is held by d / 16
-// lanes, each with two 16-byte pieces whose pairs of the rotation are both in
-// the lane: pieces l and l + rot/16 where halves are paired, pieces 2l and
-// 2l + 1 where neighbours are, so the rotation needs no exchange and the norm
-// only 3 shuffles (2 for d 64).  All pieces of a lane use cos and sin values
-// [8l, 8l + 8) of the token.  The rows of a warp are heads of one token: the
-// weights and the angles are in registers for all of them.
+// token read once for 16 (d 128) or 32 (d 64) of its heads.  Seven warps of a
+// CTA work, each on its own units (up to 4 KB of one token's heads, which are
+// contiguous) and from its own ring of them in shared memory; the eighth finds
+// the places of the units, four lanes a ring so that four look-ups are under
+// way, and fills the rings by bulk copies that run ahead.  The reads in flight
+// then do not depend on registers, and what a unit costs in instructions beside
+// its arithmetic is spent once for seven of them.  Units are dealt one to each
+// warp of the grid in turn: at any time the grid reads one run of memory, and
+// padding, which costs less, is spread evenly.
+//
+// A row of d values is held by d / 16 lanes, each with two 16-byte pieces whose
+// pairs of the rotation are both in the lane: pieces l and l + rot/16 where
+// halves are paired, pieces 2l and 2l + 1 where neighbours are, so the rotation
+// needs no exchange and the norm only 3 shuffles (2 for d 64).  All pieces of a
+// lane use cos and sin values [8l, 8l + 8) of the token.  The arithmetic is in
+// packed pairs of fp32 (f32x2), which halves its instructions; these, not the
+// reads, bound a form with plain fp32.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -26,8 +36,12 @@ namespace {
 
 __device__ unsigned int g_status_rope = 0;
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+// A CTA: seven warps that work and one that loads (two loading warps, or one CTA
+// an SM with 13 + 3 warps, were within 3 % either way).
+constexpr int kWarps = 7;
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kBatch = 4;  // lanes of the loading warp for each ring: units looked up together
+constexpr int kCtas = 2;   // CTAs an SM
 
 struct Rope {
   const float* table;
@@ -66,61 +80,86 @@ __device__ __forceinline__ void pieces(int l, int rot, bool interleaved, int& a,
   }
 }
 
-__device__ __forceinline__ void unpack8(const uint4& v, float* x) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+using tc::add2;
+using tc::f2;
+using tc::fma2;
+using tc::mul2;
+using tc::unf2;
+
+// A lane's 16 values of a row: the first and the second of its 8 pairs, packed by two.
+struct Vals {
+  uint64_t a[4], b[4];
+};
+
+// bf16 words of the lane's two pieces <-> pairs.  Where neighbours are paired, a
+// word holds a pair: the words are re-sorted into firsts and seconds.
+__device__ __forceinline__ uint64_t widen(uint32_t w) {
+  return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ Vals unpack16(const uint4& x, const uint4& y, bool inter) {
+  uint32_t u[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+  if (inter) {
+    uint32_t t[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      t[i] = __byte_perm(u[2 * i], u[2 * i + 1], 0x5410);
+      t[4 + i] = __byte_perm(u[2 * i], u[2 * i + 1], 0x7632);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = t[i];
+  }
+  Vals v;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    v.a[i] = widen(u[i]);
+    v.b[i] = widen(u[4 + i]);
   }
+  return v;
 }
-
-__device__ __forceinline__ uint4 pack8(const float* x) {
-  return make_uint4(tc::pack_bf16(x[0], x[1]), tc::pack_bf16(x[2], x[3]), tc::pack_bf16(x[4], x[5]),
-                    tc::pack_bf16(x[6], x[7]));
+__device__ __forceinline__ uint32_t narrow(uint64_t v) {
+  float lo, hi;
+  unf2(v, lo, hi);
+  return tc::pack_bf16(lo, hi);
 }
-
-__device__ __forceinline__ void load_f8(const float* p, float* x) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-
-__device__ __forceinline__ void load_weight(const void* w, bool bf16, int pa, int pb, float* x) {
-  if (bf16) {
-    unpack8(__ldg(reinterpret_cast<const uint4*>(w) + pa), x);
-    unpack8(__ldg(reinterpret_cast<const uint4*>(w) + pb), x + 8);
-  } else {
-    load_f8(static_cast<const float*>(w) + 8 * pa, x);
-    load_f8(static_cast<const float*>(w) + 8 * pb, x + 8);
-  }
-}
-
-// cos and sin of this lane's 8 pairs, where it holds any (l < rot / 16)
-__device__ __forceinline__ void load_angles(const Rope& r, int pos, int l, float* c, float* s) {
-  if (l < (r.rot >> 4)) {
-    const float* row = r.table + int64_t(pos) * r.rot + 8 * l;
-    load_f8(row, c);
-    load_f8(row + (r.rot >> 1), s);
-  }
-}
-
-// (a, b) <- (a c - b s, b c + a s) for each pair of the lane's 16 values
-__device__ __forceinline__ void rotate(float* x, const float* c, const float* s, bool interleaved, float sign) {
-  if (interleaved) {
+__device__ __forceinline__ void pack16(const Vals& v, bool inter, uint4& x, uint4& y) {
+  uint32_t u[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float a = x[2 * j], b = x[2 * j + 1], sj = sign * s[j];
-      x[2 * j] = a * c[j] - b * sj;
-      x[2 * j + 1] = b * c[j] + a * sj;
-    }
-  } else {
+  for (int i = 0; i < 4; ++i) {
+    u[i] = narrow(v.a[i]);
+    u[4 + i] = narrow(v.b[i]);
+  }
+  if (inter) {
+    uint32_t t[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float a = x[j], b = x[j + 8], sj = sign * s[j];
-      x[j] = a * c[j] - b * sj;
-      x[j + 8] = b * c[j] + a * sj;
+    for (int i = 0; i < 4; ++i) {
+      t[2 * i] = __byte_perm(u[i], u[4 + i], 0x5410);
+      t[2 * i + 1] = __byte_perm(u[i], u[4 + i], 0x7632);
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = t[i];
+  }
+  x = make_uint4(u[0], u[1], u[2], u[3]);
+  y = make_uint4(u[4], u[5], u[6], u[7]);
+}
+
+// 8 consecutive floats as 4 packed pairs
+__device__ __forceinline__ void load_p4(const float* p, uint64_t* x) {
+  const ulonglong2 a = reinterpret_cast<const ulonglong2*>(p)[0], b = reinterpret_cast<const ulonglong2*>(p)[1];
+  x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
+}
+
+// Both weights as fp32 into shared memory, by the working warps, in the order in
+// which the lanes hold a row: 16 l + j is the first of lane l's pair j, 16 l + 8 + j the second.
+template <int D>
+__device__ __forceinline__ void stage_weights(const Rope& r, float* w) {
+  for (int i = threadIdx.x; i < 2 * D; i += 32 * kWarps) {
+    const void* src = i < D ? r.wq : r.wk;
+    const int e = i % D, l = e >> 4, j = e & 7, second = (e >> 3) & 1, nr = r.rot >> 4;
+    int at;
+    if (r.interleaved) at = 16 * l + 2 * j + second;
+    else if (l < nr) at = 8 * (l + second * nr) + j;
+    else at = 16 * l + 8 * second + j;
+    w[i] = r.w_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(src)[at]) : static_cast<const float*>(src)[at];
   }
 }
 
@@ -131,12 +170,179 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
+__device__ __forceinline__ float sum2(uint64_t v) {
+  float lo, hi;
+  unf2(v, lo, hi);
+  return lo + hi;
+}
+__device__ __forceinline__ uint64_t neg2(uint64_t v) { return v ^ 0x8000000080000000ull; }
+
 template <int D>
-__device__ __forceinline__ float rstd16(const float* x, float eps) {
-  float ss = 0.f;
+__device__ __forceinline__ float rstd(const Vals& v, float eps) {
+  uint64_t s = mul2(v.a[0], v.a[0]), t = mul2(v.b[0], v.b[0]);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
-  return rsqrtf(row_sum<Geo<D>::LPR>(ss) * (1.f / D) + eps);
+  for (int i = 1; i < 4; ++i) {
+    s = fma2(v.a[i], v.a[i], s);
+    t = fma2(v.b[i], v.b[i], t);
+  }
+  return rsqrtf(row_sum<Geo<D>::LPR>(sum2(add2(s, t))) * (1.f / D) + eps);
+}
+
+// A lane's two 16-byte pieces of a bf16 row.  Where they are neighbours they
+// may leave as one 32-byte store, a whole sector (`one`).
+__device__ __forceinline__ void store_pieces(uint8_t* row, int pa, int pb, const uint4& x, const uint4& y, bool one) {
+  if (one) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(row + 16 * pa), "r"(x.x), "r"(x.y),
+                 "r"(x.z), "r"(x.w), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(row)[pa] = x;
+    reinterpret_cast<uint4*>(row)[pb] = y;
+  }
+}
+
+// ------------------------------------------------------------------ the warps' rings
+
+
+// One unit: rows of one token from head h on.  Its first `turned` rows are
+// queries or keys, the others (append) values from head 0 on, or h when there are no keys with them.
+struct Unit {
+  int32_t kind, h, rows, turned, state, token;  // kind 0: queries, 1: keys and values
+  int64_t slot;                                 // append: row of (page, head 0, slot) in the cache
+};
+enum { kUse = 0, kPad = 1, kSkip = 2 };
+
+template <int D, uint32_t DATA>
+struct Ring {
+  static constexpr uint32_t TABLE = D * 4;
+  static constexpr uint32_t STAGE = DATA + TABLE + uint32_t(sizeof(Unit));
+  // Two stages: with three or four the grid reads from so many places at once
+  // that HBM gives less (64K-token tree: 208 instead of 190 us).
+  static constexpr int NST = 2;
+  static constexpr uint32_t WARP = NST * STAGE;
+  static constexpr uint32_t OFF_FULL = kWarps * WARP;
+  static constexpr uint32_t OFF_EMPTY = OFF_FULL + kWarps * NST * 8;
+  static constexpr uint32_t OFF_FLAG = OFF_EMPTY + kWarps * NST * 8;
+  static constexpr uint32_t OFF_W = OFF_FLAG + 16;
+  static constexpr uint32_t BYTES = OFF_W + 2 * D * 4;
+  static_assert(sizeof(Unit) == 32 && NST <= kBatch && STAGE % 16 == 0 && OFF_W % 16 == 0 &&
+                    kCtas * (BYTES + 1024) <= 228 * 1024,
+                "ring");
+};
+
+// Barriers of the rings; warp w of the first eight and lane w of the ninth use set w.
+template <class R>
+struct Bars {
+  uint8_t* ring;
+  uint64_t* full;
+  uint64_t* empty;
+  volatile int* abort_flag;
+  __device__ __forceinline__ Bars(uint8_t* smem, int w)
+      : ring(smem + w * R::WARP),
+        full(reinterpret_cast<uint64_t*>(smem + R::OFF_FULL) + w * R::NST),
+        empty(reinterpret_cast<uint64_t*>(smem + R::OFF_EMPTY) + w * R::NST),
+        abort_flag(reinterpret_cast<volatile int*>(smem + R::OFF_FLAG)) {}
+  __device__ __forceinline__ void init() const {  // one thread of each ring
+    for (int s = 0; s < R::NST; ++s) {
+      tc::mbar_init(full + s, 1);
+      tc::mbar_init(empty + s, 1);
+    }
+    tc::fence_mbar_init();
+  }
+  // Lets the copies already issued land, after a wait that ran out.
+  __device__ inline void drain(int issued) const {
+    volatile int never = 0;
+    for (int j = issued > R::NST ? issued - R::NST : 0; j < issued; ++j)
+      tc::mbar_wait(full + j % R::NST, (j / R::NST) & 1, &never, &g_status_rope, 100000000ull);
+  }
+};
+
+// The loading warp arrives and goes on; the others wait until the barriers (and
+// their own weights) are there.
+__device__ __forceinline__ void ready_arrive() { asm volatile("bar.arrive 1, %0;" ::"n"(kThreads) : "memory"); }
+__device__ __forceinline__ void ready_wait() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
+
+// The units of global warp `me` of n: one of each run of n, the next one in the
+// next run, so that a warp's units are of all kinds where a token's number of
+// units divides n.
+__device__ __forceinline__ int64_t unit_of(int64_t me, int64_t n, int i) { return i * n + (me + i) % n; }
+__device__ __forceinline__ int units_for(int64_t units, int64_t me, int64_t n) {
+  const int runs = int(units / n);
+  return runs + (unit_of(me, n, runs) < units ? 1 : 0);
+}
+
+// A stage and the parity of its phase, one after another.
+template <int NST>
+struct Turn {
+  int s = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++s == NST) {
+      s = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// A unit's token and part of it, and the token's place.
+struct Place {
+  int32_t tok, part, pos, state;
+  int64_t slot;
+};
+
+// The loop of a loading warp: `look(i)` finds the place of this ring's unit i
+// (kBatch lanes look up as many of them together), `issue(place, i, stage)`
+// starts its copies.  The rings go on in step.  (Each at its own pace, polling
+// the stages instead of waiting for them, took 201 instead of 190 us on the
+// 64K-token tree: the polls take issue slots from the warps that work.)
+template <class R, bool SLOT, class Look, class Issue>
+__device__ __forceinline__ void run_loader(const Bars<R>& bar, int w, int mine, Look look, Issue issue) {
+  const int lane = threadIdx.x & 31, j = lane % kBatch;
+  Turn<R::NST> turn;
+  int most = mine, issued = 0;
+  bool dead = false;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+  for (int i0 = 0; i0 < most; i0 += kBatch) {
+    Place own{0, 0, 0, kSkip, 0};
+    if (i0 + j < mine) own = look(i0 + j);
+    for (int k = 0; k < kBatch && i0 + k < most; ++k) {
+      const int from = lane - j + k;
+      Place p;
+      p.tok = __shfl_sync(0xffffffffu, own.tok, from);
+      p.part = __shfl_sync(0xffffffffu, own.part, from);
+      p.pos = __shfl_sync(0xffffffffu, own.pos, from);
+      p.state = __shfl_sync(0xffffffffu, own.state, from);
+      p.slot = SLOT ? __shfl_sync(0xffffffffu, own.slot, from) : 0;
+      if (j == 0 && i0 + k < mine && !dead) {
+        if (tc::mbar_wait(bar.empty + turn.s, turn.phase ^ 1, bar.abort_flag, &g_status_rope)) {
+          issue(p, i0 + k, turn.s);
+          turn.next();
+          ++issued;
+        } else {
+          dead = true;
+        }
+      }
+      __syncwarp();
+    }
+  }
+  if (j == 0 && w < kWarps && *bar.abort_flag) bar.drain(issued);
+  __syncwarp();
+}
+
+// A row's place in the rope table, and whether it is padding.
+__device__ __forceinline__ void plain_place(const int32_t* positions, const int32_t* n_tokens, int t_pad, int rows,
+                                            int tok, int& pos, int& state) {
+  pos = __ldg(positions + tok);
+  state = pos < 0 ? kPad : kUse;
+  if (n_tokens) {
+    const int b = tok / t_pad;
+    if (tok - b * t_pad >= __ldg(n_tokens + b)) state = kPad;
+  }
+  if (state == kUse && pos >= rows) {
+    atomicOr(&g_status_rope, TPA_DEV_BAD_INPUT);
+    state = kPad;
+  }
 }
 
 // ------------------------------------------------------------------ forward
@@ -147,140 +353,243 @@ struct FwdParams {
   const int32_t* n_tokens;
   int64_t n_rows;
   int32_t t_pad, hq, hkv;
-  int32_t sq, skv;  // units of a token for its query rows, and for its key rows
+  int32_t sq, sk, sv;  // units of a token: of queries, of keys (with the values where sv is 0), of values
   Rows q, k, v;
   RowsOut qo, ko;
   tpa_paged_view cache;  // append
+  int32_t wide;          // the rows written are 32-byte aligned
 };
 
-// Rows of a unit: kU groups of RPW rows of one token, all loads issued before
-// the first is used (4 KB a warp in flight).
-constexpr int kU = 4;
-
-// Number of entries of the sorted array a[0..n) that are <= v, found by the
-// whole warp (32 probes a round).  Ends for any contents.
-__device__ __forceinline__ int warp_count_le(const int32_t* a, int n, int v, int lane) {
+// Number of entries of the sorted array a[0..n) that are <= v: seven probes a
+// round, which are under way together.  Ends for any contents.
+__device__ __forceinline__ int count_le(const int32_t* a, int n, int v) {
   int lo = 0, len = n;
   while (len > 0) {
-    const int step = (len + 31) >> 5;
-    const int at = (lane + 1) * step - 1;
-    const bool below = at < len && __ldg(a + lo + at) <= v;
-    const int cnt = __popc(__ballot_sync(0xffffffffu, below));
-    const int done = cnt * step;
+    const int step = (len + 7) >> 3;
+    int below = 0;
+#pragma unroll
+    for (int k = 1; k <= 7; ++k) {
+      const int at = k * step - 1;
+      below += at < len && __ldg(a + lo + at) <= v;
+    }
+    const int done = below * step;
     lo += done;
-    len = min(step - 1, len - done);
+    len = min(below < 7 ? step - 1 : len - done, len - done);
   }
   return lo;
 }
 
-template <int D, bool NORM, bool APPEND>
-__global__ void __launch_bounds__(kThreads) fwd_kernel(const FwdParams p) {
-  using G = Geo<D>;
-  const int lane = threadIdx.x & 31, l = lane % G::LPR, sub = lane / G::LPR;
-  const int per_token = p.sq + p.skv * (APPEND ? 2 : 1);
-  const int64_t unit = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int64_t tok = unit / per_token;
-  if (tok >= p.n_rows) return;
-  int part = int(unit - tok * per_token);
-  int kind = 0;  // query, key, value rows
-  if (part >= p.sq) {
-    part -= p.sq;
-    kind = 1;
-    if (APPEND && part >= p.skv) {
-      part -= p.skv;
-      kind = 2;
-    }
+// Append: position and cache row of new token `tok`.
+__device__ __forceinline__ void paged_place(const FwdParams& p, int tok, int& pos, int& state, int64_t& slot) {
+  const tpa_paged_view& c = p.cache;
+  pos = 0;
+  slot = 0;
+  state = kSkip;
+  const int s = count_le(c.offsets + 1, c.n_seqs, tok);
+  if (s >= c.n_seqs) return;  // rows behind the last sequence
+  const int first = __ldg(c.offsets + s), last = __ldg(c.offsets + s + 1), kv = __ldg(c.kv_lens + s);
+  // in 64 bits: nothing here is known to be in range yet
+  const int64_t at = int64_t(kv) - last + tok;
+  bool ok = first >= 0 && tok >= first && at >= 0 && at < int64_t(c.max_pages) * c.page_size &&
+            (!p.rope.table || at < p.rope.table_rows);
+  if (ok) {
+    const int page = __ldg(c.pages + int64_t(s) * c.page_stride + int(at) / c.page_size);
+    ok = page >= 0 && page < c.n_pages;
+    pos = int(at);
+    slot = int64_t(page) * c.n_heads_kv * c.page_size + pos % c.page_size;
   }
-  const int heads = kind == 0 ? p.hq : p.hkv;
-  const Rows src = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
-  const bool inter = p.rope.interleaved != 0;
+  if (ok)
+    state = kUse;
+  else
+    atomicOr(&g_status_rope, TPA_DEV_BAD_INPUT);
+}
+
+template <int D, bool NORM, bool APPEND>
+__global__ void __launch_bounds__(kThreads, kCtas) fwd_kernel(const FwdParams p) {
+  using G = Geo<D>;
+  constexpr int UROWS = 4096 / (D * 2);  // rows of a unit
+  using R = Ring<D, 4096>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool loads = warp == kWarps;
+  const int w = loads ? lane / kBatch : warp;  // whose ring; lanes past the last ring have no units
+  const Bars<R> bar(smem, min(w, kWarps - 1));
+  float* w_s = reinterpret_cast<float*>(smem + R::OFF_W);
+
+  const int per_token = p.sq + p.sk + p.sv;
+  const int64_t units = p.n_rows * per_token, n_warps = int64_t(gridDim.x) * kWarps;
+  const int64_t me = int64_t(w) * gridDim.x + blockIdx.x;
+  const int mine = w < kWarps ? units_for(units, me, n_warps) : 0;
+  const uint32_t table_bytes = p.rope.rot * 4;
+  if (loads) {
+    const int j = lane % kBatch;
+    if (threadIdx.x == 32 * kWarps) *bar.abort_flag = 0;
+    if (j == 0 && w < kWarps) bar.init();
+    __syncwarp();
+    ready_arrive();
+    // the rows of unit (tok, part) and the copies that bring them
+    auto describe = [&](int tok, int part, int& more) {
+      Unit u{0, 0, 0, 0, kUse, tok, 0};
+      more = 0;  // value rows behind the keys
+      if (part < p.sq) {
+        u.h = part * UROWS;
+        u.turned = u.rows = min(p.hq - u.h, UROWS);
+      } else if (part < p.sq + p.sk) {
+        u.kind = 1;
+        u.h = (part - p.sq) * UROWS;
+        u.turned = u.rows = min(p.hkv - u.h, UROWS);
+        if (APPEND && p.sv == 0) {
+          more = p.hkv;
+          u.rows += more;
+        }
+      } else {
+        u.kind = 1;
+        u.h = (part - p.sq - p.sk) * UROWS;
+        u.rows = min(p.hkv - u.h, UROWS);
+      }
+      return u;
+    };
+    auto copy_rows = [&](const Unit& u, int more, int s) {
+      const Rows& src = u.kind == 0 ? p.q : u.turned ? p.k : p.v;
+      uint8_t* st = bar.ring + s * R::STAGE;
+      const int first = u.rows - more;
+      tc::bulk_load(st, src.p + u.token * src.stride + int64_t(u.h) * (D * 2), first * (D * 2), bar.full + s);
+      if (APPEND && more) tc::bulk_load(st + first * (D * 2), p.v.p + u.token * p.v.stride, more * (D * 2), bar.full + s);
+    };
+    // the rows of the first units are on their way before their places are known
+    auto where = [&](int i) {
+      const int64_t u_at = unit_of(me, n_warps, i);
+      Place at{int(u_at / per_token), 0, 0, kSkip, 0};
+      at.part = int(u_at - int64_t(at.tok) * per_token);
+      return at;
+    };
+    int more;
+    if (j < R::NST && j < mine) {
+      const Place at = where(j);
+      copy_rows(describe(at.tok, at.part, more), more, j);
+    }
+    run_loader<R, APPEND>(
+        bar, w, mine,
+        [&](int i) {
+          Place at = where(i);
+          if constexpr (APPEND) paged_place(p, at.tok, at.pos, at.state, at.slot);
+          else plain_place(p.positions, p.n_tokens, p.t_pad, p.rope.table_rows, at.tok, at.pos, at.state);
+          return at;
+        },
+        [&](const Place& at, int i, int stage) {
+          const bool early = i < R::NST;
+          uint8_t* st = bar.ring + stage * R::STAGE;
+          uint64_t* fb = bar.full + stage;
+          Unit u = describe(at.tok, at.part, more);
+          u.state = at.state;
+          u.slot = at.slot;
+          *reinterpret_cast<Unit*>(st + 4096 + R::TABLE) = u;
+          const bool angles = at.state == kUse && u.turned > 0 && table_bytes > 0;
+          if (at.state == kUse && !early) copy_rows(u, more, stage);
+          if (angles) tc::bulk_load(st + 4096, p.rope.table + int64_t(at.pos) * p.rope.rot, table_bytes, fb);
+          tc::mbar_arrive_expect_tx(fb, (early || at.state == kUse ? u.rows * (D * 2) : 0) + (angles ? table_bytes : 0));
+        });
+    return;
+  }
+  if constexpr (NORM) stage_weights<D>(p.rope, w_s);
+  ready_wait();
+
+  const int l = lane % G::LPR, sub = lane / G::LPR;
+  const bool inter = p.rope.interleaved != 0, turns = l < (p.rope.rot >> 4);
   int pa, pb;
   pieces<D>(l, p.rope.rot, inter, pa, pb);
-
-  uint4 va[kU], vb[kU];
-  const int h0 = part * kU * G::RPW + sub;
-  const uint8_t* row = src.p + tok * src.stride + int64_t(h0) * (D * 2);
+  const bool one = p.wide && pb == pa + 1;
+  Turn<R::NST> turn;
+  for (int i = 0; i < mine; ++i, turn.next()) {
+    if (!__all_sync(0xffffffffu, tc::mbar_wait(bar.full + turn.s, turn.phase, bar.abort_flag, &g_status_rope))) break;
+    const uint8_t* st = bar.ring + turn.s * R::STAGE;
+    const Unit u = *reinterpret_cast<const Unit*>(st + 4096 + R::TABLE);
+    if (u.state != kSkip) {
+      // coefficients of the lane's pairs, the weights with them: first' = r (ca first - sb second), second' = r (cb
+      // second + sa first)
+      uint64_t ca[4], cb[4], sa[4], sb[4];
+      if (u.turned > 0 && u.state == kUse) {
+        if (turns) {
+          const float* row = reinterpret_cast<const float*>(st + 4096) + 8 * l;
+          load_p4(row, ca);
+          load_p4(row + (p.rope.rot >> 1), sa);
 #pragma unroll
-  for (int u = 0; u < kU; ++u) {
-    va[u] = vb[u] = make_uint4(0, 0, 0, 0);
-    if (h0 + u * G::RPW < heads) {
-      const uint4* r = reinterpret_cast<const uint4*>(row + u * (G::RPW * D * 2));
-      va[u] = __ldcs(r + pa);
-      vb[u] = __ldcs(r + pb);
-    }
-  }
-
-  int pos;
-  int64_t slot_row = 0;  // append: row of (page, head 0, slot) in the cache
-  bool pad = false;
-  if constexpr (APPEND) {
-    const tpa_paged_view& c = p.cache;
-    const int s = warp_count_le(c.offsets + 1, c.n_seqs, int(tok), lane);
-    if (s >= c.n_seqs) return;  // rows behind the last sequence
-    const int first = __ldg(c.offsets + s), last = __ldg(c.offsets + s + 1), kv = __ldg(c.kv_lens + s);
-    // in 64 bits: nothing here is known to be in range yet
-    const int64_t at = int64_t(kv) - last + tok;
-    bool ok = first >= 0 && tok >= first && at >= 0 && at < int64_t(c.max_pages) * c.page_size &&
-              (!p.rope.table || at < p.rope.table_rows);
-    int page = 0;
-    if (ok) {
-      page = __ldg(c.pages + int64_t(s) * c.page_stride + int(at) / c.page_size);
-      ok = page >= 0 && page < c.n_pages;
-    }
-    if (!ok) {
-      if (lane == 0) atomicOr(&g_status_rope, TPA_DEV_BAD_INPUT);
-      return;
-    }
-    pos = int(at);
-    slot_row = int64_t(page) * c.n_heads_kv * c.page_size + pos % c.page_size;
-  } else {
-    pos = __ldg(p.positions + tok);
-    if (p.n_tokens) {
-      const int64_t b = tok / p.t_pad;
-      pad = int(tok - b * p.t_pad) >= __ldg(p.n_tokens + b);
-    }
-    if (!pad && pos >= p.rope.table_rows) {
-      if (lane == 0) atomicOr(&g_status_rope, TPA_DEV_BAD_INPUT);
-      pad = true;
-    }
-    pad |= pos < 0;
-  }
-
-  float w[16], c[8], s[8];
-  if (kind < 2 && !pad) {
-    if constexpr (NORM) load_weight(kind == 0 ? p.rope.wq : p.rope.wk, p.rope.w_bf16, pa, pb, w);
-    load_angles(p.rope, pos, l, c, s);
-  }
+          for (int j = 0; j < 4; ++j) {
+            cb[j] = ca[j];
+            sb[j] = sa[j];
+          }
+        }
+        if constexpr (NORM) {
+          uint64_t wa[4], wb[4];
+          load_p4(w_s + u.kind * D + 16 * l, wa);
+          load_p4(w_s + u.kind * D + 16 * l + 8, wb);
 #pragma unroll
-  for (int u = 0; u < kU; ++u) {
-    const int h = h0 + u * G::RPW;
-    if (part * kU * G::RPW + u * G::RPW >= heads) break;  // the warp's rows end here
-    uint4 oa = va[u], ob = vb[u];
-    if (pad) {
-      oa = ob = make_uint4(0, 0, 0, 0);
-    } else if (kind < 2) {
-      float x[16];
-      unpack8(oa, x);
-      unpack8(ob, x + 8);
-      if constexpr (NORM) {
-        const float r = rstd16<D>(x, p.rope.eps);
+          for (int j = 0; j < 4; ++j) {
+            ca[j] = turns ? mul2(ca[j], wa[j]) : wa[j];
+            cb[j] = turns ? mul2(cb[j], wb[j]) : wb[j];
+            sa[j] = mul2(sa[j], wa[j]);
+            sb[j] = mul2(sb[j], wb[j]);
+          }
+        }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = x[i] * r * w[i];
+        for (int j = 0; j < 4; ++j) sb[j] = neg2(sb[j]);
       }
-      if (l < (p.rope.rot >> 4)) rotate(x, c, s, inter, 1.f);
-      oa = pack8(x);
-      ob = pack8(x + 8);
-    }
-    if (h < heads) {
+      int64_t pitch = D * 2;
       uint8_t* out;
-      if (APPEND && kind > 0)
-        out = static_cast<uint8_t*>(kind == 1 ? p.cache.k_cache : p.cache.v_cache) +
-              (slot_row + int64_t(h) * p.cache.page_size) * (D * 2);
-      else
-        out = (kind == 0 ? p.qo.p + tok * p.qo.stride : p.ko.p + tok * p.ko.stride) + int64_t(h) * (D * 2);
-      reinterpret_cast<uint4*>(out)[pa] = oa;
-      reinterpret_cast<uint4*>(out)[pb] = ob;
+      uint8_t* vout = nullptr;
+      if (APPEND && u.kind == 1) {
+        pitch = int64_t(p.cache.page_size) * (D * 2);
+        const int64_t at = u.slot * (D * 2);
+        out = static_cast<uint8_t*>(p.cache.k_cache) + at + u.h * pitch;
+        vout = static_cast<uint8_t*>(p.cache.v_cache) + at + (u.turned ? -int64_t(u.turned) : int64_t(u.h)) * pitch;
+      } else {
+        const RowsOut& o = u.kind == 0 ? p.qo : p.ko;
+        out = o.p + u.token * o.stride + int64_t(u.h) * (D * 2);
+      }
+#pragma unroll 4
+      for (int r0 = 0; r0 < u.rows; r0 += G::RPW) {
+        const int r = r0 + sub;
+        uint4 oa = make_uint4(0, 0, 0, 0), ob = oa;
+        if (u.state == kUse) {
+          // rows past the unit read what an earlier one left there, and are not written
+          const uint4* src = reinterpret_cast<const uint4*>(st + r * (D * 2));
+          oa = src[pa];
+          ob = src[pb];
+          if ((NORM || p.rope.rot > 0) && r0 < u.turned) {
+            const Vals x = unpack16(oa, ob, inter);
+            Vals y = x;
+            if (turns) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                y.a[j] = fma2(x.a[j], ca[j], mul2(x.b[j], sb[j]));
+                y.b[j] = fma2(x.b[j], cb[j], mul2(x.a[j], sa[j]));
+              }
+            } else if constexpr (NORM) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                y.a[j] = mul2(x.a[j], ca[j]);
+                y.b[j] = mul2(x.b[j], cb[j]);
+              }
+            }
+            if constexpr (NORM) {
+              const float rs = rstd<D>(x, p.rope.eps);
+              const uint64_t r2 = f2(rs, rs);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                y.a[j] = mul2(y.a[j], r2);
+                y.b[j] = mul2(y.b[j], r2);
+              }
+            }
+            if (r < u.turned) pack16(y, inter, oa, ob);
+          }
+        }
+        if (r < u.rows) {
+          store_pieces((APPEND && r >= u.turned ? vout : out) + r * pitch, pa, pb, oa, ob, one);
+        }
+      }
     }
+    __syncwarp();  // every lane has read the stage
+    if (lane == 0) tc::mbar_arrive(bar.empty + turn.s);
   }
 }
 
@@ -295,157 +604,239 @@ struct BwdParams {
   Rows gq, gk, q, k;
   RowsOut dq, dk;
   float* partial;  // [grid][2][D]
+  int32_t wide;    // dq and dk rows are 32-byte aligned
 };
 
-constexpr int kBwdU = 2;         // groups of rows whose loads a warp issues together
 constexpr int kBwdMaxGrid = 608;  // CTAs: bounds the partial sums
 
+// 16 values of a lane from a row in shared memory
 template <bool F32>
-struct Grad16 {
-  uint4 v[F32 ? 4 : 2];
-  __device__ __forceinline__ void load(const uint8_t* row, int pa, int pb) {
-    const uint4* r = reinterpret_cast<const uint4*>(row);
-    if constexpr (F32) {
-      v[0] = __ldcs(r + 2 * pa);
-      v[1] = __ldcs(r + 2 * pa + 1);
-      v[2] = __ldcs(r + 2 * pb);
-      v[3] = __ldcs(r + 2 * pb + 1);
-    } else {
-      v[0] = __ldcs(r + pa);
-      v[1] = __ldcs(r + pb);
-    }
-  }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < (F32 ? 4 : 2); ++i) v[i] = make_uint4(0, 0, 0, 0);
-  }
-  __device__ __forceinline__ void get(float* x) const {
-    if constexpr (F32) {
+__device__ __forceinline__ Vals load16(const uint8_t* row, int pa, int pb, bool inter) {
+  if constexpr (F32) {
+    Vals v;
+    load_p4(reinterpret_cast<const float*>(row) + 8 * pa, v.a);
+    load_p4(reinterpret_cast<const float*>(row) + 8 * pb, v.b);
+    if (inter) {
+      uint64_t t[8] = {v.a[0], v.a[1], v.a[2], v.a[3], v.b[0], v.b[1], v.b[2], v.b[3]};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        x[4 * i] = __uint_as_float(v[i].x);
-        x[4 * i + 1] = __uint_as_float(v[i].y);
-        x[4 * i + 2] = __uint_as_float(v[i].z);
-        x[4 * i + 3] = __uint_as_float(v[i].w);
+        float a0, b0, a1, b1;
+        unf2(t[2 * i], a0, b0);
+        unf2(t[2 * i + 1], a1, b1);
+        v.a[i] = f2(a0, a1);
+        v.b[i] = f2(b0, b1);
       }
-    } else {
-      unpack8(v[0], x);
-      unpack8(v[1], x + 8);
     }
-  }
-};
-
-template <bool F32>
-__device__ __forceinline__ void store16(uint8_t* row, int pa, int pb, const float* x) {
-  if constexpr (F32) {
-    float4* r = reinterpret_cast<float4*>(row);
-    r[2 * pa] = make_float4(x[0], x[1], x[2], x[3]);
-    r[2 * pa + 1] = make_float4(x[4], x[5], x[6], x[7]);
-    r[2 * pb] = make_float4(x[8], x[9], x[10], x[11]);
-    r[2 * pb + 1] = make_float4(x[12], x[13], x[14], x[15]);
+    return v;
   } else {
-    reinterpret_cast<uint4*>(row)[pa] = pack8(x);
-    reinterpret_cast<uint4*>(row)[pb] = pack8(x + 8);
+    return unpack16(reinterpret_cast<const uint4*>(row)[pa], reinterpret_cast<const uint4*>(row)[pb], inter);
   }
 }
 
+// 32 bytes, one whole sector, in a store
+__device__ __forceinline__ void store32(uint8_t* at, uint64_t a, uint64_t b, uint64_t c, uint64_t d) {
+  asm volatile("st.global.v4.b64 [%0], {%1, %2, %3, %4};" ::"l"(at), "l"(a), "l"(b), "l"(c), "l"(d) : "memory");
+}
+
+// `wide`: rows are 32-byte aligned.  Where a lane's 16-byte pieces lie two and
+// two together they then leave as one store; as two, each would touch half a sector.
+template <bool F32>
+__device__ __forceinline__ void store16(uint8_t* row, int pa, int pb, const Vals& v, bool inter, bool wide) {
+  if constexpr (F32) {
+    uint64_t t[8] = {v.a[0], v.a[1], v.a[2], v.a[3], v.b[0], v.b[1], v.b[2], v.b[3]};
+    if (inter) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float a0, a1, b0, b1;
+        unf2(v.a[i], a0, a1);
+        unf2(v.b[i], b0, b1);
+        t[2 * i] = f2(a0, b0);
+        t[2 * i + 1] = f2(a1, b1);
+      }
+    }
+    if (wide) {
+      store32(row + 32 * pa, t[0], t[1], t[2], t[3]);
+      store32(row + 32 * pb, t[4], t[5], t[6], t[7]);
+      return;
+    }
+    ulonglong2* a = reinterpret_cast<ulonglong2*>(row + 32 * pa);
+    ulonglong2* b = reinterpret_cast<ulonglong2*>(row + 32 * pb);
+    a[0] = make_ulonglong2(t[0], t[1]);
+    a[1] = make_ulonglong2(t[2], t[3]);
+    b[0] = make_ulonglong2(t[4], t[5]);
+    b[1] = make_ulonglong2(t[6], t[7]);
+  } else {
+    uint4 x, y;
+    pack16(v, inter, x, y);
+    store_pieces(row, pa, pb, x, y, wide && pb == pa + 1);
+  }
+}
+
+// Units of 2 KB of x and as many gradients (2 or 4 KB).  A warp takes queries
+// or keys, not both, so that it holds one weight's sums (16 registers); the
+// warps are divided as the units are.
 template <int D, bool NORM, bool GIN32, bool GOUT32>
-__global__ void __launch_bounds__(kThreads) bwd_kernel(const BwdParams p) {
+__global__ void __launch_bounds__(kThreads, kCtas) bwd_kernel(const BwdParams p) {
   using G = Geo<D>;
   constexpr int GB = GIN32 ? 4 : 2, OB = GOUT32 ? 4 : 2;
-  __shared__ float part_s[kWarps][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % G::LPR, sub = lane / G::LPR;
-  const int64_t n_warps = int64_t(gridDim.x) * kWarps, me = int64_t(blockIdx.x) * kWarps + warp;
-  const bool inter = p.rope.interleaved != 0;
+  constexpr int UROWS = 2048 / (D * 2);
+  constexpr uint32_t XOFF = UROWS * D * GB, DATA = XOFF + 2048;
+  using R = Ring<D, DATA>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool loads = warp == kWarps;
+  const int wi = loads ? lane / kBatch : warp;  // whose ring; lanes past the last ring have no units
+  const Bars<R> bar(smem, min(wi, kWarps - 1));
+  float* w_s = reinterpret_cast<float*>(smem + R::OFF_W);
+
+  const int sq = (p.hq + UROWS - 1) / UROWS, skv = (p.hkv + UROWS - 1) / UROWS;
+  const int n_warps = gridDim.x * kWarps, n_q = min(max(int(int64_t(n_warps) * sq / (sq + skv)), 1), n_warps - 1);
+  auto kind_of = [&](int w_) { return w_ * int(gridDim.x) + int(blockIdx.x) < n_q ? 0 : 1; };
+  const int kind = kind_of(wi), per_token = kind == 0 ? sq : skv, heads = kind == 0 ? p.hq : p.hkv;
+  const int me = wi * gridDim.x + blockIdx.x - (kind == 0 ? 0 : n_q), of = kind == 0 ? n_q : n_warps - n_q;
+  const int64_t units = p.n_rows * per_token;
+  const int mine = wi < kWarps ? units_for(units, me, of) : 0;
+  const uint32_t table_bytes = p.rope.rot * 4;
+  const int l = lane % G::LPR, sub = lane / G::LPR;
+  const bool inter = p.rope.interleaved != 0, turns = l < (p.rope.rot >> 4);
   int pa, pb;
   pieces<D>(l, p.rope.rot, inter, pa, pb);
 
-  for (int kind = 0; kind < 2; ++kind) {
-    const int heads = kind == 0 ? p.hq : p.hkv;
-    const int slices = (heads + G::RPW * kBwdU - 1) / (G::RPW * kBwdU);
-    const Rows g = kind == 0 ? p.gq : p.gk, x_in = kind == 0 ? p.q : p.k;
-    const RowsOut out = kind == 0 ? p.dq : p.dk;
-    float w[16], acc[16];
+  if (loads) {
+    const int j = lane % kBatch;
+    if (threadIdx.x == 32 * kWarps) *bar.abort_flag = 0;
+    if (j == 0 && wi < kWarps) bar.init();
+    __syncwarp();
+    ready_arrive();
+    const Rows g_in = kind == 0 ? p.gq : p.gk, x_in = kind == 0 ? p.q : p.k;
+    run_loader<R, false>(
+        bar, wi, mine,
+        [&](int i) {
+          const int64_t u_at = unit_of(me, of, i);
+          Place at{int(u_at / per_token), 0, 0, kPad, 0};
+          at.part = int(u_at - int64_t(at.tok) * per_token);
+          plain_place(p.positions, p.n_tokens, p.t_pad, p.rope.table_rows, at.tok, at.pos, at.state);
+          return at;
+        },
+        [&](const Place& at, int, int stage) {
+          uint8_t* st = bar.ring + stage * R::STAGE;
+          uint64_t* fb = bar.full + stage;
+          const int h = at.part * UROWS, rows = min(heads - h, UROWS);
+          *reinterpret_cast<Unit*>(st + DATA + R::TABLE) = Unit{kind, h, rows, rows, at.state, at.tok, 0};
+          if (at.state == kUse) {
+            tc::mbar_arrive_expect_tx(fb, rows * (D * (GB + (NORM ? 2 : 0))) + table_bytes);
+            tc::bulk_load(st, g_in.p + at.tok * g_in.stride + int64_t(h) * (D * GB), rows * (D * GB), fb);
+            if constexpr (NORM)
+              tc::bulk_load(st + XOFF, x_in.p + at.tok * x_in.stride + int64_t(h) * (D * 2), rows * (D * 2), fb);
+            tc::bulk_load(st + DATA, p.rope.table + int64_t(at.pos) * p.rope.rot, table_bytes, fb);
+          } else {
+            tc::mbar_arrive(fb);
+          }
+        });
+  } else {
+  if constexpr (NORM) stage_weights<D>(p.rope, w_s);
+  ready_wait();
+  Vals w, acc;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-    if constexpr (NORM) load_weight(kind == 0 ? p.rope.wq : p.rope.wk, p.rope.w_bf16, pa, pb, w);
-    const int64_t units = p.n_rows * slices;
-    for (int64_t unit = me; unit < units; unit += n_warps) {
-      const int64_t tok = unit / slices;
-      const int hbase = int(unit - tok * slices) * kBwdU * G::RPW, h0 = hbase + sub;
-      const int pos = __ldg(p.positions + tok);
-      bool pad = pos < 0;
-      if (p.n_tokens) {
-        const int64_t b = tok / p.t_pad;
-        pad |= int(tok - b * p.t_pad) >= __ldg(p.n_tokens + b);
-      }
-      if (!pad && pos >= p.rope.table_rows) {
-        if (lane == 0) atomicOr(&g_status_rope, TPA_DEV_BAD_INPUT);
-        pad = true;
-      }
-      Grad16<GIN32> gv[kBwdU];
-      Grad16<false> xv[kBwdU];
+  for (int j = 0; j < 4; ++j) acc.a[j] = acc.b[j] = 0;
+  if constexpr (NORM) {
+    load_p4(w_s + kind * D + 16 * l, w.a);
+    load_p4(w_s + kind * D + 16 * l + 8, w.b);
+  }
+  const RowsOut o = kind == 0 ? p.dq : p.dk;
+  Turn<R::NST> turn;
+  for (int i = 0; i < mine; ++i, turn.next()) {
+    if (!__all_sync(0xffffffffu, tc::mbar_wait(bar.full + turn.s, turn.phase, bar.abort_flag, &g_status_rope))) break;
+    const uint8_t* st = bar.ring + turn.s * R::STAGE;
+    const Unit u = *reinterpret_cast<const Unit*>(st + DATA + R::TABLE);
+    uint64_t c[4], sn[4];
+    if (turns && u.state == kUse) {
+      const float* row = reinterpret_cast<const float*>(st + DATA) + 8 * l;
+      load_p4(row, c);
+      load_p4(row + (p.rope.rot >> 1), sn);
+    }
+    uint8_t* out = o.p + u.token * o.stride + int64_t(u.h) * (D * OB);
+#pragma unroll 1
+    for (int r0 = 0; r0 < u.rows; r0 += G::RPW) {
+      const int r = r0 + sub;
+      const bool live = r < u.rows;
+      Vals z;
 #pragma unroll
-      for (int u = 0; u < kBwdU; ++u) {
-        gv[u].zero();
-        xv[u].zero();
-        const int h = h0 + u * G::RPW;
-        if (!pad && h < heads) {
-          gv[u].load(g.p + tok * g.stride + int64_t(h) * (D * GB), pa, pb);
-          if constexpr (NORM) xv[u].load(x_in.p + tok * x_in.stride + int64_t(h) * (D * 2), pa, pb);
-        }
-      }
-      float c[8], s[8];
-      if (!pad) load_angles(p.rope, pos, l, c, s);
+      for (int j = 0; j < 4; ++j) z.a[j] = z.b[j] = 0;
+      if (u.state == kUse) {
+        if (live) z = load16<GIN32>(st + r * (D * GB), pa, pb, inter);
+        if (turns) {
+          const Vals g = z;
 #pragma unroll
-      for (int u = 0; u < kBwdU; ++u) {
-        if (hbase + u * G::RPW >= heads) break;
-        const int h = h0 + u * G::RPW;
-        float z[16];
-        gv[u].get(z);
-        if (!pad) {
-          if (l < (p.rope.rot >> 4)) rotate(z, c, s, inter, -1.f);
-          if constexpr (NORM) {
-            float x[16];
-            xv[u].get(x);
-            const float r = rstd16<D>(x, p.rope.eps);
-            float dot = 0.f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              x[i] *= r;
-              acc[i] = fmaf(z[i], x[i], acc[i]);
-              z[i] *= w[i];
-              dot = fmaf(z[i], x[i], dot);
-            }
-            dot = row_sum<G::LPR>(dot) * (1.f / D);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) z[i] = r * (z[i] - x[i] * dot);
+          for (int j = 0; j < 4; ++j) {
+            z.a[j] = fma2(g.a[j], c[j], mul2(g.b[j], sn[j]));
+            z.b[j] = fma2(g.b[j], c[j], neg2(mul2(g.a[j], sn[j])));
           }
         }
-        if (h < heads) store16<GOUT32>(out.p + tok * out.stride + int64_t(h) * (D * OB), pa, pb, z);
-      }
-    }
-    if constexpr (NORM) {
-      // rows of the warp, then warps of the CTA, in a fixed order
+        if constexpr (NORM) {
+          // with y = r z w:  dw += (r z) x,  dx = y - x (r^2 mean(y x))
+          Vals x;
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
+          for (int j = 0; j < 4; ++j) x.a[j] = x.b[j] = 0;
+          if (live) x = load16<false>(st + XOFF + r * (D * 2), pa, pb, inter);
+          const float rs = rstd<D>(x, p.rope.eps);
+          const uint64_t r2 = live ? f2(rs, rs) : 0;  // eps may be 0, and rs of a row of zeros infinite
+          uint64_t dot[2] = {0, 0};
 #pragma unroll
-        for (int o = G::LPR; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
-      if (sub == 0) {
+          for (int j = 0; j < 4; ++j) {
+            z.a[j] = mul2(z.a[j], r2);
+            z.b[j] = mul2(z.b[j], r2);
+            acc.a[j] = fma2(z.a[j], x.a[j], acc.a[j]);
+            acc.b[j] = fma2(z.b[j], x.b[j], acc.b[j]);
+            z.a[j] = mul2(z.a[j], w.a[j]);
+            z.b[j] = mul2(z.b[j], w.b[j]);
+            dot[0] = fma2(z.a[j], x.a[j], dot[0]);
+            dot[1] = fma2(z.b[j], x.b[j], dot[1]);
+          }
+          const float m = row_sum<G::LPR>(sum2(add2(dot[0], dot[1]))) * (-1.f / D) * rs * rs;
+          const uint64_t m2 = f2(m, m);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          part_s[warp][8 * pa + i] = acc[i];
-          part_s[warp][8 * pb + i] = acc[8 + i];
+          for (int j = 0; j < 4; ++j) {
+            z.a[j] = fma2(x.a[j], m2, z.a[j]);
+            z.b[j] = fma2(x.b[j], m2, z.b[j]);
+          }
         }
       }
-      __syncthreads();
-      if (threadIdx.x < D) {
-        float t = 0.f;
+      if (live) store16<GOUT32>(out + r * (D * OB), pa, pb, z, inter, p.wide);
+    }
+    __syncwarp();  // every lane has read the stage
+    if (lane == 0) tc::mbar_arrive(bar.empty + turn.s);
+  }
+  if constexpr (NORM) {
+    // rows of the warp, then warps of the CTA, in a fixed order; a warp's ring is its own and no longer in use
+    float* mine_s = reinterpret_cast<float*>(bar.ring);
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) t += part_s[i][threadIdx.x];
-        p.partial[(int64_t(blockIdx.x) * 2 + kind) * D + threadIdx.x] = t;
+    for (int j = 0; j < 8; ++j) {
+      float lo, hi;
+      unf2(j < 4 ? acc.a[j] : acc.b[j - 4], lo, hi);
+#pragma unroll
+      for (int o_ = G::LPR; o_ < 32; o_ <<= 1) {
+        lo += __shfl_xor_sync(0xffffffffu, lo, o_);
+        hi += __shfl_xor_sync(0xffffffffu, hi, o_);
       }
-      __syncthreads();
+      if (sub == 0) {
+        // pair 2 (j % 4) and the next one, firsts or seconds
+        const int i = 2 * (j & 3), second = j >> 2;
+        const int at = inter ? 16 * l + 2 * i + second : 8 * (second ? pb : pa) + i;
+        mine_s[at] = lo;
+        mine_s[at + (inter ? 2 : 1)] = hi;
+      }
+    }
+  }
+  }
+  if constexpr (NORM) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+      float t = 0.f;
+#pragma unroll
+      for (int j = 0; j < kWarps; ++j)
+        if (kind_of(j) == i / D) t += reinterpret_cast<const float*>(smem + j * R::WARP)[i % D];
+      p.partial[int64_t(blockIdx.x) * 2 * D + i] = t;
     }
   }
   tc::grid_launch_dependents();
@@ -490,6 +881,8 @@ __global__ void __launch_bounds__(256) table_kernel(float* table, int64_t n, int
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+bool aligned32(const void* p, int64_t stride) { return ((reinterpret_cast<uintptr_t>(p) | uintptr_t(stride)) & 31) == 0; }
+
 bool rows_ok(const void* p, int64_t stride, int heads, int d, int elem) {
   // the largest strides in use are those of fused projections; 2^40 elements keep all byte offsets in 64 bits
   return p && aligned16(p) && stride >= int64_t(heads) * d && stride < (int64_t(1) << 40) && (stride * elem) % 16 == 0;
@@ -517,36 +910,52 @@ Rope make_rope(const tpa_rope_params* r) {
 }
 
 int units_of(int heads, int d) {
-  const int rows = (32 / (d / 16)) * kU;
+  const int rows = 4096 / (d * 2);
   return (heads + rows - 1) / rows;
 }
 
-template <int D, bool APPEND>
-int launch_fwd(const FwdParams& p, bool norm, cudaStream_t st) {
-  const int per_token = p.sq + p.skv * (APPEND ? 2 : 1);
-  const int64_t ctas = (p.n_rows * per_token + kWarps - 1) / kWarps;
-  if (ctas > 0x7fffffff) return TPA_ERR_INVALID_ARG;
-  if (norm)
-    fwd_kernel<D, true, APPEND><<<unsigned(ctas), kThreads, 0, st>>>(p);
-  else
-    fwd_kernel<D, false, APPEND><<<unsigned(ctas), kThreads, 0, st>>>(p);
+int num_sms() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 148;
+  }
+  return sms;
+}
+
+// Two CTAs an SM, or one for every unit where there are fewer.
+int grid_of(int64_t units) {
+  const int64_t most = kCtas * int64_t(num_sms());
+  const int64_t n = units < most ? units : most;
+  return int(n < 1 ? 1 : n < kBwdMaxGrid ? n : kBwdMaxGrid);
+}
+
+template <int D, bool NORM, bool APPEND>
+int launch_fwd_as(const FwdParams& p, cudaStream_t st) {
+  using R = Ring<D, 4096>;
+  const int per_token = p.sq + p.sk + p.sv;
+  TPA_CUDA_TRY(cudaFuncSetAttribute(fwd_kernel<D, NORM, APPEND>, cudaFuncAttributeMaxDynamicSharedMemorySize, R::BYTES));
+  fwd_kernel<D, NORM, APPEND><<<grid_of(p.n_rows * per_token), kThreads, R::BYTES, st>>>(p);
   TPA_CUDA_TRY(cudaGetLastError());
   return TPA_OK;
 }
 
-template <int D, bool GIN32, bool GOUT32>
-int launch_bwd(const BwdParams& p, bool norm, float* dwq, float* dwk, cudaStream_t st) {
-  const int rows = Geo<D>::RPW * kBwdU;
-  const int64_t units = p.n_rows * ((p.hq + rows - 1) / rows);
-  const int64_t want = (units + kWarps - 1) / kWarps;
-  const int grid = int(want < 1 ? 1 : want < kBwdMaxGrid ? want : kBwdMaxGrid);
-  if (!norm) {
-    bwd_kernel<D, false, GIN32, GOUT32><<<grid, kThreads, 0, st>>>(p);
-    TPA_CUDA_TRY(cudaGetLastError());
-    return TPA_OK;
-  }
-  bwd_kernel<D, true, GIN32, GOUT32><<<grid, kThreads, 0, st>>>(p);
+template <int D, bool APPEND>
+int launch_fwd(const FwdParams& p, bool norm, cudaStream_t st) {
+  return norm ? launch_fwd_as<D, true, APPEND>(p, st) : launch_fwd_as<D, false, APPEND>(p, st);
+}
+
+template <int D, bool NORM, bool GIN32, bool GOUT32>
+int launch_bwd_as(const BwdParams& p, float* dwq, float* dwk, cudaStream_t st) {
+  constexpr int UROWS = 2048 / (D * 2);
+  using R = Ring<D, UROWS * D * (GIN32 ? 4 : 2) + 2048>;
+  const int64_t units = p.n_rows * ((p.hq + UROWS - 1) / UROWS + (p.hkv + UROWS - 1) / UROWS);
+  const int grid = grid_of(units);
+  TPA_CUDA_TRY(cudaFuncSetAttribute(bwd_kernel<D, NORM, GIN32, GOUT32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    R::BYTES));
+  bwd_kernel<D, NORM, GIN32, GOUT32><<<grid, kThreads, R::BYTES, st>>>(p);
   TPA_CUDA_TRY(cudaGetLastError());
+  if (!NORM) return TPA_OK;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * D / 32);
   cfg.blockDim = dim3(1024);
@@ -558,6 +967,12 @@ int launch_bwd(const BwdParams& p, bool norm, float* dwq, float* dwk, cudaStream
   cfg.numAttrs = 1;
   TPA_CUDA_TRY(cudaLaunchKernelEx(&cfg, bwd_sum_kernel, static_cast<const float*>(p.partial), grid, D, dwq, dwk));
   return TPA_OK;
+}
+
+template <int D, bool GIN32, bool GOUT32>
+int launch_bwd(const BwdParams& p, bool norm, float* dwq, float* dwk, cudaStream_t st) {
+  return norm ? launch_bwd_as<D, true, GIN32, GOUT32>(p, dwq, dwk, st)
+              : launch_bwd_as<D, false, GIN32, GOUT32>(p, dwq, dwk, st);
 }
 
 }  // namespace
@@ -608,11 +1023,12 @@ extern "C" int tpa_qk_norm_rope_fwd(const int32_t* positions, const int32_t* n_t
   p.hq = n_heads_q;
   p.hkv = n_heads_kv;
   p.sq = units_of(n_heads_q, d);
-  p.skv = units_of(n_heads_kv, d);
+  p.sk = units_of(n_heads_kv, d);
   p.q = {static_cast<const uint8_t*>(q), q_stride * 2};
   p.k = {static_cast<const uint8_t*>(k), k_stride * 2};
   p.qo = {static_cast<uint8_t*>(q_out), q_out_stride * 2};
   p.ko = {static_cast<uint8_t*>(k_out), k_out_stride * 2};
+  p.wide = aligned32(q_out, p.qo.stride) && aligned32(k_out, p.ko.stride);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return d == 128 ? launch_fwd<128, false>(p, rope->q_weight, st) : launch_fwd<64, false>(p, rope->q_weight, st);
 }
@@ -670,6 +1086,7 @@ extern "C" int tpa_qk_norm_rope_bwd(const int32_t* positions, const int32_t* n_t
   p.dq = {static_cast<uint8_t*>(dq), dq_stride * go};
   p.dk = {static_cast<uint8_t*>(dk), dk_stride * go};
   p.partial = static_cast<float*>(workspace);
+  p.wide = aligned32(dq, p.dq.stride) && aligned32(dk, p.dk.stride);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   auto run = [&](auto gin, auto gout) {
     constexpr bool A = decltype(gin)::value, B = decltype(gout)::value;
@@ -716,12 +1133,14 @@ extern "C" int tpa_paged_append(const tpa_paged_view* cache, const void* k, int6
   p.hq = n_heads_q;
   p.hkv = cache->n_heads_kv;
   p.sq = n_heads_q ? units_of(n_heads_q, d) : 0;
-  p.skv = units_of(cache->n_heads_kv, d);
+  p.sk = units_of(cache->n_heads_kv, d);
+  p.sv = units_of(2 * cache->n_heads_kv, d) == 1 ? 0 : p.sk;  // keys and values in one unit where they fit
   p.q = {static_cast<const uint8_t*>(q), q_stride * 2};
   p.k = {static_cast<const uint8_t*>(k), k_stride * 2};
   p.v = {static_cast<const uint8_t*>(v), v_stride * 2};
   p.qo = {static_cast<uint8_t*>(q_out), q_out_stride * 2};
   p.cache = *cache;
+  p.wide = (!n_heads_q || aligned32(q_out, p.qo.stride)) && aligned32(cache->k_cache, 0) && aligned32(cache->v_cache, 0);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return d == 128 ? launch_fwd<128, true>(p, rope->q_weight, st) : launch_fwd<64, true>(p, rope->q_weight, st);
 }
