@@ -628,7 +628,7 @@ uint64_t tpa_paged_attn_workspace_bytes(int32_t max_q_len, int32_t n_heads_q, in
  * must be finite.
  *   q [n_rows, Hq, d] bf16, rows q_stride elements apart (a multiple of 8), 16-byte aligned
  *   o [n_rows, Hq, d] bf16, lse [n_rows, Hq] fp32 (written, rows behind the last sequence not)
- *   Hq / Hkv <= 32
+ *   Hq / Hkv <= 64
  *   max_q_len: the most new tokens of a sequence; larger ones stay right but the
  *     kernel is chosen by it.  softmax_scale <= 0 selects 1/sqrt(d).
  *   workspace: tpa_paged_attn_workspace_bytes() bytes, 256-byte aligned, of one

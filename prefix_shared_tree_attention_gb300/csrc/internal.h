@@ -33,7 +33,7 @@ int tpa_internal_status_bwd(bool clear);
 int tpa_internal_status_lmh(bool clear);
 int tpa_internal_status_rope(bool clear);
 int tpa_internal_status_verify(bool clear);
-int tpa_internal_status_paged(bool clear);
+int tpa_internal_status_pfew(bool clear);
 int tpa_internal_status_ptile(bool clear);
 
 // The per-sequence gather of the log-prob pass (logprobs.cu), shared with

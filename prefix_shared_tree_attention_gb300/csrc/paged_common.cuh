@@ -3,7 +3,7 @@
 // 128 keys are dealt to the CTAs, and the record of a tile whose steps went to
 // several CTAs.
 //
-// The steps of all tiles stand in one line, key/value head by head, sequence by
+// The steps (of 64 or 128 keys) of all tiles stand in one line, key/value head by head, sequence by
 // sequence, tile by tile, and CTA c of n takes the part [c T / n, (c + 1) T / n)
 // of its T steps: every CTA has the same work whatever the lengths, a long
 // sequence is split along its keys by as much as that needs, and a CTA has at
@@ -23,7 +23,6 @@
 
 namespace paged {
 
-constexpr int kStep = 128;     // keys of a step
 constexpr uint32_t kSmemMax = 232448;  // 227 KB opt-in per CTA
 constexpr int kMaxGrid = 160;  // CTAs of a launch, at most (one an SM)
 constexpr float kLog2e = 1.4426950408889634f;
@@ -38,6 +37,7 @@ struct Batch {
   int32_t group;     // query heads of a key/value head
   int32_t tile_tok;  // tokens of a tile
   int32_t window;    // 0: none
+  int32_t step_shift;  // a step is 1 << step_shift keys
 };
 
 struct Seq {
@@ -72,62 +72,101 @@ __device__ __forceinline__ Tile make_tile(const Batch& b, const Seq& q, int i) {
   t.pos0 = q.kv - q.n + t0;
   t.hi = max(t.pos0 + t.n, 0);
   t.lo = b.window > 0 ? max(t.pos0 - b.window + 1, 0) : 0;
-  t.step0 = t.lo / kStep;
-  t.steps = max((t.hi + kStep - 1) / kStep - t.step0, 1);
+  t.step0 = t.lo >> b.step_shift;
+  t.steps = max(((t.hi + (1 << b.step_shift) - 1) >> b.step_shift) - t.step0, 1);
   return t;
 }
 
-struct Scan {
-  long long prefix[257];  // steps of one head before the chunk of sequences of each thread
+// 64-bit quotient; nearly always both sides fit in 32 bits, where it is several times faster.
+__device__ __forceinline__ long long quot(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)(uint32_t(a) / uint32_t(b)) : a / b;
+}
+
+// How the CTAs share `total` steps: n of them, the first `rem` with size + 1 and the others with `size`.
+struct Shares {
+  int n;
+  long long size, rem;
+  __device__ __forceinline__ Shares(long long total, int grid, int min_steps) {
+    const long long want = quot(total + min_steps - 1, min_steps);
+    n = int(want < grid ? want : grid);
+    size = n > 0 ? quot(total, n) : 0;
+    rem = total - size * n;
+  }
+  __device__ __forceinline__ long long begin(int c) const { return size * c + (c < rem ? c : rem); }
+  __device__ __forceinline__ int of(long long f) const {
+    const long long edge = rem * (size + 1);
+    return int(f < edge ? quot(f, size + 1) : rem + quot(f - edge, size));
+  }
 };
 
-// Every thread of the CTA (256 of them or more; the first 256 work): fills the
-// scan, returns the steps of one head.  Reports bad sequences once (CTA 0).
-__device__ inline long long scan_batch(const Batch& b, Scan* sc, unsigned int* status) {
+// What the scan finds out: the sums of its warps, and where this CTA begins.
+struct Scan {
+  long long warp_sum[8];
+  long long item;            // flat step at which the first tile begins
+  int head, seq, i, begin;   // key/value head, sequence, tile of it, step of the tile
+  Seq q;
+};
+
+// Every thread of the CTA (256 of them or more; the first 256 work, a share of
+// the sequences each): adds up the steps and finds this CTA's first one; the
+// thread that has it among its sequences writes it down.  Reports bad
+// sequences once (CTA 0).
+__device__ inline Shares scan_batch(const Batch& b, int min_steps, Scan* sc, unsigned int* status) {
   const int tid = threadIdx.x, chunk = (b.n_seqs + 255) >> 8;
+  const int s0 = tid * chunk, s1 = min(s0 + chunk, b.n_seqs);
+  long long mine = 0, incl = 0;
+  Seq q{0, 0, 0};
   if (tid < 256) {
-    long long mine = 0;
-    const int s1 = min((tid + 1) * chunk, b.n_seqs);
-    for (int s = tid * chunk; s < s1; ++s) {
-      const Seq q = load_seq(b, s, blockIdx.x == 0 ? status : nullptr);
+    for (int s = s0; s < s1; ++s) {
+      q = load_seq(b, s, blockIdx.x == 0 ? status : nullptr);
       const int n = tiles_of(b, q.n);
       for (int i = 0; i < n; ++i) mine += make_tile(b, q, i).steps;
     }
-    long long v = mine;
+    incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long t = __shfl_up_sync(0xffffffffu, v, o);
-      if ((tid & 31) >= o) v += t;
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if ((tid & 31) >= o) incl += v;
     }
-    sc->prefix[tid + 1] = v;
+    if ((tid & 31) == 31) sc->warp_sum[tid >> 5] = incl;
   }
   __syncthreads();
-  if (tid < 256) {
-    long long before = 0;
-    for (int w = 0; w < (tid >> 5); ++w) before += sc->prefix[(w + 1) * 32];
-    const long long v = sc->prefix[tid + 1];
-    __syncwarp();
-    // all warps have read the warp totals before any overwrites them
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-    sc->prefix[tid + 1] = before + v;
-    if (tid == 0) sc->prefix[0] = 0;
+  long long per_head = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    if (w < (tid >> 5)) before += sc->warp_sum[w];
+    per_head += sc->warp_sum[w];
+  }
+  const Shares shares(per_head * b.hkv, gridDim.x, min_steps);
+  if (int(blockIdx.x) < shares.n) {
+    const long long f = shares.begin(blockIdx.x), head = quot(f, per_head);
+    long long r = f - head * per_head - (before + incl - mine);  // step among this thread's sequences
+    if (tid < 256 && r >= 0 && r < mine) {
+      for (int s = s0; s < s1; ++s) {
+        if (chunk > 1) q = load_seq(b, s, nullptr);
+        const int n = tiles_of(b, q.n);
+        for (int i = 0; i < n; ++i) {
+          const int steps = make_tile(b, q, i).steps;
+          if (r >= 0 && r < steps) {
+            sc->item = f - r;
+            sc->head = int(head);
+            sc->seq = s;
+            sc->i = i;
+            sc->begin = int(r);
+            sc->q = q;
+          }
+          r -= steps;
+        }
+      }
+    }
   }
   __syncthreads();
-  return sc->prefix[256];
+  return shares;
 }
 
-// How many CTAs share `total` steps, and the first step of CTA c.
-__device__ __forceinline__ int used_ctas(long long total, int grid, int min_steps) {
-  const long long want = (total + min_steps - 1) / min_steps;
-  return int(want < grid ? want : grid);
-}
-__device__ __forceinline__ long long cta_begin(long long total, int n, int c) { return total * c / n; }
-__device__ __forceinline__ int cta_of(long long total, int n, long long f) { return int(((f + 1) * n - 1) / total); }
-
-// Walks the tiles of the steps [f, f + left).
+// Walks the tiles of this CTA's steps.
 struct Walk {
   long long left;     // steps from `begin` of the current tile on
-  long long item;     // flat step at which the current tile begins
   int head, seq, i;   // key/value head, sequence, tile of the sequence
   int n_tiles;
   Seq q;
@@ -138,44 +177,21 @@ struct Walk {
     const long long e = begin + left;
     end = e < t.steps ? int(e) : t.steps;
   }
-  // f < total
-  __device__ inline void start(const Batch& b, const Scan* sc, long long per_head, long long f, long long count) {
-    left = count;
-    head = int(f / per_head);
-    long long r = f - head * per_head;
-    int lo = 0, hi = 256;  // the last chunk that begins at r or before
-    while (hi - lo > 1) {
-      const int m = (lo + hi) >> 1;
-      if (sc->prefix[m] <= r) lo = m;
-      else hi = m;
-    }
-    const int chunk = (b.n_seqs + 255) >> 8;
-    long long at = sc->prefix[lo];
-    for (seq = lo * chunk;; ++seq) {  // ends: the chunk holds step r
-      q = load_seq(b, seq, nullptr);
-      n_tiles = tiles_of(b, q.n);
-      for (i = 0; i < n_tiles; ++i) {
-        t = make_tile(b, q, i);
-        if (at + t.steps > r) {
-          begin = int(r - at);
-          item = f - begin;
-          take();
-          return;
-        }
-        at += t.steps;
-      }
-      if (seq + 1 >= b.n_seqs) {  // not reached with the lengths that were scanned
-        left = 0;
-        begin = end = 0;
-        return;
-      }
-    }
+  __device__ inline void start(const Batch& b, const Scan* sc, const Shares& shares) {
+    left = shares.size + (int(blockIdx.x) < shares.rem ? 1 : 0);
+    head = sc->head;
+    seq = sc->seq;
+    i = sc->i;
+    begin = sc->begin;
+    q = sc->q;
+    n_tiles = tiles_of(b, q.n);
+    t = make_tile(b, q, i);
+    take();
   }
   // To the next tile; false when this CTA's steps are done.
   __device__ inline bool next(const Batch& b) {
     left -= end - begin;
     if (left <= 0) return false;
-    item += t.steps;
     if (++i >= n_tiles) {
       i = 0;
       int tries = 0;
@@ -224,14 +240,57 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* m, uin
       : "memory");
 }
 
-// Writes the record of the tile that this CTA's first segment is a part of.
-__device__ __forceinline__ void write_split(const Params& p, const Walk& w, long long total, int n_ctas) {
+// One CTA's part of a tile, as the producer hands it to the other roles.
+struct Segment {
+  int32_t n_it;  // steps; -1: no more
+  int32_t head, first, n, pos0, lo, hi, key0, whole, slot;
+  int32_t pad_[2];
+};
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// O (+)= P V with P read from TMEM
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Writes the record of the tile that this CTA's first segment is a part of: one thread of each CTA.
+__device__ __forceinline__ void write_split(const Params& p, const Scan* sc, const Shares& sh) {
   Split s = {};
-  if (w.begin > 0) {  // the tile began in an earlier CTA
-    const int c0 = cta_of(total, n_ctas, w.item), c1 = cta_of(total, n_ctas, w.item + w.t.steps - 1);
-    if (c0 + 1 == int(blockIdx.x)) s = Split{1, w.head, w.t.first, w.t.n, c0, c1, {0, 0}};
+  if (int(blockIdx.x) < sh.n && sc->begin > 0) {  // the tile began in an earlier CTA
+    const Tile t = make_tile(p.b, sc->q, sc->i);
+    const int c0 = sh.of(sc->item), c1 = sh.of(sc->item + t.steps - 1);
+    if (c0 + 1 == int(blockIdx.x)) s = Split{1, sc->head, t.first, t.n, c0, c1, {0, 0}};
   }
   p.split[blockIdx.x] = s;
+}
+
+// Launches a kernel that may begin while the one before it in the stream ends;
+// it waits for that one itself (tc::grid_wait_prior) before it touches memory.
+template <class... Args>
+inline int launch_overlapped(void (*kernel)(Args...), dim3 grid, int threads, uint32_t smem, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  TPA_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, args...));
+  return TPA_OK;
 }
 
 // Cache rows as a matrix [n_pages * Hkv * page_size, d]: boxes of 64 columns x `rows` rows.
@@ -247,8 +306,24 @@ inline bool cache_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Queries [n_rows, Hq, d]: boxes of 64 columns x the group's heads x a sub-tile's tokens.
+inline bool query_map(CUtensorMap* m, const tpa_paged_view* c, const Params& p, int sub_tok) {
+  tmap::EncodeTiledFn fn = tmap::encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {cuuint64_t(c->head_dim), cuuint64_t(p.hq), cuuint64_t(c->n_rows)};
+  const cuuint64_t strides[2] = {cuuint64_t(c->head_dim) * 2, cuuint64_t(p.q_stride) * 2};
+  const cuuint32_t box[3] = {64, cuuint32_t(p.b.group), cuuint32_t(sub_tok)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16*>(p.q), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace paged
 
-// paged_tile.cu: launches the attention kernel for tiles of `rows` (128 or 256)
-// rows; the caller joins split tiles afterwards.
-int tpa_internal_paged_tile(const tpa_paged_view* cache, paged::Params& p, int rows, int grid, cudaStream_t stream);
+// Launch the attention kernel (the caller joins split tiles afterwards): for
+// tiles of `rows` = 16, 32 or 64 rows (paged_few.cu), and of 256 (paged_tile.cu).
+// The latter may find that it was not compiled as it assumes; it then launches nothing.
+constexpr int kPagedTileUnfit = 1;
+int tpa_internal_paged_few(const tpa_paged_view* cache, paged::Params& p, int rows, int grid, cudaStream_t stream);
+int tpa_internal_paged_tile(const tpa_paged_view* cache, paged::Params& p, int grid, cudaStream_t stream);

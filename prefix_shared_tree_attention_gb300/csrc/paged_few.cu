@@ -1,0 +1,620 @@
+// Paged attention for few rows (a decode step, drafted tokens): at most NR = 16,
+// 32 or 64 rows (tokens x heads of a key/value head's group) a tile.
+//
+// Bound by the reads of the cache; the kernel is built around them.  Two threads
+// keep the keys and values of NS steps of 128 keys (192 KB of them) on their
+// way by TMA, pages of 16 to 128 slots as boxes, across tiles.  The products
+// are turned over so that the 128-row side of the tcgen05 tiles holds keys and
+// head dimensions, of which there are enough, and the rows are the short side:
+//   S^T = K Q^T  (128 keys x NR),   O^T += V^T P^T  (D x NR, V read transposed)
+// Thread t of a warpgroup owns key t of a step: NR exponentials a thread, all
+// 128 threads at work however few rows there are.  A row's running maximum is
+// then shared by the whole warpgroup; it is moved only when some score passes it
+// by 2^8 (one vote a step finds out), which is exact, since numerator and
+// denominator keep the same one.  Sums stay per thread until the tile's end.
+// Two warpgroups take the steps in turn, each with its own maximum, sums, S^T and
+// O^T (in TMEM), so that one's softmax runs beside the other's products; the two
+// are joined at the tile's end.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "device_common.cuh"
+#include "internal.h"
+#include "paged_common.cuh"
+#include "tc.cuh"
+#include "tmap.h"
+
+namespace {
+
+__device__ unsigned int g_status_pfew = 0;
+
+using namespace paged;
+
+constexpr int KS = 128;                  // keys of a step
+constexpr uint32_t kChunk = KS * 128;    // bytes of a 64-column piece of a step's keys or values
+constexpr float kNoMax = -1.0e30f;       // running maximum (log2 units) of a row that has seen nothing
+
+template <int D, int NR>
+struct FewCfg {
+  static constexpr int NCH = D / 64;
+  static constexpr uint32_t TILE = NCH * kChunk;       // keys or values of a step
+  static constexpr uint32_t QCH = NR * 128;            // a 64-column piece of the queries
+  static constexpr uint32_t PT = NR * KS * 2;          // P^T of a warpgroup: NR rows of two 64-key pieces
+  static constexpr uint32_t FIXED = NCH * QCH + 2 * PT + 160 + 128 + NR * 48 + 1024;
+  static constexpr int NS_FIT = int((kSmemMax - 1024 - FIXED) / (2 * TILE));
+  static constexpr int NS = NS_FIT > 6 ? 6 : NS_FIT;
+  // The values come first: for d 64 the transposed product reads 128 "dimensions" from each step, the second
+  // 64 being whatever follows (the next step's, or the first keys), and their results are not used.
+  static constexpr uint32_t OFF_V = 0;
+  static constexpr uint32_t OFF_K = OFF_V + NS * TILE;
+  static constexpr uint32_t OFF_Q = OFF_K + NS * TILE;
+  static constexpr uint32_t OFF_P = OFF_Q + NCH * QCH;
+  static constexpr uint32_t OFF_SCAN = OFF_P + 2 * PT;
+  static constexpr uint32_t OFF_SEG = OFF_SCAN + 160;
+  static constexpr uint32_t OFF_F = OFF_SEG + 128;     // floats, see below: 12 NR
+  // q_full, q_empty, k_full[NS], k_empty[NS], v_full[NS], v_empty[NS], s_full[2], p_full[2], ml_full[2], o_final,
+  // o_free, drain, seg_full[2], seg_empty[2]
+  static constexpr int NBAR = 2 + 4 * NS + 6 + 3 + 4;
+  static constexpr uint32_t OFF_BAR = OFF_F + (2 * (1 + 4 + 1) + 4 + 4) * NR * 4;
+  static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr uint32_t BYTES = OFF_MISC + 32 + 1024;
+  static constexpr uint32_t TMEM_COLS = 4 * NR;
+  static_assert(sizeof(Scan) <= 160 && sizeof(Segment) * 2 <= 128 && NS >= 2 && OFF_BAR % 8 == 0, "layout");
+  static_assert(BYTES <= kSmemMax, "shared memory budget");
+};
+
+// `or` of a predicate over the 128 threads of warpgroup h
+__device__ __forceinline__ bool group_any(int h, bool v) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %2, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, 128, p;\n\t"
+      "selp.b32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(2 + h), "r"(int(v))
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void group_sync(int h) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(2 + h) : "memory"); }
+
+// For NR values a lane, reduced over the warp: the lane ends with the results
+// of rows owner .. owner + NR/32 - 1 (at least one row; several lanes then hold the same).
+// Halves the rows with each exchange, so NR + 5 exchanges in place of 5 NR.
+template <int NR, class Op>
+__device__ __forceinline__ void warp_reduce_rows(float (&v)[NR], int lane, Op op) {
+  int n = NR;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    if (n > 1) {
+      n >>= 1;
+      const bool up = lane & o;
+#pragma unroll
+      for (int i = 0; i < NR / 2; ++i)
+        if (i < n) {
+          const float send = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+          v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, o));
+        }
+    } else {
+      v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+    }
+  }
+}
+// The first row that a lane holds after warp_reduce_rows.
+template <int NR>
+__device__ __forceinline__ int owned_row(int lane) {
+  int n = NR, r = 0;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (n > 1) {
+      n >>= 1;
+      if (lane & o) r += n;
+    }
+  return r;
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[N]) {
+  static_assert(N == 8 || N == 16 || N == 32 || N == 64, "columns");
+  if constexpr (N == 8) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(at));
+  } else if constexpr (N == 16) {
+    tc::tmem_ld16(at, r);
+  } else if constexpr (N == 32) {
+    tc::tmem_ld32(at, r);
+  } else {
+    tc::tmem_ld32(at, *reinterpret_cast<uint32_t(*)[32]>(r));
+    tc::tmem_ld32(at + 32, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
+  }
+}
+
+template <int D, int NR>
+__global__ void __launch_bounds__(384, 1)
+    paged_few_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v, const Params p) {
+  using C = FewCfg<D, NR>;
+  constexpr int NCH = C::NCH, NS = C::NS;
+  constexpr uint32_t TILE = C::TILE;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sV = smem + C::OFF_V;
+  uint8_t* sK = smem + C::OFF_K;
+  uint8_t* sQ = smem + C::OFF_Q;
+  Scan* sc = reinterpret_cast<Scan*>(smem + C::OFF_SCAN);
+  volatile Segment* seg_ring = reinterpret_cast<volatile Segment*>(smem + C::OFF_SEG);
+  float* f_s = reinterpret_cast<float*>(smem + C::OFF_F);
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* k_full = q_full + 2;
+  uint64_t* k_empty = k_full + NS;
+  uint64_t* v_full = k_empty + NS;
+  uint64_t* v_empty = v_full + NS;
+  uint64_t* s_full = v_empty + NS;  // [2]
+  uint64_t* p_full = s_full + 2;    // [2]
+  uint64_t* ml_full = p_full + 2;   // [2]
+  uint64_t* o_final = ml_full + 2;
+  uint64_t* o_free = o_final + 1;
+  uint64_t* drain = o_free + 1;
+  uint64_t* seg_full = drain + 1;   // [2]
+  uint64_t* seg_empty = drain + 3;  // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+  volatile int* dead_s = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);  // [2]
+
+  const int warp = threadIdx.x >> 5;
+  constexpr int W_K = 8, W_MMA = 9, W_V = 10;
+
+  if (threadIdx.x == 0) {
+    tc::mbar_init(q_full, 1);
+    tc::mbar_init(q_empty, 1);
+    for (int s = 0; s < NS; ++s) {
+      tc::mbar_init(k_full + s, 1);
+      tc::mbar_init(k_empty + s, 1);
+      tc::mbar_init(v_full + s, 1);
+      tc::mbar_init(v_empty + s, 1);
+    }
+    for (int h = 0; h < 2; ++h) {
+      tc::mbar_init(s_full + h, 1);
+      tc::mbar_init(p_full + h, 128);
+      tc::mbar_init(ml_full + h, 128);
+      tc::mbar_init(seg_full + h, 1);
+      tc::mbar_init(seg_empty + h, 1 + 256);
+      dead_s[h] = 0;
+    }
+    tc::mbar_init(o_final, 1);
+    tc::mbar_init(o_free, 256);
+    tc::mbar_init(drain, 1);
+    *abort_flag = 0;
+    tc::fence_mbar_init();
+  }
+  // query rows that the loads do not reach are zero: their scores then do not move a maximum
+  for (int i = threadIdx.x; i < int(NCH * C::QCH / 16); i += blockDim.x)
+    reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0, 0, 0, 0);
+  tc::fence_proxy_async_smem();
+  if (warp == W_MMA) tc::tmem_alloc(tmem_slot, C::TMEM_COLS);
+  tc::tc_fence_before();
+  // From here on memory is read and written that the kernel before may write and read.
+  tc::grid_wait_prior();
+  tc::grid_launch_dependents();  // the joining kernel waits for this one's end by itself
+  const Shares shares = scan_batch(p.b, p.min_steps, sc, &g_status_pfew);
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;  // columns: S^T of the two warpgroups, then their O^T
+
+  if (int(blockIdx.x) >= shares.n) {  // nothing to do here
+    if (threadIdx.x == 0) write_split(p, sc, shares);
+  } else if (warp == W_K || warp == W_V) {
+    // ------------------------------------------------------------ producers: one thread for the keys (and the queries,
+    // and the segments that the other roles read), one for the values.  Each walks the steps.  With 16-token pages a
+    // step is 16 boxes a side; one thread alone for both took longer to issue them than HBM to deliver.
+    const bool keys = warp == W_K;
+    if (tc::elect_one()) {
+      const CUtensorMap* tm = keys ? &tm_k : &tm_v;
+      tc::tma_prefetch_desc(tm);
+      if (keys) tc::tma_prefetch_desc(&tm_q);
+      auto wait1 = [&](uint64_t* b_, uint32_t par) { return tc::mbar_wait(b_, par, abort_flag, &g_status_pfew); };
+      uint64_t* full = keys ? k_full : v_full;
+      uint64_t* empty = keys ? k_empty : v_empty;
+      uint8_t* tiles = keys ? sK : sV;
+      Walk w;
+      w.start(p.b, sc, shares);
+      const int per_step = KS >> p.b.page_shift;                    // pages of a step
+      const uint32_t page_bytes = uint32_t(128) << p.b.page_shift;  // of one 64-column piece
+      const uint32_t q_bytes = uint32_t(NCH) * p.b.tile_tok * p.b.group * 128;
+      int t = 0, s = 0, nq = 0;  // steps loaded, the next stage, segments whose queries were loaded
+      uint32_t par = 1;
+      bool ok = true, more = w.end > w.begin;
+      auto load_queries = [&](int k) {
+        if (!wait1(q_empty, (k & 1) ^ 1)) return false;
+        tc::mbar_arrive_expect_tx(q_full, q_bytes);
+        for (int c = 0; c < NCH; ++c)
+          tc::tma_load_3d(sQ + c * C::QCH, &tm_q, q_full, c * 64, w.head * p.b.group, w.t.first);
+        ++nq;
+        return true;
+      };
+      for (int k = 0; ok; ++k) {
+        const int n_it = more ? w.end - w.begin : -1;
+        const int key0 = (w.t.step0 + w.begin) * KS;
+        if (keys) {
+          if (!(ok = wait1(seg_empty + (k & 1), ((k >> 1) & 1) ^ 1))) break;
+          volatile Segment* sg = seg_ring + (k & 1);
+          sg->n_it = n_it;
+          sg->head = w.head;
+          sg->first = w.t.first;
+          sg->n = w.t.n;
+          sg->pos0 = w.t.pos0;
+          sg->lo = w.t.lo;
+          sg->hi = w.t.hi;
+          sg->key0 = key0;
+          sg->whole = w.begin == 0 && w.end == w.t.steps;
+          sg->slot = blockIdx.x * 2 + (w.begin == 0 ? 1 : 0);
+          tc::mbar_arrive(seg_full + (k & 1));
+        }
+        if (!more) break;
+        if (keys && k == 0) load_queries(0);  // later ones behind the segment's first keys
+        const int32_t* row = p.b.pages + int64_t(w.seq) * p.b.page_stride;
+        const int lo = w.t.lo, hi = w.t.hi, head = w.head;
+        // the pages of step j: -1 where none is needed.  Looked up a step ahead of their use.
+        auto look = [&](int j, int (&pg)[8]) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int ki = key0 + j * KS + (i << p.b.page_shift);
+            const bool need = j < n_it && i < per_step && ki < hi && ki + p.b.page_size > lo;
+            pg[i] = need ? __ldg(row + (ki >> p.b.page_shift)) : -1;
+            if (need && uint32_t(pg[i]) >= uint32_t(p.b.n_pages)) pg[i] = p.b.n_pages;  // out of range, see below
+          }
+        };
+        int next[8];
+        look(0, next);
+        for (int j = 0; j < n_it; ++j) {
+          int at[8], n_pg = 0;  // first cache row of each page; -1: not needed
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            int pg = next[i];
+            if (pg == p.b.n_pages) {  // never followed: page 0 is read in its place
+              atomicOr(&g_status_pfew, TPA_DEV_BAD_INPUT);
+              pg = 0;
+            }
+            at[i] = pg >= 0 ? (pg * p.b.hkv + head) << p.b.page_shift : -1;
+            n_pg += pg >= 0;
+          }
+          look(j + 1, next);
+          if (!(ok = wait1(empty + s, par))) break;
+          tc::mbar_arrive_expect_tx(full + s, n_pg * NCH * page_bytes);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (at[i] >= 0)
+#pragma unroll
+              for (int c = 0; c < NCH; ++c)
+                tma_load_2d(tiles + s * TILE + c * kChunk + i * page_bytes, tm, full + s, c * 64, at[i]);
+          ++t;
+          if (++s == NS) {
+            s = 0;
+            par ^= 1;
+          }
+          if (keys && j == 0 && k > 0 && !(ok = load_queries(k))) break;
+        }
+        if (ok) more = w.next(p.b);
+      }
+      if (*abort_flag) {  // let the copies already issued land before the CTA exits
+        volatile int never = 0;
+        for (int j = (t > NS ? t - NS : 0); j < t; ++j)
+          tc::mbar_wait(full + (j % NS), (j / NS) & 1, &never, &g_status_pfew, 100000000ull);
+        if (nq > 0) tc::mbar_wait(q_full, (nq - 1) & 1, &never, &g_status_pfew, 100000000ull);
+      }
+    }
+    __syncwarp();
+  } else if (warp == W_MMA) {
+    // ------------------------------------------------------------ MMA issuer
+    constexpr uint32_t idesc_s = tc::idesc_bf16(128, NR, false, false);
+    constexpr uint32_t idesc_o = tc::idesc_bf16(128, NR, true, false);
+    const uint64_t dK = tc::smem_desc(tc::smem_u32(sK), 16, 1024);
+    const uint64_t dQ = tc::smem_desc(tc::smem_u32(sQ), 16, 1024);
+    const uint64_t dV = tc::smem_desc(tc::smem_u32(sV), kChunk, 1024);
+    const uint64_t dP = tc::smem_desc(tc::smem_u32(smem + C::OFF_P), 16, 1024);
+    auto issue_s = [&](int h, int s) {  // S^T_h = K(s) Q^T
+      const uint64_t kb = dK + ((s * TILE) >> 4);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        tc::mma_ss(tmem + h * NR, kb + (((k >> 2) * kChunk + (k & 3) * 32) >> 4),
+                   dQ + (((k >> 2) * C::QCH + (k & 3) * 32) >> 4), idesc_s, k > 0);
+      tc::mma_commit(s_full + h);
+    };
+    auto issue_o = [&](int h, int s, bool first) {  // O^T_h (+)= V(s)^T P^T_h
+      const uint64_t vb = dV + ((s * TILE) >> 4), pb = dP + ((h * C::PT) >> 4);
+#pragma unroll
+      for (int k = 0; k < KS / 16; ++k)
+        tc::mma_ss(tmem + 2 * NR + h * NR, vb + ((k * 2048) >> 4),
+                   pb + (((k >> 2) * C::QCH + (k & 3) * 32) >> 4), idesc_o, (!first || k > 0) ? 1u : 0u);
+    };
+    auto wait1 = [&](uint64_t* b_, uint32_t par) { return tc::mbar_wait(b_, par, abort_flag, &g_status_pfew); };
+    if (tc::elect_one()) {
+      int t = 0;             // steps so far
+      int uses[2] = {0, 0};  // steps of each warpgroup so far
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        if (!(ok = wait1(seg_full + (k & 1), (k >> 1) & 1))) break;
+        const int n_it = seg_ring[k & 1].n_it;
+        tc::mbar_arrive(seg_empty + (k & 1));
+        if (n_it < 0) break;
+        if (!(ok = wait1(q_full, k & 1))) break;
+        auto start = [&](int j) {  // S^T of step j, when its keys are there
+          const int s = (t + j) % NS;
+          if (!wait1(k_full + s, ((t + j) / NS) & 1)) return false;
+          tc::tc_fence_after();
+          issue_s(j & 1, s);
+          tc::mma_commit(k_empty + s);
+          if (j + 1 == n_it) tc::mma_commit(q_empty);  // the segment's last S^T
+          return true;
+        };
+        // S^T of the segment before was read before the p_full that its last products waited for
+        if (!(ok = start(0) && (n_it < 2 || start(1)))) break;
+        for (int j = 0; ok && j < n_it; ++j) {
+          const int h = j & 1, s = (t + j) % NS;
+          if (!(ok = wait1(v_full + s, ((t + j) / NS) & 1) && wait1(p_full + h, uses[h] & 1))) break;
+          if (j == 0 && k > 0 && !(ok = wait1(o_free, (k - 1) & 1))) break;
+          ++uses[h];
+          tc::tc_fence_after();
+          issue_o(h, s, j < 2);
+          tc::mma_commit(v_empty + s);
+          if (j + 2 < n_it && !(ok = start(j + 2))) break;
+        }
+        if (ok) tc::mma_commit(o_final);
+        t += n_it;
+      }
+      if (*abort_flag) {  // let issued MMAs finish before TMEM is released
+        volatile int never = 0;
+        tc::mma_commit(drain);
+        tc::mbar_wait(drain, 0, &never, &g_status_pfew, 100000000ull);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 11) {
+    if (threadIdx.x == 352) write_split(p, sc, shares);
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ softmax of every other step
+    const int h = warp >> 2, lane = threadIdx.x & 31;
+    const int r = threadIdx.x & 127;  // key of the step, then head dimension = TMEM lane
+    const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_base + h * NR, tO = tmem + lane_base + 2 * NR;
+    uint8_t* sP = smem + C::OFF_P + h * C::PT + (r >> 6) * C::QCH + (r & 7) * 2;
+    const uint32_t p_chunk = (r >> 3) & 7;  // of the 128-byte piece of a row
+    float* m_s = f_s + h * NR;                       // running maxima
+    float* warp_s = f_s + 2 * NR + h * 4 * NR;       // the four warps' maxima, then sums
+    float* alpha_s = f_s + 10 * NR + h * NR;         // rescaling
+    float* xm_s = f_s + 12 * NR;                     // [2] maxima at the tile's end, both warpgroups'
+    float* xl_s = f_s + 14 * NR;                     // [2] sums
+    float* coef_s = f_s + 16 * NR + h * 2 * NR;      // [2] what the two O^T are multiplied by
+    auto wait_thread = [&](uint64_t* b_, uint32_t par) { return tc::mbar_wait(b_, par, abort_flag, &g_status_pfew); };
+    // The warps of a warpgroup meet in barriers, so they leave together or not at all: a failed wait is passed on
+    // through dead_s at the next vote.
+    bool fine = true;
+    auto note = [&](bool ok) {
+      if (!ok) {
+        fine = false;
+        dead_s[h] = 1;
+      }
+    };
+    int t = 0, uses = 0;
+    for (int k = 0;; ++k) {
+      note(wait_thread(seg_full + (k & 1), (k >> 1) & 1));
+      if (group_any(h, !fine)) break;
+      const volatile Segment* sg = seg_ring + (k & 1);
+      const int n_it = sg->n_it, first = sg->first, n_tok = sg->n, lo = sg->lo, hi = sg->hi, key_first = sg->key0;
+      const int slot = sg->whole ? -1 : sg->slot, head0 = sg->head * p.b.group, pos_first = sg->pos0;
+      tc::mbar_arrive(seg_empty + (k & 1));
+      if (n_it < 0) break;
+      const int live = n_tok * p.b.group;  // rows in use
+      // every row in use sees the keys in [all_lo, all_hi)
+      const int all_hi = pos_first + 1;
+      const int all_lo = p.b.window > 0 ? pos_first + n_tok - p.b.window : 0;
+      float l[NR];
+#pragma unroll
+      for (int i = 0; i < NR; ++i) l[i] = 0.f;
+      bool dead = false;
+      for (int j = h; j < n_it; j += 2) {
+        const int key0 = key_first + j * KS;
+        if (key0 < lo || key0 + KS > hi) {
+          // slots that no row sees may hold anything: zero their values, so that 0 x NaN does not come in
+          const int s = (t + j) % NS;
+          const bool there = wait_thread(v_full + s, ((t + j) / NS) & 1);
+          note(there);
+          if (there && (key0 + r < lo || key0 + r >= hi)) {
+#pragma unroll
+            for (int c = 0; c < NCH; ++c)
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<uint4*>(sV + s * TILE + c * kChunk + r * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+          }
+        }
+        note(wait_thread(s_full + h, uses & 1));
+        ++uses;
+        __syncwarp();
+        tc::tc_fence_after();
+        uint32_t raw[NR];
+        tmem_ld(tS, raw);
+        tc::tmem_ld_wait();
+        float x[NR];
+#pragma unroll
+        for (int i = 0; i < NR; ++i) x[i] = __uint_as_float(raw[i]) * p.scale_log2;
+        if (key0 + KS > all_hi || key0 < all_lo) {
+          // rows [first_row, last_row) see this thread's key
+          const int rel = key0 + r - pos_first;
+          int first_row = max(rel, 0) * p.b.group, last_row = NR;
+          if (p.b.window > 0) last_row = min(max(rel + p.b.window, 0), NR) * p.b.group;
+          if (key0 + r >= hi) last_row = 0;
+#pragma unroll
+          for (int i = 0; i < NR; ++i)
+            if (i < first_row || i >= last_row) x[i] = -INFINITY;
+        }
+        bool grow = j == h;
+#pragma unroll
+        for (int i = 0; i < NR; i += 4) {
+          const float4 m = *reinterpret_cast<const float4*>(m_s + i);
+          grow |= x[i] > m.x + kRescale || x[i + 1] > m.y + kRescale || x[i + 2] > m.z + kRescale ||
+                  x[i + 3] > m.w + kRescale;
+        }
+        if (group_any(h, grow || !fine)) {
+          if (dead_s[h]) {
+            dead = true;
+            break;
+          }
+          float v[NR];
+#pragma unroll
+          for (int i = 0; i < NR; ++i) v[i] = x[i];
+          warp_reduce_rows<NR>(v, lane, [](float a, float b) { return fmaxf(a, b); });
+          constexpr int OWN = NR > 32 ? NR / 32 : 1;
+          const int row = owned_row<NR>(lane);
+#pragma unroll
+          for (int i = 0; i < OWN; ++i) warp_s[(warp & 3) * NR + row + i] = v[i];
+          group_sync(h);
+          if (r < NR) {
+            const float before = j == h ? kNoMax : m_s[r];
+            const float top = fmaxf(fmaxf(warp_s[r], warp_s[NR + r]), fmaxf(warp_s[2 * NR + r], warp_s[3 * NR + r]));
+            const float m = fmaxf(before, top);
+            m_s[r] = m;
+            alpha_s[r] = tc::ex2(before - m);
+          }
+          group_sync(h);
+          if (j != h) {
+#pragma unroll
+            for (int i = 0; i < NR; ++i) l[i] *= alpha_s[i];
+            // O^T of this warpgroup is complete up to its step before: that product was issued before this S^T
+            uint32_t ov[NR];
+            tmem_ld(tO + h * NR, ov);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < NR; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha_s[i]);
+#pragma unroll
+            for (int c = 0; c < NR / 16; ++c)
+              tc::tmem_st16(tO + h * NR + c * 16, *reinterpret_cast<const uint32_t(*)[16]>(ov + c * 16));
+            tc::tmem_st_wait();
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < NR; i += 4) {
+          const float4 m = *reinterpret_cast<const float4*>(m_s + i);
+          const float mm[4] = {m.x, m.y, m.z, m.w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float e = tc::ex2(x[i + u] - mm[u]);
+            l[i + u] += e;
+            // P^T enters the second product as bf16, its operand type; row i + u, key r
+            *reinterpret_cast<__nv_bfloat16*>(sP + (i + u) * 128 + ((p_chunk ^ ((i + u) & 7)) << 4)) =
+                __float2bfloat16_rn(e);
+          }
+        }
+        tc::fence_proxy_async_smem();
+        tc::tc_fence_before();
+        tc::mbar_arrive(p_full + h);
+      }
+      if (dead) break;
+
+      // -------- the tile's end: sums over the warpgroup, maxima and sums of both, then half of the rows each
+      constexpr int OWN = NR > 32 ? NR / 32 : 1;
+      warp_reduce_rows<NR>(l, lane, [](float a, float b) { return a + b; });
+      const int own = owned_row<NR>(lane);
+      group_sync(h);  // warp_s of the last rescaling has been read
+#pragma unroll
+      for (int i = 0; i < OWN; ++i) warp_s[(warp & 3) * NR + own + i] = l[i];
+      group_sync(h);
+      const bool had = h < n_it;  // this warpgroup had a step
+      // Behind this o_final every thread has passed its o_free of the segment before, so nobody reads the exchange any more.
+      note(wait_thread(o_final, k & 1));
+      if (r < NR) {
+        xm_s[h * NR + r] = had ? m_s[r] : kNoMax;
+        xl_s[h * NR + r] = (warp_s[r] + warp_s[NR + r]) + (warp_s[2 * NR + r] + warp_s[3 * NR + r]);
+      }
+      tc::mbar_arrive(ml_full + h);
+      note(wait_thread(ml_full, k & 1));
+      note(wait_thread(ml_full + 1, k & 1));
+      constexpr int HR = NR / 2;  // rows of each warpgroup
+      if (r < HR && fine) {
+        const int row = h * HR + r;
+        const float m0 = xm_s[row], m1 = xm_s[NR + row], l0 = xl_s[row], l1 = xl_s[NR + row];
+        const float top = fmaxf(m0, m1);
+        float a0 = tc::ex2(m0 - top), a1 = tc::ex2(m1 - top);
+        const float sum = l0 * a0 + l1 * a1;
+        if (slot < 0) {
+          const float inv = sum > 0.f ? 1.f / sum : 0.f;
+          a0 *= inv;
+          a1 *= inv;
+        }
+        coef_s[r] = a0;
+        coef_s[NR + r] = a1;
+        if (row < live) {
+          if (slot < 0) {
+            const int tok = row / p.b.group;
+            p.lse[int64_t(first + tok) * p.hq + head0 + row - tok * p.b.group] =
+                sum > 0.f ? (top + __log2f(sum)) * kLn2 : -INFINITY;
+          } else {
+            p.part_ml[int64_t(slot) * p.rows + row] = make_float2(top, sum);
+          }
+        }
+      }
+      if (group_any(h, !fine)) break;
+      tc::tc_fence_after();
+      uint32_t o0[HR], o1[HR];
+      tmem_ld(tO + h * HR, o0);
+      tmem_ld(tO + NR + h * HR, o1);
+      tc::tmem_ld_wait();
+      tc::tc_fence_before();
+      tc::mbar_arrive(o_free);  // O^T may be overwritten by the next segment
+      const bool two = n_it > 1;  // else the second O^T was not written
+      if (r < D) {
+        int tok = (h * HR) / p.b.group, gh = h * HR - tok * p.b.group;
+#pragma unroll
+        for (int i = 0; i < HR; ++i) {
+          const int row = h * HR + i;
+          if (row < live) {
+            float v = __uint_as_float(o0[i]) * coef_s[i];
+            if (two) v = fmaf(__uint_as_float(o1[i]), coef_s[NR + i], v);
+            if (slot < 0)
+              p.o[(int64_t(first + tok) * p.hq + head0 + gh) * D + r] = __float2bfloat16_rn(v);
+            else
+              p.part_o[(int64_t(slot) * p.rows + row) * D + r] = v;
+            if (++gh == p.b.group) {
+              gh = 0;
+              ++tok;
+            }
+          }
+        }
+      }
+      t += n_it;
+    }
+  }
+
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  if (warp == W_MMA) tc::tmem_dealloc(tmem, C::TMEM_COLS);
+}
+
+template <int D, int NR>
+int launch_few(const tpa_paged_view* c, Params& p, int grid, cudaStream_t st) {
+  using C = FewCfg<D, NR>;
+  CUtensorMap tq, tk, tv;
+  p.b.tile_tok = NR / p.b.group;
+  p.b.step_shift = 7;
+  p.min_steps = 1;
+  const uint64_t rows = uint64_t(c->n_pages) * c->n_heads_kv * c->page_size;
+  if (!query_map(&tq, c, p, p.b.tile_tok) || !cache_map(&tk, c->k_cache, rows, D, c->page_size) ||
+      !cache_map(&tv, c->v_cache, rows, D, c->page_size))
+    return TPA_ERR_CUDA;
+  TPA_CUDA_TRY(cudaFuncSetAttribute(paged_few_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES));
+  return launch_overlapped(paged_few_kernel<D, NR>, dim3(grid), 384, C::BYTES, st, tq, tk, tv, static_cast<const Params>(p));
+}
+
+}  // namespace
+
+TPA_DEFINE_STATUS_READER(tpa_internal_status_pfew, g_status_pfew)
+
+int tpa_internal_paged_few(const tpa_paged_view* c, Params& p, int rows, int grid, cudaStream_t st) {
+  if (c->head_dim == 128)
+    return rows == 16 ? launch_few<128, 16>(c, p, grid, st)
+                      : rows == 32 ? launch_few<128, 32>(c, p, grid, st) : launch_few<128, 64>(c, p, grid, st);
+  return rows == 16 ? launch_few<64, 16>(c, p, grid, st)
+                    : rows == 32 ? launch_few<64, 32>(c, p, grid, st) : launch_few<64, 64>(c, p, grid, st);
+}

@@ -1,17 +1,17 @@
 // Paged attention for many rows (chunks of a prompt): tcgen05 tiles.
 //
-// A tile is NH sub-tiles of 128 rows, row r = token * group + head, so a K/V
-// tile of 128 keys is read once for NH * 128 / group tokens of all the group's
+// A tile is two sub-tiles of 128 rows, row r = token * group + head, so a K/V
+// tile of 128 keys is read once for 256 / group tokens of all the group's
 // heads.  The roles and the softmax are those of the tree attention's forward:
-//   warpgroup h < NH  softmax of sub-tile h: thread r owns row r (TMEM lane r),
+//   warpgroup 0, 1    softmax of sub-tile h: thread r owns row r (TMEM lane r),
 //                     online in the log2 domain; P goes to TMEM over S as the
 //                     bf16 operand of the second MMA; O is rescaled in TMEM
 //                     only when a row's maximum has grown by 2^8
-//   warp 4 NH         one thread: walks this CTA's steps, hands each segment to
+//   warp 8            one thread: walks this CTA's steps, hands each segment to
 //                     the other roles, loads Q, and the pages of K and V (a
 //                     page of 16 to 128 slots is a box; one of 128-byte rows
 //                     swizzled as the MMA descriptors want)
-//   warp 4 NH + 1     one thread issues the MMAs
+//   warp 9            one thread issues the MMAs
 // Bound by the tensor and exponential pipes: 4 d operations and one exponential
 // for each (row, key).
 #include <cuda.h>
@@ -35,15 +35,11 @@ using tc::fma2;
 using tc::unf2;
 
 constexpr uint32_t kChunk = 128 * 128;  // bytes of a 128-row x 64-column bf16 tile
+constexpr int kStep = 128;              // keys of a step
 
-// One CTA's part of a tile, as the producer hands it to the other roles.
-struct Segment {
-  int32_t n_it;  // steps; -1: no more
-  int32_t head, first, n, pos0, lo, hi, key0, whole, slot;
-  int32_t pad_[2];
-};
+constexpr int NH = 2;  // sub-tiles
 
-template <int D, int NH>
+template <int D>
 struct TileCfg {
   static constexpr int NCH = D / 64;
   static constexpr uint32_t TILE = NCH * kChunk;  // 128 x D bf16
@@ -53,45 +49,28 @@ struct TileCfg {
   static constexpr uint32_t OFF_K = OFF_Q + NH * TILE;
   static constexpr uint32_t OFF_V = OFF_K + NS * TILE;
   static constexpr uint32_t OFF_SCAN = OFF_V + NS * TILE;
-  static constexpr uint32_t OFF_SEG = OFF_SCAN + 2112;
+  static constexpr uint32_t OFF_SEG = OFF_SCAN + 160;
   static constexpr uint32_t OFF_BAR = OFF_SEG + 128;
   // q_full, q_empty, k_full[NS], k_empty[NS], v_full[NS], v_empty[NS], s_full[NH], p_full[NH], o_free[NH],
   // o_final, drain, seg_full[2], seg_empty[2]
   static constexpr int NBAR = 2 + 4 * NS + 3 * NH + 2 + 4;
   static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr uint32_t BYTES = OFF_MISC + 16 + 1024;
-  // Two sub-tiles: registers move from the producer/issuer warpgroup to the
+  // Registers move from the producer/issuer warpgroup to the
   // softmax warpgroups, within what the CTA was launched with.
-  static constexpr int THREADS = NH == 2 ? 384 : 256;
+  static constexpr int THREADS = 384;
   static constexpr int REG_LAUNCH = 168, REG_LOW = 120, REG_HIGH = 184;
-  static_assert(NH != 2 || REG_HIGH * 256 + REG_LOW * 128 <= REG_LAUNCH * 384, "register split");
-  static constexpr uint32_t TMEM_COLS = NH == 2 ? 512 : 256;
-  static_assert(sizeof(Scan) <= 2112 && sizeof(Segment) * 2 <= 128 && NS >= 2, "layout");
+  static_assert(REG_HIGH * 256 + REG_LOW * 128 <= REG_LAUNCH * 384, "register split");
+  static constexpr uint32_t TMEM_COLS = 512;
+  static_assert(sizeof(Scan) <= 160 && sizeof(Segment) * 2 <= 128 && NS >= 2, "layout");
   static_assert(BYTES <= kSmemMax, "shared memory budget");
 };
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
-// O (+)= P V with P read from TMEM
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                       uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-template <int D, int NH>
-__global__ void __launch_bounds__(TileCfg<D, NH>::THREADS, 1)
+template <int D>
+__global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
     paged_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const Params p) {
-  using C = TileCfg<D, NH>;
+  using C = TileCfg<D>;
   constexpr int NCH = C::NCH, NS = C::NS;
   constexpr uint32_t TILE = C::TILE;
   extern __shared__ uint8_t smem_raw[];
@@ -121,7 +100,6 @@ __global__ void __launch_bounds__(TileCfg<D, NH>::THREADS, 1)
   constexpr int W_TMA = 4 * NH, W_MMA = 4 * NH + 1;
   const int sub_tok = p.b.tile_tok / NH;  // tokens of a sub-tile
 
-  tc::grid_launch_dependents();  // the joining kernel waits for this one's end by itself
   if (threadIdx.x == 0) {
     tc::mbar_init(q_full, 1);
     tc::mbar_init(q_empty, 1);
@@ -145,21 +123,19 @@ __global__ void __launch_bounds__(TileCfg<D, NH>::THREADS, 1)
     *abort_flag = 0;
     tc::fence_mbar_init();
   }
-  const long long per_head = scan_batch(p.b, sc, &g_status_ptile);
-  const long long total = per_head * p.b.hkv;
-  const int n_ctas = used_ctas(total, gridDim.x, p.min_steps);
-  if (int(blockIdx.x) >= n_ctas) {
-    if (threadIdx.x == 0) p.split[blockIdx.x].valid = 0;
-    return;
-  }
   if (warp == W_MMA) tc::tmem_alloc(tmem_slot, C::TMEM_COLS);
   tc::tc_fence_before();
-  __syncthreads();
+  // From here on memory is read and written that the kernel before may write and read.
+  tc::grid_wait_prior();
+  tc::grid_launch_dependents();  // the joining kernel waits for this one's end by itself
+  const Shares shares = scan_batch(p.b, p.min_steps, sc, &g_status_ptile);
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp >= W_TMA) {
-    if constexpr (NH == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REG_LOW));
+  if (int(blockIdx.x) >= shares.n) {  // nothing to do here
+    if (threadIdx.x == 0) write_split(p, sc, shares);
+  } else if (warp >= W_TMA) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REG_LOW));
     if (warp == W_TMA) {
       // ---------------------------------------------------------- producer
       if (tc::elect_one()) {
@@ -167,10 +143,8 @@ __global__ void __launch_bounds__(TileCfg<D, NH>::THREADS, 1)
         tc::tma_prefetch_desc(&tm_k);
         tc::tma_prefetch_desc(&tm_v);
         auto wait1 = [&](uint64_t* b_, uint32_t par) { return tc::mbar_wait(b_, par, abort_flag, &g_status_ptile); };
-        const long long f0 = cta_begin(total, n_ctas, blockIdx.x), f1 = cta_begin(total, n_ctas, blockIdx.x + 1);
-        Walk w;
-        w.start(p.b, sc, per_head, f0, f1 - f0);
-        write_split(p, w, total, n_ctas);
+                Walk w;
+        w.start(p.b, sc, shares);
         const int per_step = kStep >> p.b.page_shift;       // pages of a step
         const uint32_t page_bytes = uint32_t(128) << p.b.page_shift;  // of one 64-column piece
         const uint32_t q_bytes = uint32_t(NH * NCH) * sub_tok * p.b.group * 128;
@@ -316,9 +290,11 @@ __global__ void __launch_bounds__(TileCfg<D, NH>::THREADS, 1)
         }
       }
       __syncwarp();
+    } else if (threadIdx.x == 32 * (W_MMA + 1)) {
+      write_split(p, sc, shares);
     }
   } else if (warp < 4 * NH) {
-    if constexpr (NH == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REG_HIGH));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REG_HIGH));
     // ------------------------------------------------------------ softmax (sub-tile h)
     const int h = warp >> 2;
     const int r = threadIdx.x & 127;  // row of the sub-tile = TMEM lane
@@ -470,26 +446,9 @@ __global__ void __launch_bounds__(TileCfg<D, NH>::THREADS, 1)
   if (warp == W_MMA) tc::tmem_dealloc(tmem, C::TMEM_COLS);
 }
 
-// launch_tile<D, 2> returns this (not a library status) when the kernel was not
-// compiled to the register count that its setmaxnreg split assumes
-constexpr int kRegsMismatch = 1;
-
-// Queries [n_rows, Hq, d]: boxes of 64 columns x the group's heads x a sub-tile's tokens.
-bool query_map(CUtensorMap* m, const tpa_paged_view* c, const Params& p, int sub_tok) {
-  tmap::EncodeTiledFn fn = tmap::encode_fn();
-  if (!fn) return false;
-  const cuuint64_t dims[3] = {cuuint64_t(c->head_dim), cuuint64_t(p.hq), cuuint64_t(c->n_rows)};
-  const cuuint64_t strides[2] = {cuuint64_t(c->head_dim) * 2, cuuint64_t(p.q_stride) * 2};
-  const cuuint32_t box[3] = {64, cuuint32_t(p.b.group), cuuint32_t(sub_tok)};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16*>(p.q), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-template <int D, int NH>
+template <int D>
 int launch_tile(const tpa_paged_view* c, Params& p, int grid, cudaStream_t st) {
-  using C = TileCfg<D, NH>;
+  using C = TileCfg<D>;
   const int sub_tok = 128 / p.b.group;
   CUtensorMap tq, tk, tv;
   const uint64_t rows = uint64_t(c->n_pages) * c->n_heads_kv * c->page_size;
@@ -498,25 +457,21 @@ int launch_tile(const tpa_paged_view* c, Params& p, int grid, cudaStream_t st) {
     return TPA_ERR_CUDA;
   p.b.tile_tok = NH * sub_tok;
   p.min_steps = 2;
-  TPA_CUDA_TRY(cudaFuncSetAttribute(paged_tile_kernel<D, NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES));
-  if constexpr (NH == 2) {
+  p.b.step_shift = 7;
+  TPA_CUDA_TRY(cudaFuncSetAttribute(paged_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES));
+  {
     cudaFuncAttributes fa;
-    TPA_CUDA_TRY(cudaFuncGetAttributes(&fa, paged_tile_kernel<D, NH>));
-    if (fa.numRegs != C::REG_LAUNCH) return kRegsMismatch;
+    TPA_CUDA_TRY(cudaFuncGetAttributes(&fa, paged_tile_kernel<D>));
+    if (fa.numRegs != C::REG_LAUNCH) return kPagedTileUnfit;  // the setmaxnreg split would not add up
   }
-  paged_tile_kernel<D, NH><<<grid, C::THREADS, C::BYTES, st>>>(tq, tk, tv, p);
-  TPA_CUDA_TRY(cudaGetLastError());
-  return TPA_OK;
+  return launch_overlapped(paged_tile_kernel<D>, dim3(grid), C::THREADS, C::BYTES, st, tq, tk, tv,
+                           static_cast<const Params>(p));
 }
 
 }  // namespace
 
 TPA_DEFINE_STATUS_READER(tpa_internal_status_ptile, g_status_ptile)
 
-int tpa_internal_paged_tile(const tpa_paged_view* c, Params& p, int rows, int grid, cudaStream_t st) {
-  if (rows == 256) {
-    const int rc = c->head_dim == 128 ? launch_tile<128, 2>(c, p, grid, st) : launch_tile<64, 2>(c, p, grid, st);
-    if (rc != kRegsMismatch) return rc;
-  }
-  return c->head_dim == 128 ? launch_tile<128, 1>(c, p, grid, st) : launch_tile<64, 1>(c, p, grid, st);
+int tpa_internal_paged_tile(const tpa_paged_view* c, Params& p, int grid, cudaStream_t st) {
+  return c->head_dim == 128 ? launch_tile<128>(c, p, grid, st) : launch_tile<64>(c, p, grid, st);
 }

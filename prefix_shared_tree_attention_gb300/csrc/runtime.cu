@@ -107,7 +107,7 @@ int tpa_sync_status(void* stream) {
   const int s[] = {tpa_internal_status_classify(true), tpa_internal_status_logprobs(true),
                    tpa_internal_status_fwd(true), tpa_internal_status_bwd(true),
                    tpa_internal_status_lmh(true), tpa_internal_status_rope(true),
-                   tpa_internal_status_verify(true), tpa_internal_status_paged(true),
+                   tpa_internal_status_verify(true), tpa_internal_status_pfew(true),
                    tpa_internal_status_ptile(true)};
   for (int x : s) {
     if (x == TPA_ERR_CUDA) return TPA_ERR_CUDA;
