@@ -104,7 +104,9 @@ struct Scan {
   long long warp_sum[8];
   long long item;            // flat step at which the first tile begins
   int head, seq, i, begin;   // key/value head, sequence, tile of it, step of the tile
+  int n_tiles;
   Seq q;
+  Tile t;
 };
 
 // Every thread of the CTA (256 of them or more; the first 256 work, a share of
@@ -146,8 +148,14 @@ __device__ inline Shares scan_batch(const Batch& b, int min_steps, Scan* sc, uns
         if (chunk > 1) q = load_seq(b, s, nullptr);
         const int n = tiles_of(b, q.n);
         for (int i = 0; i < n; ++i) {
-          const int steps = make_tile(b, q, i).steps;
+          const Tile t = make_tile(b, q, i);
+          const int steps = t.steps;
           if (r >= 0 && r < steps) {
+            // the page table's row is about to be read
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(b.pages + int64_t(s) * b.page_stride +
+                                                          min(((t.step0 + int(r)) << b.step_shift) >> b.page_shift, b.max_pages - 1)));
+            sc->t = t;
+            sc->n_tiles = n;
             sc->item = f - r;
             sc->head = int(head);
             sc->seq = s;
@@ -184,8 +192,8 @@ struct Walk {
     i = sc->i;
     begin = sc->begin;
     q = sc->q;
-    n_tiles = tiles_of(b, q.n);
-    t = make_tile(b, q, i);
+    n_tiles = sc->n_tiles;
+    t = sc->t;
     take();
   }
   // To the next tile; false when this CTA's steps are done.
@@ -268,7 +276,7 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
 __device__ __forceinline__ void write_split(const Params& p, const Scan* sc, const Shares& sh) {
   Split s = {};
   if (int(blockIdx.x) < sh.n && sc->begin > 0) {  // the tile began in an earlier CTA
-    const Tile t = make_tile(p.b, sc->q, sc->i);
+    const Tile t = sc->t;
     const int c0 = sh.of(sc->item), c1 = sh.of(sc->item + t.steps - 1);
     if (c0 + 1 == int(blockIdx.x)) s = Split{1, sc->head, t.first, t.n, c0, c1, {0, 0}};
   }

@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(384, 1)
   volatile int* dead_s = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);  // [2]
 
   const int warp = threadIdx.x >> 5;
-  constexpr int W_K = 8, W_MMA = 9, W_V = 10;
+  constexpr int W_K = 8, W_MMA = 9, W_V = 10, W_Q = 11;
 
   if (threadIdx.x == 0) {
     tc::mbar_init(q_full, 1);
@@ -190,6 +190,11 @@ __global__ void __launch_bounds__(384, 1)
     *abort_flag = 0;
     tc::fence_mbar_init();
   }
+  if (threadIdx.x == 32) {
+    tc::tma_prefetch_desc(&tm_k);
+    tc::tma_prefetch_desc(&tm_v);
+    tc::tma_prefetch_desc(&tm_q);
+  }
   // query rows that the loads do not reach are zero: their scores then do not move a maximum
   for (int i = threadIdx.x; i < int(NCH * C::QCH / 16); i += blockDim.x)
     reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0, 0, 0, 0);
@@ -206,14 +211,12 @@ __global__ void __launch_bounds__(384, 1)
   if (int(blockIdx.x) >= shares.n) {  // nothing to do here
     if (threadIdx.x == 0) write_split(p, sc, shares);
   } else if (warp == W_K || warp == W_V) {
-    // ------------------------------------------------------------ producers: one thread for the keys (and the queries,
-    // and the segments that the other roles read), one for the values.  Each walks the steps.  With 16-token pages a
+    // ------------------------------------------------------------ producers: one thread for the keys (and the
+    // segments that the other roles read), one for the values.  Each walks the steps.  With 16-token pages a
     // step is 16 boxes a side; one thread alone for both took longer to issue them than HBM to deliver.
     const bool keys = warp == W_K;
     if (tc::elect_one()) {
       const CUtensorMap* tm = keys ? &tm_k : &tm_v;
-      tc::tma_prefetch_desc(tm);
-      if (keys) tc::tma_prefetch_desc(&tm_q);
       auto wait1 = [&](uint64_t* b_, uint32_t par) { return tc::mbar_wait(b_, par, abort_flag, &g_status_pfew); };
       uint64_t* full = keys ? k_full : v_full;
       uint64_t* empty = keys ? k_empty : v_empty;
@@ -222,18 +225,9 @@ __global__ void __launch_bounds__(384, 1)
       w.start(p.b, sc, shares);
       const int per_step = KS >> p.b.page_shift;                    // pages of a step
       const uint32_t page_bytes = uint32_t(128) << p.b.page_shift;  // of one 64-column piece
-      const uint32_t q_bytes = uint32_t(NCH) * p.b.tile_tok * p.b.group * 128;
-      int t = 0, s = 0, nq = 0;  // steps loaded, the next stage, segments whose queries were loaded
+      int t = 0, s = 0;  // steps loaded, the next stage
       uint32_t par = 1;
       bool ok = true, more = w.end > w.begin;
-      auto load_queries = [&](int k) {
-        if (!wait1(q_empty, (k & 1) ^ 1)) return false;
-        tc::mbar_arrive_expect_tx(q_full, q_bytes);
-        for (int c = 0; c < NCH; ++c)
-          tc::tma_load_3d(sQ + c * C::QCH, &tm_q, q_full, c * 64, w.head * p.b.group, w.t.first);
-        ++nq;
-        return true;
-      };
       for (int k = 0; ok; ++k) {
         const int n_it = more ? w.end - w.begin : -1;
         const int key0 = (w.t.step0 + w.begin) * KS;
@@ -253,39 +247,40 @@ __global__ void __launch_bounds__(384, 1)
           tc::mbar_arrive(seg_full + (k & 1));
         }
         if (!more) break;
-        if (keys && k == 0) load_queries(0);  // later ones behind the segment's first keys
         const int32_t* row = p.b.pages + int64_t(w.seq) * p.b.page_stride;
         const int lo = w.t.lo, hi = w.t.hi, head = w.head;
-        // the pages of step j: -1 where none is needed.  Looked up a step ahead of their use.
+        // which pages of step j are needed, and their entries: read a step ahead of their use, and not looked at before
         auto look = [&](int j, int (&pg)[8]) {
+          uint32_t needed = 0;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int ki = key0 + j * KS + (i << p.b.page_shift);
             const bool need = j < n_it && i < per_step && ki < hi && ki + p.b.page_size > lo;
-            pg[i] = need ? __ldg(row + (ki >> p.b.page_shift)) : -1;
-            if (need && uint32_t(pg[i]) >= uint32_t(p.b.n_pages)) pg[i] = p.b.n_pages;  // out of range, see below
+            pg[i] = need ? __ldg(row + (ki >> p.b.page_shift)) : 0;
+            needed |= uint32_t(need) << i;
           }
+          return needed;
         };
         int next[8];
-        look(0, next);
+        uint32_t next_needed = look(0, next);
         for (int j = 0; j < n_it; ++j) {
-          int at[8], n_pg = 0;  // first cache row of each page; -1: not needed
+          int at[8];  // first cache row of each page
+          const uint32_t needed = next_needed;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             int pg = next[i];
-            if (pg == p.b.n_pages) {  // never followed: page 0 is read in its place
+            if (uint32_t(pg) >= uint32_t(p.b.n_pages)) {  // never followed: page 0 is read in its place
               atomicOr(&g_status_pfew, TPA_DEV_BAD_INPUT);
               pg = 0;
             }
-            at[i] = pg >= 0 ? (pg * p.b.hkv + head) << p.b.page_shift : -1;
-            n_pg += pg >= 0;
+            at[i] = (pg * p.b.hkv + head) << p.b.page_shift;
           }
-          look(j + 1, next);
+          next_needed = look(j + 1, next);
           if (!(ok = wait1(empty + s, par))) break;
-          tc::mbar_arrive_expect_tx(full + s, n_pg * NCH * page_bytes);
+          tc::mbar_arrive_expect_tx(full + s, __popc(needed) * NCH * page_bytes);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            if (at[i] >= 0)
+            if (needed >> i & 1)
 #pragma unroll
               for (int c = 0; c < NCH; ++c)
                 tma_load_2d(tiles + s * TILE + c * kChunk + i * page_bytes, tm, full + s, c * 64, at[i]);
@@ -294,7 +289,6 @@ __global__ void __launch_bounds__(384, 1)
             s = 0;
             par ^= 1;
           }
-          if (keys && j == 0 && k > 0 && !(ok = load_queries(k))) break;
         }
         if (ok) more = w.next(p.b);
       }
@@ -302,7 +296,6 @@ __global__ void __launch_bounds__(384, 1)
         volatile int never = 0;
         for (int j = (t > NS ? t - NS : 0); j < t; ++j)
           tc::mbar_wait(full + (j % NS), (j / NS) & 1, &never, &g_status_pfew, 100000000ull);
-        if (nq > 0) tc::mbar_wait(q_full, (nq - 1) & 1, &never, &g_status_pfew, 100000000ull);
       }
     }
     __syncwarp();
@@ -371,8 +364,28 @@ __global__ void __launch_bounds__(384, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 11) {
-    if (threadIdx.x == 352) write_split(p, sc, shares);
+  } else if (warp == W_Q) {
+    // ------------------------------------------------------------ one thread for the queries of each segment (the
+    // thread for the keys would stop at them until the segment before is done)
+    if (tc::elect_one()) {
+      const uint32_t q_bytes = uint32_t(NCH) * p.b.tile_tok * p.b.group * 128;
+      Walk w;
+      w.start(p.b, sc, shares);
+      int nq = 0;
+      bool more = w.end > w.begin;
+      while (more && tc::mbar_wait(q_empty, (nq & 1) ^ 1, abort_flag, &g_status_pfew)) {
+        tc::mbar_arrive_expect_tx(q_full, q_bytes);
+        for (int c = 0; c < NCH; ++c)
+          tc::tma_load_3d(sQ + c * C::QCH, &tm_q, q_full, c * 64, w.head * p.b.group, w.t.first);
+        if (nq++ == 0) write_split(p, sc, shares);
+        more = w.next(p.b);
+      }
+      if (*abort_flag && nq > 0) {
+        volatile int never = 0;
+        tc::mbar_wait(q_full, (nq - 1) & 1, &never, &g_status_pfew, 100000000ull);
+      }
+    }
+    __syncwarp();
   } else if (warp < 8) {
     // ------------------------------------------------------------ softmax of every other step
     const int h = warp >> 2, lane = threadIdx.x & 31;
