@@ -24,9 +24,63 @@ namespace {
 
 using namespace paged;
 
-// Joins the parts of a tile whose steps went to several CTAs: a CTA takes one
-// row, its eight warps a share of the parts each.  The parts' values, maxima
-// and sums are all loaded together; parts are added in a fixed order.
+// Joins the parts of a tile whose steps went to several CTAs.  The parts'
+// values, maxima and sums are loaded together; parts are added in a fixed order.
+// With 16 parts or fewer (the usual case: a tile on two or three CTAs) a warp
+// takes a row; with more (a long sequence by itself) the CTA's eight warps take
+// a share of one row's parts each.
+constexpr int kFewParts = 16;
+
+template <int D>
+__device__ __forceinline__ void join_row_by_warp(const Params& p, const Split& s, int r, int lane) {
+  constexpr int V = D / 32;  // columns of a lane
+  using Vec = typename std::conditional<V == 4, float4, float2>::type;
+  const int parts = s.c1 - s.c0 + 1;
+  auto slot = [&](int i) { return int64_t(2) * (s.c0 + i) + (i == 0 ? 1 : 0); };
+  float2 ml = make_float2(-INFINITY, 0.f);  // lane i: part i
+  if (lane < parts) ml = p.part_ml[slot(lane) * p.rows + r];
+  float acc[V], top = -INFINITY, mu = 0.f, a = 0.f, sum = 0.f;
+#pragma unroll
+  for (int c = 0; c < V; ++c) acc[c] = 0.f;
+#pragma unroll
+  for (int k0 = 0; k0 < kFewParts; k0 += 8) {
+    if (k0 >= parts) break;
+    Vec v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      v[k] = Vec{};
+      if (k0 + k < parts) v[k] = reinterpret_cast<const Vec*>(p.part_o + (slot(k0 + k) * p.rows + r) * D)[lane];
+    }
+    if (k0 == 0) {
+      top = warp_max_f(ml.x);
+      mu = top == -INFINITY ? 0.f : top;
+      a = tc::ex2(ml.x - mu);
+      sum = ml.y * a;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float w = __shfl_sync(0xffffffffu, a, k0 + k);
+      const float* f = reinterpret_cast<const float*>(&v[k]);
+      if (k0 + k < parts) {
+#pragma unroll
+        for (int c = 0; c < V; ++c) acc[c] = fmaf(f[c], w, acc[c]);
+      }
+    }
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const int tok = r / p.b.group, head = s.head * p.b.group + r - tok * p.b.group;
+  const int64_t row = int64_t(s.first + tok) * p.hq + head;
+  uint32_t w[V / 2];
+#pragma unroll
+  for (int c = 0; c < V / 2; ++c) w[c] = tc::pack_bf16(acc[2 * c] * inv, acc[2 * c + 1] * inv);
+  uint32_t* out = reinterpret_cast<uint32_t*>(p.o + row * D) + lane * (V / 2);
+  if constexpr (V == 4) *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+  else out[0] = w[0];
+  if (lane == 0) p.lse[row] = sum > 0.f ? (mu + __log2f(sum)) * kLn2 : -INFINITY;
+}
+
 template <int D>
 __global__ void __launch_bounds__(256, 4) paged_join_kernel(const Params p) {
   constexpr int V = D / 32;  // columns of a lane
@@ -42,6 +96,10 @@ __global__ void __launch_bounds__(256, 4) paged_join_kernel(const Params p) {
   const Split s = p.split[blockIdx.x];
   if (!s.valid) return;
   const int parts = s.c1 - s.c0 + 1;
+  if (parts <= kFewParts) {
+    for (int r = blockIdx.y * 8 + warp; r < s.n * p.b.group; r += gridDim.y * 8) join_row_by_warp<D>(p, s, r, lane);
+    return;
+  }
   auto slot = [&](int i) { return int64_t(2) * (s.c0 + i) + (i == 0 ? 1 : 0); };
   for (int r = blockIdx.y; r < s.n * p.b.group; r += gridDim.y) {
     float2 ml = make_float2(-INFINITY, 0.f);  // thread i: part i
@@ -123,10 +181,10 @@ int num_sms() {
   return sms;
 }
 
-// Rows of a tile: 16, 32 or 64 while every sequence's queries fit in them, else 256.
+// Rows of a tile: 16 or 32 while every sequence's queries fit in them, else 256.
 int tile_rows(int64_t max_q, int group) {
   const int64_t rows = max_q * group;
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 256;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : 256;
 }
 
 uint64_t part_bytes(int rows, int d) {
@@ -135,7 +193,7 @@ uint64_t part_bytes(int rows, int d) {
 
 template <int D>
 int launch_join(const Params& p, int grid, int64_t rows, cudaStream_t st) {
-  return launch_overlapped(paged_join_kernel<D>, dim3(grid, unsigned(rows < 32 ? rows : 32)), 256, 0, st,
+  return launch_overlapped(paged_join_kernel<D>, dim3(grid, unsigned(rows < 8 ? rows : 8)), 256, 0, st,
                            static_cast<const Params>(p));
 }
 
@@ -194,8 +252,8 @@ extern "C" int tpa_paged_attn_fwd(const tpa_paged_view* cache, const void* q, in
   p.split = reinterpret_cast<Split*>(ws + uint64_t(2) * kMaxGrid * R * (uint64_t(d) * 4 + 8));
   const int sms = num_sms(), grid = sms < kMaxGrid ? sms : kMaxGrid;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  int rt = R == 256 ? tpa_internal_paged_tile(cache, p, grid, st) : kPagedTileUnfit;
-  if (rt == kPagedTileUnfit) rt = tpa_internal_paged_few(cache, p, R < 64 ? R : 64, grid, st);
+  const int rt = R == 256 ? tpa_internal_paged_tile(cache, p, grid, st) : tpa_internal_paged_few(cache, p, R, grid, st);
+  if (rt == kPagedUnfit) return TPA_ERR_CUDA;
   if (rt != TPA_OK) return rt;
   return d == 128 ? launch_join<128>(p, grid, rows, st) : launch_join<64>(p, grid, rows, st);
 }

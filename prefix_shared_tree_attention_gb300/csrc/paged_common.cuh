@@ -77,25 +77,36 @@ __device__ __forceinline__ Tile make_tile(const Batch& b, const Seq& q, int i) {
   return t;
 }
 
-// 64-bit quotient; nearly always both sides fit in 32 bits, where it is several times faster.
-__device__ __forceinline__ long long quot(long long a, long long b) {
-  return ((a | b) >> 32) == 0 ? (long long)(uint32_t(a) / uint32_t(b)) : a / b;
+// Quotient below 2^20.  Integer division is a long chain of dependent
+// instructions, and every CTA's first load waits for three of them.
+__device__ __forceinline__ int small_quot(long long a, long long b) {
+  if (((a | b) >> 31) != 0) return int(a / b);
+  int q = int(__fdividef(float(int(a)), float(int(b))));  // off by one at most
+  const int r = int(a) - q * int(b);
+  if (r < 0) --q;
+  else if (r >= int(b)) ++q;
+  return q;
 }
 
 // How the CTAs share `total` steps: n of them, the first `rem` with size + 1 and the others with `size`.
 struct Shares {
   int n;
   long long size, rem;
-  __device__ __forceinline__ Shares(long long total, int grid, int min_steps) {
-    const long long want = quot(total + min_steps - 1, min_steps);
-    n = int(want < grid ? want : grid);
-    size = n > 0 ? quot(total, n) : 0;
+  __device__ __forceinline__ Shares(long long total, int grid) {
+    n = int(total < grid ? total : grid);
+    if (total < grid) {
+      size = 1;
+    } else if ((total >> 20) == 0) {
+      size = small_quot(total, grid);
+    } else {
+      size = total / grid;
+    }
     rem = total - size * n;
   }
   __device__ __forceinline__ long long begin(int c) const { return size * c + (c < rem ? c : rem); }
   __device__ __forceinline__ int of(long long f) const {
     const long long edge = rem * (size + 1);
-    return int(f < edge ? quot(f, size + 1) : rem + quot(f - edge, size));
+    return f < edge ? small_quot(f, size + 1) : int(rem) + small_quot(f - edge, size);
   }
 };
 
@@ -113,7 +124,7 @@ struct Scan {
 // the sequences each): adds up the steps and finds this CTA's first one; the
 // thread that has it among its sequences writes it down.  Reports bad
 // sequences once (CTA 0).
-__device__ inline Shares scan_batch(const Batch& b, int min_steps, Scan* sc, unsigned int* status) {
+__device__ inline Shares scan_batch(const Batch& b, Scan* sc, unsigned int* status) {
   const int tid = threadIdx.x, chunk = (b.n_seqs + 255) >> 8;
   const int s0 = tid * chunk, s1 = min(s0 + chunk, b.n_seqs);
   long long mine = 0, incl = 0;
@@ -139,9 +150,9 @@ __device__ inline Shares scan_batch(const Batch& b, int min_steps, Scan* sc, uns
     if (w < (tid >> 5)) before += sc->warp_sum[w];
     per_head += sc->warp_sum[w];
   }
-  const Shares shares(per_head * b.hkv, gridDim.x, min_steps);
+  const Shares shares(per_head * b.hkv, gridDim.x);
   if (int(blockIdx.x) < shares.n) {
-    const long long f = shares.begin(blockIdx.x), head = quot(f, per_head);
+    const long long f = shares.begin(blockIdx.x), head = small_quot(f, per_head);
     long long r = f - head * per_head - (before + incl - mine);  // step among this thread's sequences
     if (tid < 256 && r >= 0 && r < mine) {
       for (int s = s0; s < s1; ++s) {
@@ -235,7 +246,7 @@ struct Params {
   float2* part_ml;  // [2 grid][R]: maximum (log2 units) and sum
   Split* split;     // [grid]
   int64_t q_stride;
-  int32_t hq, min_steps, rows;  // rows: R, of a part
+  int32_t hq, rows;  // rows: R, of a part
   float scale_log2;
 };
 
@@ -330,8 +341,8 @@ inline bool query_map(CUtensorMap* m, const tpa_paged_view* c, const Params& p, 
 }  // namespace paged
 
 // Launch the attention kernel (the caller joins split tiles afterwards): for
-// tiles of `rows` = 16, 32 or 64 rows (paged_few.cu), and of 256 (paged_tile.cu).
-// The latter may find that it was not compiled as it assumes; it then launches nothing.
-constexpr int kPagedTileUnfit = 1;
+// tiles of `rows` = 16 or 32 rows (paged_few.cu), and of 256 (paged_tile.cu).
+// Either may find that it was not compiled as it assumes; it then launches nothing.
+constexpr int kPagedUnfit = 1;
 int tpa_internal_paged_few(const tpa_paged_view* cache, paged::Params& p, int rows, int grid, cudaStream_t stream);
 int tpa_internal_paged_tile(const tpa_paged_view* cache, paged::Params& p, int grid, cudaStream_t stream);

@@ -1,5 +1,5 @@
-// Paged attention for few rows (a decode step, drafted tokens): at most NR = 16,
-// 32 or 64 rows (tokens x heads of a key/value head's group) a tile.
+// Paged attention for few rows (a decode step, drafted tokens): at most NR = 16
+// or 32 rows (tokens x heads of a key/value head's group) a tile.
 //
 // Bound by the reads of the cache; the kernel is built around them.  Two threads
 // keep the keys and values of NS steps of 128 keys (192 KB of them) on their
@@ -13,8 +13,9 @@
 // by 2^8 (one vote a step finds out), which is exact, since numerator and
 // denominator keep the same one.  Sums stay per thread until the tile's end.
 // Two warpgroups take the steps in turn, each with its own maximum, sums, S^T and
-// O^T (in TMEM), so that one's softmax runs beside the other's products; the two
-// are joined at the tile's end.
+// O^T (in TMEM), so that one's softmax runs beside the other's products.  At a
+// tile's end they go on with the next; a third joins the two and writes the
+// tile out, from the one of two sets of O^T that the next tile does not use.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -41,7 +42,7 @@ struct FewCfg {
   static constexpr uint32_t TILE = NCH * kChunk;       // keys or values of a step
   static constexpr uint32_t QCH = NR * 128;            // a 64-column piece of the queries
   static constexpr uint32_t PT = NR * KS * 2;          // P^T of a warpgroup: NR rows of two 64-key pieces
-  static constexpr uint32_t FIXED = NCH * QCH + 2 * PT + 160 + 128 + NR * 48 + 1024;
+  static constexpr uint32_t FIXED = NCH * QCH + 2 * PT + 160 + 192 + NR * 136 + 1024;
   static constexpr int NS_FIT = int((kSmemMax - 1024 - FIXED) / (2 * TILE));
   static constexpr int NS = NS_FIT > 6 ? 6 : NS_FIT;
   // The values come first: for d 64 the transposed product reads 128 "dimensions" from each step, the second
@@ -52,15 +53,18 @@ struct FewCfg {
   static constexpr uint32_t OFF_P = OFF_Q + NCH * QCH;
   static constexpr uint32_t OFF_SCAN = OFF_P + 2 * PT;
   static constexpr uint32_t OFF_SEG = OFF_SCAN + 160;
-  static constexpr uint32_t OFF_F = OFF_SEG + 128;     // floats, see below: 12 NR
-  // q_full, q_empty, k_full[NS], k_empty[NS], v_full[NS], v_empty[NS], s_full[2], p_full[2], ml_full[2], o_final,
-  // o_free, drain, seg_full[2], seg_empty[2]
-  static constexpr int NBAR = 2 + 4 * NS + 6 + 3 + 4;
-  static constexpr uint32_t OFF_BAR = OFF_F + (2 * (1 + 4 + 1) + 4 + 4) * NR * 4;
+  static constexpr uint32_t OFF_F = OFF_SEG + 192;     // floats, see below: 34 NR
+  // q_full, q_empty, k_full[NS], k_empty[NS], v_full[NS], v_empty[NS], s_full[2], p_full[2], ml_full[2], ml_free[2],
+  // o_final[2], o_free[2], drain, seg_full[4], seg_empty[4]
+  static constexpr int NBAR = 2 + 4 * NS + 12 + 1 + 8;
+  static constexpr uint32_t OFF_BAR = OFF_F + 34 * NR * 4;
   static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr uint32_t BYTES = OFF_MISC + 32 + 1024;
-  static constexpr uint32_t TMEM_COLS = 4 * NR;
-  static_assert(sizeof(Scan) <= 160 && sizeof(Segment) * 2 <= 128 && NS >= 2 && OFF_BAR % 8 == 0, "layout");
+  static constexpr uint32_t TMEM_COLS = 8 * NR;  // 2 NR of S^T and 4 NR of O^T, rounded up to a power of two
+  // Registers move from the loading, issuing and writing warps to the softmax warpgroups.
+  static constexpr int THREADS = 512, REG_LAUNCH = 128, REG_LOW = 88, REG_HIGH = 168;
+  static_assert(REG_HIGH * 256 + REG_LOW * 256 <= REG_LAUNCH * 512, "register split");
+  static_assert(sizeof(Scan) <= 160 && sizeof(Segment) * 4 <= 192 && NS >= 2 && OFF_BAR % 8 == 0, "layout");
   static_assert(BYTES <= kSmemMax, "shared memory budget");
 };
 
@@ -132,7 +136,7 @@ __device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[N]) {
 }
 
 template <int D, int NR>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(512, 1)
     paged_few_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const Params p) {
   using C = FewCfg<D, NR>;
@@ -146,6 +150,10 @@ __global__ void __launch_bounds__(384, 1)
   Scan* sc = reinterpret_cast<Scan*>(smem + C::OFF_SCAN);
   volatile Segment* seg_ring = reinterpret_cast<volatile Segment*>(smem + C::OFF_SEG);
   float* f_s = reinterpret_cast<float*>(smem + C::OFF_F);
+  // handed to the writing warpgroup, by parity of the segment: maxima [2][2][NR], sums [2][2][4 warps][NR]
+  float* xm_s = f_s + 12 * NR;
+  float* xl_s = f_s + 16 * NR;
+  float* coef_s = f_s + 32 * NR;  // [2][NR] what the two O^T are multiplied by
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* q_empty = q_full + 1;
   uint64_t* k_full = q_full + 2;
@@ -155,14 +163,15 @@ __global__ void __launch_bounds__(384, 1)
   uint64_t* s_full = v_empty + NS;  // [2]
   uint64_t* p_full = s_full + 2;    // [2]
   uint64_t* ml_full = p_full + 2;   // [2]
-  uint64_t* o_final = ml_full + 2;
-  uint64_t* o_free = o_final + 1;
-  uint64_t* drain = o_free + 1;
-  uint64_t* seg_full = drain + 1;   // [2]
-  uint64_t* seg_empty = drain + 3;  // [2]
+  uint64_t* ml_free = ml_full + 2;  // [2]
+  uint64_t* o_final = ml_free + 2;  // [2]
+  uint64_t* o_free = o_final + 2;   // [2]
+  uint64_t* drain = o_free + 2;
+  uint64_t* seg_full = drain + 1;   // [4]
+  uint64_t* seg_empty = drain + 5;  // [4]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
-  volatile int* dead_s = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);  // [2]
+  volatile int* dead_s = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);  // [3]
 
   const int warp = threadIdx.x >> 5;
   constexpr int W_K = 8, W_MMA = 9, W_V = 10, W_Q = 11;
@@ -179,13 +188,16 @@ __global__ void __launch_bounds__(384, 1)
     for (int h = 0; h < 2; ++h) {
       tc::mbar_init(s_full + h, 1);
       tc::mbar_init(p_full + h, 128);
-      tc::mbar_init(ml_full + h, 128);
-      tc::mbar_init(seg_full + h, 1);
-      tc::mbar_init(seg_empty + h, 1 + 256);
-      dead_s[h] = 0;
+      tc::mbar_init(ml_full + h, 256);
+      tc::mbar_init(ml_free + h, 128);
+      tc::mbar_init(o_final + h, 1);
+      tc::mbar_init(o_free + h, 128);
     }
-    tc::mbar_init(o_final, 1);
-    tc::mbar_init(o_free, 256);
+    for (int s = 0; s < 4; ++s) {
+      tc::mbar_init(seg_full + s, 1);
+      tc::mbar_init(seg_empty + s, 1 + 256 + 128);
+    }
+    for (int h = 0; h < 3; ++h) dead_s[h] = 0;
     tc::mbar_init(drain, 1);
     *abort_flag = 0;
     tc::fence_mbar_init();
@@ -204,13 +216,16 @@ __global__ void __launch_bounds__(384, 1)
   // From here on memory is read and written that the kernel before may write and read.
   tc::grid_wait_prior();
   tc::grid_launch_dependents();  // the joining kernel waits for this one's end by itself
-  const Shares shares = scan_batch(p.b, p.min_steps, sc, &g_status_pfew);
+  const Shares shares = scan_batch(p.b, sc, &g_status_pfew);
   tc::tc_fence_after();
-  const uint32_t tmem = *tmem_slot;  // columns: S^T of the two warpgroups, then their O^T
+  const uint32_t tmem = *tmem_slot;  // columns: S^T of the two warpgroups, then two sets of their O^T
+  auto o_col = [](int k, int h) { return uint32_t(2 * NR + ((k & 1) * 2 + h) * NR); };  // of segment k
 
   if (int(blockIdx.x) >= shares.n) {  // nothing to do here
     if (threadIdx.x == 0) write_split(p, sc, shares);
-  } else if (warp == W_K || warp == W_V) {
+  } else if (warp >= 8 && warp < 12) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REG_LOW));
+  if (warp == W_K || warp == W_V) {
     // ------------------------------------------------------------ producers: one thread for the keys (and the
     // segments that the other roles read), one for the values.  Each walks the steps.  With 16-token pages a
     // step is 16 boxes a side; one thread alone for both took longer to issue them than HBM to deliver.
@@ -232,8 +247,8 @@ __global__ void __launch_bounds__(384, 1)
         const int n_it = more ? w.end - w.begin : -1;
         const int key0 = (w.t.step0 + w.begin) * KS;
         if (keys) {
-          if (!(ok = wait1(seg_empty + (k & 1), ((k >> 1) & 1) ^ 1))) break;
-          volatile Segment* sg = seg_ring + (k & 1);
+          if (!(ok = wait1(seg_empty + (k & 3), ((k >> 2) & 1) ^ 1))) break;
+          volatile Segment* sg = seg_ring + (k & 3);
           sg->n_it = n_it;
           sg->head = w.head;
           sg->first = w.t.first;
@@ -244,7 +259,7 @@ __global__ void __launch_bounds__(384, 1)
           sg->key0 = key0;
           sg->whole = w.begin == 0 && w.end == w.t.steps;
           sg->slot = blockIdx.x * 2 + (w.begin == 0 ? 1 : 0);
-          tc::mbar_arrive(seg_full + (k & 1));
+          tc::mbar_arrive(seg_full + (k & 3));
         }
         if (!more) break;
         const int32_t* row = p.b.pages + int64_t(w.seq) * p.b.page_stride;
@@ -315,11 +330,11 @@ __global__ void __launch_bounds__(384, 1)
                    dQ + (((k >> 2) * C::QCH + (k & 3) * 32) >> 4), idesc_s, k > 0);
       tc::mma_commit(s_full + h);
     };
-    auto issue_o = [&](int h, int s, bool first) {  // O^T_h (+)= V(s)^T P^T_h
+    auto issue_o = [&](int k_, int h, int s, bool first) {  // O^T_h (+)= V(s)^T P^T_h
       const uint64_t vb = dV + ((s * TILE) >> 4), pb = dP + ((h * C::PT) >> 4);
 #pragma unroll
       for (int k = 0; k < KS / 16; ++k)
-        tc::mma_ss(tmem + 2 * NR + h * NR, vb + ((k * 2048) >> 4),
+        tc::mma_ss(tmem + o_col(k_, h), vb + ((k * 2048) >> 4),
                    pb + (((k >> 2) * C::QCH + (k & 3) * 32) >> 4), idesc_o, (!first || k > 0) ? 1u : 0u);
     };
     auto wait1 = [&](uint64_t* b_, uint32_t par) { return tc::mbar_wait(b_, par, abort_flag, &g_status_pfew); };
@@ -328,9 +343,9 @@ __global__ void __launch_bounds__(384, 1)
       int uses[2] = {0, 0};  // steps of each warpgroup so far
       bool ok = true;
       for (int k = 0; ok; ++k) {
-        if (!(ok = wait1(seg_full + (k & 1), (k >> 1) & 1))) break;
-        const int n_it = seg_ring[k & 1].n_it;
-        tc::mbar_arrive(seg_empty + (k & 1));
+        if (!(ok = wait1(seg_full + (k & 3), (k >> 2) & 1))) break;
+        const int n_it = seg_ring[k & 3].n_it;
+        tc::mbar_arrive(seg_empty + (k & 3));
         if (n_it < 0) break;
         if (!(ok = wait1(q_full, k & 1))) break;
         auto start = [&](int j) {  // S^T of step j, when its keys are there
@@ -347,14 +362,14 @@ __global__ void __launch_bounds__(384, 1)
         for (int j = 0; ok && j < n_it; ++j) {
           const int h = j & 1, s = (t + j) % NS;
           if (!(ok = wait1(v_full + s, ((t + j) / NS) & 1) && wait1(p_full + h, uses[h] & 1))) break;
-          if (j == 0 && k > 0 && !(ok = wait1(o_free, (k - 1) & 1))) break;
+          if (j == 0 && !(ok = wait1(o_free + (k & 1), ((k >> 1) & 1) ^ 1))) break;
           ++uses[h];
           tc::tc_fence_after();
-          issue_o(h, s, j < 2);
+          issue_o(k, h, s, j < 2);
           tc::mma_commit(v_empty + s);
           if (j + 2 < n_it && !(ok = start(j + 2))) break;
         }
-        if (ok) tc::mma_commit(o_final);
+        if (ok) tc::mma_commit(o_final + (k & 1));
         t += n_it;
       }
       if (*abort_flag) {  // let issued MMAs finish before TMEM is released
@@ -386,20 +401,19 @@ __global__ void __launch_bounds__(384, 1)
       }
     }
     __syncwarp();
+  }
   } else if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REG_HIGH));
     // ------------------------------------------------------------ softmax of every other step
     const int h = warp >> 2, lane = threadIdx.x & 31;
     const int r = threadIdx.x & 127;  // key of the step, then head dimension = TMEM lane
     const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lane_base + h * NR, tO = tmem + lane_base + 2 * NR;
+    const uint32_t tS = tmem + lane_base + h * NR;
     uint8_t* sP = smem + C::OFF_P + h * C::PT + (r >> 6) * C::QCH + (r & 7) * 2;
     const uint32_t p_chunk = (r >> 3) & 7;  // of the 128-byte piece of a row
-    float* m_s = f_s + h * NR;                       // running maxima
-    float* warp_s = f_s + 2 * NR + h * 4 * NR;       // the four warps' maxima, then sums
-    float* alpha_s = f_s + 10 * NR + h * NR;         // rescaling
-    float* xm_s = f_s + 12 * NR;                     // [2] maxima at the tile's end, both warpgroups'
-    float* xl_s = f_s + 14 * NR;                     // [2] sums
-    float* coef_s = f_s + 16 * NR + h * 2 * NR;      // [2] what the two O^T are multiplied by
+    float* m_s = f_s + h * NR;                  // running maxima
+    float* warp_s = f_s + 2 * NR + h * 4 * NR;  // the four warps' maxima
+    float* alpha_s = f_s + 10 * NR + h * NR;    // rescaling
     auto wait_thread = [&](uint64_t* b_, uint32_t par) { return tc::mbar_wait(b_, par, abort_flag, &g_status_pfew); };
     // The warps of a warpgroup meet in barriers, so they leave together or not at all: a failed wait is passed on
     // through dead_s at the next vote.
@@ -412,14 +426,13 @@ __global__ void __launch_bounds__(384, 1)
     };
     int t = 0, uses = 0;
     for (int k = 0;; ++k) {
-      note(wait_thread(seg_full + (k & 1), (k >> 1) & 1));
+      note(wait_thread(seg_full + (k & 3), (k >> 2) & 1));
       if (group_any(h, !fine)) break;
-      const volatile Segment* sg = seg_ring + (k & 1);
-      const int n_it = sg->n_it, first = sg->first, n_tok = sg->n, lo = sg->lo, hi = sg->hi, key_first = sg->key0;
-      const int slot = sg->whole ? -1 : sg->slot, head0 = sg->head * p.b.group, pos_first = sg->pos0;
-      tc::mbar_arrive(seg_empty + (k & 1));
+      const volatile Segment* sg = seg_ring + (k & 3);
+      const int n_it = sg->n_it, n_tok = sg->n, lo = sg->lo, hi = sg->hi, key_first = sg->key0, pos_first = sg->pos0;
+      tc::mbar_arrive(seg_empty + (k & 3));
       if (n_it < 0) break;
-      const int live = n_tok * p.b.group;  // rows in use
+      const uint32_t tO = tmem + lane_base + o_col(k, h);
       // every row in use sees the keys in [all_lo, all_hi)
       const int all_hi = pos_first + 1;
       const int all_lo = p.b.window > 0 ? pos_first + n_tok - p.b.window : 0;
@@ -496,13 +509,13 @@ __global__ void __launch_bounds__(384, 1)
             for (int i = 0; i < NR; ++i) l[i] *= alpha_s[i];
             // O^T of this warpgroup is complete up to its step before: that product was issued before this S^T
             uint32_t ov[NR];
-            tmem_ld(tO + h * NR, ov);
+            tmem_ld(tO, ov);
             tc::tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < NR; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha_s[i]);
 #pragma unroll
             for (int c = 0; c < NR / 16; ++c)
-              tc::tmem_st16(tO + h * NR + c * 16, *reinterpret_cast<const uint32_t(*)[16]>(ov + c * 16));
+              tc::tmem_st16(tO + c * 16, *reinterpret_cast<const uint32_t(*)[16]>(ov + c * 16));
             tc::tmem_st_wait();
           }
         }
@@ -525,28 +538,50 @@ __global__ void __launch_bounds__(384, 1)
       }
       if (dead) break;
 
-      // -------- the tile's end: sums over the warpgroup, maxima and sums of both, then half of the rows each
-      constexpr int OWN = NR > 32 ? NR / 32 : 1;
+      // -------- the tile's end: the maxima and this warp's sums go to the writing warpgroup
       warp_reduce_rows<NR>(l, lane, [](float a, float b) { return a + b; });
-      const int own = owned_row<NR>(lane);
-      group_sync(h);  // warp_s of the last rescaling has been read
+      note(wait_thread(ml_free + (k & 1), ((k >> 1) & 1) ^ 1));
+      if (fine) {
+        float* xm = xm_s + (k & 1) * 2 * NR + h * NR;
+        float* xl = xl_s + (k & 1) * 8 * NR + (h * 4 + (warp & 3)) * NR;
+        constexpr int OWN = NR > 32 ? NR / 32 : 1;
+        const int own = owned_row<NR>(lane);
 #pragma unroll
-      for (int i = 0; i < OWN; ++i) warp_s[(warp & 3) * NR + own + i] = l[i];
-      group_sync(h);
-      const bool had = h < n_it;  // this warpgroup had a step
-      // Behind this o_final every thread has passed its o_free of the segment before, so nobody reads the exchange any more.
-      note(wait_thread(o_final, k & 1));
-      if (r < NR) {
-        xm_s[h * NR + r] = had ? m_s[r] : kNoMax;
-        xl_s[h * NR + r] = (warp_s[r] + warp_s[NR + r]) + (warp_s[2 * NR + r] + warp_s[3 * NR + r]);
+        for (int i = 0; i < OWN; ++i) xl[own + i] = l[i];
+        if (r < NR) xm[r] = h < n_it ? m_s[r] : kNoMax;  // (a warpgroup without a step has no maxima)
       }
-      tc::mbar_arrive(ml_full + h);
-      note(wait_thread(ml_full, k & 1));
-      note(wait_thread(ml_full + 1, k & 1));
-      constexpr int HR = NR / 2;  // rows of each warpgroup
-      if (r < HR && fine) {
-        const int row = h * HR + r;
-        const float m0 = xm_s[row], m1 = xm_s[NR + row], l0 = xl_s[row], l1 = xl_s[NR + row];
+      tc::mbar_arrive(ml_full + (k & 1));
+      t += n_it;
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REG_LOW));
+    // ------------------------------------------------------------ the tile's end: the two O^T joined and written
+    const int r = threadIdx.x & 127;  // head dimension = TMEM lane, and row of the coefficients
+    const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
+    bool fine = true;
+    auto note = [&](bool ok) {
+      if (!ok) {
+        fine = false;
+        dead_s[2] = 1;
+      }
+    };
+    auto wait_thread = [&](uint64_t* b_, uint32_t par) { return tc::mbar_wait(b_, par, abort_flag, &g_status_pfew); };
+    for (int k = 0;; ++k) {
+      note(wait_thread(seg_full + (k & 3), (k >> 2) & 1));
+      if (group_any(2, !fine)) break;
+      const volatile Segment* sg = seg_ring + (k & 3);
+      const int n_it = sg->n_it, first = sg->first, live = sg->n * p.b.group;
+      const int slot = sg->whole ? -1 : sg->slot, head0 = sg->head * p.b.group;
+      tc::mbar_arrive(seg_empty + (k & 3));
+      if (n_it < 0) break;
+      note(wait_thread(ml_full + (k & 1), (k >> 1) & 1));
+      note(wait_thread(o_final + (k & 1), (k >> 1) & 1));
+      if (r < NR && fine) {
+        const float* xm = xm_s + (k & 1) * 2 * NR;
+        const float* xl = xl_s + (k & 1) * 8 * NR;
+        const float m0 = xm[r], m1 = xm[NR + r];
+        const float l0 = (xl[r] + xl[NR + r]) + (xl[2 * NR + r] + xl[3 * NR + r]);
+        const float l1 = (xl[4 * NR + r] + xl[5 * NR + r]) + (xl[6 * NR + r] + xl[7 * NR + r]);
         const float top = fmaxf(m0, m1);
         float a0 = tc::ex2(m0 - top), a1 = tc::ex2(m1 - top);
         const float sum = l0 * a0 + l1 * a1;
@@ -557,45 +592,49 @@ __global__ void __launch_bounds__(384, 1)
         }
         coef_s[r] = a0;
         coef_s[NR + r] = a1;
-        if (row < live) {
+        if (r < live) {
           if (slot < 0) {
-            const int tok = row / p.b.group;
-            p.lse[int64_t(first + tok) * p.hq + head0 + row - tok * p.b.group] =
+            const int tok = r / p.b.group;
+            p.lse[int64_t(first + tok) * p.hq + head0 + r - tok * p.b.group] =
                 sum > 0.f ? (top + __log2f(sum)) * kLn2 : -INFINITY;
           } else {
-            p.part_ml[int64_t(slot) * p.rows + row] = make_float2(top, sum);
+            p.part_ml[int64_t(slot) * p.rows + r] = make_float2(top, sum);
           }
         }
       }
-      if (group_any(h, !fine)) break;
+      if (group_any(2, !fine)) break;  // (the coefficients are there)
       tc::tc_fence_after();
-      uint32_t o0[HR], o1[HR];
-      tmem_ld(tO + h * HR, o0);
-      tmem_ld(tO + NR + h * HR, o1);
-      tc::tmem_ld_wait();
-      tc::tc_fence_before();
-      tc::mbar_arrive(o_free);  // O^T may be overwritten by the next segment
       const bool two = n_it > 1;  // else the second O^T was not written
-      if (r < D) {
-        int tok = (h * HR) / p.b.group, gh = h * HR - tok * p.b.group;
+      int tok = 0, gh = 0;
 #pragma unroll
-        for (int i = 0; i < HR; ++i) {
-          const int row = h * HR + i;
-          if (row < live) {
-            float v = __uint_as_float(o0[i]) * coef_s[i];
-            if (two) v = fmaf(__uint_as_float(o1[i]), coef_s[NR + i], v);
-            if (slot < 0)
-              p.o[(int64_t(first + tok) * p.hq + head0 + gh) * D + r] = __float2bfloat16_rn(v);
-            else
-              p.part_o[(int64_t(slot) * p.rows + row) * D + r] = v;
-            if (++gh == p.b.group) {
-              gh = 0;
-              ++tok;
+      for (int c = 0; c < NR; c += 16) {
+        uint32_t x[16], y[16];
+        tc::tmem_ld16(tmem + lane_base + o_col(k, 0) + c, x);
+        tc::tmem_ld16(tmem + lane_base + o_col(k, 1) + c, y);
+        tc::tmem_ld_wait();
+        if (c + 16 == NR) {  // the segment after next may have the maxima's, sums' and O^T's places
+          tc::tc_fence_before();
+          tc::mbar_arrive(ml_free + (k & 1));
+          tc::mbar_arrive(o_free + (k & 1));
+        }
+        if (r < D) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (c + i < live) {
+              float v = __uint_as_float(x[i]) * coef_s[c + i];
+              if (two) v = fmaf(__uint_as_float(y[i]), coef_s[NR + c + i], v);
+              if (slot < 0)
+                p.o[(int64_t(first + tok) * p.hq + head0 + gh) * D + r] = __float2bfloat16_rn(v);
+              else
+                p.part_o[(int64_t(slot) * p.rows + c + i) * D + r] = v;
+              if (++gh == p.b.group) {
+                gh = 0;
+                ++tok;
+              }
             }
           }
         }
       }
-      t += n_it;
     }
   }
 
@@ -611,13 +650,16 @@ int launch_few(const tpa_paged_view* c, Params& p, int grid, cudaStream_t st) {
   CUtensorMap tq, tk, tv;
   p.b.tile_tok = NR / p.b.group;
   p.b.step_shift = 7;
-  p.min_steps = 1;
   const uint64_t rows = uint64_t(c->n_pages) * c->n_heads_kv * c->page_size;
   if (!query_map(&tq, c, p, p.b.tile_tok) || !cache_map(&tk, c->k_cache, rows, D, c->page_size) ||
       !cache_map(&tv, c->v_cache, rows, D, c->page_size))
     return TPA_ERR_CUDA;
   TPA_CUDA_TRY(cudaFuncSetAttribute(paged_few_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES));
-  return launch_overlapped(paged_few_kernel<D, NR>, dim3(grid), 384, C::BYTES, st, tq, tk, tv, static_cast<const Params>(p));
+  cudaFuncAttributes fa;
+  TPA_CUDA_TRY(cudaFuncGetAttributes(&fa, paged_few_kernel<D, NR>));
+  if (fa.numRegs != C::REG_LAUNCH) return kPagedUnfit;  // the setmaxnreg split would not add up
+  return launch_overlapped(paged_few_kernel<D, NR>, dim3(grid), C::THREADS, C::BYTES, st, tq, tk, tv,
+                           static_cast<const Params>(p));
 }
 
 }  // namespace
@@ -625,9 +667,6 @@ int launch_few(const tpa_paged_view* c, Params& p, int grid, cudaStream_t st) {
 TPA_DEFINE_STATUS_READER(tpa_internal_status_pfew, g_status_pfew)
 
 int tpa_internal_paged_few(const tpa_paged_view* c, Params& p, int rows, int grid, cudaStream_t st) {
-  if (c->head_dim == 128)
-    return rows == 16 ? launch_few<128, 16>(c, p, grid, st)
-                      : rows == 32 ? launch_few<128, 32>(c, p, grid, st) : launch_few<128, 64>(c, p, grid, st);
-  return rows == 16 ? launch_few<64, 16>(c, p, grid, st)
-                    : rows == 32 ? launch_few<64, 32>(c, p, grid, st) : launch_few<64, 64>(c, p, grid, st);
+  if (c->head_dim == 128) return rows == 16 ? launch_few<128, 16>(c, p, grid, st) : launch_few<128, 32>(c, p, grid, st);
+  return rows == 16 ? launch_few<64, 16>(c, p, grid, st) : launch_few<64, 32>(c, p, grid, st);
 }

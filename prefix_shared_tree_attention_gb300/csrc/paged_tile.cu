@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
   // From here on memory is read and written that the kernel before may write and read.
   tc::grid_wait_prior();
   tc::grid_launch_dependents();  // the joining kernel waits for this one's end by itself
-  const Shares shares = scan_batch(p.b, p.min_steps, sc, &g_status_ptile);
+  const Shares shares = scan_batch(p.b, sc, &g_status_ptile);
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
@@ -456,13 +456,12 @@ int launch_tile(const tpa_paged_view* c, Params& p, int grid, cudaStream_t st) {
       !cache_map(&tv, c->v_cache, rows, D, c->page_size))
     return TPA_ERR_CUDA;
   p.b.tile_tok = NH * sub_tok;
-  p.min_steps = 2;
   p.b.step_shift = 7;
   TPA_CUDA_TRY(cudaFuncSetAttribute(paged_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES));
   {
     cudaFuncAttributes fa;
     TPA_CUDA_TRY(cudaFuncGetAttributes(&fa, paged_tile_kernel<D>));
-    if (fa.numRegs != C::REG_LAUNCH) return kPagedTileUnfit;  // the setmaxnreg split would not add up
+    if (fa.numRegs != C::REG_LAUNCH) return kPagedUnfit;  // the setmaxnreg split would not add up
   }
   return launch_overlapped(paged_tile_kernel<D>, dim3(grid), C::THREADS, C::BYTES, st, tq, tk, tv,
                            static_cast<const Params>(p));
