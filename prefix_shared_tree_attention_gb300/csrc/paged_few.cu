@@ -20,6 +20,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "device_common.cuh"
 #include "internal.h"
 #include "paged_common.cuh"
@@ -238,8 +240,6 @@ __global__ void __launch_bounds__(512, 1)
       uint8_t* tiles = keys ? sK : sV;
       Walk w;
       w.start(p.b, sc, shares);
-      const int per_step = KS >> p.b.page_shift;                    // pages of a step
-      const uint32_t page_bytes = uint32_t(128) << p.b.page_shift;  // of one 64-column piece
       int t = 0, s = 0;  // steps loaded, the next stage
       uint32_t par = 1;
       bool ok = true, more = w.end > w.begin;
@@ -264,46 +264,52 @@ __global__ void __launch_bounds__(512, 1)
         if (!more) break;
         const int32_t* row = p.b.pages + int64_t(w.seq) * p.b.page_stride;
         const int lo = w.t.lo, hi = w.t.hi, head = w.head;
-        // which pages of step j are needed, and their entries: read a step ahead of their use, and not looked at before
-        auto look = [&](int j, int (&pg)[8]) {
+        // The copies of step j, N pages of it.  The entries of the page table come from L1, a line of them fetched ahead.
+        auto load_step = [&](int j, auto n_pages) {
+          constexpr int N = decltype(n_pages)::value;
+          int at[N];  // first cache row of each page that is needed
           uint32_t needed = 0;
+          const int first_page = (key0 + j * KS) >> p.b.page_shift;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int ki = key0 + j * KS + (i << p.b.page_shift);
-            const bool need = j < n_it && i < per_step && ki < hi && ki + p.b.page_size > lo;
-            pg[i] = need ? __ldg(row + (ki >> p.b.page_shift)) : 0;
+          for (int i = 0; i < N; ++i) {
+            const int ki = key0 + j * KS + i * (KS / N);
+            const bool need = ki < hi && ki + KS / N > lo;
+            at[i] = need ? __ldg(row + first_page + i) : 0;
             needed |= uint32_t(need) << i;
           }
-          return needed;
-        };
-        int next[8];
-        uint32_t next_needed = look(0, next);
-        for (int j = 0; j < n_it; ++j) {
-          int at[8];  // first cache row of each page
-          const uint32_t needed = next_needed;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            int pg = next[i];
-            if (uint32_t(pg) >= uint32_t(p.b.n_pages)) {  // never followed: page 0 is read in its place
+          for (int i = 0; i < N; ++i) {
+            if (uint32_t(at[i]) >= uint32_t(p.b.n_pages)) {  // never followed: page 0 is read in its place
               atomicOr(&g_status_pfew, TPA_DEV_BAD_INPUT);
-              pg = 0;
+              at[i] = 0;
             }
-            at[i] = (pg * p.b.hkv + head) << p.b.page_shift;
+            at[i] = (at[i] * p.b.hkv + head) * (KS / N);
           }
-          next_needed = look(j + 1, next);
-          if (!(ok = wait1(empty + s, par))) break;
-          tc::mbar_arrive_expect_tx(full + s, __popc(needed) * NCH * page_bytes);
+          if (!wait1(empty + s, par)) return false;
+          constexpr uint32_t kBytes = 128 * (KS / N);  // a 64-column piece of a page
+          tc::mbar_arrive_expect_tx(full + s, __popc(needed) * NCH * kBytes);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
+          for (int i = 0; i < N; ++i)
             if (needed >> i & 1)
 #pragma unroll
               for (int c = 0; c < NCH; ++c)
-                tma_load_2d(tiles + s * TILE + c * kChunk + i * page_bytes, tm, full + s, c * 64, at[i]);
+                tma_load_2d(tiles + s * TILE + c * kChunk + i * kBytes, tm, full + s, c * 64, at[i]);
+          if (first_page + 32 < p.b.max_pages) asm volatile("prefetch.global.L1 [%0];" ::"l"(row + first_page + 32));
           ++t;
           if (++s == NS) {
             s = 0;
             par ^= 1;
           }
+          return true;
+        };
+        auto load_steps = [&](auto n_pages) {
+          for (int j = 0; ok && j < n_it; ++j) ok = load_step(j, n_pages);
+        };
+        switch (KS >> p.b.page_shift) {
+          case 1: load_steps(std::integral_constant<int, 1>()); break;
+          case 2: load_steps(std::integral_constant<int, 2>()); break;
+          case 4: load_steps(std::integral_constant<int, 4>()); break;
+          default: load_steps(std::integral_constant<int, 8>()); break;
         }
         if (ok) more = w.next(p.b);
       }
