@@ -448,12 +448,18 @@ __global__ void __launch_bounds__(512, 1)
       bool dead = false;
       for (int j = h; j < n_it; j += 2) {
         const int key0 = key_first + j * KS;
+        note(wait_thread(s_full + h, uses & 1));
+        ++uses;
         if (key0 < lo || key0 + KS > hi) {
-          // slots that no row sees may hold anything: zero their values, so that 0 x NaN does not come in
+          // slots that no row sees may hold anything: zero their values, so that 0 x NaN does not come in.  This S^T
+          // was issued behind the products with V of every step up to j - 2, so those V have landed and the wait can
+          // only end with this step's; before S^T, the stage's last V could still be under way, whose end has the
+          // parity that a wait for this one takes for its own.
+          static_assert(NS >= 2, "the stage's last V is of a step before j - 1");
           const int s = (t + j) % NS;
           const bool there = wait_thread(v_full + s, ((t + j) / NS) & 1);
           note(there);
-          if (there && (key0 + r < lo || key0 + r >= hi)) {
+          if (there && fine && (key0 + r < lo || key0 + r >= hi)) {
 #pragma unroll
             for (int c = 0; c < NCH; ++c)
 #pragma unroll
@@ -461,8 +467,6 @@ __global__ void __launch_bounds__(512, 1)
                 *reinterpret_cast<uint4*>(sV + s * TILE + c * kChunk + r * 128 + i * 16) = make_uint4(0, 0, 0, 0);
           }
         }
-        note(wait_thread(s_full + h, uses & 1));
-        ++uses;
         __syncwarp();
         tc::tc_fence_after();
         uint32_t raw[NR];

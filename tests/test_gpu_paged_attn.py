@@ -167,6 +167,20 @@ def test_many_sequences(tpa, n):
     _check_values(b, o, lse, only=set(range(0, n, 37)) | {n - 1})
 
 
+@pytest.mark.parametrize("case", [(64, 1, 300, 3000, 32, 8, 128), (16, 5, 1000, 8000, 32, 8, 128),
+                                  (16, 8, 1000, 8000, 16, 4, 64), (12, 1, 990, 1030, 32, 8, 128)])
+def test_tiles_that_follow_one_another(tpa, case):
+    """Many steps and several tiles for every CTA: a tile's last, ragged step runs beside the loads of those before it."""
+    n, q_len, least, most, hq, hkv, d = case
+    rng = np.random.default_rng(17)
+    b = Batch([q_len] * n, [int(x) for x in rng.integers(least, most, n)], hq, hkv, d, 16, seed=17)
+    first = [x.clone() for x in _run(tpa, b)]
+    _check_values(b, *first)
+    for _ in range(6):
+        assert all(torch.equal(x, y) for x, y in zip(first, _run(tpa, b)))
+    tpa.sync_status()
+
+
 @pytest.mark.parametrize("q_len", [1, 5])
 def test_one_long_sequence(tpa, q_len):
     b = Batch([q_len], [70001], 8, 2, 128, 128, seed=4)
