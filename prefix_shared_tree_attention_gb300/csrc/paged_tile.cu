@@ -12,6 +12,8 @@
 //                     page of 16 to 128 slots is a box; one of 128-byte rows
 //                     swizzled as the MMA descriptors want)
 //   warp 9            one thread issues the MMAs
+// A tile whose tokens all fit in the first sub-tile (a sequence's last tile; one
+// new token next to others' chunks) leaves the second one's work out.
 // Bound by the tensor and exponential pipes: 4 d operations and one exponential
 // for each (row, key).
 #include <cuda.h>
@@ -143,11 +145,11 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         tc::tma_prefetch_desc(&tm_k);
         tc::tma_prefetch_desc(&tm_v);
         auto wait1 = [&](uint64_t* b_, uint32_t par) { return tc::mbar_wait(b_, par, abort_flag, &g_status_ptile); };
-                Walk w;
+        Walk w;
         w.start(p.b, sc, shares);
         const int per_step = kStep >> p.b.page_shift;       // pages of a step
         const uint32_t page_bytes = uint32_t(128) << p.b.page_shift;  // of one 64-column piece
-        const uint32_t q_bytes = uint32_t(NH * NCH) * sub_tok * p.b.group * 128;
+        const uint32_t q_bytes = uint32_t(NCH) * sub_tok * p.b.group * 128;  // of a sub-tile
         int kt = 0, vt = 0;
         bool ok = true, more = w.end > w.begin;
         for (int k = 0; ok; ++k) {
@@ -168,8 +170,9 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
           tc::mbar_arrive(seg_full + (k & 1));
           if (!more) break;
           if (!(ok = wait1(q_empty, (k & 1) ^ 1))) break;
-          tc::mbar_arrive_expect_tx(q_full, q_bytes);
-          for (int h = 0; h < NH; ++h)
+          const int nh = w.t.n > sub_tok ? NH : 1;
+          tc::mbar_arrive_expect_tx(q_full, nh * q_bytes);
+          for (int h = 0; h < nh; ++h)
             for (int c = 0; c < NCH; ++c)
               tc::tma_load_3d(sQ + h * TILE + c * kChunk, &tm_q, q_full, c * 64, w.head * p.b.group,
                               w.t.first + h * sub_tok);
@@ -246,25 +249,29 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
       };
       auto wait1 = [&](uint64_t* b_, uint32_t par) { return tc::mbar_wait(b_, par, abort_flag, &g_status_ptile); };
       if (tc::elect_one()) {
-        int t = 0;  // steps so far
+        int t = 0;                    // steps so far
+        int uses[NH] = {}, segs[NH] = {};  // of them each sub-tile's, and its segments
         bool ok = true;
         for (int k = 0; ok; ++k) {
           if (!(ok = wait1(seg_full + (k & 1), (k >> 1) & 1))) break;
-          const int n_it = seg_ring[k & 1].n_it;
+          const int n_it = seg_ring[k & 1].n_it, nh = seg_ring[k & 1].n > sub_tok ? NH : 1;
           tc::mbar_arrive(seg_empty + (k & 1));
           if (n_it < 0) break;
           if (!(ok = wait1(q_full, k & 1) && wait1(k_full + t % NS, (t / NS) & 1))) break;
           tc::tc_fence_after();
-          for (int h = 0; h < NH; ++h) issue_s(h, t % NS);
+          for (int h = 0; h < nh; ++h) issue_s(h, t % NS);
           tc::mma_commit(k_empty + t % NS);
           if (n_it == 1) tc::mma_commit(q_empty);
           for (int j = 0; ok && j < n_it; ++j) {
             const int g = t + j, sv = g % NS, s1 = (g + 1) % NS;
             const bool more = j + 1 < n_it;
             if (!(ok = wait1(v_full + sv, (g / NS) & 1))) break;
-            for (int h = 0; h < NH && ok; ++h) {
-              if (!(ok = wait1(p_full + h, g & 1))) break;
-              if (j == 0 && k > 0 && !(ok = wait1(o_free + h, (k - 1) & 1))) break;
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
+              if (h >= nh) break;
+              if (!(ok = wait1(p_full + h, uses[h] & 1))) break;
+              ++uses[h];
+              if (j == 0 && segs[h]++ > 0 && !(ok = wait1(o_free + h, segs[h] & 1))) break;
               tc::tc_fence_after();
               issue_pv(h, sv, j == 0);
               if (more) {
@@ -306,7 +313,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
     auto wait_all = [&](uint64_t* b_, uint32_t par) {
       return __all_sync(0xffffffffu, tc::mbar_wait(b_, par, abort_flag, &g_status_ptile));
     };
-    int tb = 0;
+    int tb = 0, uses = 0;  // steps so far, and of them this sub-tile's
     bool ok = true;
     for (int k = 0; ok; ++k) {
       if (!wait_all(seg_full + (k & 1), (k >> 1) & 1)) break;
@@ -315,6 +322,13 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
       const int slot = sg->whole ? -1 : sg->slot, head = sg->head * p.b.group + gh, pos_first = sg->pos0;
       tc::mbar_arrive(seg_empty + (k & 1));
       if (n_it < 0) break;
+      if (h * sub_tok >= n_tok) {
+        // Nothing in this sub-tile.  The segment's end is waited for all the same: the stages' barriers are then
+        // never more than one phase ahead of what this warpgroup has seen.
+        if (!wait_all(o_final, k & 1)) break;
+        tb += n_it;
+        continue;
+      }
       const bool live = r < sub_tok * p.b.group && tok < n_tok;
       const int pos = live ? pos_first + tok : -1;
       // every live row of the sub-tile sees the keys in [all_lo, all_hi)
@@ -336,7 +350,8 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
           }
           tc::fence_proxy_async_smem();
         }
-        if (!wait_all(s_full + h, (tb + j) & 1)) { ok = false; break; }
+        if (!wait_all(s_full + h, uses & 1)) { ok = false; break; }
+        ++uses;
         tc::tc_fence_after();
         uint32_t sv[128];
 #pragma unroll

@@ -168,12 +168,14 @@ def test_many_sequences(tpa, n):
 
 
 @pytest.mark.parametrize("case", [(64, 1, 300, 3000, 32, 8, 128), (16, 5, 1000, 8000, 32, 8, 128),
-                                  (16, 8, 1000, 8000, 16, 4, 64), (12, 1, 990, 1030, 32, 8, 128)])
+                                  (16, 8, 1000, 8000, 16, 4, 64), (12, 1, 990, 1030, 32, 8, 128),
+                                  (24, (1, 32, 33, 70, 140), 300, 2500, 8, 2, 128), (24, (1, 10, 70), 300, 2500, 16, 2, 64)])
 def test_tiles_that_follow_one_another(tpa, case):
     """Many steps and several tiles for every CTA: a tile's last, ragged step runs beside the loads of those before it."""
     n, q_len, least, most, hq, hkv, d = case
     rng = np.random.default_rng(17)
-    b = Batch([q_len] * n, [int(x) for x in rng.integers(least, most, n)], hq, hkv, d, 16, seed=17)
+    q_lens = [q_len] * n if isinstance(q_len, int) else [int(x) for x in rng.choice(q_len, n)]
+    b = Batch(q_lens, [int(x) for x in rng.integers(least, most, n)], hq, hkv, d, 16, seed=17)
     first = [x.clone() for x in _run(tpa, b)]
     _check_values(b, *first)
     for _ in range(6):
