@@ -172,13 +172,17 @@ __global__ void __launch_bounds__(256, 4) paged_join_kernel(const Params p) {
 
 // ------------------------------------------------------------------ host side
 
-int num_sms() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+// Multiprocessors of the current device, after a check that the kernels run on it.
+int device_sms(int* sms) {
+  int dev = 0, major = 0, minor = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
     (void)cudaGetLastError();
-    return 148;
+    return TPA_ERR_CUDA;
   }
-  return sms;
+  return major == 10 && minor == 3 ? TPA_OK : TPA_ERR_UNSUPPORTED_DEVICE;
 }
 
 // Rows of a tile: 16 or 32 while every sequence's queries fit in them, else 256.
@@ -250,7 +254,10 @@ extern "C" int tpa_paged_attn_fwd(const tpa_paged_view* cache, const void* q, in
   p.part_o = reinterpret_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float2*>(ws + uint64_t(2) * kMaxGrid * R * d * 4);
   p.split = reinterpret_cast<Split*>(ws + uint64_t(2) * kMaxGrid * R * (uint64_t(d) * 4 + 8));
-  const int sms = num_sms(), grid = sms < kMaxGrid ? sms : kMaxGrid;
+  int sms = 0;
+  const int dv = device_sms(&sms);
+  if (dv != TPA_OK) return dv;
+  const int grid = sms < kMaxGrid ? sms : kMaxGrid;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int rt = R == 256 ? tpa_internal_paged_tile(cache, p, grid, st) : tpa_internal_paged_few(cache, p, R, grid, st);
   if (rt == kPagedUnfit) return TPA_ERR_CUDA;

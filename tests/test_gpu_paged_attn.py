@@ -74,7 +74,8 @@ CASES = [  # q_lens, kv_lens, hq, hkv, d, page, extra rows
     ([9, 9], [2000, 9], 5, 5, 128, 32, 0), ([33], [33], 4, 4, 64, 16, 3), ([200], [200], 8, 2, 128, 16, 0),
     ([130, 1, 257, 7], [700, 80, 257, 1500], 8, 2, 128, 64, 5), ([100], [1000], 3, 1, 64, 128, 0),
     ([129, 64], [129, 999], 7, 1, 128, 32, 0), ([0, 0], [0, 30], 4, 2, 64, 16, 3), ([300], [4000], 24, 8, 128, 128, 0),
-    ([65], [640], 10, 2, 64, 32, 0), ([40, 40], [41, 1000], 32, 1, 128, 16, 0)]
+    ([65], [640], 10, 2, 64, 32, 0), ([40, 40], [41, 1000], 32, 1, 128, 16, 0),
+    ([1, 1, 3], [900, 64, 130], 64, 1, 128, 16, 1), ([1, 2], [333, 3], 66, 2, 64, 32, 0)]
 
 
 @pytest.mark.parametrize("window", [0, 1, 100, 300])

@@ -74,8 +74,8 @@ def test_no_drafts(tpa):
 
 def test_borders(tpa):
     """u of 0 and just below 1, weights at the ends of the row and of its parts, rows of zeros, equal rows."""
-    V = 1024  # 128 parts of 8
-    S = 12
+    V = 1024  # 64 parts of 16
+    S = 13
     p = torch.zeros((S, 2, V))
     q = torch.zeros((S, 1, V))
     x = torch.zeros((S, 1), dtype=torch.int32)
@@ -94,7 +94,9 @@ def test_borders(tpa):
     p[9, 0, 3] = 3e-39; p[9, 0, 700] = 1e-38; un[9] = 0.9     # noqa: E702  subnormal weights
     p[10, 0, 2] = 1.0; p[10, 0, 900] = 2.0 ** -60; un[10] = 1 - 2.0 ** -24  # noqa: E702
     p[11, 0, 0] = 1.0; u[11] = 0.0; p[11, 1, 4] = 1.0         # noqa: E702
+    p[12, 0, 15] = 0.5; p[12, 0, 16] = 0.5; un[12] = 0.5      # noqa: E702  a tie between two parts
     t, a = _check(tpa, p, x, u, un, q)
+    assert t[12, 0] == 16
     assert t[0, 0] == 1023 and t[1, 0] == 15 and t[2, 0] == 8 and t[3, 0] == -1 and t[4, 0] == 0
     assert t[5].tolist() == [0, -1] and t[6].tolist() == [0, 1000] and t[7, 0] == 9 and t[11].tolist() == [0, 4]
     tpa.sync_status()
