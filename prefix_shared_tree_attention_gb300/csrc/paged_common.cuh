@@ -16,6 +16,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "device_common.cuh"
 #include "tc.cuh"
@@ -292,6 +293,72 @@ __device__ __forceinline__ void write_split(const Params& p, const Scan* sc, con
     if (c0 + 1 == int(blockIdx.x)) s = Split{1, sc->head, t.first, t.n, c0, c1, {0, 0}};
   }
   p.split[blockIdx.x] = s;
+}
+
+// The ring of stages that one thread fills with the keys (or the values) of this CTA's steps.
+struct LoadRing {
+  uint64_t* full;
+  uint64_t* empty;
+  uint8_t* tiles;
+  int t = 0, s = 0;  // steps loaded, the next stage
+  uint32_t par = 1;  // and the parity of its `empty`
+};
+
+// Loads steps [0, n_it) of a segment, KS keys each from key0 on, the pages that hold keys of [lo, hi) of them: a page
+// is a box for each 64 columns.  Unrolled for the number of pages of a step.  The entries of the page table come from
+// L1, a line of them fetched ahead.  False when a wait gave up.
+template <int KS, int NS, int NCH, class Wait>
+__device__ __forceinline__ bool load_steps(const Batch& b, LoadRing& ring, const CUtensorMap* tm, const int32_t* row,
+                                           int head, int key0, int n_it, int lo, int hi, unsigned int* status, Wait wait1) {
+  auto load_step = [&](int j, auto n_pages) {
+    constexpr int N = decltype(n_pages)::value;
+    int at[N];  // first cache row of each page that is needed
+    uint32_t needed = 0;
+    const int first_page = (key0 + j * KS) >> b.page_shift;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int ki = key0 + j * KS + i * (KS / N);
+      const bool need = ki < hi && ki + KS / N > lo;
+      at[i] = need ? __ldg(row + first_page + i) : 0;
+      needed |= uint32_t(need) << i;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (uint32_t(at[i]) >= uint32_t(b.n_pages)) {  // never followed: page 0 is read in its place
+        atomicOr(status, TPA_DEV_BAD_INPUT);
+        at[i] = 0;
+      }
+      at[i] = (at[i] * b.hkv + head) * (KS / N);
+    }
+    if (!wait1(ring.empty + ring.s, ring.par)) return false;
+    constexpr uint32_t kBytes = 128 * (KS / N);  // a 64-column piece of a page
+    tc::mbar_arrive_expect_tx(ring.full + ring.s, __popc(needed) * NCH * kBytes);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (needed >> i & 1)
+#pragma unroll
+        for (int c = 0; c < NCH; ++c)
+          tma_load_2d(ring.tiles + ring.s * (NCH * KS * 128) + c * (KS * 128) + i * kBytes, tm, ring.full + ring.s, c * 64,
+                      at[i]);
+    if (first_page + 32 < b.max_pages) asm volatile("prefetch.global.L1 [%0];" ::"l"(row + first_page + 32));
+    ++ring.t;
+    if (++ring.s == NS) {
+      ring.s = 0;
+      ring.par ^= 1;
+    }
+    return true;
+  };
+  auto all = [&](auto n_pages) {
+    bool ok = true;
+    for (int j = 0; ok && j < n_it; ++j) ok = load_step(j, n_pages);
+    return ok;
+  };
+  switch (KS >> b.page_shift) {
+    case 1: return all(std::integral_constant<int, 1>());
+    case 2: return all(std::integral_constant<int, 2>());
+    case 4: return all(std::integral_constant<int, 4>());
+    default: return all(std::integral_constant<int, 8>());
+  }
 }
 
 // Launches a kernel that may begin while the one before it in the stream ends;

@@ -20,8 +20,6 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include <type_traits>
-
 #include "device_common.cuh"
 #include "internal.h"
 #include "paged_common.cuh"
@@ -235,13 +233,9 @@ __global__ void __launch_bounds__(512, 1)
     if (tc::elect_one()) {
       const CUtensorMap* tm = keys ? &tm_k : &tm_v;
       auto wait1 = [&](uint64_t* b_, uint32_t par) { return tc::mbar_wait(b_, par, abort_flag, &g_status_pfew); };
-      uint64_t* full = keys ? k_full : v_full;
-      uint64_t* empty = keys ? k_empty : v_empty;
-      uint8_t* tiles = keys ? sK : sV;
+      LoadRing ring{keys ? k_full : v_full, keys ? k_empty : v_empty, keys ? sK : sV};
       Walk w;
       w.start(p.b, sc, shares);
-      int t = 0, s = 0;  // steps loaded, the next stage
-      uint32_t par = 1;
       bool ok = true, more = w.end > w.begin;
       for (int k = 0; ok; ++k) {
         const int n_it = more ? w.end - w.begin : -1;
@@ -264,59 +258,13 @@ __global__ void __launch_bounds__(512, 1)
         if (!more) break;
         const int32_t* row = p.b.pages + int64_t(w.seq) * p.b.page_stride;
         const int lo = w.t.lo, hi = w.t.hi, head = w.head;
-        // The copies of step j, N pages of it.  The entries of the page table come from L1, a line of them fetched ahead.
-        auto load_step = [&](int j, auto n_pages) {
-          constexpr int N = decltype(n_pages)::value;
-          int at[N];  // first cache row of each page that is needed
-          uint32_t needed = 0;
-          const int first_page = (key0 + j * KS) >> p.b.page_shift;
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const int ki = key0 + j * KS + i * (KS / N);
-            const bool need = ki < hi && ki + KS / N > lo;
-            at[i] = need ? __ldg(row + first_page + i) : 0;
-            needed |= uint32_t(need) << i;
-          }
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            if (uint32_t(at[i]) >= uint32_t(p.b.n_pages)) {  // never followed: page 0 is read in its place
-              atomicOr(&g_status_pfew, TPA_DEV_BAD_INPUT);
-              at[i] = 0;
-            }
-            at[i] = (at[i] * p.b.hkv + head) * (KS / N);
-          }
-          if (!wait1(empty + s, par)) return false;
-          constexpr uint32_t kBytes = 128 * (KS / N);  // a 64-column piece of a page
-          tc::mbar_arrive_expect_tx(full + s, __popc(needed) * NCH * kBytes);
-#pragma unroll
-          for (int i = 0; i < N; ++i)
-            if (needed >> i & 1)
-#pragma unroll
-              for (int c = 0; c < NCH; ++c)
-                tma_load_2d(tiles + s * TILE + c * kChunk + i * kBytes, tm, full + s, c * 64, at[i]);
-          if (first_page + 32 < p.b.max_pages) asm volatile("prefetch.global.L1 [%0];" ::"l"(row + first_page + 32));
-          ++t;
-          if (++s == NS) {
-            s = 0;
-            par ^= 1;
-          }
-          return true;
-        };
-        auto load_steps = [&](auto n_pages) {
-          for (int j = 0; ok && j < n_it; ++j) ok = load_step(j, n_pages);
-        };
-        switch (KS >> p.b.page_shift) {
-          case 1: load_steps(std::integral_constant<int, 1>()); break;
-          case 2: load_steps(std::integral_constant<int, 2>()); break;
-          case 4: load_steps(std::integral_constant<int, 4>()); break;
-          default: load_steps(std::integral_constant<int, 8>()); break;
-        }
+        ok = load_steps<KS, NS, NCH>(p.b, ring, tm, row, head, key0, n_it, lo, hi, &g_status_pfew, wait1);
         if (ok) more = w.next(p.b);
       }
       if (*abort_flag) {  // let the copies already issued land before the CTA exits
         volatile int never = 0;
-        for (int j = (t > NS ? t - NS : 0); j < t; ++j)
-          tc::mbar_wait(full + (j % NS), (j / NS) & 1, &never, &g_status_pfew, 100000000ull);
+        for (int j = (ring.t > NS ? ring.t - NS : 0); j < ring.t; ++j)
+          tc::mbar_wait(ring.full + (j % NS), (j / NS) & 1, &never, &g_status_pfew, 100000000ull);
       }
     }
     __syncwarp();

@@ -7,8 +7,8 @@
 //                     online in the log2 domain; P goes to TMEM over S as the
 //                     bf16 operand of the second MMA; O is rescaled in TMEM
 //                     only when a row's maximum has grown by 2^8
-//   warp 8            one thread: walks this CTA's steps, hands each segment to
-//                     the other roles, loads Q, and the pages of K and V (a
+//   warps 8, 10, 11   one thread each: walk this CTA's steps and load the pages of
+//                     K (and hand each segment to the other roles), of V, and Q (a
 //                     page of 16 to 128 slots is a box; one of 128-byte rows
 //                     swizzled as the MMA descriptors want)
 //   warp 9            one thread issues the MMAs
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
 
   const int warp = threadIdx.x >> 5;
-  constexpr int W_TMA = 4 * NH, W_MMA = 4 * NH + 1;
+  constexpr int W_K = 4 * NH, W_MMA = W_K + 1, W_V = W_K + 2, W_Q = W_K + 3;
   const int sub_tok = p.b.tile_tok / NH;  // tokens of a sub-tile
 
   if (threadIdx.x == 0) {
@@ -136,91 +136,73 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
 
   if (int(blockIdx.x) >= shares.n) {  // nothing to do here
     if (threadIdx.x == 0) write_split(p, sc, shares);
-  } else if (warp >= W_TMA) {
+  } else if (warp >= W_K) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REG_LOW));
-    if (warp == W_TMA) {
-      // ---------------------------------------------------------- producer
+    if (warp == W_K || warp == W_V) {
+      // ---------------------------------------------------------- producers: one thread for the keys (and the segments
+      // that the other roles read), one for the values; each walks the steps.  One thread for both, with the queries
+      // too, was what the MMAs waited for: 3000 cycles a step, whatever the head size.
+      const bool keys = warp == W_K;
       if (tc::elect_one()) {
-        tc::tma_prefetch_desc(&tm_q);
-        tc::tma_prefetch_desc(&tm_k);
-        tc::tma_prefetch_desc(&tm_v);
+        const CUtensorMap* tm = keys ? &tm_k : &tm_v;
+        tc::tma_prefetch_desc(tm);
         auto wait1 = [&](uint64_t* b_, uint32_t par) { return tc::mbar_wait(b_, par, abort_flag, &g_status_ptile); };
+        LoadRing ring{keys ? k_full : v_full, keys ? k_empty : v_empty, keys ? sK : sV};
         Walk w;
         w.start(p.b, sc, shares);
-        const int per_step = kStep >> p.b.page_shift;       // pages of a step
-        const uint32_t page_bytes = uint32_t(128) << p.b.page_shift;  // of one 64-column piece
-        const uint32_t q_bytes = uint32_t(NCH) * sub_tok * p.b.group * 128;  // of a sub-tile
-        int kt = 0, vt = 0;
         bool ok = true, more = w.end > w.begin;
         for (int k = 0; ok; ++k) {
-          if (!(ok = wait1(seg_empty + (k & 1), ((k >> 1) & 1) ^ 1))) break;
-          volatile Segment* sg = seg_ring + (k & 1);
           const int n_it = more ? w.end - w.begin : -1;
           const int key0 = (w.t.step0 + w.begin) * kStep;
-          sg->n_it = n_it;
-          sg->head = w.head;
-          sg->first = w.t.first;
-          sg->n = w.t.n;
-          sg->pos0 = w.t.pos0;
-          sg->lo = w.t.lo;
-          sg->hi = w.t.hi;
-          sg->key0 = key0;
-          sg->whole = w.begin == 0 && w.end == w.t.steps;
-          sg->slot = blockIdx.x * 2 + (w.begin == 0 ? 1 : 0);
-          tc::mbar_arrive(seg_full + (k & 1));
+          if (keys) {
+            if (!(ok = wait1(seg_empty + (k & 1), ((k >> 1) & 1) ^ 1))) break;
+            volatile Segment* sg = seg_ring + (k & 1);
+            sg->n_it = n_it;
+            sg->head = w.head;
+            sg->first = w.t.first;
+            sg->n = w.t.n;
+            sg->pos0 = w.t.pos0;
+            sg->lo = w.t.lo;
+            sg->hi = w.t.hi;
+            sg->key0 = key0;
+            sg->whole = w.begin == 0 && w.end == w.t.steps;
+            sg->slot = blockIdx.x * 2 + (w.begin == 0 ? 1 : 0);
+            tc::mbar_arrive(seg_full + (k & 1));
+          }
           if (!more) break;
-          if (!(ok = wait1(q_empty, (k & 1) ^ 1))) break;
+          ok = load_steps<kStep, NS, NCH>(p.b, ring, tm, p.b.pages + int64_t(w.seq) * p.b.page_stride, w.head, key0, n_it,
+                                          w.t.lo, w.t.hi, &g_status_ptile, wait1);
+          if (ok) more = w.next(p.b);
+        }
+        if (*abort_flag) {  // let the copies already issued land before the CTA exits
+          volatile int never = 0;
+          for (int j = (ring.t > NS ? ring.t - NS : 0); j < ring.t; ++j)
+            tc::mbar_wait(ring.full + (j % NS), (j / NS) & 1, &never, &g_status_ptile, 100000000ull);
+        }
+      }
+      __syncwarp();
+    } else if (warp == W_Q) {
+      // ---------------------------------------------------------- one thread for the queries of each segment
+      if (tc::elect_one()) {
+        tc::tma_prefetch_desc(&tm_q);
+        const uint32_t q_bytes = uint32_t(NCH) * sub_tok * p.b.group * 128;  // of a sub-tile
+        Walk w;
+        w.start(p.b, sc, shares);
+        int nq = 0;
+        bool more = w.end > w.begin;
+        while (more && tc::mbar_wait(q_empty, (nq & 1) ^ 1, abort_flag, &g_status_ptile)) {
           const int nh = w.t.n > sub_tok ? NH : 1;
           tc::mbar_arrive_expect_tx(q_full, nh * q_bytes);
           for (int h = 0; h < nh; ++h)
             for (int c = 0; c < NCH; ++c)
               tc::tma_load_3d(sQ + h * TILE + c * kChunk, &tm_q, q_full, c * 64, w.head * p.b.group,
                               w.t.first + h * sub_tok);
-          const int32_t* row = p.b.pages + int64_t(w.seq) * p.b.page_stride;
-          const int lo = w.t.lo, hi = w.t.hi, head = w.head;
-          // K runs ahead of V by one step: the MMAs need K(j+1) before V(j)
-          int kj = 0, vj = 0;
-          while (kj < n_it || vj < n_it) {
-            const bool do_k = kj < n_it && kj <= vj + 1;
-            const int j = do_k ? kj : vj;
-            const int key = key0 + j * kStep;
-            int pg[8], n_pg = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int ki = key + (i << p.b.page_shift);
-              const bool need = i < per_step && ki < hi && ki + p.b.page_size > lo;
-              pg[i] = need ? __ldg(row + (ki >> p.b.page_shift)) : -1;
-              if (need && (pg[i] < 0 || pg[i] >= p.b.n_pages)) {  // never followed: page 0 is read in its place
-                atomicOr(&g_status_ptile, TPA_DEV_BAD_INPUT);
-                pg[i] = 0;
-              }
-              n_pg += need;
-            }
-            const int gx = (do_k ? kt : vt) + j, s = gx % NS;
-            if (!(ok = wait1((do_k ? k_empty : v_empty) + s, ((gx / NS) & 1) ^ 1))) break;
-            uint64_t* fb = (do_k ? k_full : v_full) + s;
-            uint8_t* dst = (do_k ? sK : sV) + s * TILE;
-            tc::mbar_arrive_expect_tx(fb, n_pg * NCH * page_bytes);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              if (pg[i] < 0) continue;
-              const int r0 = (pg[i] * p.b.hkv + head) << p.b.page_shift;
-#pragma unroll
-              for (int c = 0; c < NCH; ++c)
-                tma_load_2d(dst + c * kChunk + i * page_bytes, do_k ? &tm_k : &tm_v, fb, c * 64, r0);
-            }
-            if (do_k) ++kj; else ++vj;
-          }
-          kt += kj;
-          vt += vj;
-          if (ok) more = w.next(p.b);
+          if (nq++ == 0) write_split(p, sc, shares);
+          more = w.next(p.b);
         }
-        if (*abort_flag) {  // let the copies already issued land before the CTA exits
+        if (*abort_flag && nq > 0) {
           volatile int never = 0;
-          for (int j = (kt > NS ? kt - NS : 0); j < kt; ++j)
-            tc::mbar_wait(k_full + (j % NS), (j / NS) & 1, &never, &g_status_ptile, 100000000ull);
-          for (int j = (vt > NS ? vt - NS : 0); j < vt; ++j)
-            tc::mbar_wait(v_full + (j % NS), (j / NS) & 1, &never, &g_status_ptile, 100000000ull);
+          tc::mbar_wait(q_full, (nq - 1) & 1, &never, &g_status_ptile, 100000000ull);
         }
       }
       __syncwarp();
@@ -297,8 +279,6 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         }
       }
       __syncwarp();
-    } else if (threadIdx.x == 32 * (W_MMA + 1)) {
-      write_split(p, sc, shares);
     }
   } else if (warp < 4 * NH) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REG_HIGH));
