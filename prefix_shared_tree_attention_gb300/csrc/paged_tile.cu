@@ -14,8 +14,13 @@
 //   warp 9            one thread issues the MMAs
 // A tile whose tokens all fit in the first sub-tile (a sequence's last tile; one
 // new token next to others' chunks) leaves the second one's work out.
-// Bound by the tensor and exponential pipes: 4 d operations and one exponential
-// for each (row, key).
+// Work: 4 d operations and one exponential for each (row, key).  Bound by the way
+// from a step's scores to the next's, which each sub-tile goes alone: at d 128
+// 1024 cycles of MMAs, 1350 of softmax and 600 of handing over by barriers, so that
+// with two sub-tiles the MMAs run 68 % of the time.  4001 tokens after 28002 cached
+// ones, 32/8 heads: 1.30 to 1.38 ms with the clock, 1430 to 1510 TFLOP/s (measured
+// GEMM rates: 1939 in a burst, 1739 sustained).  Polling the barriers without
+// suspending, and one arrival a warp instead of one a thread, gave nothing or lost 2 %.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -53,9 +58,9 @@ struct TileCfg {
   static constexpr uint32_t OFF_SCAN = OFF_V + NS * TILE;
   static constexpr uint32_t OFF_SEG = OFF_SCAN + 160;
   static constexpr uint32_t OFF_BAR = OFF_SEG + 128;
-  // q_full, q_empty, k_full[NS], k_empty[NS], v_full[NS], v_empty[NS], s_full[NH], p_full[NH], o_free[NH],
+  // q_full, q_empty, k_full[NS], k_empty[NS], v_full[NS], v_empty[NS], s_full[NH], p_full[2 NH], o_free[NH],
   // o_final, drain, seg_full[2], seg_empty[2]
-  static constexpr int NBAR = 2 + 4 * NS + 3 * NH + 2 + 4;
+  static constexpr int NBAR = 2 + 4 * NS + 4 * NH + 2 + 4;
   static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr uint32_t BYTES = OFF_MISC + 16 + 1024;
   // Registers move from the producer/issuer warpgroup to the
@@ -64,6 +69,10 @@ struct TileCfg {
   static constexpr int REG_LAUNCH = 168, REG_LOW = 120, REG_HIGH = 184;
   static_assert(REG_HIGH * 256 + REG_LOW * 128 <= REG_LAUNCH * 384, "register split");
   static constexpr uint32_t TMEM_COLS = 512;
+  // P is handed over in this many parts, so that its product can begin while the rest is formed.  Two shorten the way
+  // from scores to scores where it is what the MMAs wait for: 4001 tokens at d 64 495 -> 451 us.  At d 128, with twice
+  // the MMA work in the same softmax, they cost 1 to 2 % (8 chunks of 512: 160.5 -> 162.5 us).
+  static constexpr int PARTS = D == 64 ? 2 : 1;
   static_assert(sizeof(Scan) <= 160 && sizeof(Segment) * 2 <= 128 && NS >= 2, "layout");
   static_assert(BYTES <= kSmemMax, "shared memory budget");
 };
@@ -73,7 +82,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
     paged_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const Params p) {
   using C = TileCfg<D>;
-  constexpr int NCH = C::NCH, NS = C::NS;
+  constexpr int NCH = C::NCH, NS = C::NS, PARTS = C::PARTS;
   constexpr uint32_t TILE = C::TILE;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -89,8 +98,8 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
   uint64_t* v_full = k_empty + NS;
   uint64_t* v_empty = v_full + NS;
   uint64_t* s_full = v_empty + NS;
-  uint64_t* p_full = s_full + NH;
-  uint64_t* o_free = p_full + NH;
+  uint64_t* p_full = s_full + NH;  // [part][sub-tile]
+  uint64_t* o_free = p_full + 2 * NH;
   uint64_t* o_final = o_free + NH;
   uint64_t* drain = o_final + 1;
   uint64_t* seg_full = drain + 1;   // [2]
@@ -114,6 +123,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
     for (int h = 0; h < NH; ++h) {
       tc::mbar_init(s_full + h, 1);
       tc::mbar_init(p_full + h, 128);
+      tc::mbar_init(p_full + NH + h, 128);
       tc::mbar_init(o_free + h, 128);
     }
     tc::mbar_init(o_final, 1);
@@ -222,10 +232,10 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         }
         tc::mma_commit(s_full + h);
       };
-      auto issue_pv = [&](int h, int s, bool first) {  // O_h (+)= P_h V(s)
+      auto issue_pv = [&](int h, int s, int part, bool first) {  // O_h (+)= P_h V(s), a part of the keys
         const uint64_t vb = dV + ((s * TILE) >> 4);
 #pragma unroll
-        for (int k = 0; k < kStep / 16; ++k)
+        for (int k = part * (8 / PARTS); k < (part + 1) * (8 / PARTS); ++k)
           mma_ts(tmem + 128 * NH + h * 128, tmem + h * 128 + k * 8, vb + ((k * 2048) >> 4), idesc_pv,
                  (!first || k > 0) ? 1u : 0u);
       };
@@ -251,11 +261,15 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
               if (h >= nh) break;
-              if (!(ok = wait1(p_full + h, uses[h] & 1))) break;
+#pragma unroll
+              for (int part = 0; ok && part < PARTS; ++part) {
+                if (!(ok = wait1(p_full + part * NH + h, uses[h] & 1))) break;
+                if (part == 0 && j == 0 && segs[h]++ > 0 && !(ok = wait1(o_free + h, segs[h] & 1))) break;
+                tc::tc_fence_after();
+                issue_pv(h, sv, part, part == 0 && j == 0);
+              }
+              if (!ok) break;
               ++uses[h];
-              if (j == 0 && segs[h]++ > 0 && !(ok = wait1(o_free + h, segs[h] & 1))) break;
-              tc::tc_fence_after();
-              issue_pv(h, sv, j == 0);
               if (more) {
                 if (h == 0 && !(ok = wait1(k_full + s1, ((g + 1) / NS) & 1))) break;
                 tc::tc_fence_after();
@@ -362,36 +376,48 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         }
         const float m_use = (m_run == -INFINITY) ? 0.f : m_run;
         const uint64_t negm = f2(-m_use, -m_use);
-        uint64_t sum2[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};  // 4 chains
-        uint32_t pk[64];
+        auto rescale = [&] {  // O holds the result of the step before: s_full was committed after it
+          if (j < 1 || !__any_sync(0xffffffffu, resc)) return;
+          constexpr int W = PARTS > 1 ? 16 : 32;  // columns at a time: while the scores are held there is room for 16
 #pragma unroll
-        for (int c = 0; c < 64; ++c) {
-          float a, bb;
-          unf2(fma2(f2(__uint_as_float(sv[2 * c]), __uint_as_float(sv[2 * c + 1])), sl2, negm), a, bb);
-          const float p0 = tc::ex2(a), p1 = tc::ex2(bb);
-          sum2[c & 3] = add2(sum2[c & 3], f2(p0, p1));
-          pk[c] = tc::pack_bf16(p0, p1);
+          for (int c = 0; c < D; c += W) {
+            uint32_t ov[W];
+            if constexpr (W == 16) tc::tmem_ld16(tO + c, ov);
+            else tc::tmem_ld32(tO + c, ov);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int u = 0; u < W; ++u) ov[u] = __float_as_uint(__uint_as_float(ov[u]) * alpha);
+            if constexpr (W == 16) tc::tmem_st16(tO + c, ov);
+            else tc::tmem_st32(tO + c, ov);
+          }
+        };
+        if (PARTS > 1) rescale();
+        // P goes over the first 64 columns of S
+        uint64_t sum2[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};  // 4 chains
+#pragma unroll
+        for (int part = 0; part < PARTS; ++part) {
+          constexpr int N = 64 / PARTS;
+          uint32_t pk[N];
+#pragma unroll
+          for (int c = 0; c < N; ++c) {
+            const int at = part * 2 * N + 2 * c;
+            float a, bb;
+            unf2(fma2(f2(__uint_as_float(sv[at]), __uint_as_float(sv[at + 1])), sl2, negm), a, bb);
+            const float p0 = tc::ex2(a), p1 = tc::ex2(bb);
+            sum2[c & 3] = add2(sum2[c & 3], f2(p0, p1));
+            pk[c] = tc::pack_bf16(p0, p1);
+          }
+          if (PARTS == 1) rescale();  // here the scores' registers are free
+#pragma unroll
+          for (int c = 0; c < N; c += 32)
+            tc::tmem_st32(tS + part * N + c, *reinterpret_cast<const uint32_t(*)[32]>(pk + c));
+          tc::tmem_st_wait();
+          tc::tc_fence_before();
+          tc::mbar_arrive(p_full + part * NH + h);
         }
         float s_lo, s_hi;
         unf2(add2(add2(sum2[0], sum2[1]), add2(sum2[2], sum2[3])), s_lo, s_hi);
         l_run = l_run * alpha + (s_lo + s_hi);
-        // O holds the result of the step before: s_full was committed after it
-        if (j >= 1 && __any_sync(0xffffffffu, resc)) {
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t ov[32];
-            tc::tmem_ld32(tO + c * 32, ov);
-            tc::tmem_ld_wait();
-#pragma unroll
-            for (int u = 0; u < 32; ++u) ov[u] = __float_as_uint(__uint_as_float(ov[u]) * alpha);
-            tc::tmem_st32(tO + c * 32, ov);
-          }
-        }
-        tc::tmem_st32(tS, *reinterpret_cast<const uint32_t(*)[32]>(pk));  // P over the first 64 columns of S
-        tc::tmem_st32(tS + 32, *reinterpret_cast<const uint32_t(*)[32]>(pk + 32));
-        tc::tmem_st_wait();
-        tc::tc_fence_before();
-        tc::mbar_arrive(p_full + h);
       }
       if (!ok || !wait_all(o_final, k & 1)) { ok = false; break; }
       tc::tc_fence_after();
