@@ -36,8 +36,9 @@ namespace {
 
 __device__ unsigned int g_status_rope = 0;
 
-// A CTA: seven warps that work and one that loads (two loading warps, or one CTA
-// an SM with 13 + 3 warps, were within 3 % either way).
+// A CTA: seven warps that work and one that loads.  (One CTA an SM with 13 + 3
+// warps was within 3 % either way; a second loading warp leaves 96 registers a
+// thread and took 236 instead of 195 us on the 64K-token tree.)
 constexpr int kWarps = 7;
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kBatch = 4;  // lanes of the loading warp for each ring: units looked up together
@@ -216,9 +217,9 @@ template <int D, uint32_t DATA>
 struct Ring {
   static constexpr uint32_t TABLE = D * 4;
   static constexpr uint32_t STAGE = DATA + TABLE + uint32_t(sizeof(Unit));
-  // Two stages: with three or four the grid reads from so many places at once
-  // that HBM gives less (64K-token tree: 208 instead of 190 us).
-  static constexpr int NST = 2;
+  // Three stages where the rings of two CTAs fit beside each other (20K tokens appended: 42.8 us, with two 47.5;
+  // the 64K-token tree 194.5 and 196.5 us).
+  static constexpr int NST = kCtas * (3 * kWarps * STAGE + 2048) <= 227 * 1024 ? 3 : 2;
   static constexpr uint32_t WARP = NST * STAGE;
   static constexpr uint32_t OFF_FULL = kWarps * WARP;
   static constexpr uint32_t OFF_EMPTY = OFF_FULL + kWarps * NST * 8;
