@@ -376,6 +376,17 @@ def _launch_stream(stream, first: torch.Tensor, *tensors) -> int:
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_ptr(stream)
 
 
+def _new(stream, shape, dtype: torch.dtype, device) -> torch.Tensor:
+    """Uninitialised memory of the stream that the call runs on: what the
+    current one still has under way cannot reach it, and it is used again, once
+    dropped, behind the call."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    st = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(st):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _head_rows(name: str, t: torch.Tensor, dtypes=(torch.bfloat16,)) -> tuple[int, int, int, int]:
     """(rows, row stride, heads, d) of a tensor [..., H, d] whose heads are
     contiguous and whose leading dimensions are evenly spaced rows."""
@@ -412,7 +423,7 @@ def rope_table(n_positions: int, rot_dim: int, base: float = 10000.0, inv_freq: 
             raise ValueError("inv_freq must hold rot_dim / 2 frequencies")
         fr = (C.c_double * len(inv_freq))(*[float(f) for f in inv_freq])
     if out is None:
-        out = torch.empty((n_positions, rot_dim), dtype=torch.float32, device=device)
+        out = _new(stream, (n_positions, rot_dim), torch.float32, device)
     if out.dtype != torch.float32 or not out.is_contiguous() or tuple(out.shape) != (n_positions, rot_dim):
         raise ValueError("out must be a contiguous fp32 tensor [n_positions, rot_dim]")
     st = _launch_stream(stream, out)
@@ -471,8 +482,8 @@ def qk_norm_rope_fwd(positions: "torch.Tensor | DeviceTree", q: torch.Tensor, k:
         raise ValueError("q and k must have the same rows and head_dim")
     pos, n_tok, t_pad, pbuf = _positions(positions, rows)
     rp = _rope_params(table, q_weight, k_weight, eps, interleaved, d)
-    qo, ko = out if out is not None else (torch.empty(q.shape, dtype=q.dtype, device=q.device),
-                                          torch.empty(k.shape, dtype=k.dtype, device=k.device))
+    qo, ko = out if out is not None else (_new(stream, q.shape, q.dtype, q.device),
+                                          _new(stream, k.shape, k.dtype, k.device))
     st = _launch_stream(stream, q, k, table, q_weight, k_weight, pbuf, qo, ko)
     if qo.shape != q.shape or ko.shape != k.shape:
         raise ValueError("out must be shaped like q and k")
@@ -508,16 +519,16 @@ def qk_norm_rope_bwd(positions: "torch.Tensor | DeviceTree", dq_out: torch.Tenso
             raise ValueError("q and k must be given with the weights, shaped like dq_out and dk_out")
         sq, sk = _head_rows("q", q)[1], _head_rows("k", k)[1]
     dev = dq_out.device
-    dq, dk = out if out is not None else (torch.empty(dq_out.shape, dtype=grad_dtype, device=dev),
-                                          torch.empty(dk_out.shape, dtype=grad_dtype, device=dev))
+    dq, dk = out if out is not None else (_new(stream, dq_out.shape, grad_dtype, dev),
+                                          _new(stream, dk_out.shape, grad_dtype, dev))
     if dq.shape != dq_out.shape or dk.shape != dk_out.shape or dq.dtype != grad_dtype or dk.dtype != grad_dtype:
         raise ValueError("out must be shaped like dq_out and dk_out and of grad_dtype")
     so, sko = _head_rows("out[0]", dq, _GRAD)[1], _head_rows("out[1]", dk, _GRAD)[1]
     dwq = dwk = None
     if norm:
-        dwq, dwk = (torch.empty(d, dtype=torch.float32, device=dev) for _ in range(2))
+        dwq, dwk = (_new(stream, d, torch.float32, dev) for _ in range(2))
         if workspace is None:
-            workspace = torch.empty(int(lib().tpa_qk_norm_rope_bwd_workspace_bytes(d)), dtype=torch.uint8, device=dev)
+            workspace = _new(stream, int(lib().tpa_qk_norm_rope_bwd_workspace_bytes(d)), torch.uint8, dev)
     st = _launch_stream(stream, dq_out, dk_out, table, q_weight, k_weight, pbuf, dq, dk, workspace, *((q, k) if norm else ()))
     check("tpa_qk_norm_rope_bwd", lib().tpa_qk_norm_rope_bwd(
         pos, n_tok, t_pad, rows, dq_out.data_ptr(), sgq, dk_out.data_ptr(), sgk, _GRAD[dq_out.dtype],
@@ -573,7 +584,7 @@ def paged_append(k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Tens
         if rows_q != rows or dq != d:
             raise ValueError("q must have the rows and head_dim of k")
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = _new(stream, q.shape, q.dtype, q.device)
         if q_out.shape != q.shape:
             raise ValueError("q_out must be shaped like q")
         so = _head_rows("q_out", q_out)[1]
@@ -604,15 +615,15 @@ def paged_attn_fwd(k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Te
     if q.dim() != 3:
         raise ValueError("q must be [tokens, Hq, d]")
     cache, hkv = _paged_view(k_cache, v_cache, pages, offsets, kv_lens, rows, None, d)
-    o = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else out
+    o = _new(stream, q.shape, q.dtype, q.device) if out is None else out
     if lse is None:
-        lse = torch.empty((rows, Hq), dtype=torch.float32, device=q.device)
+        lse = _new(stream, (rows, Hq), torch.float32, q.device)
     if o.shape != q.shape or o.dtype != q.dtype or not o.is_contiguous():
         raise ValueError("out must be contiguous bf16 shaped like q")
     if lse.shape != (rows, Hq) or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous fp32 tensor [tokens, Hq]")
     if workspace is None:
-        workspace = torch.empty(paged_attn_workspace_bytes(max_q_len, Hq, hkv, d), dtype=torch.uint8, device=q.device)
+        workspace = _new(stream, paged_attn_workspace_bytes(max_q_len, Hq, hkv, d), torch.uint8, q.device)
     st = _launch_stream(stream, q, o, lse, workspace, k_cache, v_cache, pages, offsets, kv_lens)
     check("tpa_paged_attn_fwd", lib().tpa_paged_attn_fwd(
         cache, q.data_ptr(), sq, o.data_ptr(), lse.data_ptr(), Hq, int(max_q_len),
@@ -655,8 +666,8 @@ def verify_drafts(target_probs: torch.Tensor, draft_tokens: torch.Tensor, u_acce
         if (V > 1 and d1 != 1) or (K > 1 and dr != V):
             raise ValueError("draft_probs must have contiguous sequences")
     if out is None:
-        out = (torch.empty((S, K1), dtype=i32, device=target_probs.device),
-               torch.empty(S, dtype=i32, device=target_probs.device))
+        out = (_new(stream, (S, K1), i32, target_probs.device),
+               _new(stream, S, i32, target_probs.device))
     tokens, n_accepted = out
     if (tokens.dtype != i32 or tokens.shape != (S, K1) or not tokens.is_contiguous() or
             n_accepted.dtype != i32 or n_accepted.shape != (S,) or not n_accepted.is_contiguous()):

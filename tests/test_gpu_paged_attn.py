@@ -289,6 +289,37 @@ def test_streams_graphs_and_repeats(tpa, q_len, kv):
     tpa.sync_status()
 
 
+@pytest.mark.parametrize("raw", [False, True])
+def test_results_of_a_call_on_another_stream_are_its_own(tpa, raw):
+    """What the current stream still writes to memory that was given back does not reach the outputs of a call on
+    another one, nor the other way round its workspace memory that is handed out again."""
+    b = Batch([2] * 8, [3000] * 8, 8, 2, 128, 16, seed=14)
+    table = tpa.rope_table(3000, 128)
+    p, x = torch.softmax(torch.randn((4, 3, 9000), device="cuda"), -1), torch.randint(0, 9000, (4, 2), device="cuda").int()
+    u, un = torch.rand((4, 2), device="cuda"), torch.rand(4, device="cuda")
+    at = torch.arange(b.total, device="cuda", dtype=torch.int32)
+
+    def calls(stream=None):
+        q, k = tpa.qk_norm_rope_fwd(at, b.q, b.k, table, stream=stream)
+        return (tpa.rope_table(3000, 128, stream=stream), q, k, *tpa.qk_norm_rope_bwd(at, b.q, b.k, None, None, table, stream=stream)[:2],
+                tpa.paged_append(*b.cache, b.k, b.v, q=b.q, table=table, stream=stream),
+                *tpa.paged_attn_fwd(*b.cache, b.q, max_q_len=2, stream=stream), *tpa.verify_drafts(p, x, u, un, stream=stream))
+
+    want = [z.clone() for z in calls()]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    mine = [torch.empty_like(z) for z in want for _ in range(3)]
+    torch.cuda._sleep(100_000_000)
+    for z in mine:
+        z.fill_(7)
+    del mine, z
+    got = calls(side.cuda_stream if raw else side)
+    after = [torch.empty_like(z).fill_(7) for z in want]  # noqa: F841
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
+    tpa.sync_status()
+
+
 @pytest.mark.parametrize("d,hq,hkv", [(64, 4, 2), (128, 8, 1)])
 def test_the_sampled_policy_is_the_trained_one(tpa, d, hq, hkv):
     """A packed tree's attention on the training side, and the same sequences on the sampling side: their prompts in

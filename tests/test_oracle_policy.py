@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle.paged import attend_sequence
 from oracle.rope import norm_rope, norm_rope_grad, rope_angles
 from oracle.verify import verify_drafts
 
@@ -80,3 +81,24 @@ def test_verify_by_hand():
     t, n = verify_drafts(np.array([[[0.0, 1.0], [1.0, 0.0]]], np.float32), np.array([[1]], np.int32),
                          np.array([[1.0]], np.float32), np.array([0.5], np.float32))
     assert t.tolist() == [[1, -1]] and n.tolist() == [0]
+
+
+@pytest.mark.parametrize("n,kv,window", [(1, 1, 0), (5, 9, 0), (4, 12, 3), (6, 4, 0), (3, 0, 0), (2, 30, 1)])
+def test_attention_over_a_cache_against_the_library(n, kv, window):
+    """The last n tokens of kv, causal at the end, grouped heads; rows before the first cached token see nothing."""
+    g = torch.Generator().manual_seed(n + kv)
+    q = torch.randn((n, 6, 16), generator=g, dtype=torch.float64)
+    k, v = (torch.randn((kv, 2, 16), generator=g, dtype=torch.float64) for _ in range(2))
+    o, lse, size = attend_sequence(q, k, v, window)
+    i, j = torch.arange(kv - n, kv)[:, None], torch.arange(kv)[None]
+    seen = (j <= i) & (j > i - (window or kv + 1))
+    rows = seen.any(1)
+    assert (o[~rows] == 0).all() and torch.isneginf(lse[~rows]).all() and torch.isfinite(lse[rows]).all()
+    if rows.any():
+        want = torch.nn.functional.scaled_dot_product_attention(
+            q[rows].transpose(0, 1), k.repeat_interleave(3, 1).transpose(0, 1), v.repeat_interleave(3, 1).transpose(0, 1),
+            attn_mask=seen[rows]).transpose(0, 1)
+        assert (o[rows] - want).abs().max() < 1e-13 and (size[rows] >= o[rows].abs() - 1e-13).all()
+        x = torch.einsum("nhd,hkd->nhk", q[rows], k.repeat_interleave(3, 1).transpose(0, 1)) / 4.0
+        p = (x - lse[rows][..., None]).exp() * seen[rows][:, None]
+        assert (p.sum(-1) - 1).abs().max() < 1e-13
