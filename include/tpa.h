@@ -564,7 +564,7 @@ int tpa_qk_norm_rope_bwd(const int32_t* positions, const int32_t* n_tokens, int3
  * in pages of page_size token slots,
  *   k_cache, v_cache [n_pages, Hkv, page_size, d] bf16 (device, 16-byte aligned),
  * page_size in {16, 32, 64, 128}, d in {64, 128}, n_pages * Hkv * page_size
- * < 2^31.  Token t of sequence s is slot t % page_size of page
+ * < 2^31, max_pages * page_size < 2^30.  Token t of sequence s is slot t % page_size of page
  * pages[s][t / page_size]; sequences may share the pages of a common prefix.
  * A batch is described by
  *   pages [n_seqs, max_pages] int32, rows page_stride elements apart,
@@ -589,7 +589,7 @@ typedef struct {
   const int32_t* kv_lens;
   int32_t n_pages, page_size, n_seqs, max_pages, page_stride;
   int32_t n_heads_kv, head_dim;
-  int32_t n_rows;           /* rows of the call's q, k, v: >= offsets[n_seqs] */
+  int32_t n_rows;           /* rows of the call's q, k, v: >= offsets[n_seqs], < 2^30 */
 } tpa_paged_view;
 
 /*

@@ -242,7 +242,8 @@ extern "C" int tpa_paged_attn_fwd(const tpa_paged_view* cache, const void* q, in
   p.b.hkv = hkv;
   p.b.n_rows = cache->n_rows;
   p.b.group = group;
-  p.b.window = window;
+  // positions are below 2^30: a longer window reaches no further, and differences with this one stay in 32 bits
+  p.b.window = window < (1 << 30) ? window : 1 << 30;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.q_stride = q_stride;
   p.o = static_cast<__nv_bfloat16*>(o);

@@ -83,7 +83,7 @@ __device__ __forceinline__ Tile make_tile(const Batch& b, const Seq& q, int i) {
 __device__ __forceinline__ int small_quot(long long a, long long b) {
   if (((a | b) >> 31) != 0) return int(a / b);
   int q = int(__fdividef(float(int(a)), float(int(b))));  // off by one at most
-  const int r = int(a) - q * int(b);
+  const int r = int(uint32_t(a) - uint32_t(q) * uint32_t(b));  // in [-b, 2 b), whatever q * b passes
   if (r < 0) --q;
   else if (r >= int(b)) ++q;
   return q;

@@ -1107,10 +1107,10 @@ int tpa_internal_check_paged(const tpa_paged_view* c) {
   if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
     return TPA_ERR_INVALID_ARG;
   if (c->n_pages < 1 || c->n_seqs < 1 || c->max_pages < 1 || c->page_stride < c->max_pages || c->n_rows < 0 ||
-      c->n_heads_kv < 1 || c->n_heads_kv > 65535)
+      c->n_rows >= (1 << 30) || c->n_heads_kv < 1 || c->n_heads_kv > 65535)
     return TPA_ERR_INVALID_ARG;
   if (int64_t(c->n_pages) * c->n_heads_kv >= (int64_t(1) << 31) / c->page_size) return TPA_ERR_INVALID_ARG;
-  // positions are held in 32 bits
+  // positions, and differences of them and of rows, are held in 32 bits
   if (int64_t(c->max_pages) * c->page_size >= (int64_t(1) << 30)) return TPA_ERR_INVALID_ARG;
   return TPA_OK;
 }

@@ -184,6 +184,16 @@ def test_tiles_that_follow_one_another(tpa, case):
     tpa.sync_status()
 
 
+@pytest.mark.parametrize("q_lens", [(1, 3, 2), (200, 7, 64)])
+def test_windows_past_every_position(tpa, q_lens):
+    b = Batch(list(q_lens), [700, 5, 129], 8, 2, 128, 16, seed=21)  # the second has more new tokens than cached ones, or few
+    want = _run(tpa, b)
+    for window in (701, 1 << 30, (1 << 30) + 1, 2 ** 31 - 1):
+        assert all(torch.equal(x, y) for x, y in zip(want, _run(tpa, b, window)))
+    tpa.sync_status()
+    _check_values(b, *want)
+
+
 @pytest.mark.parametrize("q_len", [1, 5])
 def test_one_long_sequence(tpa, q_len):
     b = Batch([q_len], [70001], 8, 2, 128, 128, seed=4)

@@ -96,7 +96,7 @@ def _paged(**kw):
 BAD_PAGED = [
     dict(k_cache=None), dict(v_cache=None), dict(pages=None), dict(offsets=None), dict(kv_lens=None),
     dict(k_cache=P + 8), dict(v_cache=P + 2), dict(head_dim=80), dict(page_size=8), dict(page_size=48),
-    dict(page_size=256), dict(n_pages=0), dict(n_seqs=0), dict(max_pages=0), dict(page_stride=3), dict(n_rows=-1),
+    dict(page_size=256), dict(n_pages=0), dict(n_seqs=0), dict(max_pages=0), dict(page_stride=3), dict(n_rows=-1), dict(n_rows=1 << 30),
     dict(n_heads_kv=0), dict(n_pages=1 << 27, n_heads_kv=1), dict(max_pages=1 << 27, page_stride=1 << 27)]
 
 
