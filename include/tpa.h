@@ -654,10 +654,11 @@ int tpa_paged_attn_fwd(const tpa_paged_view* cache, const void* q, int64_t q_str
  * next token is the lowest v with  sum_{w <= v} r(w) > u_next * sum_w r(w),
  *   r = max(p_a - q_a, 0) when a < n_drafts (p_a where that leaves nothing),
  *   r = p_a               when a = n_drafts,
- * sums in fp64 (should rounding leave none, the last v with r(v) > 0; a row of zeros gives -1).
+ * sums as pairs of fp32, good to 2^-44 of the whole, in a fixed order (should rounding leave none, the last v with
+ * r(v) > 0; a row of zeros gives -1).
  *   target [n_seqs, K+1, vocab] fp32: p_0 .. p_K; sequences target_stride and
- *     rows vocab elements apart; need not be normalised (entries >= 0; a
- *     negative or NaN entry counts as 0)
+ *     rows vocab elements apart; need not be normalised (entries >= 0 and
+ *     finite; a negative or NaN entry counts as 0)
  *   draft [n_seqs, K, vocab] fp32: q_0 .. q_{K-1}, or NULL: q_i is all on x_i
  *   draft_tokens [n_seqs, K] int32; a token outside [0, vocab) does not stand and is reported
  *   n_drafts [n_seqs] int32 in [0, K] (NULL: K; out of range: clamped and reported)
