@@ -57,10 +57,11 @@ __device__ __forceinline__ Seq load_seq(const Batch& b, int s, unsigned int* sta
 
 // Tile i of a sequence: n tokens from row `first`, the first of them at
 // position pos0 (negative where there are more new tokens than cached ones).
-// Keys outside [lo, hi) are seen by none of its tokens.  At least one step, so
-// that a tile that sees nothing still has its rows written.
+// Keys outside [lo, hi) are seen by none of its tokens; those from hi to `end`,
+// the sequence's cached tokens, by later ones.  At least one step, so that a tile
+// that sees nothing still has its rows written.
 struct Tile {
-  int first, n, pos0, lo, hi, step0, steps;
+  int first, n, pos0, lo, hi, end, step0, steps;
 };
 
 __device__ __forceinline__ int tiles_of(const Batch& b, int n) { return (n + b.tile_tok - 1) / b.tile_tok; }
@@ -72,6 +73,7 @@ __device__ __forceinline__ Tile make_tile(const Batch& b, const Seq& q, int i) {
   t.n = min(b.tile_tok, q.n - t0);
   t.pos0 = q.kv - q.n + t0;
   t.hi = max(t.pos0 + t.n, 0);
+  t.end = q.kv;
   t.lo = b.window > 0 ? max(t.pos0 - b.window + 1, 0) : 0;
   t.step0 = t.lo >> b.step_shift;
   t.steps = max(((t.hi + (1 << b.step_shift) - 1) >> b.step_shift) - t.step0, 1);

@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             sg->n = w.t.n;
             sg->pos0 = w.t.pos0;
             sg->lo = w.t.lo;
-            sg->hi = w.t.hi;
+            sg->hi = w.t.end;
             sg->key0 = key0;
             sg->whole = w.begin == 0 && w.end == w.t.steps;
             sg->slot = blockIdx.x * 2 + (w.begin == 0 ? 1 : 0);
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
           }
           if (!more) break;
           ok = load_steps<kStep, NS, NCH>(p.b, ring, tm, p.b.pages + int64_t(w.seq) * p.b.page_stride, w.head, key0, n_it,
-                                          w.t.lo, w.t.hi, &g_status_ptile, wait1);
+                                          w.t.lo, w.t.end, &g_status_ptile, wait1);
           if (ok) more = w.next(p.b);
         }
         if (*abort_flag) {  // let the copies already issued land before the CTA exits
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
     for (int k = 0; ok; ++k) {
       if (!wait_all(seg_full + (k & 1), (k >> 1) & 1)) break;
       const volatile Segment* sg = seg_ring + (k & 1);
-      const int n_it = sg->n_it, first = sg->first, n_tok = sg->n, lo = sg->lo, hi = sg->hi, key_first = sg->key0;
+      const int n_it = sg->n_it, first = sg->first, n_tok = sg->n, lo = sg->lo, end = sg->hi, key_first = sg->key0;
       const int slot = sg->whole ? -1 : sg->slot, head = sg->head * p.b.group + gh, pos_first = sg->pos0;
       tc::mbar_arrive(seg_empty + (k & 1));
       if (n_it < 0) break;
@@ -334,16 +334,17 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
       float m_run = -INFINITY, l_run = 0.f;
       for (int j = 0; j < n_it; ++j) {
         const int key0 = key_first + j * kStep;
-        if (key0 < lo || key0 + kStep > hi) {
-          // slots that no row sees may hold anything: zero their values, so that 0 x NaN does not come in
+        if (key0 < lo || key0 + kStep > end) {
+          // Slots that no row sees may hold anything: zero their values, so that 0 x NaN does not come in.  (Those from
+          // the last key that this tile sees to the sequence's end are loaded, and finite: other rows see them.)
           const int g = tb + j, sv_ = g % NS;
           if (!wait_all(v_full + sv_, (g / NS) & 1)) { ok = false; break; }
-          if (key0 + r < lo || key0 + r >= hi) {
+          const int head_rows = min(max(lo - key0, 0), kStep), live_rows = min(max(end - key0, 0), kStep);
 #pragma unroll
-            for (int c = 0; c < NCH; ++c)
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<uint4*>(sV + sv_ * TILE + c * kChunk + r * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+          for (int c = 0; c < NCH; ++c) {
+            uint4* v = reinterpret_cast<uint4*>(sV + sv_ * TILE + c * kChunk);
+            for (int i = r; i < head_rows * 8; i += 128) v[i] = make_uint4(0, 0, 0, 0);
+            for (int i = live_rows * 8 + r; i < kStep * 8; i += 128) v[i] = make_uint4(0, 0, 0, 0);
           }
           tc::fence_proxy_async_smem();
         }
@@ -355,10 +356,15 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         for (int c = 0; c < 4; ++c) tc::tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sv + c * 32));
         tc::tmem_ld_wait();
         if (key0 + kStep > all_hi || key0 < all_lo) {
-          const int last = pos - key0, before = p.b.window > 0 ? last - p.b.window : -1;
+          const int last = pos - key0;
 #pragma unroll
           for (int c = 0; c < 128; ++c)
-            if (c > last || c <= before) sv[c] = 0xff800000u;  // -inf
+            if (c > last) sv[c] = 0xff800000u;  // -inf
+          if (p.b.window > 0) {
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              if (c <= last - p.b.window) sv[c] = 0xff800000u;
+          }
         }
         // row max: 8 independent chains, then a short tree
         float mxs[8];
