@@ -407,12 +407,14 @@ __global__ void __launch_bounds__(512, 1)
           const int s = (t + j) % NS;
           const bool there = wait_thread(v_full + s, ((t + j) / NS) & 1);
           note(there);
-          if (there && fine && (key0 + r < lo || key0 + r >= hi)) {
+          if (there && fine) {
+            const int head_rows = min(max(lo - key0, 0), KS), live_rows = min(max(hi - key0, 0), KS);
 #pragma unroll
-            for (int c = 0; c < NCH; ++c)
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<uint4*>(sV + s * TILE + c * kChunk + r * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+            for (int c = 0; c < NCH; ++c) {
+              uint4* v = reinterpret_cast<uint4*>(sV + s * TILE + c * kChunk);
+              for (int i = r; i < head_rows * 8; i += 128) v[i] = make_uint4(0, 0, 0, 0);
+              for (int i = live_rows * 8 + r; i < KS * 8; i += 128) v[i] = make_uint4(0, 0, 0, 0);
+            }
           }
         }
         __syncwarp();
