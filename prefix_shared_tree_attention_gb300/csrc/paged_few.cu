@@ -45,18 +45,20 @@ struct FewCfg {
   static constexpr uint32_t FIXED = NCH * QCH + 2 * PT + 160 + 192 + NR * 136 + 1024;
   static constexpr int NS_FIT = int((kSmemMax - 1024 - FIXED) / (2 * TILE));
   static constexpr int NS = NS_FIT > 6 ? 6 : NS_FIT;
+  // Queries of the next segment beside the present one's, where they fit (not with 32 rows at d 128).
+  static constexpr int NQ = FIXED + NCH * QCH + 2 * NS * TILE + 1024 <= kSmemMax ? 2 : 1;
   // The values come first: for d 64 the transposed product reads 128 "dimensions" from each step, the second
   // 64 being whatever follows (the next step's, or the first keys), and their results are not used.
   static constexpr uint32_t OFF_V = 0;
   static constexpr uint32_t OFF_K = OFF_V + NS * TILE;
   static constexpr uint32_t OFF_Q = OFF_K + NS * TILE;
-  static constexpr uint32_t OFF_P = OFF_Q + NCH * QCH;
+  static constexpr uint32_t OFF_P = OFF_Q + NQ * NCH * QCH;
   static constexpr uint32_t OFF_SCAN = OFF_P + 2 * PT;
   static constexpr uint32_t OFF_SEG = OFF_SCAN + 160;
   static constexpr uint32_t OFF_F = OFF_SEG + 192;     // floats, see below: 34 NR
-  // q_full, q_empty, k_full[NS], k_empty[NS], v_full[NS], v_empty[NS], s_full[2], p_full[2], ml_full[2], ml_free[2],
+  // q_full[2], q_empty[2], k_full[NS], k_empty[NS], v_full[NS], v_empty[NS], s_full[2], p_full[2], ml_full[2], ml_free[2],
   // o_final[2], o_free[2], drain, seg_full[4], seg_empty[4]
-  static constexpr int NBAR = 2 + 4 * NS + 12 + 1 + 8;
+  static constexpr int NBAR = 4 + 4 * NS + 12 + 1 + 8;
   static constexpr uint32_t OFF_BAR = OFF_F + 34 * NR * 4;
   static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr uint32_t BYTES = OFF_MISC + 32 + 1024;
@@ -140,7 +142,7 @@ __global__ void __launch_bounds__(512, 1)
     paged_few_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const Params p) {
   using C = FewCfg<D, NR>;
-  constexpr int NCH = C::NCH, NS = C::NS;
+  constexpr int NCH = C::NCH, NS = C::NS, NQ = C::NQ;
   constexpr uint32_t TILE = C::TILE;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -155,8 +157,8 @@ __global__ void __launch_bounds__(512, 1)
   float* xl_s = f_s + 16 * NR;
   float* coef_s = f_s + 32 * NR;  // [2][NR] what the two O^T are multiplied by
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-  uint64_t* q_empty = q_full + 1;
-  uint64_t* k_full = q_full + 2;
+  uint64_t* q_empty = q_full + 2;
+  uint64_t* k_full = q_full + 4;
   uint64_t* k_empty = k_full + NS;
   uint64_t* v_full = k_empty + NS;
   uint64_t* v_empty = v_full + NS;
@@ -177,8 +179,10 @@ __global__ void __launch_bounds__(512, 1)
   constexpr int W_K = 8, W_MMA = 9, W_V = 10, W_Q = 11;
 
   if (threadIdx.x == 0) {
-    tc::mbar_init(q_full, 1);
-    tc::mbar_init(q_empty, 1);
+    for (int s = 0; s < NQ; ++s) {
+      tc::mbar_init(q_full + s, 1);
+      tc::mbar_init(q_empty + s, 1);
+    }
     for (int s = 0; s < NS; ++s) {
       tc::mbar_init(k_full + s, 1);
       tc::mbar_init(k_empty + s, 1);
@@ -208,7 +212,7 @@ __global__ void __launch_bounds__(512, 1)
     tc::tma_prefetch_desc(&tm_q);
   }
   // query rows that the loads do not reach are zero: their scores then do not move a maximum
-  for (int i = threadIdx.x; i < int(NCH * C::QCH / 16); i += blockDim.x)
+  for (int i = threadIdx.x; i < int(NQ * NCH * C::QCH / 16); i += blockDim.x)
     reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0, 0, 0, 0);
   tc::fence_proxy_async_smem();
   if (warp == W_MMA) tc::tmem_alloc(tmem_slot, C::TMEM_COLS);
@@ -276,12 +280,12 @@ __global__ void __launch_bounds__(512, 1)
     const uint64_t dQ = tc::smem_desc(tc::smem_u32(sQ), 16, 1024);
     const uint64_t dV = tc::smem_desc(tc::smem_u32(sV), kChunk, 1024);
     const uint64_t dP = tc::smem_desc(tc::smem_u32(smem + C::OFF_P), 16, 1024);
-    auto issue_s = [&](int h, int s) {  // S^T_h = K(s) Q^T
-      const uint64_t kb = dK + ((s * TILE) >> 4);
+    auto issue_s = [&](int h, int s, int qb) {  // S^T_h = K(s) Q^T
+      const uint64_t kb = dK + ((s * TILE) >> 4), q = dQ + ((qb * NCH * C::QCH) >> 4);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k)
         tc::mma_ss(tmem + h * NR, kb + (((k >> 2) * kChunk + (k & 3) * 32) >> 4),
-                   dQ + (((k >> 2) * C::QCH + (k & 3) * 32) >> 4), idesc_s, k > 0);
+                   q + (((k >> 2) * C::QCH + (k & 3) * 32) >> 4), idesc_s, k > 0);
       tc::mma_commit(s_full + h);
     };
     auto issue_o = [&](int k_, int h, int s, bool first) {  // O^T_h (+)= V(s)^T P^T_h
@@ -293,38 +297,50 @@ __global__ void __launch_bounds__(512, 1)
     };
     auto wait1 = [&](uint64_t* b_, uint32_t par) { return tc::mbar_wait(b_, par, abort_flag, &g_status_pfew); };
     if (tc::elect_one()) {
+      // The scores run two steps ahead of the products with V, over the ends of tiles: a tile of one or two steps
+      // would else go all the way from its scores to its products alone.
+      int ks = 0, ns = 0, js = 0, ts = 0, qb = 0;  // for the scores: segments begun, steps and step of the last, steps so far
+      bool ended = false;
+      auto start = [&] {  // S^T of the next step, when its keys are there
+        if (ended) return true;
+        if (js == ns) {
+          if (!wait1(seg_full + (ks & 3), (ks >> 2) & 1)) return false;
+          ns = seg_ring[ks & 3].n_it;
+          ended = ns < 0;
+          if (ended) return true;
+          qb = ks % NQ;
+          if (!wait1(q_full + qb, (ks / NQ) & 1)) return false;
+          js = 0;
+          ++ks;
+        }
+        const int s = ts % NS;
+        if (!wait1(k_full + s, (ts / NS) & 1)) return false;
+        tc::tc_fence_after();
+        issue_s(ts & 1, s, qb);
+        tc::mma_commit(k_empty + s);
+        if (++js == ns) tc::mma_commit(q_empty + qb);  // the segment's last S^T
+        ++ts;
+        return true;
+      };
       int t = 0;             // steps so far
       int uses[2] = {0, 0};  // steps of each warpgroup so far
-      bool ok = true;
-      for (int k = 0; ok; ++k) {
-        if (!(ok = wait1(seg_full + (k & 3), (k >> 2) & 1))) break;
+      bool ok = start() && start();
+      for (int k = 0; ok && t < ts; ++k) {
         const int n_it = seg_ring[k & 3].n_it;
         tc::mbar_arrive(seg_empty + (k & 3));
-        if (n_it < 0) break;
-        if (!(ok = wait1(q_full, k & 1))) break;
-        auto start = [&](int j) {  // S^T of step j, when its keys are there
-          const int s = (t + j) % NS;
-          if (!wait1(k_full + s, ((t + j) / NS) & 1)) return false;
-          tc::tc_fence_after();
-          issue_s(j & 1, s);
-          tc::mma_commit(k_empty + s);
-          if (j + 1 == n_it) tc::mma_commit(q_empty);  // the segment's last S^T
-          return true;
-        };
-        // S^T of the segment before was read before the p_full that its last products waited for
-        if (!(ok = start(0) && (n_it < 2 || start(1)))) break;
         for (int j = 0; ok && j < n_it; ++j) {
-          const int h = j & 1, s = (t + j) % NS;
-          if (!(ok = wait1(v_full + s, ((t + j) / NS) & 1) && wait1(p_full + h, uses[h] & 1))) break;
+          const int h = t & 1, s = t % NS;
+          if (!(ok = wait1(v_full + s, (t / NS) & 1) && wait1(p_full + h, uses[h] & 1))) break;
           if (j == 0 && !(ok = wait1(o_free + (k & 1), ((k >> 1) & 1) ^ 1))) break;
           ++uses[h];
           tc::tc_fence_after();
           issue_o(k, h, s, j < 2);
           tc::mma_commit(v_empty + s);
-          if (j + 2 < n_it && !(ok = start(j + 2))) break;
+          if (j + 1 == n_it) tc::mma_commit(o_final + (k & 1));
+          ++t;
+          // this warpgroup's S^T was read before the p_full just waited for
+          ok = start();
         }
-        if (ok) tc::mma_commit(o_final + (k & 1));
-        t += n_it;
       }
       if (*abort_flag) {  // let issued MMAs finish before TMEM is released
         volatile int never = 0;
@@ -342,16 +358,18 @@ __global__ void __launch_bounds__(512, 1)
       w.start(p.b, sc, shares);
       int nq = 0;
       bool more = w.end > w.begin;
-      while (more && tc::mbar_wait(q_empty, (nq & 1) ^ 1, abort_flag, &g_status_pfew)) {
-        tc::mbar_arrive_expect_tx(q_full, q_bytes);
+      while (more && tc::mbar_wait(q_empty + nq % NQ, ((nq / NQ) & 1) ^ 1, abort_flag, &g_status_pfew)) {
+        const int qb = nq % NQ;
+        tc::mbar_arrive_expect_tx(q_full + qb, q_bytes);
         for (int c = 0; c < NCH; ++c)
-          tc::tma_load_3d(sQ + c * C::QCH, &tm_q, q_full, c * 64, w.head * p.b.group, w.t.first);
+          tc::tma_load_3d(sQ + (qb * NCH + c) * C::QCH, &tm_q, q_full + qb, c * 64, w.head * p.b.group, w.t.first);
         if (nq++ == 0) write_split(p, sc, shares);
         more = w.next(p.b);
       }
-      if (*abort_flag && nq > 0) {
+      if (*abort_flag) {
         volatile int never = 0;
-        tc::mbar_wait(q_full, (nq - 1) & 1, &never, &g_status_pfew, 100000000ull);
+        for (int j = (nq > NQ ? nq - NQ : 0); j < nq; ++j)
+          tc::mbar_wait(q_full + j % NQ, (j / NQ) & 1, &never, &g_status_pfew, 100000000ull);
       }
     }
     __syncwarp();
@@ -394,7 +412,8 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
       for (int i = 0; i < NR; ++i) l[i] = 0.f;
       bool dead = false;
-      for (int j = h; j < n_it; j += 2) {
+      const int j0 = (t ^ h) & 1;  // this warpgroup's first step: the two take all steps in turn
+      for (int j = j0; j < n_it; j += 2) {
         const int key0 = key_first + j * KS;
         note(wait_thread(s_full + h, uses & 1));
         ++uses;
@@ -435,7 +454,7 @@ __global__ void __launch_bounds__(512, 1)
           for (int i = 0; i < NR; ++i)
             if (i < first_row || i >= last_row) x[i] = -INFINITY;
         }
-        bool grow = j == h;
+        bool grow = j == j0;
 #pragma unroll
         for (int i = 0; i < NR; i += 4) {
           const float4 m = *reinterpret_cast<const float4*>(m_s + i);
@@ -457,14 +476,14 @@ __global__ void __launch_bounds__(512, 1)
           for (int i = 0; i < OWN; ++i) warp_s[(warp & 3) * NR + row + i] = v[i];
           group_sync(h);
           if (r < NR) {
-            const float before = j == h ? kNoMax : m_s[r];
+            const float before = j == j0 ? kNoMax : m_s[r];
             const float top = fmaxf(fmaxf(warp_s[r], warp_s[NR + r]), fmaxf(warp_s[2 * NR + r], warp_s[3 * NR + r]));
             const float m = fmaxf(before, top);
             m_s[r] = m;
             alpha_s[r] = tc::ex2(before - m);
           }
           group_sync(h);
-          if (j != h) {
+          if (j != j0) {
 #pragma unroll
             for (int i = 0; i < NR; ++i) l[i] *= alpha_s[i];
             // O^T of this warpgroup is complete up to its step before: that product was issued before this S^T
@@ -508,7 +527,7 @@ __global__ void __launch_bounds__(512, 1)
         const int own = owned_row<NR>(lane);
 #pragma unroll
         for (int i = 0; i < OWN; ++i) xl[own + i] = l[i];
-        if (r < NR) xm[r] = h < n_it ? m_s[r] : kNoMax;  // (a warpgroup without a step has no maxima)
+        if (r < NR) xm[r] = j0 < n_it ? m_s[r] : kNoMax;  // (a warpgroup without a step has no maxima)
       }
       tc::mbar_arrive(ml_full + (k & 1));
       t += n_it;
@@ -526,6 +545,7 @@ __global__ void __launch_bounds__(512, 1)
       }
     };
     auto wait_thread = [&](uint64_t* b_, uint32_t par) { return tc::mbar_wait(b_, par, abort_flag, &g_status_pfew); };
+    int t = 0;
     for (int k = 0;; ++k) {
       note(wait_thread(seg_full + (k & 3), (k >> 2) & 1));
       if (group_any(2, !fine)) break;
@@ -564,7 +584,8 @@ __global__ void __launch_bounds__(512, 1)
       }
       if (group_any(2, !fine)) break;  // (the coefficients are there)
       tc::tc_fence_after();
-      const bool two = n_it > 1;  // else the second O^T was not written
+      // with one step, one of the two O^T was not written
+      const bool has0 = n_it > 1 || (t & 1) == 0, has1 = n_it > 1 || (t & 1) == 1;
       int tok = 0, gh = 0;
 #pragma unroll
       for (int c = 0; c < NR; c += 16) {
@@ -581,8 +602,8 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             if (c + i < live) {
-              float v = __uint_as_float(x[i]) * coef_s[c + i];
-              if (two) v = fmaf(__uint_as_float(y[i]), coef_s[NR + c + i], v);
+              float v = has0 ? __uint_as_float(x[i]) * coef_s[c + i] : 0.f;
+              if (has1) v = fmaf(__uint_as_float(y[i]), coef_s[NR + c + i], v);
               if (slot < 0)
                 p.o[(int64_t(first + tok) * p.hq + head0 + gh) * D + r] = __float2bfloat16_rn(v);
               else
@@ -595,6 +616,7 @@ __global__ void __launch_bounds__(512, 1)
           }
         }
       }
+      t += n_it;
     }
   }
 
