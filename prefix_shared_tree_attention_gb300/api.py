@@ -482,13 +482,15 @@ def qk_norm_rope_fwd(positions: "torch.Tensor | DeviceTree", q: torch.Tensor, k:
         raise ValueError("q and k must have the same rows and head_dim")
     pos, n_tok, t_pad, pbuf = _positions(positions, rows)
     rp = _rope_params(table, q_weight, k_weight, eps, interleaved, d)
-    qo, ko = out if out is not None else (_new(stream, q.shape, q.dtype, q.device),
-                                          _new(stream, k.shape, k.dtype, k.device))
-    st = _launch_stream(stream, q, k, table, q_weight, k_weight, pbuf, qo, ko)
-    if qo.shape != q.shape or ko.shape != k.shape:
-        raise ValueError("out must be shaped like q and k")
-    _, so, _, _ = _head_rows("out[0]", qo)
-    _, sko, _, _ = _head_rows("out[1]", ko)
+    st = _launch_stream(stream, q, k, table, q_weight, k_weight, pbuf, *(out or ()))
+    if out is None:
+        qo, ko = _new(stream, q.shape, q.dtype, q.device), _new(stream, k.shape, k.dtype, k.device)
+        so, sko = Hq * d, Hkv * d
+    else:
+        qo, ko = out
+        if qo.shape != q.shape or ko.shape != k.shape:
+            raise ValueError("out must be shaped like q and k")
+        so, sko = _head_rows("out[0]", qo)[1], _head_rows("out[1]", ko)[1]
     check("tpa_qk_norm_rope_fwd", lib().tpa_qk_norm_rope_fwd(
         pos, n_tok, t_pad, rows, q.data_ptr(), sq, k.data_ptr(), sk, rp, qo.data_ptr(), so, ko.data_ptr(), sko, Hq,
         Hkv, d, st))
@@ -519,17 +521,21 @@ def qk_norm_rope_bwd(positions: "torch.Tensor | DeviceTree", dq_out: torch.Tenso
             raise ValueError("q and k must be given with the weights, shaped like dq_out and dk_out")
         sq, sk = _head_rows("q", q)[1], _head_rows("k", k)[1]
     dev = dq_out.device
-    dq, dk = out if out is not None else (_new(stream, dq_out.shape, grad_dtype, dev),
-                                          _new(stream, dk_out.shape, grad_dtype, dev))
-    if dq.shape != dq_out.shape or dk.shape != dk_out.shape or dq.dtype != grad_dtype or dk.dtype != grad_dtype:
-        raise ValueError("out must be shaped like dq_out and dk_out and of grad_dtype")
-    so, sko = _head_rows("out[0]", dq, _GRAD)[1], _head_rows("out[1]", dk, _GRAD)[1]
+    st = _launch_stream(stream, dq_out, dk_out, table, q_weight, k_weight, pbuf, workspace, *(out or ()),
+                        *((q, k) if norm else ()))
+    if out is None:
+        dq, dk = _new(stream, dq_out.shape, grad_dtype, dev), _new(stream, dk_out.shape, grad_dtype, dev)
+        so, sko = Hq * d, Hkv * d
+    else:
+        dq, dk = out
+        if dq.shape != dq_out.shape or dk.shape != dk_out.shape or dq.dtype != grad_dtype or dk.dtype != grad_dtype:
+            raise ValueError("out must be shaped like dq_out and dk_out and of grad_dtype")
+        so, sko = _head_rows("out[0]", dq, _GRAD)[1], _head_rows("out[1]", dk, _GRAD)[1]
     dwq = dwk = None
     if norm:
         dwq, dwk = (_new(stream, d, torch.float32, dev) for _ in range(2))
         if workspace is None:
             workspace = _new(stream, int(lib().tpa_qk_norm_rope_bwd_workspace_bytes(d)), torch.uint8, dev)
-    st = _launch_stream(stream, dq_out, dk_out, table, q_weight, k_weight, pbuf, dq, dk, workspace, *((q, k) if norm else ()))
     check("tpa_qk_norm_rope_bwd", lib().tpa_qk_norm_rope_bwd(
         pos, n_tok, t_pad, rows, dq_out.data_ptr(), sgq, dk_out.data_ptr(), sgk, _GRAD[dq_out.dtype],
         q.data_ptr() if norm else None, sq, k.data_ptr() if norm else None, sk, rp, dq.data_ptr(), so,
@@ -583,14 +589,16 @@ def paged_append(k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Tens
         rows_q, sq, Hq, dq = _head_rows("q", q)
         if rows_q != rows or dq != d:
             raise ValueError("q must have the rows and head_dim of k")
-        if q_out is None:
-            q_out = _new(stream, q.shape, q.dtype, q.device)
-        if q_out.shape != q.shape:
-            raise ValueError("q_out must be shaped like q")
-        so = _head_rows("q_out", q_out)[1]
+        so = Hq * d
+        if q_out is not None:
+            if q_out.shape != q.shape:
+                raise ValueError("q_out must be shaped like q")
+            so = _head_rows("q_out", q_out)[1]
     elif q_out is not None:
         raise ValueError("q_out without q")
     st = _launch_stream(stream, k, v, q, q_out, k_cache, v_cache, pages, offsets, kv_lens, table, q_weight, k_weight)
+    if q is not None and q_out is None:
+        q_out = _new(stream, q.shape, q.dtype, q.device)
     check("tpa_paged_append", lib().tpa_paged_append(cache, k.data_ptr(), sk, v.data_ptr(), sv, _ptr(q), sq,
                                                      _ptr(q_out), so, Hq, rp, st))
     return q_out
@@ -615,16 +623,19 @@ def paged_attn_fwd(k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Te
     if q.dim() != 3:
         raise ValueError("q must be [tokens, Hq, d]")
     cache, hkv = _paged_view(k_cache, v_cache, pages, offsets, kv_lens, rows, None, d)
-    o = _new(stream, q.shape, q.dtype, q.device) if out is None else out
+    st = _launch_stream(stream, q, out, lse, workspace, k_cache, v_cache, pages, offsets, kv_lens)
+    if out is None:
+        o = _new(stream, q.shape, q.dtype, q.device)
+    else:
+        o = out
+        if o.shape != q.shape or o.dtype != q.dtype or not o.is_contiguous():
+            raise ValueError("out must be contiguous bf16 shaped like q")
     if lse is None:
         lse = _new(stream, (rows, Hq), torch.float32, q.device)
-    if o.shape != q.shape or o.dtype != q.dtype or not o.is_contiguous():
-        raise ValueError("out must be contiguous bf16 shaped like q")
-    if lse.shape != (rows, Hq) or lse.dtype != torch.float32 or not lse.is_contiguous():
+    elif lse.shape != (rows, Hq) or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous fp32 tensor [tokens, Hq]")
     if workspace is None:
         workspace = _new(stream, paged_attn_workspace_bytes(max_q_len, Hq, hkv, d), torch.uint8, q.device)
-    st = _launch_stream(stream, q, o, lse, workspace, k_cache, v_cache, pages, offsets, kv_lens)
     check("tpa_paged_attn_fwd", lib().tpa_paged_attn_fwd(
         cache, q.data_ptr(), sq, o.data_ptr(), lse.data_ptr(), Hq, int(max_q_len),
         float(softmax_scale or 0.0), int(window), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
@@ -665,14 +676,15 @@ def verify_drafts(target_probs: torch.Tensor, draft_tokens: torch.Tensor, u_acce
         ds, dr, d1 = draft_probs.stride()
         if (V > 1 and d1 != 1) or (K > 1 and dr != V):
             raise ValueError("draft_probs must have contiguous sequences")
+    st = _launch_stream(stream, target_probs, draft_tokens, u_accept, u_next, draft_probs, n_drafts, *(out or ()))
     if out is None:
-        out = (_new(stream, (S, K1), i32, target_probs.device),
-               _new(stream, S, i32, target_probs.device))
-    tokens, n_accepted = out
-    if (tokens.dtype != i32 or tokens.shape != (S, K1) or not tokens.is_contiguous() or
-            n_accepted.dtype != i32 or n_accepted.shape != (S,) or not n_accepted.is_contiguous()):
-        raise ValueError("out must be contiguous int32 tensors [S, K+1] and [S]")
-    st = _launch_stream(stream, target_probs, draft_tokens, u_accept, u_next, draft_probs, n_drafts, tokens, n_accepted)
+        dev = target_probs.device
+        tokens, n_accepted = _new(stream, (S, K1), i32, dev), _new(stream, S, i32, dev)
+    else:
+        tokens, n_accepted = out
+        if (tokens.dtype != i32 or tokens.shape != (S, K1) or not tokens.is_contiguous() or
+                n_accepted.dtype != i32 or n_accepted.shape != (S,) or not n_accepted.is_contiguous()):
+            raise ValueError("out must be contiguous int32 tensors [S, K+1] and [S]")
     if S == 1:
         ts, ds = K1 * V, K * V
     check("tpa_verify_drafts", lib().tpa_verify_drafts(

@@ -206,6 +206,14 @@ def test_longer_chunks_than_said(tpa):
     b = Batch([1, 90, 4], [300, 500, 4], 8, 2, 128, 16, seed=6)
     o, lse = _run(tpa, b, max_q=1)
     _check_values(b, o, lse)
+    o, lse = _run(tpa, b, max_q=5000)
+    _check_values(b, o, lse)
+
+
+def test_shorter_chunks_than_said(tpa):
+    b = Batch([1, 0, 2, 1], [300, 500, 2, 4000], 8, 2, 128, 16, seed=6, extra=2)
+    o, lse = _run(tpa, b, max_q=64)
+    _check_values(b, o, lse)
 
 
 def test_query_slices(tpa):
