@@ -202,6 +202,63 @@ __device__ __forceinline__ void store_pieces(uint8_t* row, int pa, int pb, const
   }
 }
 
+// What a lane's pairs are multiplied by, the weights with it:
+// first' = r (ca first - sb second), second' = r (cb second + sa first), sb held negative.
+struct Coefs {
+  uint64_t ca[4], cb[4], sa[4], sb[4];
+
+  // From the cosines and sines in ca and sa, where `turns` (the lane's pairs are among those turned), and the weights.
+  template <bool NORM>
+  __device__ __forceinline__ void weigh(bool turns, const uint64_t (&wa)[4], const uint64_t (&wb)[4]) {
+    if (turns) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        cb[j] = ca[j];
+        sb[j] = sa[j];
+      }
+    }
+    if constexpr (NORM) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        ca[j] = turns ? mul2(ca[j], wa[j]) : wa[j];
+        cb[j] = turns ? mul2(cb[j], wb[j]) : wb[j];
+        sa[j] = mul2(sa[j], wa[j]);
+        sb[j] = mul2(sb[j], wb[j]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sb[j] = neg2(sb[j]);
+  }
+
+  template <int D, bool NORM>
+  __device__ __forceinline__ Vals apply(const Vals& x, bool turns, float eps) const {
+    Vals y = x;
+    if (turns) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        y.a[j] = fma2(x.a[j], ca[j], mul2(x.b[j], sb[j]));
+        y.b[j] = fma2(x.b[j], cb[j], mul2(x.a[j], sa[j]));
+      }
+    } else if constexpr (NORM) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        y.a[j] = mul2(x.a[j], ca[j]);
+        y.b[j] = mul2(x.b[j], cb[j]);
+      }
+    }
+    if constexpr (NORM) {
+      const float rs = rstd<D>(x, eps);
+      const uint64_t r2 = f2(rs, rs);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        y.a[j] = mul2(y.a[j], r2);
+        y.b[j] = mul2(y.b[j], r2);
+      }
+    }
+    return y;
+  }
+};
+
 // ------------------------------------------------------------------ the warps' rings
 
 
@@ -506,34 +563,19 @@ __global__ void __launch_bounds__(kThreads, kCtas) fwd_kernel(const FwdParams p)
     const uint8_t* st = bar.ring + turn.s * R::STAGE;
     const Unit u = *reinterpret_cast<const Unit*>(st + 4096 + R::TABLE);
     if (u.state != kSkip) {
-      // coefficients of the lane's pairs, the weights with them: first' = r (ca first - sb second), second' = r (cb
-      // second + sa first)
-      uint64_t ca[4], cb[4], sa[4], sb[4];
+      Coefs c;
       if (u.turned > 0 && u.state == kUse) {
+        uint64_t wa[4], wb[4];
         if (turns) {
           const float* row = reinterpret_cast<const float*>(st + 4096) + 8 * l;
-          load_p4(row, ca);
-          load_p4(row + (p.rope.rot >> 1), sa);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            cb[j] = ca[j];
-            sb[j] = sa[j];
-          }
+          load_p4(row, c.ca);
+          load_p4(row + (p.rope.rot >> 1), c.sa);
         }
         if constexpr (NORM) {
-          uint64_t wa[4], wb[4];
           load_p4(w_s + u.kind * D + 16 * l, wa);
           load_p4(w_s + u.kind * D + 16 * l + 8, wb);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            ca[j] = turns ? mul2(ca[j], wa[j]) : wa[j];
-            cb[j] = turns ? mul2(cb[j], wb[j]) : wb[j];
-            sa[j] = mul2(sa[j], wa[j]);
-            sb[j] = mul2(sb[j], wb[j]);
-          }
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sb[j] = neg2(sb[j]);
+        c.weigh<NORM>(turns, wa, wb);
       }
       int64_t pitch = D * 2;
       uint8_t* out;
@@ -557,30 +599,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) fwd_kernel(const FwdParams p)
           oa = src[pa];
           ob = src[pb];
           if ((NORM || p.rope.rot > 0) && r0 < u.turned) {
-            const Vals x = unpack16(oa, ob, inter);
-            Vals y = x;
-            if (turns) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                y.a[j] = fma2(x.a[j], ca[j], mul2(x.b[j], sb[j]));
-                y.b[j] = fma2(x.b[j], cb[j], mul2(x.a[j], sa[j]));
-              }
-            } else if constexpr (NORM) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                y.a[j] = mul2(x.a[j], ca[j]);
-                y.b[j] = mul2(x.b[j], cb[j]);
-              }
-            }
-            if constexpr (NORM) {
-              const float rs = rstd<D>(x, p.rope.eps);
-              const uint64_t r2 = f2(rs, rs);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                y.a[j] = mul2(y.a[j], r2);
-                y.b[j] = mul2(y.b[j], r2);
-              }
-            }
+            const Vals y = c.apply<D, NORM>(unpack16(oa, ob, inter), turns, p.rope.eps);
             if (r < u.turned) pack16(y, inter, oa, ob);
           }
         }
@@ -591,6 +610,96 @@ __global__ void __launch_bounds__(kThreads, kCtas) fwd_kernel(const FwdParams p)
     }
     __syncwarp();  // every lane has read the stage
     if (lane == 0) tc::mbar_arrive(bar.empty + turn.s);
+  }
+}
+
+// The same with every d / 16 lanes taking a row by themselves, straight from
+// memory: 24 warps an SM hide the way from position to angles to results.  What
+// a row costs is nearly the same whatever its token has, where a ring's unit costs the
+// most of 4 KB even if it has 256 bytes: see use_rows().
+constexpr int kRowThreads = 256, kRowCtas = 3;
+
+template <int D, bool NORM, bool APPEND>
+__global__ void __launch_bounds__(kRowThreads, kRowCtas) fwd_rows_kernel(const FwdParams p) {
+  using G = Geo<D>;
+  constexpr int ROWS = kRowThreads / G::LPR;  // of a CTA at a time
+  __shared__ __align__(16) float w_s[2 * D];
+  if constexpr (NORM) {
+    stage_weights<D>(p.rope, w_s);
+    __syncthreads();
+  }
+  const int l = threadIdx.x % G::LPR, sub = threadIdx.x / G::LPR, heads = p.hq + (APPEND ? 2 : 1) * p.hkv;
+  const bool inter = p.rope.interleaved != 0, turns = l < (p.rope.rot >> 4);
+  int pa, pb;
+  pieces<D>(l, p.rope.rot, inter, pa, pb);
+  const bool one = p.wide && pb == pa + 1;
+  // the CTA's first row as token and head, and what a step adds to them
+  const int64_t base = int64_t(blockIdx.x) * ROWS, step = int64_t(gridDim.x) * ROWS;
+  int64_t tok0 = base / heads;
+  const int64_t d_tok = step / heads;
+  int h0 = int(base - tok0 * heads);
+  const int d_h = int(step - d_tok * heads);
+  for (; tok0 < p.n_rows; tok0 += d_tok) {
+    const unsigned at = unsigned(h0 + sub), over = at / unsigned(heads);
+    const int64_t tok = tok0 + over;
+    int h = int(at - over * unsigned(heads));
+    int pos = 0, state = kSkip;
+    int64_t slot = 0;
+    if (tok < p.n_rows) {
+      if constexpr (APPEND) paged_place(p, int(tok), pos, state, slot);
+      else plain_place(p.positions, p.n_tokens, p.t_pad, p.rope.table_rows, int(tok), pos, state);
+    }
+    const Rows* src = &p.q;
+    int kind = 0;  // 0: queries, 1: keys, 2: values
+    if (h >= p.hq) {
+      h -= p.hq;
+      kind = 1;
+      src = &p.k;
+      if (APPEND && h >= p.hkv) {
+        h -= p.hkv;
+        kind = 2;
+        src = &p.v;
+      }
+    }
+    uint4 oa = make_uint4(0, 0, 0, 0), ob = oa;
+    if (state == kUse) {
+      const uint4* x = reinterpret_cast<const uint4*>(src->p + tok * src->stride + int64_t(h) * (D * 2));
+      oa = x[pa];
+      ob = x[pb];
+    }
+    if (NORM || p.rope.rot > 0) {
+      // the lanes of a row agree; those of rows without one take part in the sums with zeros
+      Coefs c;
+      uint64_t wa[4], wb[4];
+      if (turns) {
+        const float* row = p.rope.table + int64_t(state == kUse ? pos : 0) * p.rope.rot + 8 * l;
+        load_p4(row, c.ca);
+        load_p4(row + (p.rope.rot >> 1), c.sa);
+      }
+      if constexpr (NORM) {
+        load_p4(w_s + (kind ? D : 0) + 16 * l, wa);
+        load_p4(w_s + (kind ? D : 0) + 16 * l + 8, wb);
+      }
+      c.weigh<NORM>(turns, wa, wb);
+      const Vals y = c.apply<D, NORM>(unpack16(oa, ob, inter), turns, p.rope.eps);
+      if (state == kUse && kind < 2) pack16(y, inter, oa, ob);
+    }
+    if (state != kSkip) {
+      uint8_t* to;
+      if (APPEND && kind) {
+        to = static_cast<uint8_t*>(kind == 1 ? p.cache.k_cache : p.cache.v_cache) +
+             (slot + int64_t(h) * p.cache.page_size) * (D * 2);
+      } else {
+        const RowsOut& dst = kind ? p.ko : p.qo;
+        to = dst.p + tok * dst.stride + int64_t(h) * (D * 2);
+      }
+      store_pieces(to, pa, pb, oa, ob, one);
+    }
+    h0 += d_h;
+    if (h0 >= heads) {
+      h0 -= heads;
+      ++tok0;
+    }
   }
 }
 
@@ -924,6 +1033,16 @@ int num_sms() {
   return sms;
 }
 
+// Row by row instead of through rings: tokens of few heads, whose units would be small (16384 of which 14000 real, d 128:
+// 2/1 heads 10.2 us instead of 22.1, 4/4 21.4 and 22.9, 8/8 38.5 and 29.6; 16000 appended: 2/1 heads 17.0 instead of
+// 26.5, 4/2 30.5 and 27.3, d 64 8/2 23.0 and 24.9), and calls of one pass over the grid, where the rings' start
+// counts (32/8 heads: 100 tokens 3.5 us instead of 4.5, 200 4.2 and 4.75, 400 5.5 and 5.2; one appended token 3.8
+// and 5.0, 200 5.5 and 6.2, 800 11.2 and 8.8).
+bool use_rows(const FwdParams& p, int d, bool append) {
+  const int64_t token = int64_t(p.hq + (append ? 2 : 1) * p.hkv) * d * 2;
+  return token <= (append ? 1536 : 2048) || token * p.n_rows <= (2 << 20);
+}
+
 // Two CTAs an SM, or one for every unit where there are fewer.
 int grid_of(int64_t units) {
   const int64_t most = kCtas * int64_t(num_sms());
@@ -933,6 +1052,13 @@ int grid_of(int64_t units) {
 
 template <int D, bool NORM, bool APPEND>
 int launch_fwd_as(const FwdParams& p, cudaStream_t st) {
+  if (use_rows(p, D, APPEND)) {
+    constexpr int rows = kRowThreads / Geo<D>::LPR;
+    const int64_t n = (p.n_rows * (p.hq + (APPEND ? 2 : 1) * p.hkv) + rows - 1) / rows, most = kRowCtas * int64_t(num_sms());
+    fwd_rows_kernel<D, NORM, APPEND><<<unsigned(n < most ? n : most), kRowThreads, 0, st>>>(p);
+    TPA_CUDA_TRY(cudaGetLastError());
+    return TPA_OK;
+  }
   using R = Ring<D, 4096>;
   const int per_token = p.sq + p.sk + p.sv;
   TPA_CUDA_TRY(cudaFuncSetAttribute(fwd_kernel<D, NORM, APPEND>, cudaFuncAttributeMaxDynamicSharedMemorySize, R::BYTES));

@@ -56,7 +56,8 @@ CASES = [  # q_lens, kv_lens, hq, hkv, d, page, extra rows
     ([1], [1], 1, 1, 64, 16, 0), ([1] * 9, [1, 16, 17, 33, 5, 100, 64, 65, 2], 32, 8, 128, 16, 3),
     ([5, 0, 1, 300, 0], [5, 40, 129, 300, 0], 8, 2, 128, 64, 10), ([70, 33], [170, 33], 10, 5, 64, 32, 0),
     ([1] * 100, list(range(1, 101)), 3, 1, 128, 128, 28), ([0, 0, 3], [0, 9, 3], 4, 4, 64, 16, 1),
-    ([257], [1000], 33, 11, 64, 128, 0)]
+    ([257], [1000], 33, 11, 64, 128, 0), ([500, 1, 90], [500, 700, 130], 16, 4, 128, 64, 5),
+    ([900], [900], 20, 20, 128, 16, 3), ([999, 1, 1], [999, 1, 30], 1, 1, 128, 32, 40)]
 
 
 @pytest.mark.parametrize("case", CASES)
@@ -78,11 +79,12 @@ def test_slices_of_a_fused_projection(tpa):
     _check(tpa, b, tpa.rope_table(10, 128), None, None)
 
 
-def test_bad_batches_are_reported_and_skipped(tpa):
+@pytest.mark.parametrize("hq,hkv,extra", [(4, 2, 0), (8, 4, 1100)])  # few bytes and many: other kernels
+def test_bad_batches_are_reported_and_skipped(tpa, hq, hkv, extra):
     table = tpa.rope_table(64, 64)
 
     def run(change, skipped, moved=()):
-        b = Batch([2, 3, 1], [20, 3, 33], 4, 2, 64, 16, seed=5)
+        b = Batch([2, 3, 1], [20, 3, 33], hq, hkv, 64, 16, seed=5, extra=extra)
         good = b.k_cache.clone(), b.v_cache.clone()
         want = tpa.paged_append(*good, b.pages, b.offsets, b.kv_lens, b.k, b.v, q=b.q, table=table)
         page, slot = b.slots()
@@ -93,7 +95,7 @@ def test_bad_batches_are_reported_and_skipped(tpa):
             tpa.sync_status()
         tpa.sync_status()
         keep = [i for i in range(6) if i not in skipped and i not in moved]
-        assert torch.equal(got[keep], want[keep]) and (got[sorted(skipped)] == 7.0).all()
+        assert torch.equal(got[keep], want[keep]) and (got[sorted(skipped)] == 7.0).all() and (got[6:] == 7.0).all()
         for c, w in zip((b.k_cache, b.v_cache), good):
             assert torch.equal(c[page, :, slot][keep], w[page, :, slot][keep])
 
@@ -125,10 +127,11 @@ def test_positions_past_the_table(tpa):
     assert torch.equal(before, b.k_cache)
 
 
-def test_unordered_offsets_end_and_stay_inside(tpa):
+@pytest.mark.parametrize("hq,hkv,extra", [(4, 2, 0), (8, 4, 1100)])
+def test_unordered_offsets_end_and_stay_inside(tpa, hq, hkv, extra):
     # no promise but that nothing outside the tensors is touched and the call is reported or skipped
     for off in ([0, 5, 2, 6], [3, 3, 3, 3], [0, 2, 5, 1000], [-7, 2, 5, 6], [6, 5, 2, 0], [0, 2 ** 31 - 1, -2 ** 31, 6]):
-        b = Batch([2, 3, 1], [20, 3, 33], 4, 2, 64, 16, seed=5)
+        b = Batch([2, 3, 1], [20, 3, 33], hq, hkv, 64, 16, seed=5, extra=extra)
         b.offsets.copy_(torch.tensor(off, dtype=torch.int32))
         bk, kc = guarded(b.k_cache.shape, torch.bfloat16)
         bv, vc = guarded(b.v_cache.shape, torch.bfloat16)

@@ -56,7 +56,11 @@ CASES = [  # rows, hq, hkv, d, rot, interleaved, weights, fused
     (7, 3, 1, 128, 128, True, "bf16", False), (33, 5, 5, 64, 32, False, "bf16", True),
     (100, 17, 1, 128, 64, True, None, True), (257, 9, 3, 128, 16, False, "f32", False),
     (64, 4, 4, 64, 16, True, None, False), (1025, 40, 8, 64, 48, False, "f32", True),
-    (300, 33, 33, 128, 112, False, "f32", True)]
+    (300, 33, 33, 128, 112, False, "f32", True), (1500, 16, 4, 128, 128, False, "f32", True),
+    (2500, 12, 12, 64, 32, True, "bf16", False), (5000, 2, 1, 128, 128, False, "f32", True)]
+
+# Calls of few bytes and of many take other kernels
+SIZES = [(50, 4, 2, 64), (700, 16, 4, 128)]
 
 
 def _weights(kind, w):
@@ -150,8 +154,9 @@ def test_table(tpa):
         assert ((got - ref).abs() <= 2.0 ** -24 * ref.abs() + 8 * n * 2.0 ** -52).all()
 
 
-def test_padding_may_hold_anything(tpa):
-    q, k, pos, (wq, wk) = _inputs(50, 4, 2, 64, 3)
+@pytest.mark.parametrize("rows,hq,hkv,d", SIZES)
+def test_padding_may_hold_anything(tpa, rows, hq, hkv, d):
+    q, k, pos, (wq, wk) = _inputs(rows, hq, hkv, d, 3)
     pos[10:20] = -1
     clean = tpa.qk_norm_rope_fwd(pos.cuda(), q, k, (table := tpa.rope_table(500, 64)), wq, wk)
     g = [torch.randn(x.shape, device="cuda") for x in (q, k)]
@@ -165,18 +170,20 @@ def test_padding_may_hold_anything(tpa):
     assert all(torch.equal(a, b) for a, b in zip((*clean, *gclean), (*dirty, *gdirty)))
 
 
-def test_infinite_value_beside_the_rotation(tpa):
+@pytest.mark.parametrize("rows,heads", [(2, 1), (900, 20)])
+def test_infinite_value_beside_the_rotation(tpa, rows, heads):
     # without a norm a value that is not turned passes as it is, its neighbours too
-    q = torch.ones((2, 1, 64), dtype=torch.bfloat16, device="cuda")
+    q = torch.ones((rows, heads, 64), dtype=torch.bfloat16, device="cuda")
     q[:, :, 33] = float("inf")
-    pos = torch.tensor([3, 4], dtype=torch.int32, device="cuda")
+    pos = torch.arange(rows, dtype=torch.int32, device="cuda") % 8
     table = tpa.rope_table(8, 32)
     got, _ = tpa.qk_norm_rope_fwd(pos, q, q.clone(), table)
     assert torch.equal(got[..., 32:], q[..., 32:])
 
 
-def test_position_past_the_table(tpa):
-    q, k, pos, (wq, wk) = _inputs(9, 4, 2, 64, 4)
+@pytest.mark.parametrize("rows,hq,hkv,d", [(9, 4, 2, 64), (700, 16, 4, 128)])
+def test_position_past_the_table(tpa, rows, hq, hkv, d):
+    q, k, pos, (wq, wk) = _inputs(rows, hq, hkv, d, 4)
     pos = pos.clamp(min=0)
     table = tpa.rope_table(500, 64)
     want = tpa.qk_norm_rope_fwd(pos.cuda(), q, k, table, wq, wk)
@@ -186,7 +193,7 @@ def test_position_past_the_table(tpa):
     with pytest.raises(tpa.TpaError, match="INVALID_ARG"):
         tpa.sync_status()
     tpa.sync_status()
-    keep = [i for i in range(9) if i not in (3, 5)]
+    keep = [i for i in range(rows) if i not in (3, 5)]
     for a, b in zip(got, want):
         assert torch.equal(a[keep], b[keep]) and (a[[3, 5]] == 0).all()
     got = tpa.qk_norm_rope_bwd(bad.cuda(), *want, q, k, table, wq, wk)
@@ -195,12 +202,13 @@ def test_position_past_the_table(tpa):
     assert (got[0][[3, 5]] == 0).all() and all(torch.isfinite(x).all() for x in got)
 
 
-def test_in_place_and_strided_outputs(tpa):
-    q, k, pos, (wq, wk) = _inputs(70, 8, 2, 128, 6, fused=True)
+@pytest.mark.parametrize("rows", [70, 1100])
+def test_in_place_and_strided_outputs(tpa, rows):
+    q, k, pos, (wq, wk) = _inputs(rows, 8, 2, 128, 6, fused=True)
     pos, table = pos.cuda(), tpa.rope_table(500, 128)
     want = tpa.qk_norm_rope_fwd(pos, q, k, table, wq, wk)
-    fresh = torch.zeros((70, 12 * 128), dtype=torch.bfloat16, device="cuda")
-    views = fresh[:, :1024].view(70, 8, 128), fresh[:, 1024:1280].view(70, 2, 128)
+    fresh = torch.zeros((rows, 12 * 128), dtype=torch.bfloat16, device="cuda")
+    views = fresh[:, :1024].view(rows, 8, 128), fresh[:, 1024:1280].view(rows, 2, 128)
     tpa.qk_norm_rope_fwd(pos, q, k, table, wq, wk, out=views)
     assert all(torch.equal(a, b) for a, b in zip(views, want)) and (fresh[:, 1280:] == 0).all()
     gw = tpa.qk_norm_rope_bwd(pos, *want, q, k, table, wq, wk)
@@ -211,19 +219,31 @@ def test_in_place_and_strided_outputs(tpa):
     assert torch.equal(q, want[0]) and torch.equal(k, want[1])
 
 
-def test_rows_far_apart(tpa):
+@pytest.mark.parametrize("hq,hkv", [(2, 1), (400, 20)])
+def test_rows_far_apart(tpa, hq, hkv):
     # byte offsets past 2^32: 5 GB between the first row and the last
     rows, stride = 40, 1 << 26
     flat = torch.empty(rows * stride, dtype=torch.bfloat16, device="cuda")
-    q = flat.as_strided((rows, 2, 64), (stride, 64, 1))
-    k = flat[256:].as_strided((rows, 1, 64), (stride, 64, 1))
-    src, ksrc, pos, (wq, wk) = _inputs(rows, 2, 1, 64, 8)
+    q = flat.as_strided((rows, hq, 64), (stride, 64, 1))
+    k = flat[64 * hq:].as_strided((rows, hkv, 64), (stride, 64, 1))
+    src, ksrc, pos, (wq, wk) = _inputs(rows, hq, hkv, 64, 8)
     q.copy_(src)
     k.copy_(ksrc)
     table = tpa.rope_table(500, 64)
     want = tpa.qk_norm_rope_fwd(pos.cuda(), src, ksrc, table, wq, wk)
     got = tpa.qk_norm_rope_fwd(pos.cuda(), q, k, table, wq, wk, out=(q, k))
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("hq,hkv,d,norm", [(32, 8, 128, True), (12, 6, 64, False)])
+def test_the_same_in_one_call_and_in_many(tpa, hq, hkv, d, norm):
+    q, k, pos, (wq, wk) = _inputs(1300, hq, hkv, d, 12, fused=True)
+    pos, table = pos.cuda(), tpa.rope_table(500, d)
+    w = (wq, wk) if norm else (None, None)
+    want = tpa.qk_norm_rope_fwd(pos, q, k, table, *w)
+    parts = [tpa.qk_norm_rope_fwd(pos[i:i + 37], q[i:i + 37], k[i:i + 37], table, *w) for i in range(0, 1300, 37)]
+    assert all(torch.equal(torch.cat(x), y) for x, y in zip(zip(*parts), want))
+    tpa.sync_status()
 
 
 def test_no_rows(tpa):
