@@ -13,7 +13,9 @@
 // then do not depend on registers, and what a unit costs in instructions beside
 // its arithmetic is spent once for seven of them.  Units are dealt one to each
 // warp of the grid in turn: at any time the grid reads one run of memory, and
-// padding, which costs less, is spread evenly.
+// padding, which costs less, is spread evenly.  Small calls, and tokens of so few
+// heads that units would be small, go row by row straight from memory instead
+// (fwd_rows_kernel, bwd_rows_kernel; the choice is use_rows()'s).
 //
 // A row of d values is held by d / 16 lanes, each with two 16-byte pieces whose
 // pairs of the rotation are both in the lane: pieces l and l + rot/16 where
@@ -782,6 +784,156 @@ __device__ __forceinline__ void store16(uint8_t* row, int pa, int pb, const Vals
   }
 }
 
+// Where in a row the first value of a lane's packed pair j is (0..3: firsts, 4..7: seconds); the other is 1 further, or
+// 2 where neighbours are paired.
+__device__ __forceinline__ int weight_at(int j, int l, int pa, int pb, bool inter) {
+  const int i = 2 * (j & 3), second = j >> 2;
+  return inter ? 16 * l + 2 * i + second : 8 * (second ? pb : pa) + i;
+}
+
+// The gradient of a row, in z from that of its result: R(p)^T first, then with y = r z w: dw += (r z) x (`add`),
+// dx = y - x (r^2 mean(y x)).
+template <int D, bool NORM, class Add>
+__device__ __forceinline__ void grad_row(Vals& z, const Vals& x, const uint64_t (&c)[4], const uint64_t (&sn)[4],
+                                         const Vals& w, bool turns, bool live, float eps, Add add) {
+  if (turns) {
+    const Vals g = z;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      z.a[j] = fma2(g.a[j], c[j], mul2(g.b[j], sn[j]));
+      z.b[j] = fma2(g.b[j], c[j], neg2(mul2(g.a[j], sn[j])));
+    }
+  }
+  if constexpr (NORM) {
+    const float rs = rstd<D>(x, eps);
+    const uint64_t r2 = live ? f2(rs, rs) : 0;  // eps may be 0, and rs of a row of zeros infinite
+    uint64_t dot[2] = {0, 0};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      z.a[j] = mul2(z.a[j], r2);
+      z.b[j] = mul2(z.b[j], r2);
+    }
+    add(z, x);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      z.a[j] = mul2(z.a[j], w.a[j]);
+      z.b[j] = mul2(z.b[j], w.b[j]);
+      dot[0] = fma2(z.a[j], x.a[j], dot[0]);
+      dot[1] = fma2(z.b[j], x.b[j], dot[1]);
+    }
+    const float m = row_sum<Geo<D>::LPR>(sum2(add2(dot[0], dot[1]))) * (-1.f / D) * (live ? rs * rs : 0.f);
+    const uint64_t m2 = f2(m, m);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      z.a[j] = fma2(x.a[j], m2, z.a[j]);
+      z.b[j] = fma2(x.b[j], m2, z.b[j]);
+    }
+  }
+}
+
+// Row by row, as fwd_rows_kernel; a lane holds the sums of both weights.
+constexpr int kBwdRowCtas = 2;
+
+template <int D, bool NORM, bool GIN32, bool GOUT32>
+__global__ void __launch_bounds__(kRowThreads, kBwdRowCtas) bwd_rows_kernel(const BwdParams p) {
+  using G = Geo<D>;
+  constexpr int GB = GIN32 ? 4 : 2, OB = GOUT32 ? 4 : 2, ROWS = kRowThreads / G::LPR;
+  __shared__ __align__(16) float w_s[NORM ? 2 * D : 4];
+  __shared__ float sum_s[NORM ? kRowThreads / 32 : 1][2 * D];
+  if constexpr (NORM) {
+    stage_weights<D>(p.rope, w_s);
+    __syncthreads();
+  }
+  const int l = threadIdx.x % G::LPR, sub = threadIdx.x / G::LPR, heads = p.hq + p.hkv;
+  const bool inter = p.rope.interleaved != 0, turns = l < (p.rope.rot >> 4);
+  int pa, pb;
+  pieces<D>(l, p.rope.rot, inter, pa, pb);
+  const int64_t base = int64_t(blockIdx.x) * ROWS, step = int64_t(gridDim.x) * ROWS;
+  int64_t tok0 = base / heads;
+  const int64_t d_tok = step / heads;
+  int h0 = int(base - tok0 * heads);
+  const int d_h = int(step - d_tok * heads);
+  Vals acc[2];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) acc[0].a[j] = acc[0].b[j] = acc[1].a[j] = acc[1].b[j] = 0;
+  for (; tok0 < p.n_rows; tok0 += d_tok) {
+    const unsigned at = unsigned(h0 + sub), over = at / unsigned(heads);
+    const int64_t tok = tok0 + over;
+    const int head = int(at - over * unsigned(heads)), kind = head < p.hq ? 0 : 1, h = kind ? head - p.hq : head;
+    int pos = 0, state = kSkip;
+    if (tok < p.n_rows) plain_place(p.positions, p.n_tokens, p.t_pad, p.rope.table_rows, int(tok), pos, state);
+    const bool live = state == kUse;
+    Vals z, x, w;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) z.a[j] = z.b[j] = x.a[j] = x.b[j] = 0;
+    uint64_t c[4], sn[4];
+    if (live) {
+      const Rows& g = kind ? p.gk : p.gq;
+      z = load16<GIN32>(g.p + tok * g.stride + int64_t(h) * (D * GB), pa, pb, inter);
+      if constexpr (NORM) {
+        const Rows& src = kind ? p.k : p.q;
+        x = load16<false>(src.p + tok * src.stride + int64_t(h) * (D * 2), pa, pb, inter);
+      }
+    }
+    if (turns) {
+      const float* row = p.rope.table + int64_t(live ? pos : 0) * p.rope.rot + 8 * l;
+      load_p4(row, c);
+      load_p4(row + (p.rope.rot >> 1), sn);
+    }
+    if constexpr (NORM) {
+      load_p4(w_s + kind * D + 16 * l, w.a);
+      load_p4(w_s + kind * D + 16 * l + 8, w.b);
+    }
+    grad_row<D, NORM>(z, x, c, sn, w, turns, live, p.rope.eps, [&](const Vals& zx, const Vals& x_) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint64_t a = mul2(zx.a[j], x_.a[j]), b = mul2(zx.b[j], x_.b[j]);
+        acc[0].a[j] = add2(acc[0].a[j], kind == 0 ? a : 0);
+        acc[0].b[j] = add2(acc[0].b[j], kind == 0 ? b : 0);
+        acc[1].a[j] = add2(acc[1].a[j], kind == 1 ? a : 0);
+        acc[1].b[j] = add2(acc[1].b[j], kind == 1 ? b : 0);
+      }
+    });
+    if (state != kSkip) {
+      const RowsOut& o = kind ? p.dk : p.dq;
+      store16<GOUT32>(o.p + tok * o.stride + int64_t(h) * (D * OB), pa, pb, z, inter, p.wide);
+    }
+    h0 += d_h;
+    if (h0 >= heads) {
+      h0 -= heads;
+      ++tok0;
+    }
+  }
+  if constexpr (NORM) {
+    // rows of the warp, then warps of the CTA, in a fixed order
+#pragma unroll
+    for (int kind = 0; kind < 2; ++kind)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float lo, hi;
+        unf2(j < 4 ? acc[kind].a[j] : acc[kind].b[j - 4], lo, hi);
+#pragma unroll
+        for (int o_ = G::LPR; o_ < 32; o_ <<= 1) {
+          lo += __shfl_xor_sync(0xffffffffu, lo, o_);
+          hi += __shfl_xor_sync(0xffffffffu, hi, o_);
+        }
+        if ((threadIdx.x & 31) < G::LPR) {
+          const int at = weight_at(j, l, pa, pb, inter);
+          sum_s[threadIdx.x >> 5][kind * D + at] = lo;
+          sum_s[threadIdx.x >> 5][kind * D + at + (inter ? 2 : 1)] = hi;
+        }
+      }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * D; i += kRowThreads) {
+      float t = 0.f;
+#pragma unroll
+      for (int j = 0; j < kRowThreads / 32; ++j) t += sum_s[j][i];
+      p.partial[int64_t(blockIdx.x) * 2 * D + i] = t;
+    }
+  }
+  tc::grid_launch_dependents();
+}
+
 // Units of 2 KB of x and as many gradients (2 or 4 KB).  A warp takes queries
 // or keys, not both, so that it holds one weight's sums (16 registers); the
 // warps are divided as the units are.
@@ -875,42 +1027,19 @@ __global__ void __launch_bounds__(kThreads, kCtas) bwd_kernel(const BwdParams p)
       for (int j = 0; j < 4; ++j) z.a[j] = z.b[j] = 0;
       if (u.state == kUse) {
         if (live) z = load16<GIN32>(st + r * (D * GB), pa, pb, inter);
-        if (turns) {
-          const Vals g = z;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            z.a[j] = fma2(g.a[j], c[j], mul2(g.b[j], sn[j]));
-            z.b[j] = fma2(g.b[j], c[j], neg2(mul2(g.a[j], sn[j])));
-          }
-        }
+        Vals x;
         if constexpr (NORM) {
-          // with y = r z w:  dw += (r z) x,  dx = y - x (r^2 mean(y x))
-          Vals x;
 #pragma unroll
           for (int j = 0; j < 4; ++j) x.a[j] = x.b[j] = 0;
           if (live) x = load16<false>(st + XOFF + r * (D * 2), pa, pb, inter);
-          const float rs = rstd<D>(x, p.rope.eps);
-          const uint64_t r2 = live ? f2(rs, rs) : 0;  // eps may be 0, and rs of a row of zeros infinite
-          uint64_t dot[2] = {0, 0};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            z.a[j] = mul2(z.a[j], r2);
-            z.b[j] = mul2(z.b[j], r2);
-            acc.a[j] = fma2(z.a[j], x.a[j], acc.a[j]);
-            acc.b[j] = fma2(z.b[j], x.b[j], acc.b[j]);
-            z.a[j] = mul2(z.a[j], w.a[j]);
-            z.b[j] = mul2(z.b[j], w.b[j]);
-            dot[0] = fma2(z.a[j], x.a[j], dot[0]);
-            dot[1] = fma2(z.b[j], x.b[j], dot[1]);
-          }
-          const float m = row_sum<G::LPR>(sum2(add2(dot[0], dot[1]))) * (-1.f / D) * rs * rs;
-          const uint64_t m2 = f2(m, m);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            z.a[j] = fma2(x.a[j], m2, z.a[j]);
-            z.b[j] = fma2(x.b[j], m2, z.b[j]);
-          }
         }
+        grad_row<D, NORM>(z, x, c, sn, w, turns, live, p.rope.eps, [&](const Vals& zx, const Vals& x_) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            acc.a[j] = fma2(zx.a[j], x_.a[j], acc.a[j]);
+            acc.b[j] = fma2(zx.b[j], x_.b[j], acc.b[j]);
+          }
+        });
       }
       if (live) store16<GOUT32>(out + r * (D * OB), pa, pb, z, inter, p.wide);
     }
@@ -930,9 +1059,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) bwd_kernel(const BwdParams p)
         hi += __shfl_xor_sync(0xffffffffu, hi, o_);
       }
       if (sub == 0) {
-        // pair 2 (j % 4) and the next one, firsts or seconds
-        const int i = 2 * (j & 3), second = j >> 2;
-        const int at = inter ? 16 * l + 2 * i + second : 8 * (second ? pb : pa) + i;
+        const int at = weight_at(j, l, pa, pb, inter);
         mine_s[at] = lo;
         mine_s[at + (inter ? 2 : 1)] = hi;
       }
@@ -1072,15 +1199,30 @@ int launch_fwd(const FwdParams& p, bool norm, cudaStream_t st) {
   return norm ? launch_fwd_as<D, true, APPEND>(p, st) : launch_fwd_as<D, false, APPEND>(p, st);
 }
 
+// As use_rows(): 16384 rows, bf16 gradients: d 128 2/1 heads 17.7 us instead of 23.3, 4/2 28.2 and 23.7, d 64 4/2 16.2
+// instead of 22.6, 8/2 22.8 both; 32/8 heads: 100 rows 5.5 us instead of 7.0, 200 7.05 and 7.7, 400 8.8 and 8.3.
+bool use_bwd_rows(const BwdParams& p, int d) {
+  const int64_t token = int64_t(p.hq + p.hkv) * d * 2;
+  return token <= 1024 || token * p.n_rows <= (2 << 20);
+}
+
 template <int D, bool NORM, bool GIN32, bool GOUT32>
 int launch_bwd_as(const BwdParams& p, float* dwq, float* dwk, cudaStream_t st) {
   constexpr int UROWS = 2048 / (D * 2);
   using R = Ring<D, UROWS * D * (GIN32 ? 4 : 2) + 2048>;
   const int64_t units = p.n_rows * ((p.hq + UROWS - 1) / UROWS + (p.hkv + UROWS - 1) / UROWS);
-  const int grid = grid_of(units);
-  TPA_CUDA_TRY(cudaFuncSetAttribute(bwd_kernel<D, NORM, GIN32, GOUT32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    R::BYTES));
-  bwd_kernel<D, NORM, GIN32, GOUT32><<<grid, kThreads, R::BYTES, st>>>(p);
+  int grid = grid_of(units);
+  if (use_bwd_rows(p, D)) {
+    constexpr int rows = kRowThreads / Geo<D>::LPR;
+    const int64_t n = (p.n_rows * (p.hq + p.hkv) + rows - 1) / rows, most = kBwdRowCtas * int64_t(num_sms());
+    grid = int(n < 1 ? 1 : n < most ? n : most);
+    if (grid > kBwdMaxGrid) grid = kBwdMaxGrid;
+    bwd_rows_kernel<D, NORM, GIN32, GOUT32><<<grid, kRowThreads, 0, st>>>(p);
+  } else {
+    TPA_CUDA_TRY(cudaFuncSetAttribute(bwd_kernel<D, NORM, GIN32, GOUT32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      R::BYTES));
+    bwd_kernel<D, NORM, GIN32, GOUT32><<<grid, kThreads, R::BYTES, st>>>(p);
+  }
   TPA_CUDA_TRY(cudaGetLastError());
   if (!NORM) return TPA_OK;
   cudaLaunchConfig_t cfg = {};
