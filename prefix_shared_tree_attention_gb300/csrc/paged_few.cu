@@ -89,8 +89,8 @@ __device__ __forceinline__ bool group_any(int h, bool v) {
 }
 __device__ __forceinline__ void group_sync(int h) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(2 + h) : "memory"); }
 
-// For NR values a lane, reduced over the warp: the lane ends with the results
-// of rows owner .. owner + NR/32 - 1 (at least one row; several lanes then hold the same).
+// NR <= 32 values a lane, reduced over the warp: the lane ends with the result of
+// the row that owned_row names, in v[0] (with 16 rows, two lanes hold each).
 // Halves the rows with each exchange, so NR + 5 exchanges in place of 5 NR.
 template <int NR, class Op>
 __device__ __forceinline__ void warp_reduce_rows(float (&v)[NR], int lane, Op op) {
@@ -111,7 +111,7 @@ __device__ __forceinline__ void warp_reduce_rows(float (&v)[NR], int lane, Op op
     }
   }
 }
-// The first row that a lane holds after warp_reduce_rows.
+// The row that a lane holds after warp_reduce_rows.
 template <int NR>
 __device__ __forceinline__ int owned_row(int lane) {
   int n = NR, r = 0;
@@ -126,19 +126,9 @@ __device__ __forceinline__ int owned_row(int lane) {
 
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[N]) {
-  static_assert(N == 8 || N == 16 || N == 32 || N == 64, "columns");
-  if constexpr (N == 8) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(at));
-  } else if constexpr (N == 16) {
-    tc::tmem_ld16(at, r);
-  } else if constexpr (N == 32) {
-    tc::tmem_ld32(at, r);
-  } else {
-    tc::tmem_ld32(at, *reinterpret_cast<uint32_t(*)[32]>(r));
-    tc::tmem_ld32(at + 32, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
-  }
+  static_assert(N == 16 || N == 32, "columns");
+  if constexpr (N == 16) tc::tmem_ld16(at, r);
+  else tc::tmem_ld32(at, r);
 }
 
 template <int D, int NR>
@@ -474,10 +464,7 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
           for (int i = 0; i < NR; ++i) v[i] = x[i];
           warp_reduce_rows<NR>(v, lane, [](float a, float b) { return fmaxf(a, b); });
-          constexpr int OWN = NR > 32 ? NR / 32 : 1;
-          const int row = owned_row<NR>(lane);
-#pragma unroll
-          for (int i = 0; i < OWN; ++i) warp_s[(warp & 3) * NR + row + i] = v[i];
+          warp_s[(warp & 3) * NR + owned_row<NR>(lane)] = v[0];
           group_sync(h);
           if (r < NR) {
             const float before = j == j0 ? kNoMax : m_s[r];
@@ -527,10 +514,7 @@ __global__ void __launch_bounds__(512, 1)
       if (fine) {
         float* xm = xm_s + (k & 1) * 2 * NR + h * NR;
         float* xl = xl_s + (k & 1) * 8 * NR + (h * 4 + (warp & 3)) * NR;
-        constexpr int OWN = NR > 32 ? NR / 32 : 1;
-        const int own = owned_row<NR>(lane);
-#pragma unroll
-        for (int i = 0; i < OWN; ++i) xl[own + i] = l[i];
+        xl[owned_row<NR>(lane)] = l[0];
         if (r < NR) xm[r] = j0 < n_it ? m_s[r] : kNoMax;  // (a warpgroup without a step has no maxima)
       }
       tc::mbar_arrive(ml_full + (k & 1));
