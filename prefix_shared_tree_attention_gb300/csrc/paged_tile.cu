@@ -61,8 +61,8 @@ struct TileCfg {
   static constexpr uint32_t OFF_SEG = OFF_SCAN + 160;
   static constexpr uint32_t OFF_BAR = OFF_SEG + 128;
   // q_full, q_empty, k_full[NS], k_empty[NS], v_full[NS], v_empty[NS], s_full[NH], p_full[2 NH], o_free[NH],
-  // o_final, drain, seg_full[2], seg_empty[2]
-  static constexpr int NBAR = 2 + 4 * NS + 4 * NH + 2 + 4;
+  // o_final[NH], drain, seg_full[2], seg_empty[2]
+  static constexpr int NBAR = 2 + 4 * NS + 5 * NH + 1 + 4;
   static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr uint32_t BYTES = OFF_MISC + 16 + 1024;
   // Registers move from the producer/issuer warpgroup to the
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
   uint64_t* p_full = s_full + NH;  // [part][sub-tile]
   uint64_t* o_free = p_full + 2 * NH;
   uint64_t* o_final = o_free + NH;
-  uint64_t* drain = o_final + 1;
+  uint64_t* drain = o_final + NH;
   uint64_t* seg_full = drain + 1;   // [2]
   uint64_t* seg_empty = drain + 3;  // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
@@ -127,8 +127,8 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
       tc::mbar_init(p_full + h, 128);
       tc::mbar_init(p_full + NH + h, 128);
       tc::mbar_init(o_free + h, 128);
+      tc::mbar_init(o_final + h, 1);
     }
-    tc::mbar_init(o_final, 1);
     tc::mbar_init(drain, 1);
     for (int s = 0; s < 2; ++s) {
       tc::mbar_init(seg_full + s, 1);
@@ -272,6 +272,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
               }
               if (!ok) break;
               ++uses[h];
+              if (!more) tc::mma_commit(o_final + h);
               if (more) {
                 if (h == 0 && !(ok = wait1(k_full + s1, ((g + 1) / NS) & 1))) break;
                 tc::tc_fence_after();
@@ -285,7 +286,6 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
               if (j + 2 == n_it) tc::mma_commit(q_empty);  // the segment's last S was just issued
             }
           }
-          if (ok) tc::mma_commit(o_final);
           t += n_it;
         }
         if (*abort_flag) {  // let issued MMAs finish before TMEM is released
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
     auto wait_all = [&](uint64_t* b_, uint32_t par) {
       return __all_sync(0xffffffffu, tc::mbar_wait(b_, par, abort_flag, &g_status_ptile));
     };
-    int tb = 0, uses = 0;  // steps so far, and of them this sub-tile's
+    int tb = 0, uses = 0, segs = 0;  // steps so far, of them this sub-tile's, and its segments
     bool ok = true;
     for (int k = 0; ok; ++k) {
       if (!wait_all(seg_full + (k & 1), (k >> 1) & 1)) break;
@@ -319,10 +319,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
       const int slot = sg->whole ? -1 : sg->slot, head = sg->head * p.b.group + gh, pos_first = sg->pos0;
       tc::mbar_arrive(seg_empty + (k & 1));
       if (n_it < 0) break;
-      if (h * sub_tok >= n_tok) {
-        // Nothing in this sub-tile.  The segment's end is waited for all the same: the stages' barriers are then
-        // never more than one phase ahead of what this warpgroup has seen.
-        if (!wait_all(o_final, k & 1)) break;
+      if (h * sub_tok >= n_tok) {  // nothing in this sub-tile
         tb += n_it;
         continue;
       }
@@ -334,9 +331,13 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
       float m_run = -INFINITY, l_run = 0.f;
       for (int j = 0; j < n_it; ++j) {
         const int key0 = key_first + j * kStep;
+        if (!wait_all(s_full + h, uses & 1)) { ok = false; break; }
+        ++uses;
         if (key0 < lo || key0 + kStep > end) {
           // Slots that no row sees may hold anything: zero their values, so that 0 x NaN does not come in.  (Those from
-          // the last key that this tile sees to the sequence's end are loaded, and finite: other rows see them.)
+          // the last key that this tile sees to the sequence's end are loaded, and finite: other rows see them.)  This S was
+          // issued behind waits for the V of all steps before, so the stage's last V has landed and this wait can only
+          // end with this step's.
           const int g = tb + j, sv_ = g % NS;
           if (!wait_all(v_full + sv_, (g / NS) & 1)) { ok = false; break; }
           const int head_rows = min(max(lo - key0, 0), kStep), live_rows = min(max(end - key0, 0), kStep);
@@ -348,8 +349,6 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
           }
           tc::fence_proxy_async_smem();
         }
-        if (!wait_all(s_full + h, uses & 1)) { ok = false; break; }
-        ++uses;
         tc::tc_fence_after();
         uint32_t sv[128];
 #pragma unroll
@@ -428,7 +427,8 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         unf2(add2(add2(sum2[0], sum2[1]), add2(sum2[2], sum2[3])), s_lo, s_hi);
         l_run = l_run * alpha + (s_lo + s_hi);
       }
-      if (!ok || !wait_all(o_final, k & 1)) { ok = false; break; }
+      if (!ok || !wait_all(o_final + h, segs & 1)) { ok = false; break; }
+      ++segs;
       tc::tc_fence_after();
       const float inv = slot < 0 ? (l_run > 0.f ? 1.f / l_run : 0.f) : 1.f;
       const int64_t row = int64_t(first + tok) * p.hq + head;
@@ -465,15 +465,16 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         }
       };
       if (slot < 0) {
+        uint32_t ov[D];
+#pragma unroll
+        for (int c = 0; c < D; c += 32) tc::tmem_ld32(tO + c, *reinterpret_cast<uint32_t(*)[32]>(ov + c));
+        loaded(true);
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
-          uint32_t ov[64], w[32];
-          tc::tmem_ld32(tO + c * 64, *reinterpret_cast<uint32_t(*)[32]>(ov));
-          tc::tmem_ld32(tO + c * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(ov + 32));
-          loaded(c == D / 64 - 1);
+          uint32_t w[32];
 #pragma unroll
           for (int x = 0; x < 32; ++x)
-            w[x] = tc::pack_bf16(__uint_as_float(ov[2 * x]) * inv, __uint_as_float(ov[2 * x + 1]) * inv);
+            w[x] = tc::pack_bf16(__uint_as_float(ov[64 * c + 2 * x]) * inv, __uint_as_float(ov[64 * c + 2 * x + 1]) * inv);
           write_piece(c, w);
         }
       } else {
