@@ -72,8 +72,9 @@ struct TileCfg {
   static_assert(REG_HIGH * 256 + REG_LOW * 128 <= REG_LAUNCH * 384, "register split");
   static constexpr uint32_t TMEM_COLS = 512;
   // P is handed over in this many parts, so that its product can begin while the rest is formed.  Two shorten the way
-  // from scores to scores where it is what the MMAs wait for: 4001 tokens at d 64 495 -> 451 us.  At d 128, with twice
-  // the MMA work in the same softmax, they cost 1 to 2 % (8 chunks of 512: 160.5 -> 162.5 us).
+  // from scores to scores where it is what the MMAs wait for: 4001 tokens at d 64 495 -> 450 us (now 461, since the
+  // sub-tiles' ends are apart).  At d 128, with twice the MMA work in the same softmax, they cost 1 to 2 % (8 chunks
+  // of 512: 160.5 -> 162.5 us).
   static constexpr int PARTS = D == 64 ? 2 : 1;
   static_assert(sizeof(Scan) <= 160 && sizeof(Segment) * 2 <= 128 && NS >= 2, "layout");
   static_assert(BYTES <= kSmemMax, "shared memory budget");
@@ -436,7 +437,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
       // The rows leave through shared memory, 128 bytes of each at a time and a warp's rows by itself, so that a store
       // covers four whole lines.  Straight from the registers, where each of a store's 32 pieces is in a line of its
       // own, a tile's end took 5500 cycles (10000 for a part in fp32), two to three steps' time: 8 chunks of 512 tokens
-      // 160.5 us, so 148.5.
+      // 160.5 us, so 148.5 (now 135).
       uint8_t* const to = slot < 0 ? reinterpret_cast<uint8_t*>(p.o) : reinterpret_cast<uint8_t*>(p.part_o);
       const int64_t mine = live ? (slot < 0 ? row * (D * 2) : prow * (D * 4)) : -1;
       int64_t at[8];  // of rows 4 i + lane / 8
