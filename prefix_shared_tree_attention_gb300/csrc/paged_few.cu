@@ -469,9 +469,12 @@ __global__ void __launch_bounds__(512, 1)
           if (r < NR) {
             const float before = j == j0 ? kNoMax : m_s[r];
             const float top = fmaxf(fmaxf(warp_s[r], warp_s[NR + r]), fmaxf(warp_s[2 * NR + r], warp_s[3 * NR + r]));
-            const float m = fmaxf(before, top);
+            // Rows behind the tile's own (the load brings the next sequence's queries, or padding) never pass an infinite
+            // maximum, so they have no say in when the others' are moved: a row's bits are its sequence's alone.
+            const bool live = r < n_tok * p.b.group;
+            const float m = live ? fmaxf(before, top) : INFINITY;
             m_s[r] = m;
-            alpha_s[r] = tc::ex2(before - m);
+            alpha_s[r] = live ? tc::ex2(before - m) : 1.f;
           }
           group_sync(h);
           if (j != j0) {
