@@ -45,13 +45,14 @@ struct Seq {
   int first, n, kv;  // first row, new tokens, cached tokens
 };
 
-// A sequence whose numbers are out of range has no tokens (and is reported).
+// A sequence whose numbers are out of range has no tokens (and is reported); so are rows before the first sequence.
 __device__ __forceinline__ Seq load_seq(const Batch& b, int s, unsigned int* status) {
   const int o0 = __ldg(b.offsets + s), o1 = __ldg(b.offsets + s + 1), kv = __ldg(b.kv_lens + s);
   if (o0 < 0 || o1 < o0 || o1 > b.n_rows || kv < 0 || kv > (int64_t(b.max_pages) << b.page_shift)) {
     if (status) atomicOr(status, TPA_DEV_BAD_INPUT);
     return Seq{0, 0, 0};
   }
+  if (status && s == 0 && o0 != 0) atomicOr(status, TPA_DEV_BAD_INPUT);
   return Seq{o0, o1 - o0, kv};
 }
 

@@ -1,9 +1,11 @@
 """Batches over a paged cache: a sequence's results are its own whatever stands
-in the rows beside it."""
+in the rows beside it, and every batch that breaks its description is reported."""
 import pytest
 import torch
 
+from oracle.paged import attend_sequence
 from _paged import Batch
+from _pipeline import check_guards, guarded
 
 pytestmark = pytest.mark.gpu
 
@@ -53,3 +55,41 @@ def test_queries_of_other_rows_do_not_matter(tpa, q_len, hq, hkv, d, window):
         b.q[middle, :, 0] = fill
         assert all(torch.equal(x[others], y[others]) for x, y in zip(want, run())), fill
     tpa.sync_status()
+
+
+# offsets and lengths of three sequences in six rows (and padding behind them), and which sequences they leave as they are
+BROKEN = [([0, 5, 2, 6], [20, 3, 33], ()), ([3, 3, 3, 3], [20, 3, 33], ()), ([0, 2, 5, 5000], [20, 3, 33], (0, 1)),
+          ([-7, 2, 5, 6], [20, 3, 33], (1, 2)), ([6, 5, 2, 0], [20, 3, 33], ()),
+          ([0, 2 ** 31 - 1, -2 ** 31, 6], [20, 3, 33], ()), ([0, 5, 2, 2], [20, 3, 33], ()),
+          ([1, 2, 5, 6], [20, 3, 33], (1, 2)), ([0, 5, 5000, 5000], [20, 5000, 33], ()), ([0, 2, 5, 5], [20, 3, -1], (0, 1)),
+          ([0, 2, 2, 3], [20, 1000, 33], (0,)), ([0, 2, 2, 3], [20, -2 ** 31, 33], (0,))]
+
+
+def _broken(off, lens, hq, hkv, extra):
+    b = Batch([2, 3, 1], [20, 3, 33], hq, hkv, 64, 16, seed=5, extra=extra)
+    b.offsets.copy_(torch.tensor(off, dtype=torch.int32))
+    b.kv_lens.copy_(torch.tensor(lens, dtype=torch.int32))
+    return b
+
+
+def _reported(tpa):
+    with pytest.raises(tpa.TpaError, match="INVALID_ARG"):
+        tpa.sync_status()
+    tpa.sync_status()
+
+
+@pytest.mark.parametrize("off,lens,good", BROKEN)
+@pytest.mark.parametrize("max_q", [3, 200])  # the one kernel and the other
+def test_broken_batches_are_reported_by_the_attention(tpa, off, lens, good, max_q):
+    b = _broken(off, lens, 4, 2, 0)
+    bo, o = guarded(b.q.shape, torch.bfloat16)
+    bl, lse = guarded(b.q.shape[:2], torch.float32)
+    tpa.paged_attn_fwd(*b.cache, b.q, max_q_len=max_q, out=o, lse=lse)
+    _reported(tpa)
+    check_guards(bo, "o")
+    check_guards(bl, "lse")
+    for s in good:
+        rows = slice(off[s], off[s + 1])
+        ref, _, size = attend_sequence(b.q[rows].cpu(), b.sequence(s, b.k_cache), b.sequence(s, b.v_cache))
+        # as in test_gpu_paged_attn.py: bf16 probabilities, fp32 scores and sums, a bf16 result
+        assert ((o[rows].double().cpu() - ref).abs() <= (2.0 ** -8 + 2.0 ** -14) * size + 2.0 ** -8 * ref.abs()).all(), s
