@@ -450,8 +450,8 @@ __device__ __forceinline__ void paged_place(const FwdParams& p, int tok, int& po
   const int first = __ldg(c.offsets + s), last = __ldg(c.offsets + s + 1), kv = __ldg(c.kv_lens + s);
   // in 64 bits: nothing here is known to be in range yet
   const int64_t at = int64_t(kv) - last + tok;
-  bool ok = first >= 0 && tok >= first && at >= 0 && at < int64_t(c.max_pages) * c.page_size &&
-            (!p.rope.table || at < p.rope.table_rows);
+  bool ok = first >= 0 && tok >= first && tok < last && last <= p.n_rows && at >= 0 &&
+            at < int64_t(c.max_pages) * c.page_size && (!p.rope.table || at < p.rope.table_rows);
   if (ok) {
     const int page = __ldg(c.pages + int64_t(s) * c.page_stride + int(at) / c.page_size);
     ok = page >= 0 && page < c.n_pages;
@@ -462,6 +462,30 @@ __device__ __forceinline__ void paged_place(const FwdParams& p, int tok, int& po
     state = kUse;
   else
     atomicOr(&g_status_rope, TPA_DEV_BAD_INPUT);
+}
+
+// Append: the numbers of sequence s, the attention's conditions on them.  The tokens' own look-ups do not meet all: a
+// search of offsets out of order may pass over them, and a sequence without new tokens is nobody's.
+struct SeqNumbers {
+  int32_t o0 = 0, o1 = 0, kv = 0;
+  __device__ __forceinline__ void load(const tpa_paged_view& c, int64_t s) {
+    o0 = __ldg(c.offsets + s);
+    o1 = __ldg(c.offsets + s + 1);
+    kv = __ldg(c.kv_lens + s);
+  }
+  __device__ __forceinline__ void check(const FwdParams& p, int64_t s) const {
+    if (o0 < 0 || o1 < o0 || o1 > p.n_rows || (s == 0 && o0 != 0) || kv < 0 ||
+        kv > int64_t(p.cache.max_pages) * p.cache.page_size)
+      atomicOr(&g_status_rope, TPA_DEV_BAD_INPUT);
+  }
+};
+// Sequences s, s + step, ... of the batch.
+__device__ __forceinline__ void check_seqs(const FwdParams& p, int64_t s, int64_t step) {
+  for (; s < p.cache.n_seqs; s += step) {
+    SeqNumbers q;
+    q.load(p.cache, s);
+    q.check(p, s);
+  }
 }
 
 template <int D, bool NORM, bool APPEND>
@@ -553,6 +577,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) fwd_kernel(const FwdParams p)
   }
   if constexpr (NORM) stage_weights<D>(p.rope, w_s);
   ready_wait();
+  // beside the first units' way here
+  if constexpr (APPEND) check_seqs(p, int64_t(blockIdx.x) * (32 * kWarps) + threadIdx.x, int64_t(gridDim.x) * (32 * kWarps));
 
   const int l = lane % G::LPR, sub = lane / G::LPR;
   const bool inter = p.rope.interleaved != 0, turns = l < (p.rope.rot >> 4);
@@ -626,6 +652,10 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas) fwd_rows_kernel(const F
   using G = Geo<D>;
   constexpr int ROWS = kRowThreads / G::LPR;  // of a CTA at a time
   __shared__ __align__(16) float w_s[2 * D];
+  // one sequence a thread is loaded here and looked at behind the rows, which do not wait for it
+  const int64_t seq = int64_t(blockIdx.x) * kRowThreads + threadIdx.x;
+  SeqNumbers numbers;
+  if (APPEND && seq < p.cache.n_seqs) numbers.load(p.cache, seq);
   if constexpr (NORM) {
     stage_weights<D>(p.rope, w_s);
     __syncthreads();
@@ -702,6 +732,10 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas) fwd_rows_kernel(const F
       h0 -= heads;
       ++tok0;
     }
+  }
+  if constexpr (APPEND) {
+    if (seq < p.cache.n_seqs) numbers.check(p, seq);
+    check_seqs(p, seq + int64_t(gridDim.x) * kRowThreads, int64_t(gridDim.x) * kRowThreads);
   }
 }
 

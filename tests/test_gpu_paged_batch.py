@@ -1,5 +1,6 @@
 """Batches over a paged cache: a sequence's results are its own whatever stands
-in the rows beside it, and every batch that breaks its description is reported."""
+in the rows beside it, and every batch that breaks its description is reported
+by the append and by the attention alike."""
 import pytest
 import torch
 
@@ -93,3 +94,30 @@ def test_broken_batches_are_reported_by_the_attention(tpa, off, lens, good, max_
         ref, _, size = attend_sequence(b.q[rows].cpu(), b.sequence(s, b.k_cache), b.sequence(s, b.v_cache))
         # as in test_gpu_paged_attn.py: bf16 probabilities, fp32 scores and sums, a bf16 result
         assert ((o[rows].double().cpu() - ref).abs() <= (2.0 ** -8 + 2.0 ** -14) * size + 2.0 ** -8 * ref.abs()).all(), s
+
+
+@pytest.mark.parametrize("off,lens,good", BROKEN)
+@pytest.mark.parametrize("hq,hkv,extra", [(4, 2, 0), (8, 4, 1100)])  # few bytes and many: other kernels
+def test_broken_batches_are_reported_by_the_append(tpa, off, lens, good, hq, hkv, extra):
+    b = _broken(off, lens, hq, hkv, extra)
+    before = b.k_cache.clone(), b.v_cache.clone()
+    bq, qo = guarded(b.q.shape, torch.bfloat16)
+    tpa.paged_append(*b.cache, b.k, b.v, q=b.q, q_out=qo)
+    _reported(tpa)
+    check_guards(bq, "q_out")
+    # what is written is the value of some row, in a slot that a sequence's own length reaches
+    reach = torch.zeros((b.n_pages, b.page), dtype=torch.bool)
+    for s, n in enumerate(lens):
+        for j in range(max(0, min(n, len(b.rows[s]) * b.page))):
+            if b.rows[s][j // b.page] >= 0:
+                reach[b.rows[s][j // b.page], j % b.page] = True
+    for old, new in zip(before, (b.k_cache, b.v_cache)):
+        moved = (old != new).any(-1).any(1).cpu()
+        assert not (moved & ~reach).any()
+    for s in good:
+        pos = torch.arange(lens[s] - (off[s + 1] - off[s]), lens[s])
+        page = torch.tensor(b.rows[s])[pos // b.page]
+        rows = slice(off[s], off[s + 1])
+        assert torch.equal(b.k_cache.cpu()[page, :, pos % b.page], b.k[rows].cpu()), s
+        assert torch.equal(b.v_cache.cpu()[page, :, pos % b.page], b.v[rows].cpu()), s
+        assert torch.equal(qo[rows], b.q[rows]), s
