@@ -571,13 +571,14 @@ int tpa_qk_norm_rope_bwd(const int32_t* positions, const int32_t* n_tokens, int3
  *   offsets [n_seqs + 1] int32, non-decreasing from 0: the new tokens of
  *     sequence s are rows [offsets[s], offsets[s+1]) of the call's tensors
  *     (a sequence may have none); rows from offsets[n_seqs] on are padding,
- *     neither used nor written,
+ *     neither used nor written.  n_seqs = 0 with n_rows = 0 is no work (pages
+ *     and kv_lens may then be NULL, max_pages and max_q_len 0),
  *   kv_lens [n_seqs] int32: tokens of sequence s in the cache, the new ones
  *     (its last) included,
  * all in device memory and read by the kernels, so a captured call can be
  * replayed after they change.  Values out of range (a page outside
- * [0, n_pages), more tokens than max_pages hold, an offset out of order or
- * above the call's rows) are reported by tpa_sync_status
+ * [0, n_pages) that is needed, more tokens than max_pages hold, an offset out of
+ * order, above the call's rows or, the first, not 0) are reported by tpa_sync_status
  * (TPA_ERR_INVALID_ARG); nothing outside the tensors is read or written.    */
 /* ------------------------------------------------------------------------ */
 

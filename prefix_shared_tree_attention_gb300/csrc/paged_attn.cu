@@ -218,8 +218,8 @@ extern "C" int tpa_paged_attn_fwd(const tpa_paged_view* cache, const void* q, in
   const int rc = tpa_internal_check_paged(cache);
   if (rc != TPA_OK) return rc;
   const int d = cache->head_dim, hkv = cache->n_heads_kv;
-  if (n_heads_q < 1 || n_heads_q > 65535 || n_heads_q % hkv || n_heads_q / hkv > 64 || max_q_len < 1 || window < 0 ||
-      std::isnan(softmax_scale) || std::isinf(softmax_scale))
+  if (n_heads_q < 1 || n_heads_q > 65535 || n_heads_q % hkv || n_heads_q / hkv > 64 || window < 0 ||
+      max_q_len < (cache->n_rows ? 1 : 0) || std::isnan(softmax_scale) || std::isinf(softmax_scale))
     return TPA_ERR_INVALID_ARG;
   if (cache->n_rows == 0) return TPA_OK;
   auto al = [](const void* x, uintptr_t a) { return (reinterpret_cast<uintptr_t>(x) & (a - 1)) == 0; };

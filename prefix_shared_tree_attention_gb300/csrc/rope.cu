@@ -1403,12 +1403,15 @@ extern "C" int tpa_qk_norm_rope_bwd(const int32_t* positions, const int32_t* n_t
 }
 
 int tpa_internal_check_paged(const tpa_paged_view* c) {
-  if (!c || !c->k_cache || !c->v_cache || !c->pages || !c->offsets || !c->kv_lens) return TPA_ERR_INVALID_ARG;
+  if (!c || !c->k_cache || !c->v_cache || !c->offsets) return TPA_ERR_INVALID_ARG;
   if (!aligned16(c->k_cache) || !aligned16(c->v_cache)) return TPA_ERR_INVALID_ARG;
   if (c->head_dim != 64 && c->head_dim != 128) return TPA_ERR_INVALID_ARG;
   if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
     return TPA_ERR_INVALID_ARG;
-  if (c->n_pages < 1 || c->n_seqs < 1 || c->max_pages < 1 || c->page_stride < c->max_pages || c->n_rows < 0 ||
+  // a batch of no sequences has no rows; its arrays of one entry a sequence may be anything
+  const bool none = c->n_seqs == 0 && c->n_rows == 0;
+  if (!none && (c->n_seqs < 1 || !c->pages || !c->kv_lens)) return TPA_ERR_INVALID_ARG;
+  if (c->n_pages < 1 || c->max_pages < (none ? 0 : 1) || c->page_stride < c->max_pages || c->n_rows < 0 ||
       c->n_rows >= (1 << 30) || c->n_heads_kv < 1 || c->n_heads_kv > 65535)
     return TPA_ERR_INVALID_ARG;
   if (int64_t(c->n_pages) * c->n_heads_kv >= (int64_t(1) << 31) / c->page_size) return TPA_ERR_INVALID_ARG;

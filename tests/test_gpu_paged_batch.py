@@ -1,6 +1,6 @@
 """Batches over a paged cache: a sequence's results are its own whatever stands
-in the rows beside it, and every batch that breaks its description is reported
-by the append and by the attention alike."""
+in the rows beside it, every batch that breaks its description is reported by
+the append and by the attention alike, and a batch without sequences is no work."""
 import pytest
 import torch
 
@@ -121,3 +121,14 @@ def test_broken_batches_are_reported_by_the_append(tpa, off, lens, good, hq, hkv
         assert torch.equal(b.k_cache.cpu()[page, :, pos % b.page], b.k[rows].cpu()), s
         assert torch.equal(b.v_cache.cpu()[page, :, pos % b.page], b.v[rows].cpu()), s
         assert torch.equal(qo[rows], b.q[rows]), s
+
+
+def test_a_batch_without_sequences(tpa):
+    b = Batch([1], [5], 4, 2, 64, 16, seed=1)
+    none = dict(pages=b.pages[:0], offsets=b.offsets[:1], kv_lens=b.kv_lens[:0])
+    q = tpa.paged_append(b.k_cache, b.v_cache, **none, k=b.k[:0], v=b.v[:0], q=b.q[:0])
+    assert q.shape == (0, 4, 64)
+    for max_q in (0, 1, 100):
+        o, lse = tpa.paged_attn_fwd(b.k_cache, b.v_cache, **none, q=q, max_q_len=max_q)
+        assert o.shape == (0, 4, 64) and lse.shape == (0, 4)
+    tpa.sync_status()

@@ -1,0 +1,53 @@
+"""Calls of the policy's operators that have to be refused, or taken as no
+work, before anything is launched (CPU)."""
+import ctypes as C
+
+import pytest
+
+P = 4096  # an aligned address that no such call follows
+
+
+@pytest.fixture(scope="module")
+def tpa():
+    import prefix_shared_tree_attention_gb300 as tpa
+    tpa.lib()
+    return tpa
+
+
+def _view(**kw):
+    from prefix_shared_tree_attention_gb300._abi import PagedView
+    v = PagedView()
+    v.k_cache = v.v_cache = v.pages = v.offsets = v.kv_lens = P
+    v.n_pages, v.page_size, v.n_seqs, v.max_pages, v.page_stride = 10, 16, 2, 4, 4
+    v.n_heads_kv, v.head_dim, v.n_rows = 2, 64, 0
+    for k, x in kw.items():
+        setattr(v, k, x)
+    return v
+
+
+NONE = [dict(n_seqs=0), dict(n_seqs=0, pages=None, kv_lens=None), dict(n_seqs=0, pages=None, kv_lens=None, max_pages=0, page_stride=0)]
+
+
+def _append(L, view):
+    from prefix_shared_tree_attention_gb300._abi import RopeParams
+    return L.tpa_paged_append(C.byref(view), None, 128, None, 128, None, 0, None, 0, 0, C.byref(RopeParams()), None)
+
+
+def _attend(L, view, max_q=1):
+    return L.tpa_paged_attn_fwd(C.byref(view), None, 256, None, None, 4, max_q, 0.0, 0, None, 0, None)
+
+
+@pytest.mark.parametrize("kw", NONE)
+def test_no_sequences_are_no_work(tpa, kw):
+    assert _append(tpa.lib(), _view(**kw)) == 0
+    assert _attend(tpa.lib(), _view(**kw)) == 0 and _attend(tpa.lib(), _view(**kw), max_q=0) == 0
+
+
+@pytest.mark.parametrize("kw", [dict(n_seqs=0, n_rows=1), dict(n_seqs=-1), dict(n_seqs=0, k_cache=None), dict(n_seqs=0, page_size=8),
+                                dict(n_seqs=0, offsets=None), dict(n_seqs=0, max_pages=-1), dict(max_pages=0), dict(pages=None)])
+def test_other_views_stay_refused(tpa, kw):
+    assert _append(tpa.lib(), _view(**kw)) == -1 and _attend(tpa.lib(), _view(**kw)) == -1
+
+
+def test_most_new_tokens_below_zero(tpa):
+    assert _attend(tpa.lib(), _view(), max_q=-1) == -1 and _attend(tpa.lib(), _view(n_rows=1), max_q=0) == -1
