@@ -387,6 +387,12 @@ def _new(stream, shape, dtype: torch.dtype, device) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _whole_workspace(workspace) -> None:
+    """A workspace's size is counted from its elements: each has to have memory of its own, behind the one before."""
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+
+
 def _head_rows(name: str, t: torch.Tensor, dtypes=(torch.bfloat16,)) -> tuple[int, int, int, int]:
     """(rows, row stride, heads, d) of a tensor [..., H, d] whose heads are
     contiguous and whose leading dimensions are evenly spaced rows."""
@@ -520,6 +526,7 @@ def qk_norm_rope_bwd(positions: "torch.Tensor | DeviceTree", dq_out: torch.Tenso
         if q is None or k is None or q.shape != dq_out.shape or k.shape != dk_out.shape:
             raise ValueError("q and k must be given with the weights, shaped like dq_out and dk_out")
         sq, sk = _head_rows("q", q)[1], _head_rows("k", k)[1]
+    _whole_workspace(workspace)
     dev = dq_out.device
     st = _launch_stream(stream, dq_out, dk_out, table, q_weight, k_weight, pbuf, workspace, *(out or ()),
                         *((q, k) if norm else ()))
@@ -623,6 +630,7 @@ def paged_attn_fwd(k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Te
     if q.dim() != 3:
         raise ValueError("q must be [tokens, Hq, d]")
     cache, hkv = _paged_view(k_cache, v_cache, pages, offsets, kv_lens, rows, None, d)
+    _whole_workspace(workspace)
     st = _launch_stream(stream, q, out, lse, workspace, k_cache, v_cache, pages, offsets, kv_lens)
     if out is None:
         o = _new(stream, q.shape, q.dtype, q.device)

@@ -3,6 +3,7 @@ work, before anything is launched (CPU)."""
 import ctypes as C
 
 import pytest
+import torch
 
 P = 4096  # an aligned address that no such call follows
 
@@ -51,3 +52,25 @@ def test_other_views_stay_refused(tpa, kw):
 
 def test_most_new_tokens_below_zero(tpa):
     assert _attend(tpa.lib(), _view(), max_q=-1) == -1 and _attend(tpa.lib(), _view(n_rows=1), max_q=0) == -1
+
+
+@pytest.fixture
+def call():
+    bf = torch.bfloat16
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    cache = torch.zeros((3, 2, 16, 64), dtype=bf)
+    return dict(k_cache=cache, v_cache=cache.clone(), pages=i32(2, 3), offsets=i32(3), kv_lens=i32(2),
+                q=torch.zeros((4, 4, 64), dtype=bf), max_q_len=2)
+
+
+def test_a_workspace_has_all_its_bytes(tpa, call):
+    # a broadcast byte has as many elements as are asked for, and memory for one
+    ws = torch.zeros(1, dtype=torch.uint8).expand(1 << 26)
+    with pytest.raises(ValueError, match="workspace"):
+        tpa.paged_attn_fwd(**call, workspace=ws)
+    with pytest.raises(ValueError, match="workspace"):
+        tpa.paged_attn_fwd(**call, workspace=torch.zeros(1 << 20, dtype=torch.uint8)[::2])
+    q, k = torch.zeros((4, 4, 64), dtype=torch.bfloat16), torch.zeros((4, 2, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="workspace"):
+        tpa.qk_norm_rope_bwd(torch.zeros(4, dtype=torch.int32), q, k, q, k, torch.zeros((8, 64)), torch.ones(64), torch.ones(64),
+                             workspace=ws)
