@@ -387,6 +387,14 @@ def _new(stream, shape, dtype: torch.dtype, device) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _int32(name: str, value) -> int:
+    """A whole number that the library takes in 32 bits (ctypes would cut off the others)."""
+    n = int(value)
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError(f"{name} must fit in 32 bits")
+    return n
+
+
 def _whole_workspace(workspace) -> None:
     """A workspace's size is counted from its elements: each has to have memory of its own, behind the one before."""
     if workspace is not None and not workspace.is_contiguous():
@@ -424,6 +432,7 @@ def rope_table(n_positions: int, rot_dim: int, base: float = 10000.0, inv_freq: 
     [n_positions, rot_dim], cos | sin, made once for a model.  ``inv_freq``
     gives the rot_dim / 2 frequencies in place of ``base`` ** (-2 j / rot_dim)."""
     fr = None
+    n_positions, rot_dim = _int32("n_positions", n_positions), _int32("rot_dim", rot_dim)
     if inv_freq is not None:
         if len(inv_freq) != rot_dim // 2:
             raise ValueError("inv_freq must hold rot_dim / 2 frequencies")
@@ -433,8 +442,8 @@ def rope_table(n_positions: int, rot_dim: int, base: float = 10000.0, inv_freq: 
     if out.dtype != torch.float32 or not out.is_contiguous() or tuple(out.shape) != (n_positions, rot_dim):
         raise ValueError("out must be a contiguous fp32 tensor [n_positions, rot_dim]")
     st = _launch_stream(stream, out)
-    check("tpa_rope_table", lib().tpa_rope_table(out.data_ptr(), int(n_positions), int(rot_dim), float(base), fr,
-                                                 float(scale), st))
+    check("tpa_rope_table", lib().tpa_rope_table(out.data_ptr(), n_positions, rot_dim, float(base), fr, float(scale),
+                                                 st))
     return out
 
 
@@ -612,7 +621,9 @@ def paged_append(k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Tens
 
 
 def paged_attn_workspace_bytes(max_q_len: int, n_heads_q: int, n_heads_kv: int, head_dim: int) -> int:
-    return int(lib().tpa_paged_attn_workspace_bytes(int(max_q_len), int(n_heads_q), int(n_heads_kv), int(head_dim)))
+    return int(lib().tpa_paged_attn_workspace_bytes(
+        _int32("max_q_len", max_q_len), _int32("n_heads_q", n_heads_q), _int32("n_heads_kv", n_heads_kv),
+        _int32("head_dim", head_dim)))
 
 
 def paged_attn_fwd(k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Tensor, offsets: torch.Tensor,
@@ -629,6 +640,10 @@ def paged_attn_fwd(k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Te
     rows, sq, Hq, d = _head_rows("q", q)
     if q.dim() != 3:
         raise ValueError("q must be [tokens, Hq, d]")
+    max_q_len, window = _int32("max_q_len", max_q_len), int(window)
+    if window < 0:
+        raise ValueError("window must not be negative")
+    window = min(window, 2 ** 31 - 1)  # longer than any sequence
     cache, hkv = _paged_view(k_cache, v_cache, pages, offsets, kv_lens, rows, None, d)
     _whole_workspace(workspace)
     st = _launch_stream(stream, q, out, lse, workspace, k_cache, v_cache, pages, offsets, kv_lens)
@@ -645,8 +660,8 @@ def paged_attn_fwd(k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Te
     if workspace is None:
         workspace = _new(stream, paged_attn_workspace_bytes(max_q_len, Hq, hkv, d), torch.uint8, q.device)
     check("tpa_paged_attn_fwd", lib().tpa_paged_attn_fwd(
-        cache, q.data_ptr(), sq, o.data_ptr(), lse.data_ptr(), Hq, int(max_q_len),
-        float(softmax_scale or 0.0), int(window), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        cache, q.data_ptr(), sq, o.data_ptr(), lse.data_ptr(), Hq, max_q_len,
+        float(softmax_scale or 0.0), window, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
         st))
     return o, lse
 
@@ -666,6 +681,8 @@ def verify_drafts(target_probs: torch.Tensor, draft_tokens: torch.Tensor, u_acce
         raise ValueError("target_probs must be [S, K+1, V] and draft_tokens [S, K]")
     S, K1, V = target_probs.shape
     K = K1 - 1
+    for name, n in (("the number of sequences", S), ("the number of drafts", K), ("the vocabulary", V)):
+        _int32(name, n)
     i32, f32 = torch.int32, torch.float32
     if draft_tokens.dtype != i32 or draft_tokens.shape != (S, K) or not draft_tokens.is_contiguous():
         raise ValueError("draft_tokens must be a contiguous int32 tensor [S, K]")

@@ -132,3 +132,13 @@ def test_a_batch_without_sequences(tpa):
         o, lse = tpa.paged_attn_fwd(b.k_cache, b.v_cache, **none, q=q, max_q_len=max_q)
         assert o.shape == (0, 4, 64) and lse.shape == (0, 4)
     tpa.sync_status()
+
+
+@pytest.mark.parametrize("q_len", [1, 150])
+def test_windows_past_32_bits(tpa, q_len):
+    b = Batch([q_len], [700], 4, 2, 64, 16, seed=1)
+    want = tpa.paged_attn_fwd(*b.cache, b.q, max_q_len=q_len)
+    for window in (2 ** 31, 2 ** 32 + 5, 2 ** 63):
+        got = tpa.paged_attn_fwd(*b.cache, b.q, max_q_len=q_len, window=window)
+        assert all(torch.equal(x, y) for x, y in zip(want, got)), window
+    tpa.sync_status()

@@ -74,3 +74,20 @@ def test_a_workspace_has_all_its_bytes(tpa, call):
     with pytest.raises(ValueError, match="workspace"):
         tpa.qk_norm_rope_bwd(torch.zeros(4, dtype=torch.int32), q, k, q, k, torch.zeros((8, 64)), torch.ones(64), torch.ones(64),
                              workspace=ws)
+
+
+def test_numbers_past_32_bits_are_not_cut(tpa, call):
+    for window in (-1, -2 ** 32 + 5, -2 ** 63):
+        with pytest.raises(ValueError, match="window"):
+            tpa.paged_attn_fwd(**call, window=window)
+    for most in (2 ** 31, 2 ** 32 + 1, -2 ** 32 + 1):
+        with pytest.raises(ValueError, match="max_q_len"):
+            tpa.paged_attn_fwd(**{**call, "max_q_len": most})
+        with pytest.raises(ValueError, match="max_q_len"):
+            tpa.paged_attn_workspace_bytes(most, 4, 2, 64)
+    with pytest.raises(ValueError, match="n_positions"):
+        tpa.rope_table(2 ** 32 + 1, 16, device="meta")
+    long = torch.zeros((1, 1, 1)).expand(2 ** 32 + 1, 1, 1)  # as many sequences, of one probability each
+    with pytest.raises(ValueError, match="sequences"):
+        tpa.verify_drafts(long, torch.zeros((1, 0), dtype=torch.int32).expand(2 ** 32 + 1, 0),
+                          torch.zeros((1, 0)).expand(2 ** 32 + 1, 0), torch.zeros(1).expand(2 ** 32 + 1))
