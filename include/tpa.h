@@ -655,8 +655,8 @@ int tpa_paged_attn_fwd(const tpa_paged_view* cache, const void* q, int64_t q_str
  * next token is the lowest v with  sum_{w <= v} r(w) > u_next * sum_w r(w),
  *   r = max(p_a - q_a, 0) when a < n_drafts (p_a where that leaves nothing),
  *   r = p_a               when a = n_drafts,
- * sums as pairs of fp32, good to 2^-44 of the whole, in a fixed order (should rounding leave none, the last v with
- * r(v) > 0; a row of zeros gives -1).
+ * sums as pairs of fp32, within 2^-41 + vocab 2^-56 of the whole, in a fixed order (should rounding leave none, the
+ * last v with r(v) > 0; a row of zeros gives -1; a row's sum has to be below the largest fp32).
  *   target [n_seqs, K+1, vocab] fp32: p_0 .. p_K; sequences target_stride and
  *     rows vocab elements apart; need not be normalised (entries >= 0 and
  *     finite; a negative or NaN entry counts as 0)

@@ -11,8 +11,11 @@
 //
 // A draw has to be the same whatever the order of summation, so sums are held
 // to far more than fp32: every weight and every sum is an unevaluated pair
-// hi + lo of fp32, formed by error-free additions (Knuth's and Dekker's), good
-// to about 2^-46 of the sum.  fp64 would do, but this GPU has so few of its units
+// hi + lo of fp32, formed by error-free additions (Knuth's and Dekker's).  With
+// u = 2^-24, an addition of two pairs is off by at most 3 u^2 of its result and
+// one of a run of 8 weights to a lane's pair (Sum) by 12 u^2, so that a draw's
+// sums are within 2^-41 + vocab 2^-56 of the row's (64 parts of 32 lanes with two pairs each;
+// some 30 additions between them).  fp64 would do, but this GPU has so few of its units
 // that the reductions alone took longer than the reads (part sums, prefix sums and the search in
 // fp64: 42 us for 64 sequences at vocabulary 151936).
 #include <cuda_runtime.h>
@@ -78,7 +81,9 @@ __device__ __forceinline__ bool operator>(const Pair& a, const Pair& b) {
   return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo);
 }
 
-// A running sum of weights; normalised when it is taken.
+// A running sum of weights.  The low halves are added up in plain fp32 and stay below 2 k + 1 units of u times the
+// sum for k weights behind the last tidy(), whose roundings then are off by k^2 + 4 k units of u^2 of it: 96 for a run
+// of 8.  Left to grow, they cost a row of 2^27 entries all but 2^-24.
 struct Sum {
   float hi = 0.f, lo = 0.f;
   __device__ __forceinline__ void add(float p, float q) {
@@ -88,7 +93,12 @@ struct Sum {
     hi = s.hi;
     lo = __fadd_rn(lo, __fadd_rn(s.lo, l));
   }
-  __device__ __forceinline__ Pair value() const { return normal(hi, lo); }
+  __device__ __forceinline__ void tidy() {
+    const Pair s = normal(hi, lo);
+    hi = s.hi;
+    lo = s.lo;
+  }
+  __device__ __forceinline__ Pair value() const { return Pair{hi, lo}; }
 };
 
 __device__ __forceinline__ Pair shfl_pair(const Pair& v, int from) {
@@ -156,6 +166,8 @@ __device__ __forceinline__ Pair part_sum(const Row& r, int i0, int i1, int lane)
         a.add(at == 2 ? 0.f : p[u].z, q[u].z);
         b.add(at == 3 ? 0.f : p[u].w, q[u].w);
       }
+      a.tidy();
+      b.tidy();
     }
   } else {
     constexpr int kU = 8;
@@ -169,6 +181,8 @@ __device__ __forceinline__ Pair part_sum(const Row& r, int i0, int i1, int lane)
       }
 #pragma unroll
       for (int u = 0; u < kU; ++u) (u & 1 ? b : a).add(p[u], q[u]);
+      a.tidy();
+      b.tidy();
     }
   }
   return warp_sum(a.value() + b.value());
