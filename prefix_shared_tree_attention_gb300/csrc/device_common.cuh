@@ -44,24 +44,16 @@ __device__ __forceinline__ bool dbg_ok(bool ok, unsigned int* status) {
     }                                             \
   } while (0)
 
-// Reads and optionally clears a device status word.  Must run after the
-// stream that may have written it has been synchronised.
+// Defines what tpa_sync_status reads a translation unit's status word by: its
+// address on the current device (NULL on an error).
 #define TPA_DEFINE_STATUS_READER(fn_name, symbol)                                  \
-  int fn_name(bool clear) {                                                        \
-    unsigned int v = 0;                                                            \
-    if (cudaMemcpyFromSymbol(&v, symbol, sizeof(v)) != cudaSuccess) {              \
+  unsigned int* fn_name() {                                                        \
+    void* at = nullptr;                                                            \
+    if (cudaGetSymbolAddress(&at, symbol) != cudaSuccess) {                        \
       (void)cudaGetLastError();                                                    \
-      return TPA_ERR_CUDA;                                                         \
+      return nullptr;                                                              \
     }                                                                              \
-    if (clear && v != 0) {                                                         \
-      const unsigned int z = 0;                                                    \
-      if (cudaMemcpyToSymbol(symbol, &z, sizeof(z)) != cudaSuccess) {              \
-        (void)cudaGetLastError();                                                  \
-        return TPA_ERR_CUDA;                                                       \
-      }                                                                            \
-    }                                                                              \
-    if (v & TPA_DEV_BAD_INPUT) return TPA_ERR_INVALID_ARG;                         \
-    return v == 0 ? TPA_OK : TPA_ERR_DEVICE_TIMEOUT;                               \
+    return static_cast<unsigned int*>(at);                                         \
   }
 
 __device__ __forceinline__ int warp_sum(int v) {

@@ -23,18 +23,17 @@ struct TpaNvtxRange {
 
 uint64_t tpa_internal_blob_bytes(const tpa_tree* tree);
 
-// Each CUDA translation unit keeps its own device status word; these read
-// (and clear) it.  They return TPA_OK, TPA_ERR_DEVICE_TIMEOUT, TPA_ERR_INVALID_ARG
-// (an input outside its range was skipped) or TPA_ERR_CUDA.
-int tpa_internal_status_classify(bool clear);
-int tpa_internal_status_logprobs(bool clear);
-int tpa_internal_status_fwd(bool clear);
-int tpa_internal_status_bwd(bool clear);
-int tpa_internal_status_lmh(bool clear);
-int tpa_internal_status_rope(bool clear);
-int tpa_internal_status_verify(bool clear);
-int tpa_internal_status_pfew(bool clear);
-int tpa_internal_status_ptile(bool clear);
+// Each CUDA translation unit keeps its own device status word (codes: device_common.cuh); these give its address on the
+// current device, NULL on an error.  tpa_sync_status reads and clears them together.
+unsigned int* tpa_internal_status_classify();
+unsigned int* tpa_internal_status_logprobs();
+unsigned int* tpa_internal_status_fwd();
+unsigned int* tpa_internal_status_bwd();
+unsigned int* tpa_internal_status_lmh();
+unsigned int* tpa_internal_status_rope();
+unsigned int* tpa_internal_status_verify();
+unsigned int* tpa_internal_status_pfew();
+unsigned int* tpa_internal_status_ptile();
 
 // The per-sequence gather of the log-prob pass (logprobs.cu), shared with
 // the fused LM-head path: seq_entropy[t] = pos_entropy[position of token t],

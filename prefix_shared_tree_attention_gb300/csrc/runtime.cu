@@ -3,6 +3,8 @@
 // kernel's device status word.
 #include <cuda_runtime.h>
 
+#include <mutex>
+
 #include "device_common.cuh"
 #include "internal.h"
 #include "tpa.h"
@@ -29,6 +31,18 @@ bool mask_layout(int32_t n_trees, int32_t t_pad, MaskLayout* L) {
   L->line_count = o; o = align256(o + 4 * B * 2 * n);
   L->total = o;
   return true;
+}
+
+// The translation units' status words are brought together by a kernel and read by one copy: a copy for each of the
+// nine took 84 us a call.  Both run on the legacy default stream.
+constexpr int kStatusWords = 9;
+struct StatusWords {
+  unsigned int* at[kStatusWords];
+};
+__device__ unsigned int g_gathered[kStatusWords];
+
+__global__ void gather_status_kernel(const StatusWords w) {
+  if (threadIdx.x < kStatusWords) g_gathered[threadIdx.x] = atomicExch(w.at[threadIdx.x], 0u);
 }
 }  // namespace
 
@@ -103,16 +117,22 @@ int tpa_sync_status(void* stream) {
     (void)cudaGetLastError();
     return TPA_ERR_CUDA;
   }
-  int worst = TPA_OK;
-  const int s[] = {tpa_internal_status_classify(true), tpa_internal_status_logprobs(true),
-                   tpa_internal_status_fwd(true), tpa_internal_status_bwd(true),
-                   tpa_internal_status_lmh(true), tpa_internal_status_rope(true),
-                   tpa_internal_status_verify(true), tpa_internal_status_pfew(true),
-                   tpa_internal_status_ptile(true)};
-  for (int x : s) {
-    if (x == TPA_ERR_CUDA) return TPA_ERR_CUDA;
-    if (x != TPA_OK) worst = x;
+  StatusWords w = {{tpa_internal_status_classify(), tpa_internal_status_logprobs(), tpa_internal_status_fwd(),
+                    tpa_internal_status_bwd(), tpa_internal_status_lmh(), tpa_internal_status_rope(),
+                    tpa_internal_status_verify(), tpa_internal_status_pfew(), tpa_internal_status_ptile()}};
+  for (unsigned int* at : w.at)
+    if (!at) return TPA_ERR_CUDA;
+  unsigned int v[kStatusWords] = {};
+  {
+    static std::mutex one_at_a_time;  // g_gathered is read before another thread's kernel writes it
+    const std::lock_guard<std::mutex> hold(one_at_a_time);
+    gather_status_kernel<<<1, 32>>>(w);
+    TPA_CUDA_TRY(cudaGetLastError());
+    TPA_CUDA_TRY(cudaMemcpyFromSymbol(v, g_gathered, sizeof(v)));
   }
+  int worst = TPA_OK;
+  for (unsigned int x : v)
+    if (x) worst = x & TPA_DEV_BAD_INPUT ? TPA_ERR_INVALID_ARG : TPA_ERR_DEVICE_TIMEOUT;
   return worst;
 }
 
