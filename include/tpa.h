@@ -45,7 +45,8 @@ enum tpa_status_code {
   TPA_ERR_CUDA = -5,               /* a CUDA runtime call or kernel launch failed */
   TPA_ERR_DEVICE_TIMEOUT = -6,     /* a kernel's bounded wait ran out (kernel returned early) */
   TPA_ERR_UNSUPPORTED_DEVICE = -7, /* current device is not compute capability 10.3 */
-  TPA_ERR_BUFFER_TOO_SMALL = -8    /* a caller buffer is smaller than required */
+  TPA_ERR_BUFFER_TOO_SMALL = -8,   /* a caller buffer is smaller than required */
+  TPA_ERR_BAD_BUILD = -9           /* a kernel was compiled with another number of registers than it divides up */
 };
 
 /* ------------------------------------------------------------------------ */
@@ -637,7 +638,7 @@ uint64_t tpa_paged_attn_workspace_bytes(int32_t max_q_len, int32_t n_heads_q, in
  * fp32 sums and statistics; probabilities are bf16 operands of the second
  * product.  Deterministic.  Two kernels on `stream`.  Errors:
  * TPA_ERR_INVALID_ARG, TPA_ERR_BUFFER_TOO_SMALL, TPA_ERR_UNSUPPORTED_DEVICE,
- * TPA_ERR_CUDA.
+ * TPA_ERR_BAD_BUILD, TPA_ERR_CUDA.
  */
 int tpa_paged_attn_fwd(const tpa_paged_view* cache, const void* q, int64_t q_stride, void* o, float* lse,
                        int32_t n_heads_q, int32_t max_q_len, float softmax_scale, int32_t window,

@@ -11,7 +11,7 @@ TPA_OK = 0
 STATUS = {
     0: "TPA_OK", -1: "TPA_ERR_INVALID_ARG", -2: "TPA_ERR_EMPTY_SEQUENCE", -3: "TPA_ERR_SEQ_TOO_LONG",
     -4: "TPA_ERR_NO_MEMORY", -5: "TPA_ERR_CUDA", -6: "TPA_ERR_DEVICE_TIMEOUT",
-    -7: "TPA_ERR_UNSUPPORTED_DEVICE", -8: "TPA_ERR_BUFFER_TOO_SMALL",
+    -7: "TPA_ERR_UNSUPPORTED_DEVICE", -8: "TPA_ERR_BUFFER_TOO_SMALL", -9: "TPA_ERR_BAD_BUILD",
 }
 BLOCK_SIZE = 128
 LOGITS_COMPACT, LOGITS_PADDED = 0, 1

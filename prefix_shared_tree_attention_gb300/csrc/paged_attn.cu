@@ -261,7 +261,6 @@ extern "C" int tpa_paged_attn_fwd(const tpa_paged_view* cache, const void* q, in
   const int grid = sms < kMaxGrid ? sms : kMaxGrid;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int rt = R == 256 ? tpa_internal_paged_tile(cache, p, grid, st) : tpa_internal_paged_few(cache, p, R, grid, st);
-  if (rt == kPagedUnfit) return TPA_ERR_CUDA;
   if (rt != TPA_OK) return rt;
   return d == 128 ? launch_join<128>(p, grid, rows, st) : launch_join<64>(p, grid, rows, st);
 }

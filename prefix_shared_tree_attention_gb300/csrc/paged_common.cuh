@@ -412,7 +412,7 @@ inline bool query_map(CUtensorMap* m, const tpa_paged_view* c, const Params& p, 
 
 // Launch the attention kernel (the caller joins split tiles afterwards): for
 // tiles of `rows` = 16 or 32 rows (paged_few.cu), and of 256 (paged_tile.cu).
-// Either may find that it was not compiled as it assumes; it then launches nothing.
-constexpr int kPagedUnfit = 1;
+// Either may find that it was not compiled with the registers that its warps
+// divide up; it then launches nothing (TPA_ERR_BAD_BUILD).
 int tpa_internal_paged_few(const tpa_paged_view* cache, paged::Params& p, int rows, int grid, cudaStream_t stream);
 int tpa_internal_paged_tile(const tpa_paged_view* cache, paged::Params& p, int grid, cudaStream_t stream);

@@ -630,7 +630,7 @@ int launch_few(const tpa_paged_view* c, Params& p, int grid, cudaStream_t st) {
   TPA_CUDA_TRY(cudaFuncSetAttribute(paged_few_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES));
   cudaFuncAttributes fa;
   TPA_CUDA_TRY(cudaFuncGetAttributes(&fa, paged_few_kernel<D, NR>));
-  if (fa.numRegs != C::REG_LAUNCH) return kPagedUnfit;  // the setmaxnreg split would not add up
+  if (fa.numRegs != C::REG_LAUNCH) return TPA_ERR_BAD_BUILD;  // the setmaxnreg split would not add up
   return launch_overlapped(paged_few_kernel<D, NR>, dim3(grid), C::THREADS, C::BYTES, st, tq, tk, tv,
                            static_cast<const Params>(p));
 }

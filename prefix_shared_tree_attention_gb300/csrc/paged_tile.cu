@@ -518,7 +518,7 @@ int launch_tile(const tpa_paged_view* c, Params& p, int grid, cudaStream_t st) {
   {
     cudaFuncAttributes fa;
     TPA_CUDA_TRY(cudaFuncGetAttributes(&fa, paged_tile_kernel<D>));
-    if (fa.numRegs != C::REG_LAUNCH) return kPagedUnfit;  // the setmaxnreg split would not add up
+    if (fa.numRegs != C::REG_LAUNCH) return TPA_ERR_BAD_BUILD;  // the setmaxnreg split would not add up
   }
   return launch_overlapped(paged_tile_kernel<D>, dim3(grid), C::THREADS, C::BYTES, st, tq, tk, tv,
                            static_cast<const Params>(p));

@@ -59,6 +59,7 @@ const char* tpa_status_string(int s) {
     case TPA_ERR_DEVICE_TIMEOUT: return "TPA_ERR_DEVICE_TIMEOUT";
     case TPA_ERR_UNSUPPORTED_DEVICE: return "TPA_ERR_UNSUPPORTED_DEVICE";
     case TPA_ERR_BUFFER_TOO_SMALL: return "TPA_ERR_BUFFER_TOO_SMALL";
+    case TPA_ERR_BAD_BUILD: return "TPA_ERR_BAD_BUILD";
     default: return "TPA_ERR_UNKNOWN";
   }
 }

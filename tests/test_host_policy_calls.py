@@ -91,3 +91,11 @@ def test_numbers_past_32_bits_are_not_cut(tpa, call):
     with pytest.raises(ValueError, match="sequences"):
         tpa.verify_drafts(long, torch.zeros((1, 0), dtype=torch.int32).expand(2 ** 32 + 1, 0),
                           torch.zeros((1, 0)).expand(2 ** 32 + 1, 0), torch.zeros(1).expand(2 ** 32 + 1))
+
+
+def test_a_build_that_does_not_fit_has_its_own_status(tpa):
+    from prefix_shared_tree_attention_gb300 import STATUS
+    assert STATUS[-9] == "TPA_ERR_BAD_BUILD"
+    f = tpa.lib().tpa_status_string
+    f.restype = C.c_char_p
+    assert f(-9) == b"TPA_ERR_BAD_BUILD"
