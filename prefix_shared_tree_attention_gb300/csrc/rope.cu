@@ -1197,11 +1197,12 @@ int num_sms() {
 // Row by row instead of through rings: tokens of few heads, whose units would be small (16384 of which 14000 real, d 128:
 // 2/1 heads 10.2 us instead of 22.1, 4/4 21.4 and 22.9, 8/8 38.5 and 29.6; 16000 appended: 2/1 heads 17.0 instead of
 // 26.5, 4/2 30.5 and 27.3, d 64 8/2 23.0 and 24.9), and calls of one pass over the grid, where the rings' start
-// counts (32/8 heads: 100 tokens 3.5 us instead of 4.5, 200 4.2 and 4.75, 400 5.5 and 5.2; one appended token 3.8
-// and 5.0, 200 5.5 and 6.2, 800 11.2 and 8.8).
+// counts (32/8 heads: 100 tokens 3.3 us instead of 4.3, 200 3.9 and 4.65, 300 4.5 and 4.85, 400 5.55 and 5.05; one
+// appended token 3.7 and 4.75, 200 5.3 and 5.9, 250 6.2 and 6.15, 400 8.15 and 6.4; 16/2 heads, 400 appended 5.45
+// and 6.1, 600 6.6 both, 800 8.2 and 7.3): up to 3 MB.
 bool use_rows(const FwdParams& p, int d, bool append) {
   const int64_t token = int64_t(p.hq + (append ? 2 : 1) * p.hkv) * d * 2;
-  return token <= (append ? 1536 : 2048) || token * p.n_rows <= (2 << 20);
+  return token <= (append ? 1536 : 2048) || token * p.n_rows <= (3 << 20);
 }
 
 // Two CTAs an SM, or one for every unit where there are fewer.
@@ -1233,8 +1234,11 @@ int launch_fwd(const FwdParams& p, bool norm, cudaStream_t st) {
   return norm ? launch_fwd_as<D, true, APPEND>(p, st) : launch_fwd_as<D, false, APPEND>(p, st);
 }
 
-// As use_rows(): 16384 rows, bf16 gradients: d 128 2/1 heads 17.7 us instead of 23.3, 4/2 28.2 and 23.7, d 64 4/2 16.2
-// instead of 22.6, 8/2 22.8 both; 32/8 heads: 100 rows 5.5 us instead of 7.0, 200 7.05 and 7.7, 400 8.8 and 8.3.
+// As use_rows(), by the values of a token and of the call whatever the gradients' type, since the borders are the same
+// (bf16 and fp32): 16384 rows, d 128 2/1 heads 13.9 us instead of 22.3 and 19.2 instead of 24.4, 4/2 27.5 (rings 23.5)
+// and 31.0 (28.0), d 64 4/2 12.7 instead of 21.4 and 17.7 instead of 23.0, 8/2 22.1 (22.4) and 26.2 (25.4); 32/8
+// heads: 100 rows 5.55 instead of 6.8 and 5.65 instead of 6.9, 200 7.2 (7.5) and 7.5 (7.6), 250 7.7 (7.65) and 8.0
+// (7.7), 400 8.7 (8.0) and 8.95 (8.45).  Beyond 2 MB of bf16 values rings.
 bool use_bwd_rows(const BwdParams& p, int d) {
   const int64_t token = int64_t(p.hq + p.hkv) * d * 2;
   return token <= 1024 || token * p.n_rows <= (2 << 20);

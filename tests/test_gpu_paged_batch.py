@@ -1,6 +1,7 @@
 """Batches over a paged cache: a sequence's results are its own whatever stands
 in the rows beside it, every batch that breaks its description is reported by
-the append and by the attention alike, and a batch without sequences is no work."""
+the append and by the attention alike, and a batch without sequences is no work.
+Sizes on both sides of the borders between kernels."""
 import pytest
 import torch
 
@@ -97,7 +98,7 @@ def test_broken_batches_are_reported_by_the_attention(tpa, off, lens, good, max_
 
 
 @pytest.mark.parametrize("off,lens,good", BROKEN)
-@pytest.mark.parametrize("hq,hkv,extra", [(4, 2, 0), (8, 4, 1100)])  # few bytes and many: other kernels
+@pytest.mark.parametrize("hq,hkv,extra", [(4, 2, 0), (8, 4, 4000)])  # few bytes and many: other kernels
 def test_broken_batches_are_reported_by_the_append(tpa, off, lens, good, hq, hkv, extra):
     b = _broken(off, lens, hq, hkv, extra)
     before = b.k_cache.clone(), b.v_cache.clone()
@@ -121,6 +122,48 @@ def test_broken_batches_are_reported_by_the_append(tpa, off, lens, good, hq, hkv
         assert torch.equal(b.k_cache.cpu()[page, :, pos % b.page], b.k[rows].cpu()), s
         assert torch.equal(b.v_cache.cpu()[page, :, pos % b.page], b.v[rows].cpu()), s
         assert torch.equal(qo[rows], b.q[rows]), s
+
+
+@pytest.mark.parametrize("extra", [0, 4000])
+def test_bad_pages_and_lengths_of_the_append(tpa, extra):
+    def run(change, skipped):
+        b = Batch([2, 3, 1], [20, 3, 33], 8, 4, 64, 16, seed=5, extra=extra)
+        good = b.k_cache.clone(), b.v_cache.clone()
+        want = tpa.paged_append(*good, b.pages, b.offsets, b.kv_lens, b.k, b.v, q=b.q)
+        page, slot = b.slots()
+        change(b)
+        got = torch.full_like(b.q, 7.0)
+        tpa.paged_append(*b.cache, b.k, b.v, q=b.q, q_out=got)
+        _reported(tpa)
+        keep = [i for i in range(6) if i not in skipped]
+        assert torch.equal(got[keep], want[keep]) and (got[list(skipped)] == 7.0).all() and (got[6:] == 7.0).all()
+        for c, w in zip((b.k_cache, b.v_cache), good):
+            assert torch.equal(c[page, :, slot][keep], w[page, :, slot][keep])
+
+    for value in (-1, 1000, 2 ** 31 - 1):
+        run(lambda b: b.pages[0].__setitem__(1, value), (0, 1))
+    for value in (-1, -2 ** 31):
+        run(lambda b: b.kv_lens.__setitem__(1, value), (2, 3, 4))
+    for value in (49, 2 ** 31 - 1):
+        run(lambda b: b.kv_lens.__setitem__(2, value), (5,))
+
+
+@pytest.mark.parametrize("rows", [70, 2000])
+def test_rotation_in_place_and_into_strided_rows(tpa, rows):
+    g = torch.Generator().manual_seed(6)
+    qkv = torch.randn((rows, 12 * 128), generator=g).to(torch.bfloat16).cuda()
+    q, k = qkv[:, :1024].view(rows, 8, 128), qkv[:, 1024:1280].view(rows, 2, 128)
+    w = [(1 + 0.3 * torch.randn(128, generator=g)).cuda() for _ in range(2)]
+    pos, table = torch.randint(-1, 500, (rows,), generator=g, dtype=torch.int32).cuda(), tpa.rope_table(500, 128)
+    want = tpa.qk_norm_rope_fwd(pos, q, k, table, *w)
+    fresh = torch.zeros_like(qkv)
+    views = fresh[:, :1024].view(rows, 8, 128), fresh[:, 1024:1280].view(rows, 2, 128)
+    tpa.qk_norm_rope_fwd(pos, q, k, table, *w, out=views)
+    assert all(torch.equal(a, b) for a, b in zip(views, want)) and (fresh[:, 1280:] == 0).all()
+    rest = qkv[:, 1280:].clone()
+    tpa.qk_norm_rope_fwd(pos, q, k, table, *w, out=(q, k))
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(qkv[:, 1280:], rest)
+    tpa.sync_status()
 
 
 def test_a_batch_without_sequences(tpa):
