@@ -234,7 +234,6 @@ extern "C" int tpa_paged_attn_fwd(const tpa_paged_view* cache, const void* q, in
   p.b.offsets = cache->offsets;
   p.b.kv_lens = cache->kv_lens;
   p.b.n_pages = cache->n_pages;
-  p.b.page_size = cache->page_size;
   p.b.page_shift = cache->page_size == 16 ? 4 : cache->page_size == 32 ? 5 : cache->page_size == 64 ? 6 : 7;
   p.b.n_seqs = cache->n_seqs;
   p.b.max_pages = cache->max_pages;

@@ -3,7 +3,7 @@
 // 128 keys are dealt to the CTAs, and the record of a tile whose steps went to
 // several CTAs.
 //
-// The steps (of 64 or 128 keys) of all tiles stand in one line, key/value head by head, sequence by
+// The steps of all tiles stand in one line, key/value head by head, sequence by
 // sequence, tile by tile, and CTA c of n takes the part [c T / n, (c + 1) T / n)
 // of its T steps: every CTA has the same work whatever the lengths, a long
 // sequence is split along its keys by as much as that needs, and a CTA has at
@@ -28,17 +28,17 @@ constexpr uint32_t kSmemMax = 232448;  // 227 KB opt-in per CTA
 constexpr int kMaxGrid = 160;  // CTAs of a launch, at most (one an SM)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kStepShift = 7, kStep = 1 << kStepShift;  // keys of a step
 constexpr float kRescale = 8.0f;  // log2 units: the running maximum is kept while the new one is not this much larger
 
 struct Batch {
   const int32_t* pages;
   const int32_t* offsets;
   const int32_t* kv_lens;
-  int32_t n_pages, page_size, page_shift, n_seqs, max_pages, page_stride, hkv, n_rows;
+  int32_t n_pages, page_shift, n_seqs, max_pages, page_stride, hkv, n_rows;
   int32_t group;     // query heads of a key/value head
   int32_t tile_tok;  // tokens of a tile
   int32_t window;    // 0: none
-  int32_t step_shift;  // a step is 1 << step_shift keys
 };
 
 struct Seq {
@@ -76,8 +76,8 @@ __device__ __forceinline__ Tile make_tile(const Batch& b, const Seq& q, int i) {
   t.hi = max(t.pos0 + t.n, 0);
   t.end = q.kv;
   t.lo = b.window > 0 ? max(t.pos0 - b.window + 1, 0) : 0;
-  t.step0 = t.lo >> b.step_shift;
-  t.steps = max(((t.hi + (1 << b.step_shift) - 1) >> b.step_shift) - t.step0, 1);
+  t.step0 = t.lo >> kStepShift;
+  t.steps = max(((t.hi + kStep - 1) >> kStepShift) - t.step0, 1);
   return t;
 }
 
@@ -168,7 +168,7 @@ __device__ inline Shares scan_batch(const Batch& b, Scan* sc, unsigned int* stat
           if (r >= 0 && r < steps) {
             // the page table's row is about to be read
             asm volatile("prefetch.global.L1 [%0];" ::"l"(b.pages + int64_t(s) * b.page_stride +
-                                                          min(((t.step0 + int(r)) << b.step_shift) >> b.page_shift, b.max_pages - 1)));
+                                                          min(((t.step0 + int(r)) << kStepShift) >> b.page_shift, b.max_pages - 1)));
             sc->t = t;
             sc->n_tiles = n;
             sc->item = f - r;
@@ -307,21 +307,21 @@ struct LoadRing {
   uint32_t par = 1;  // and the parity of its `empty`
 };
 
-// Loads steps [0, n_it) of a segment, KS keys each from key0 on, the pages that hold keys of [lo, hi) of them: a page
+// Loads steps [0, n_it) of a segment from key0 on, the pages that hold keys of [lo, hi) of them: a page
 // is a box for each 64 columns.  Unrolled for the number of pages of a step.  The entries of the page table come from
 // L1, a line of them fetched ahead.  False when a wait gave up.
-template <int KS, int NS, int NCH, class Wait>
+template <int NS, int NCH, class Wait>
 __device__ __forceinline__ bool load_steps(const Batch& b, LoadRing& ring, const CUtensorMap* tm, const int32_t* row,
                                            int head, int key0, int n_it, int lo, int hi, unsigned int* status, Wait wait1) {
   auto load_step = [&](int j, auto n_pages) {
     constexpr int N = decltype(n_pages)::value;
     int at[N];  // first cache row of each page that is needed
     uint32_t needed = 0;
-    const int first_page = (key0 + j * KS) >> b.page_shift;
+    const int first_page = (key0 + j * kStep) >> b.page_shift;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int ki = key0 + j * KS + i * (KS / N);
-      const bool need = ki < hi && ki + KS / N > lo;
+      const int ki = key0 + j * kStep + i * (kStep / N);
+      const bool need = ki < hi && ki + kStep / N > lo;
       at[i] = need ? __ldg(row + first_page + i) : 0;
       needed |= uint32_t(need) << i;
     }
@@ -331,17 +331,17 @@ __device__ __forceinline__ bool load_steps(const Batch& b, LoadRing& ring, const
         atomicOr(status, TPA_DEV_BAD_INPUT);
         at[i] = 0;
       }
-      at[i] = (at[i] * b.hkv + head) * (KS / N);
+      at[i] = (at[i] * b.hkv + head) * (kStep / N);
     }
     if (!wait1(ring.empty + ring.s, ring.par)) return false;
-    constexpr uint32_t kBytes = 128 * (KS / N);  // a 64-column piece of a page
+    constexpr uint32_t kBytes = 128 * (kStep / N);  // a 64-column piece of a page
     tc::mbar_arrive_expect_tx(ring.full + ring.s, __popc(needed) * NCH * kBytes);
 #pragma unroll
     for (int i = 0; i < N; ++i)
       if (needed >> i & 1)
 #pragma unroll
         for (int c = 0; c < NCH; ++c)
-          tma_load_2d(ring.tiles + ring.s * (NCH * KS * 128) + c * (KS * 128) + i * kBytes, tm, ring.full + ring.s, c * 64,
+          tma_load_2d(ring.tiles + ring.s * (NCH * kStep * 128) + c * (kStep * 128) + i * kBytes, tm, ring.full + ring.s, c * 64,
                       at[i]);
     if (first_page + 32 < b.max_pages) asm volatile("prefetch.global.L1 [%0];" ::"l"(row + first_page + 32));
     ++ring.t;
@@ -356,7 +356,7 @@ __device__ __forceinline__ bool load_steps(const Batch& b, LoadRing& ring, const
     for (int j = 0; ok && j < n_it; ++j) ok = load_step(j, n_pages);
     return ok;
   };
-  switch (KS >> b.page_shift) {
+  switch (kStep >> b.page_shift) {
     case 1: return all(std::integral_constant<int, 1>());
     case 2: return all(std::integral_constant<int, 2>());
     case 4: return all(std::integral_constant<int, 4>());

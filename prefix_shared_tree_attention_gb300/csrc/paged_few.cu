@@ -36,8 +36,7 @@ __device__ unsigned int g_status_pfew = 0;
 
 using namespace paged;
 
-constexpr int KS = 128;                  // keys of a step
-constexpr uint32_t kChunk = KS * 128;    // bytes of a 64-column piece of a step's keys or values
+constexpr uint32_t kChunk = kStep * 128;    // bytes of a 64-column piece of a step's keys or values
 constexpr float kNoMax = -1.0e30f;       // running maximum (log2 units) of a row that has seen nothing
 
 template <int D, int NR>
@@ -45,7 +44,7 @@ struct FewCfg {
   static constexpr int NCH = D / 64;
   static constexpr uint32_t TILE = NCH * kChunk;       // keys or values of a step
   static constexpr uint32_t QCH = NR * 128;            // a 64-column piece of the queries
-  static constexpr uint32_t PT = NR * KS * 2;          // P^T of a warpgroup: NR rows of two 64-key pieces
+  static constexpr uint32_t PT = NR * kStep * 2;          // P^T of a warpgroup: NR rows of two 64-key pieces
   static constexpr uint32_t FIXED = NCH * QCH + 2 * PT + 160 + 192 + NR * 136 + 1024;
   static constexpr int NS_FIT = int((kSmemMax - 1024 - FIXED) / (2 * TILE));
   static constexpr int NS = NS_FIT > 6 ? 6 : NS_FIT;
@@ -237,7 +236,7 @@ __global__ void __launch_bounds__(512, 1)
       bool ok = true, more = w.end > w.begin;
       for (int k = 0; ok; ++k) {
         const int n_it = more ? w.end - w.begin : -1;
-        const int key0 = (w.t.step0 + w.begin) * KS;
+        const int key0 = (w.t.step0 + w.begin) * kStep;
         if (keys) {
           if (!(ok = wait1(seg_empty + (k & 3), ((k >> 2) & 1) ^ 1))) break;
           volatile Segment* sg = seg_ring + (k & 3);
@@ -256,7 +255,7 @@ __global__ void __launch_bounds__(512, 1)
         if (!more) break;
         const int32_t* row = p.b.pages + int64_t(w.seq) * p.b.page_stride;
         const int lo = w.t.lo, hi = w.t.hi, head = w.head;
-        ok = load_steps<KS, NS, NCH>(p.b, ring, tm, row, head, key0, n_it, lo, hi, &g_status_pfew, wait1);
+        ok = load_steps<NS, NCH>(p.b, ring, tm, row, head, key0, n_it, lo, hi, &g_status_pfew, wait1);
         if (ok) more = w.next(p.b);
       }
       if (*abort_flag) {  // let the copies already issued land before the CTA exits
@@ -285,7 +284,7 @@ __global__ void __launch_bounds__(512, 1)
     auto issue_o = [&](int k_, int h, int s, bool first) {  // O^T_h (+)= V(s)^T P^T_h
       const uint64_t vb = dV + ((s * TILE) >> 4), pb = dP + ((h * C::PT) >> 4);
 #pragma unroll
-      for (int k = 0; k < KS / 16; ++k)
+      for (int k = 0; k < kStep / 16; ++k)
         tc::mma_ss(tmem + o_col(k_, h), vb + ((k * 2048) >> 4),
                    pb + (((k >> 2) * C::QCH + (k & 3) * 32) >> 4), idesc_o, (!first || k > 0) ? 1u : 0u);
     };
@@ -408,10 +407,10 @@ __global__ void __launch_bounds__(512, 1)
       bool dead = false;
       const int j0 = (t ^ h) & 1;  // this warpgroup's first step: the two take all steps in turn
       for (int j = j0; j < n_it; j += 2) {
-        const int key0 = key_first + j * KS;
+        const int key0 = key_first + j * kStep;
         note(wait_thread(s_full + h, uses & 1));
         ++uses;
-        if (key0 < lo || key0 + KS > hi) {
+        if (key0 < lo || key0 + kStep > hi) {
           // slots that no row sees may hold anything: zero their values, so that 0 x NaN does not come in.  This S^T
           // was issued behind the products with V of every step up to j - 2, so those V have landed and the wait can
           // only end with this step's; before S^T, the stage's last V could still be under way, whose end has the
@@ -421,12 +420,12 @@ __global__ void __launch_bounds__(512, 1)
           const bool there = wait_thread(v_full + s, ((t + j) / NS) & 1);
           note(there);
           if (there && fine) {
-            const int head_rows = min(max(lo - key0, 0), KS), live_rows = min(max(hi - key0, 0), KS);
+            const int head_rows = min(max(lo - key0, 0), kStep), live_rows = min(max(hi - key0, 0), kStep);
 #pragma unroll
             for (int c = 0; c < NCH; ++c) {
               uint4* v = reinterpret_cast<uint4*>(sV + s * TILE + c * kChunk);
               for (int i = r; i < head_rows * 8; i += 128) v[i] = make_uint4(0, 0, 0, 0);
-              for (int i = live_rows * 8 + r; i < KS * 8; i += 128) v[i] = make_uint4(0, 0, 0, 0);
+              for (int i = live_rows * 8 + r; i < kStep * 8; i += 128) v[i] = make_uint4(0, 0, 0, 0);
             }
           }
         }
@@ -438,7 +437,7 @@ __global__ void __launch_bounds__(512, 1)
         float x[NR];
 #pragma unroll
         for (int i = 0; i < NR; ++i) x[i] = __uint_as_float(raw[i]) * p.scale_log2;
-        if (key0 + KS > all_hi || key0 < all_lo) {
+        if (key0 + kStep > all_hi || key0 < all_lo) {
           // rows [first_row, last_row) see this thread's key
           const int rel = key0 + r - pos_first;
           int first_row = max(rel, 0) * p.b.group, last_row = NR;
@@ -622,7 +621,6 @@ int launch_few(const tpa_paged_view* c, Params& p, int grid, cudaStream_t st) {
   using C = FewCfg<D, NR>;
   CUtensorMap tq, tk, tv;
   p.b.tile_tok = NR / p.b.group;
-  p.b.step_shift = 7;
   const uint64_t rows = uint64_t(c->n_pages) * c->n_heads_kv * c->page_size;
   if (!query_map(&tq, c, p, p.b.tile_tok) || !cache_map(&tk, c->k_cache, rows, D, c->page_size) ||
       !cache_map(&tv, c->v_cache, rows, D, c->page_size))

@@ -42,7 +42,6 @@ using tc::fma2;
 using tc::unf2;
 
 constexpr uint32_t kChunk = 128 * 128;  // bytes of a 128-row x 64-column bf16 tile
-constexpr int kStep = 128;              // keys of a step
 
 constexpr int NH = 2;  // sub-tiles
 
@@ -183,7 +182,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             tc::mbar_arrive(seg_full + (k & 1));
           }
           if (!more) break;
-          ok = load_steps<kStep, NS, NCH>(p.b, ring, tm, p.b.pages + int64_t(w.seq) * p.b.page_stride, w.head, key0, n_it,
+          ok = load_steps<NS, NCH>(p.b, ring, tm, p.b.pages + int64_t(w.seq) * p.b.page_stride, w.head, key0, n_it,
                                           w.t.lo, w.t.end, &g_status_ptile, wait1);
           if (ok) more = w.next(p.b);
         }
@@ -513,7 +512,6 @@ int launch_tile(const tpa_paged_view* c, Params& p, int grid, cudaStream_t st) {
       !cache_map(&tv, c->v_cache, rows, D, c->page_size))
     return TPA_ERR_CUDA;
   p.b.tile_tok = NH * sub_tok;
-  p.b.step_shift = 7;
   TPA_CUDA_TRY(cudaFuncSetAttribute(paged_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES));
   {
     cudaFuncAttributes fa;

@@ -290,7 +290,7 @@ struct Ring {
                 "ring");
 };
 
-// Barriers of the rings; warp w of the first eight and lane w of the ninth use set w.
+// Barriers of the rings: set w is that of working warp w and of the four lanes of the loading warp that fill its ring.
 template <class R>
 struct Bars {
   uint8_t* ring;
