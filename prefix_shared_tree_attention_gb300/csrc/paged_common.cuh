@@ -45,14 +45,13 @@ struct Seq {
   int first, n, kv;  // first row, new tokens, cached tokens
 };
 
-// A sequence whose numbers are out of range has no tokens (and is reported); so are rows before the first sequence.
+// A sequence whose numbers are out of range has no tokens (and is reported).
 __device__ __forceinline__ Seq load_seq(const Batch& b, int s, unsigned int* status) {
   const int o0 = __ldg(b.offsets + s), o1 = __ldg(b.offsets + s + 1), kv = __ldg(b.kv_lens + s);
   if (o0 < 0 || o1 < o0 || o1 > b.n_rows || kv < 0 || kv > (int64_t(b.max_pages) << b.page_shift)) {
     if (status) atomicOr(status, TPA_DEV_BAD_INPUT);
     return Seq{0, 0, 0};
   }
-  if (status && s == 0 && o0 != 0) atomicOr(status, TPA_DEV_BAD_INPUT);
   return Seq{o0, o1 - o0, kv};
 }
 
@@ -287,8 +286,10 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
       : "memory");
 }
 
-// Writes the record of the tile that this CTA's first segment is a part of: one thread of each CTA.
-__device__ __forceinline__ void write_split(const Params& p, const Scan* sc, const Shares& sh) {
+// Writes the record of the tile that this CTA's first segment is a part of: one thread of each CTA, behind its first
+// loads.  Rows before the first sequence are reported here, where nothing waits for it.
+__device__ __forceinline__ void write_split(const Params& p, const Scan* sc, const Shares& sh, unsigned int* status) {
+  if (blockIdx.x == 0 && __ldg(p.b.offsets) != 0) atomicOr(status, TPA_DEV_BAD_INPUT);
   Split s = {};
   if (int(blockIdx.x) < sh.n && sc->begin > 0) {  // the tile began in an earlier CTA
     const Tile t = sc->t;

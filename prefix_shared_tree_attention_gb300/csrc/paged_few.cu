@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(512, 1)
   auto o_col = [](int k, int h) { return uint32_t(2 * NR + ((k & 1) * 2 + h) * NR); };  // of segment k
 
   if (int(blockIdx.x) >= shares.n) {  // nothing to do here
-    if (threadIdx.x == 0) write_split(p, sc, shares);
+    if (threadIdx.x == 0) write_split(p, sc, shares, &g_status_pfew);
   } else if (warp >= 8 && warp < 12) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REG_LOW));
   if (warp == W_K || warp == W_V) {
@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(512, 1)
         tc::mbar_arrive_expect_tx(q_full + qb, q_bytes);
         for (int c = 0; c < NCH; ++c)
           tc::tma_load_3d(sQ + (qb * NCH + c) * C::QCH, &tm_q, q_full + qb, c * 64, w.head * p.b.group, w.t.first);
-        if (nq++ == 0) write_split(p, sc, shares);
+        if (nq++ == 0) write_split(p, sc, shares, &g_status_pfew);
         more = w.next(p.b);
       }
       if (*abort_flag) {
@@ -401,6 +401,10 @@ __global__ void __launch_bounds__(512, 1)
       // every row in use sees the keys in [all_lo, all_hi)
       const int all_hi = pos_first + 1;
       const int all_lo = p.b.window > 0 ? pos_first + n_tok - p.b.window : 0;
+      // Rows behind the tile's own (the load brings the next sequence's queries, or padding) never pass an infinite
+      // maximum, so they have no say in when the others' are moved: a row's bits are its sequence's alone.  Their own
+      // sums may then be no numbers; nobody reads them.
+      const float floor_r = r < n_tok * p.b.group ? kNoMax : INFINITY;
       float l[NR];
 #pragma unroll
       for (int i = 0; i < NR; ++i) l[i] = 0.f;
@@ -466,14 +470,11 @@ __global__ void __launch_bounds__(512, 1)
           warp_s[(warp & 3) * NR + owned_row<NR>(lane)] = v[0];
           group_sync(h);
           if (r < NR) {
-            const float before = j == j0 ? kNoMax : m_s[r];
+            const float before = j == j0 ? floor_r : m_s[r];
             const float top = fmaxf(fmaxf(warp_s[r], warp_s[NR + r]), fmaxf(warp_s[2 * NR + r], warp_s[3 * NR + r]));
-            // Rows behind the tile's own (the load brings the next sequence's queries, or padding) never pass an infinite
-            // maximum, so they have no say in when the others' are moved: a row's bits are its sequence's alone.
-            const bool live = r < n_tok * p.b.group;
-            const float m = live ? fmaxf(before, top) : INFINITY;
+            const float m = fmaxf(before, top);
             m_s[r] = m;
-            alpha_s[r] = live ? tc::ex2(before - m) : 1.f;
+            alpha_s[r] = tc::ex2(before - m);
           }
           group_sync(h);
           if (j != j0) {
@@ -546,7 +547,8 @@ __global__ void __launch_bounds__(512, 1)
       if (n_it < 0) break;
       note(wait_thread(ml_full + (k & 1), (k >> 1) & 1));
       note(wait_thread(o_final + (k & 1), (k >> 1) & 1));
-      if (r < NR && fine) {
+      // (of the tile's own rows: the quotient of a sum that is no number takes a long way, 5 us for 256 short sequences)
+      if (r < live && fine) {
         const float* xm = xm_s + (k & 1) * 2 * NR;
         const float* xl = xl_s + (k & 1) * 8 * NR;
         const float m0 = xm[r], m1 = xm[NR + r];
@@ -562,14 +564,12 @@ __global__ void __launch_bounds__(512, 1)
         }
         coef_s[r] = a0;
         coef_s[NR + r] = a1;
-        if (r < live) {
-          if (slot < 0) {
-            const int tok = r / p.b.group;
-            p.lse[int64_t(first + tok) * p.hq + head0 + r - tok * p.b.group] =
-                sum > 0.f ? (top + __log2f(sum)) * kLn2 : -INFINITY;
-          } else {
-            p.part_ml[int64_t(slot) * p.rows + r] = make_float2(top, sum);
-          }
+        if (slot < 0) {
+          const int tok = r / p.b.group;
+          p.lse[int64_t(first + tok) * p.hq + head0 + r - tok * p.b.group] =
+              sum > 0.f ? (top + __log2f(sum)) * kLn2 : -INFINITY;
+        } else {
+          p.part_ml[int64_t(slot) * p.rows + r] = make_float2(top, sum);
         }
       }
       if (group_any(2, !fine)) break;  // (the coefficients are there)

@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
   const uint32_t tmem = *tmem_slot;
 
   if (int(blockIdx.x) >= shares.n) {  // nothing to do here
-    if (threadIdx.x == 0) write_split(p, sc, shares);
+    if (threadIdx.x == 0) write_split(p, sc, shares, &g_status_ptile);
   } else if (warp >= W_K) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REG_LOW));
     if (warp == W_K || warp == W_V) {
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             for (int c = 0; c < NCH; ++c)
               tc::tma_load_3d(sQ + h * TILE + c * kChunk, &tm_q, q_full, c * 64, w.head * p.b.group,
                               w.t.first + h * sub_tok);
-          if (nq++ == 0) write_split(p, sc, shares);
+          if (nq++ == 0) write_split(p, sc, shares, &g_status_ptile);
           more = w.next(p.b);
         }
         if (*abort_flag && nq > 0) {
