@@ -627,7 +627,8 @@ uint64_t tpa_paged_attn_workspace_bytes(int32_t max_q_len, int32_t n_heads_q, in
  * O = 0 and LSE = -inf.  Slots that no token of the batch sees may hold
  * anything, NaN included, and pages that hold only such slots are not read
  * (their table entries may be anything); the keys and values of seen slots
- * must be finite.
+ * must be finite, and scores (scale q . k) below 2^20 in magnitude: they are
+ * fp32, with steps of 2^-4 there.
  *   q [n_rows, Hq, d] bf16, rows q_stride elements apart (a multiple of 8), 16-byte aligned
  *   o [n_rows, Hq, d] bf16, lse [n_rows, Hq] fp32 (written, rows behind the last sequence not)
  *   Hq / Hkv <= 64

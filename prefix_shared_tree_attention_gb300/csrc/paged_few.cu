@@ -19,7 +19,7 @@
 // next tile does not use.  In the middle of a batch a step's 64 KB (d 128) take
 // 2950 cycles, what HBM gives an SM; the start (lengths, first pages, first
 // keys: 7 us) and the joining of cut tiles (3 us) come on top: 64 sequences of 300
-// to 3000 tokens, 440 MB, 79 us; 256 of 50 to 600, where a tile has three steps, 81.5 us for 342 MB.
+// to 3000 tokens, 440 MB, 78 us; 256 of 50 to 600, where a tile has three steps, 80.4 us for 342 MB.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

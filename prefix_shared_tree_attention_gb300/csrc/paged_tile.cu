@@ -17,10 +17,13 @@
 // Work: 4 d operations and one exponential for each (row, key).  Bound by the way
 // from a step's scores to the next's, which each sub-tile goes alone: at d 128
 // 1024 cycles of MMAs, 1350 of softmax and 600 of handing over by barriers, so that
-// with two sub-tiles the MMAs run 68 % of the time.  4001 tokens after 28002 cached
-// ones, 32/8 heads: 1.30 to 1.38 ms with the clock, 1430 to 1510 TFLOP/s (measured
-// GEMM rates: 1939 in a burst, 1739 sustained).  Polling the barriers without
-// suspending, and one arrival a warp instead of one a thread, gave nothing or lost 2 %.
+// with two sub-tiles the MMAs run 69 % of the time (72 by the counters).  4001 tokens
+// after 28002 cached ones, 32/8 heads: 1.30 to 1.43 ms with the clock that the power cap
+// leaves, 1380 to 1510 TFLOP/s (measured GEMM rates: 1939 in a burst, 1739 sustained).
+// Polling the barriers without suspending, and one arrival a warp instead of one a
+// thread, gave nothing or lost 2 %.
+// Few rows cost no more here than in the kernel made for them: one chunk of 512 tokens
+// beside 63 single ones of other sequences takes 114 us, the two by themselves 32 and 79.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -71,7 +74,7 @@ struct TileCfg {
   static_assert(REG_HIGH * 256 + REG_LOW * 128 <= REG_LAUNCH * 384, "register split");
   static constexpr uint32_t TMEM_COLS = 512;
   // P is handed over in this many parts, so that its product can begin while the rest is formed.  Two shorten the way
-  // from scores to scores where it is what the MMAs wait for: 4001 tokens at d 64 495 -> 450 us (now 461, since the
+  // from scores to scores where it is what the MMAs wait for: 4001 tokens at d 64 495 -> 450 us (now 462, since the
   // sub-tiles' ends are apart).  At d 128, with twice the MMA work in the same softmax, they cost 1 to 2 % (8 chunks
   // of 512: 160.5 -> 162.5 us).
   static constexpr int PARTS = D == 64 ? 2 : 1;

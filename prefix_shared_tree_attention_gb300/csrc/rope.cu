@@ -1195,8 +1195,8 @@ int num_sms() {
 }
 
 // Row by row instead of through rings: tokens of few heads, whose units would be small (16384 of which 14000 real, d 128:
-// 2/1 heads 10.2 us instead of 22.1, 4/4 21.4 and 22.9, 8/8 38.5 and 29.6; 16000 appended: 2/1 heads 17.0 instead of
-// 26.5, 4/2 30.5 and 27.3, d 64 8/2 23.0 and 24.9), and calls of one pass over the grid, where the rings' start
+// 2/1 heads 9.0 us instead of 21.4, 4/4 21.2 and 22.6, 8/8 39.0 and 29.7; 16000 appended: 2/1 heads 16.7 instead of
+// 26.0, 4/2 30.3 and 26.5, d 64 8/2 22.0 and 24.4), and calls of one pass over the grid, where the rings' start
 // counts (32/8 heads: 100 tokens 3.3 us instead of 4.3, 200 3.9 and 4.65, 300 4.5 and 4.85, 400 5.55 and 5.05; one
 // appended token 3.7 and 4.75, 200 5.3 and 5.9, 250 6.2 and 6.15, 400 8.15 and 6.4; 16/2 heads, 400 appended 5.45
 // and 6.1, 600 6.6 both, 800 8.2 and 7.3): up to 3 MB.
