@@ -1,6 +1,7 @@
 """Batches over a paged cache: a sequence's results are its own whatever stands
 in the rows beside it, every batch that breaks its description is reported by
-the append and by the attention alike, and a batch without sequences is no work.
+the append and by the attention alike, a batch without sequences is no work, and
+a captured step goes on while sequences grow.
 Sizes on both sides of the borders between kernels."""
 import pytest
 import torch
@@ -184,4 +185,47 @@ def test_windows_past_32_bits(tpa, q_len):
     for window in (2 ** 31, 2 ** 32 + 5, 2 ** 63):
         got = tpa.paged_attn_fwd(*b.cache, b.q, max_q_len=q_len, window=window)
         assert all(torch.equal(x, y) for x, y in zip(want, got)), window
+    tpa.sync_status()
+
+
+@pytest.mark.parametrize("drafts", [0, 3, 60])  # a token each, drafts, chunks: every attention kernel
+def test_a_captured_sampling_step(tpa, drafts):
+    """Append, attention, a projection to the vocabulary and the verification in one graph, replayed while the sequences
+    grow over a slice of a wider page table: the same as call by call."""
+    S, hq, hkv, d, page, V = 3, 8, 2, 64, 16, 500
+    new = drafts + 1
+    b = Batch([new] * S, [40 + 4 * new, 7 + 4 * new, 300 + 4 * new], hq, hkv, d, page, seed=4, spare=0, extra=2)
+    wide = torch.full((S, b.pages.shape[1] + 5), -1, dtype=torch.int32, device="cuda")
+    wide[:, 2:2 + b.pages.shape[1]] = b.pages
+    pages = wide[:, 2:2 + b.pages.shape[1]]
+    table = tpa.rope_table(600, d)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    w = [1 + 0.2 * torch.randn(d, generator=g, device="cuda") for _ in range(2)]
+    head = torch.randn((hq * d, V), generator=g, device="cuda") * 0.3
+    x = torch.randint(0, V, (S, drafts), generator=g, device="cuda", dtype=torch.int32)
+    u, un = torch.rand((S, drafts), generator=g, device="cuda"), torch.rand(S, generator=g, device="cuda")
+
+    def step(kc, vc):
+        q = tpa.paged_append(kc, vc, pages, b.offsets, b.kv_lens, b.k, b.v, q=b.q, table=table, q_weight=w[0], k_weight=w[1])
+        q[S * new:] = 0
+        o, lse = tpa.paged_attn_fwd(kc, vc, pages, b.offsets, b.kv_lens, q, max_q_len=new)
+        p = torch.softmax(o[:S * new].reshape(S, new, hq * d).float() @ head, -1)
+        return (q[:S * new], o[:S * new], lse[:S * new], *tpa.verify_drafts(p, x, u, un))
+
+    eager = b.k_cache.clone(), b.v_cache.clone()
+    b.kv_lens -= 3 * new
+    lens = b.kv_lens.clone()
+    step(eager[0].clone(), eager[1].clone())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = step(b.k_cache, b.v_cache)
+    for i in range(4):
+        for t in (b.q, b.k, b.v):
+            t.copy_(torch.randn(t.shape, generator=g, device="cuda"))
+        b.kv_lens.copy_(lens + i * new)
+        want = step(*eager)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, c) for a, c in zip((*want, *eager), (*kept, b.k_cache, b.v_cache))), i
     tpa.sync_status()
