@@ -402,8 +402,8 @@ __global__ void __launch_bounds__(512, 1)
       const int all_hi = pos_first + 1;
       const int all_lo = p.b.window > 0 ? pos_first + n_tok - p.b.window : 0;
       // Rows behind the tile's own (the load brings the next sequence's queries, or padding) never pass an infinite
-      // maximum, so they have no say in when the others' are moved: a row's bits are its sequence's alone.  Their own
-      // sums may then be no numbers; nobody reads them.
+      // maximum, so they have no say in when the others' are moved, and no bit of those depends on what they hold.  Their
+      // own sums may then be no numbers; nobody reads them.
       const float floor_r = r < n_tok * p.b.group ? kNoMax : INFINITY;
       float l[NR];
 #pragma unroll
