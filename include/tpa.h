@@ -645,6 +645,127 @@ int tpa_paged_attn_fwd(const tpa_paged_view* cache, const void* q, int64_t q_str
                        int32_t n_heads_q, int32_t max_q_len, float softmax_scale, int32_t window,
                        void* workspace, uint64_t workspace_bytes, void* stream);
 
+/*
+ * tpa_paged_attn_tree_fwd — tpa_paged_attn_fwd for drafted trees: the new
+ * tokens of a sequence are not a chain, and which of them a token sees is given
+ * by bits.  With base = kv_lens[s] - (new tokens of s), new token i of sequence
+ * s (its key and value in slot base + i) sees
+ *   every key j < base, and j > positions[row] - window when window > 0;
+ *   the new token j <= i, in slot base + j, where bit j % 32 of masks[row][j / 32] is set
+ *   (its own among them: a mask without it leaves it out).
+ *   masks [n_rows, mask_words] int32, mask_words in [1, 32]: a sequence has at
+ *     most 32 mask_words new tokens (one with more has its rows left unwritten and is reported)
+ *   positions [n_rows] int32, read with window > 0 only (may be NULL without);
+ *     a sequence's i-th new token's in [base, base + i]: others read as the nearer of the two
+ * (tpa_draft_masks makes both from the tree's parents.)  The keys and values of
+ * all of a sequence's kv_lens[s] tokens must be finite.  Everything else, errors too, as
+ * tpa_paged_attn_fwd; masks of chains give its results,
+ * bit for bit without a window.
+ */
+int tpa_paged_attn_tree_fwd(const tpa_paged_view* cache, const void* q, int64_t q_stride, const int32_t* masks,
+                            int32_t mask_words, const int32_t* positions, void* o, float* lse, int32_t n_heads_q,
+                            int32_t max_q_len, float softmax_scale, int32_t window, void* workspace,
+                            uint64_t workspace_bytes, void* stream);
+
+/*
+ * tpa_paged_compact — keep an accepted path: for each sequence the keys and
+ * values in slots base + path[s][i], i < n_accepted[s], move to slots base + i (base as
+ * above), and new_lens[s] = base + n_accepted[s].  What is behind is left as it was.
+ *   cache: as above; k_cache and v_cache hold n_layers caches one behind another,
+ *     [n_layers, n_pages, Hkv, page_size, d], of the same pages
+ *   path [n_seqs, max_path] int32, rising, path[s][i] >= i; n_accepted [n_seqs] int32
+ *   new_lens [n_seqs] int32 (written; not kv_lens itself)
+ * A sequence whose path is none (not rising, beyond its new tokens, n_accepted
+ * out of range) or whose lengths are out of range is left as it was, new_lens[s] = kv_lens[s], and is
+ * reported.  One kernel.  Errors: TPA_ERR_INVALID_ARG, TPA_ERR_CUDA.
+ */
+int tpa_paged_compact(const tpa_paged_view* cache, int32_t n_layers, const int32_t* path, const int32_t* n_accepted,
+                      int32_t max_path, int32_t* new_lens, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* The pages of a cache.  refs [n_pages] int32 counts the uses of each page (0:
+ * free; zeroed by the caller before the first call), pages [n_seqs, max_pages]
+ * int32 holds each sequence's pages at the head of its row and negative numbers
+ * behind them (filled with -1 by the caller before the first call), kv_lens
+ * [n_seqs] int32 its tokens.  All are device memory and read and written by the kernels, so
+ * captured calls can be replayed.  Free pages are handed out lowest first, in
+ * the order of the rows: the same calls give the same tables.  n_free [1] int32 (written) is
+ * the number of free pages that are left; too few pages hand out none, and
+ * n_free is then minus the number that is missing.  A page number >= n_pages in a table, or one given back that
+ * was not in use, is reported (TPA_ERR_INVALID_ARG by tpa_sync_status) and not followed.  At most 8192 rows
+ * (of the table in resize, of src and dst in fork) and 2^23 pages.             */
+/* ------------------------------------------------------------------------ */
+
+typedef struct {
+  void* k_cache;            /* [n_layers, n_pages, Hkv, page_size, d] bf16, 16-byte aligned (tpa_paged_fork only) */
+  void* v_cache;
+  int32_t* pages;
+  int32_t* kv_lens;
+  int32_t* refs;
+  int32_t n_layers, n_pages, page_size, n_heads_kv, head_dim;  /* layers, heads and d: tpa_paged_fork only */
+  int32_t n_seqs, max_pages, page_stride;
+} tpa_paged_pool;
+
+/*
+ * tpa_paged_resize — give every row the pages that its length needs,
+ * ceil(kv_lens[s] / page_size): those behind them go back (a length of 0 frees the sequence),
+ * those that are missing are handed out.  A length that is negative or more than max_pages hold is
+ * reported and its row left as it is.  With too few pages no row grows (what goes back has gone back).
+ * One kernel.  Errors: TPA_ERR_INVALID_ARG, TPA_ERR_CUDA.
+ */
+int tpa_paged_resize(const tpa_paged_pool* pool, int32_t* n_free, void* stream);
+
+/*
+ * tpa_paged_fork — row dst[f] becomes a copy of row src[f], for all f < n_forks:
+ * what dst held goes back, the whole pages of src are shared, the tokens of its last, partly filled page are
+ * copied (all layers, keys and values) into a page of dst's own, and kv_lens[dst] = kv_lens[src].  So
+ * each sequence alone has the page that it writes next, as long as no sequence is cut back into a shared page and
+ * appended to there.
+ *   src, dst [n_forks] int32 (device): rows; a row may be the src of many forks.
+ * A call in which a row is out of range, is dst twice or both src and dst, or has a src of a length out of range
+ * is not done: it is reported, and n_free is INT32_MIN.  With too few pages the dst rows are left empty, of length 0.
+ * Two kernels.  Errors: TPA_ERR_INVALID_ARG, TPA_ERR_CUDA.
+ */
+int tpa_paged_fork(const tpa_paged_pool* pool, const int32_t* src, const int32_t* dst, int32_t n_forks, int32_t* n_free,
+                   void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Sampling from logits, from given uniform numbers.                          */
+/* ------------------------------------------------------------------------ */
+
+enum { TPA_LOGITS_F32 = 0, TPA_LOGITS_BF16 = 1 };
+
+typedef struct {            /* each: an array of one entry a row (device), or NULL and the one value for all rows */
+  const float* temperature; /* 0 (the first of the largest logits) or in [1e-6, 1e6] */
+  const float* top_p;       /* in [0, 1]; 1: all */
+  const float* min_p;       /* in [0, 1]; 0: all */
+  const int32_t* top_k;     /* <= 0: all */
+  float temperature_all, top_p_all, min_p_all;
+  int32_t top_k_all;
+} tpa_sample_params;
+
+/*
+ * tpa_sample_tokens — the next token of each row of logits.  With x_v the
+ * row's logits, w_v = exp((x_v - max x) / temperature), and the tokens in the order of x, highest
+ * first, equal ones by index:
+ *   top_k keeps the first top_k;  of those, top_p keeps the shortest run from the first on (one token at least)
+ *   whose weights reach top_p of theirs together;  of those, min_p keeps the ones with w_v >= min_p.
+ * The token is the lowest v with  sum_{w <= v, kept} > u * sum_kept  (the last kept one for u >= 1), and
+ * logp its log-probability among the kept ones, log(w_v / sum_kept).
+ *   logits [n_rows, vocab] fp32 or bf16 (TPA_LOGITS_*), rows row_stride >= vocab elements apart, aligned to an
+ *     element (16-byte aligned rows are not needed).  NaN counts as -inf, +inf as the largest finite
+ *     number.  -inf (a masked token) is never drawn; a row of nothing else gives -1 and NaN.
+ *   u [n_rows] fp32 in [0, 1);  tokens [n_rows] int32, logp [n_rows] fp32 (written)
+ *   vocab <= 2^30
+ * Weights are within 2^-29 of themselves and cut off below 2^-43 of the largest one for a vocabulary of 2^18 (2^-(61 - log2
+ * vocab)), and their sums are exact: borders of top_p, min_p and the draw are those of the formulas to within
+ * that.  Deterministic; a row's result does not depend on the others.  Parameters in arrays that are out of range
+ * give -1 and NaN in their rows and are reported; a single value out of range is refused.  One kernel, one cluster of
+ * CTAs a row.  Errors: TPA_ERR_INVALID_ARG, TPA_ERR_CUDA.
+ */
+int tpa_sample_tokens(const void* logits, int32_t logits_type, int64_t row_stride, int32_t n_rows, int32_t vocab,
+                      const tpa_sample_params* params, const float* u, int32_t* tokens, float* logp, void* stream);
+
 /* ------------------------------------------------------------------------ */
 /* Drafted tokens (speculative sampling): the policy's probabilities decide
  * how many of a sequence's drafted tokens stand, and the next one is drawn.  */
@@ -675,6 +796,40 @@ int tpa_verify_drafts(const float* target, int64_t target_stride, const float* d
                       const int32_t* draft_tokens, const int32_t* n_drafts, const float* u_accept,
                       const float* u_next, int32_t* tokens, int32_t* n_accepted, int32_t n_seqs, int32_t max_drafts,
                       int32_t vocab, void* stream);
+
+/*
+ * Drafted trees.  A batch's new tokens are described by offsets as for a paged
+ * cache (offsets [n_seqs + 1], n_rows rows); parents [n_rows] int32 gives for each the
+ * number of its parent among its sequence's new tokens, below its own, or -1 for one whose parent is the last
+ * cached token before them.  A tree has at most 1024 tokens.  Parents and offsets out of
+ * range are reported by tpa_sync_status (TPA_ERR_INVALID_ARG): the token counts as without parent (masks) or is not
+ * accepted, the sequence is passed over.
+ *
+ * tpa_draft_masks — what tpa_paged_attn_tree_fwd reads, and the positions at which a tree's tokens are rotated:
+ *   positions [n_rows] int32 (written): kv_lens[s] - (new tokens of s) + the token's ancestors among them
+ *   masks [n_rows, mask_words] int32 (written): bit j % 32 of word j / 32 for the token itself and each of its
+ *     ancestors j among the new tokens, with window > 0 those less than window positions before it
+ *   mask_words in [1, 32], 32 mask_words >= the new tokens of any sequence
+ * One kernel.  Errors: TPA_ERR_INVALID_ARG, TPA_ERR_CUDA.
+ */
+int tpa_draft_masks(const int32_t* parents, const int32_t* offsets, const int32_t* kv_lens, int32_t n_seqs, int32_t n_rows,
+                    int32_t window, int32_t* positions, int32_t* masks, int32_t mask_words, void* stream);
+
+/*
+ * tpa_accept_drafts — the path that the sampled tokens follow through each drafted tree.  Row 0 of a sequence is its last
+ * sampled token and stands; behind a standing row r stands its first child whose drafted token is
+ * the one sampled behind r.  With every row's token drawn from the policy (tpa_sample_tokens), the tokens
+ * along the path are distributed as the policy's own, whatever was drafted.
+ *   draft_tokens [n_rows] int32: each row's own token; sampled [n_rows] int32: the token drawn behind it
+ *   path [n_seqs, max_path] int32 (written): the standing rows (numbers among the sequence's new tokens), then -1
+ *   tokens [n_seqs, max_path] int32 (written): sampled[path[i]], the sequence's next tokens, then -1
+ *   n_accepted [n_seqs] int32 (written): the standing rows, row 0 among them (0 without new tokens)
+ *   max_path in [1, 1024]: a path ends there at the latest
+ * One kernel.  Errors: TPA_ERR_INVALID_ARG, TPA_ERR_CUDA.
+ */
+int tpa_accept_drafts(const int32_t* parents, const int32_t* offsets, const int32_t* draft_tokens, const int32_t* sampled,
+                      int32_t n_seqs, int32_t n_rows, int32_t* tokens, int32_t* path, int32_t* n_accepted,
+                      int32_t max_path, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Status                                                                    */

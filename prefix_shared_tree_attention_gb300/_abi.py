@@ -19,6 +19,7 @@ GRAD_F32, GRAD_BF16 = 0, 1
 WEIGHT_F32, WEIGHT_BF16 = 0, 1
 BALANCE_FFD, BALANCE_KK = 0, 1
 MASK_U8, MASK_BITS = 0, 1
+LOGITS_F32, LOGITS_BF16 = 0, 1
 
 _i32p = C.POINTER(C.c_int32)
 _i64p = C.POINTER(C.c_int64)
@@ -80,10 +81,29 @@ class PagedView(C.Structure):
     ]
 
 
-# The two structures above as bytes: what the bindings of short calls pass in their place.
+class PagedPool(C.Structure):
+    _fields_ = [
+        ("k_cache", C.c_void_p), ("v_cache", C.c_void_p), ("pages", C.c_void_p), ("kv_lens", C.c_void_p),
+        ("refs", C.c_void_p), ("n_layers", C.c_int32), ("n_pages", C.c_int32), ("page_size", C.c_int32),
+        ("n_heads_kv", C.c_int32), ("head_dim", C.c_int32), ("n_seqs", C.c_int32), ("max_pages", C.c_int32),
+        ("page_stride", C.c_int32),
+    ]
+
+
+class SampleParams(C.Structure):
+    _fields_ = [
+        ("temperature", C.c_void_p), ("top_p", C.c_void_p), ("min_p", C.c_void_p), ("top_k", C.c_void_p),
+        ("temperature_all", C.c_float), ("top_p_all", C.c_float), ("min_p_all", C.c_float), ("top_k_all", C.c_int32),
+    ]
+
+
+# The structures above as bytes: what the bindings of short calls pass in their place.
 ROPE_PARAMS = struct.Struct("@PiiiiPPfi")
 PAGED_VIEW = struct.Struct("@PPPPPiiiiiiii")
+PAGED_POOL = struct.Struct("@PPPPPiiiiiiii")
+SAMPLE_PARAMS = struct.Struct("@PPPPfffi")
 assert ROPE_PARAMS.size == C.sizeof(RopeParams) and PAGED_VIEW.size == C.sizeof(PagedView)
+assert PAGED_POOL.size == C.sizeof(PagedPool) and SAMPLE_PARAMS.size == C.sizeof(SampleParams)
 
 # name -> (restype, argtypes); every symbol declared in include/tpa.h
 PROTOTYPES = {
@@ -140,6 +160,18 @@ PROTOTYPES = {
     "tpa_paged_attn_workspace_bytes": (C.c_uint64, [C.c_int32, C.c_int32, C.c_int32, C.c_int32]),
     "tpa_paged_attn_fwd": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_int32,
                                      C.c_int32, C.c_float, C.c_int32, C.c_void_p, C.c_uint64, C.c_void_p]),
+    "tpa_paged_attn_tree_fwd": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p, C.c_int32, C.c_void_p, C.c_void_p,
+                                          C.c_void_p, C.c_int32, C.c_int32, C.c_float, C.c_int32, C.c_void_p, C.c_uint64,
+                                          C.c_void_p]),
+    "tpa_paged_compact": (C.c_int, [C.c_void_p, C.c_int32, C.c_void_p, C.c_void_p, C.c_int32, C.c_void_p, C.c_void_p]),
+    "tpa_paged_resize": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p]),
+    "tpa_paged_fork": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int32, C.c_void_p, C.c_void_p]),
+    "tpa_sample_tokens": (C.c_int, [C.c_void_p, C.c_int32, C.c_int64, C.c_int32, C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p,
+                                    C.c_void_p, C.c_void_p]),
+    "tpa_draft_masks": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_void_p, C.c_void_p,
+                                  C.c_int32, C.c_void_p]),
+    "tpa_accept_drafts": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int32, C.c_int32, C.c_void_p, C.c_void_p,
+                                    C.c_void_p, C.c_int32, C.c_void_p]),
     "tpa_verify_drafts": (C.c_int, [C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p,
                                     C.c_void_p, C.c_void_p, C.c_void_p, C.c_int32, C.c_int32, C.c_int32,
                                     C.c_void_p]),

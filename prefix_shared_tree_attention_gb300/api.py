@@ -9,9 +9,9 @@ from typing import Sequence
 import numpy as np
 import torch
 
-from ._abi import (BALANCE_FFD, BALANCE_KK, GRAD_BF16, GRAD_F32, LOGITS_COMPACT, LOGITS_PADDED, MASK_BITS,
-                   MASK_U8, PAGED_VIEW, ROPE_PARAMS, WEIGHT_BF16, WEIGHT_F32, BlockMaskView, PackingMetrics, TreeInfo,
-                   TreeView, check, lib)
+from ._abi import (BALANCE_FFD, BALANCE_KK, GRAD_BF16, GRAD_F32, LOGITS_BF16, LOGITS_COMPACT, LOGITS_F32, LOGITS_PADDED,
+                   MASK_BITS, MASK_U8, PAGED_POOL, PAGED_VIEW, ROPE_PARAMS, SAMPLE_PARAMS, WEIGHT_BF16, WEIGHT_F32,
+                   BlockMaskView, PackingMetrics, TreeInfo, TreeView, check, lib)
 
 
 def _stream_ptr(stream) -> int:
@@ -637,6 +637,37 @@ def paged_attn_fwd(k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Te
     The batch is described as for ``paged_append``, which is called first (its
     result is ``q``); ``max_q_len`` is the most new tokens of any sequence and
     ``window`` limits each token to that many keys (0: all)."""
+    return _paged_attend(k_cache, v_cache, pages, offsets, kv_lens, q, None, None, max_q_len, softmax_scale, window, out, lse,
+                         workspace, stream)
+
+
+def paged_attn_tree_fwd(k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Tensor, offsets: torch.Tensor,
+                        kv_lens: torch.Tensor, q: torch.Tensor, masks: torch.Tensor, max_q_len: int,
+                        positions: torch.Tensor | None = None, softmax_scale: float | None = None, window: int = 0,
+                        out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                        workspace: torch.Tensor | None = None, stream=None):
+    """``paged_attn_fwd`` for drafted trees (tpa_paged_attn_tree_fwd): a new token
+    sees what its sequence has cached before the new ones, and of those the ones
+    whose bits its row of ``masks`` [tokens, words] int32 has set.
+
+    ``draft_masks`` makes the masks from a tree's parents (once a step, for all
+    layers), and the ``positions`` that are needed with a ``window``; give it the same window.
+    The workspace is ``paged_attn_fwd``'s."""
+    if masks.dtype != torch.int32 or masks.dim() != 2 or masks.shape[0] != q.shape[0] or not masks.is_contiguous():
+        raise ValueError("masks must be a contiguous int32 tensor [tokens, words]")
+    if not 1 <= masks.shape[1] <= 32:
+        raise ValueError("masks must have 1 to 32 words a row")
+    if positions is not None and (positions.dtype != torch.int32 or positions.shape != q.shape[:1] or
+                                  not positions.is_contiguous()):
+        raise ValueError("positions must be a contiguous int32 tensor [tokens]")
+    if positions is None and window:
+        raise ValueError("a window needs the tokens' positions")
+    return _paged_attend(k_cache, v_cache, pages, offsets, kv_lens, q, masks, positions, max_q_len, softmax_scale, window, out,
+                         lse, workspace, stream)
+
+
+def _paged_attend(k_cache, v_cache, pages, offsets, kv_lens, q, masks, positions, max_q_len, softmax_scale, window, out, lse,
+                  workspace, stream):
     rows, sq, Hq, d = _head_rows("q", q)
     if q.dim() != 3:
         raise ValueError("q must be [tokens, Hq, d]")
@@ -646,7 +677,7 @@ def paged_attn_fwd(k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Te
     window = min(window, 2 ** 31 - 1)  # longer than any sequence
     cache, hkv = _paged_view(k_cache, v_cache, pages, offsets, kv_lens, rows, None, d)
     _whole_workspace(workspace)
-    st = _launch_stream(stream, q, out, lse, workspace, k_cache, v_cache, pages, offsets, kv_lens)
+    st = _launch_stream(stream, q, out, lse, workspace, k_cache, v_cache, pages, offsets, kv_lens, masks, positions)
     if out is None:
         o = _new(stream, q.shape, q.dtype, q.device)
     else:
@@ -659,10 +690,13 @@ def paged_attn_fwd(k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Te
         raise ValueError("lse must be a contiguous fp32 tensor [tokens, Hq]")
     if workspace is None:
         workspace = _new(stream, paged_attn_workspace_bytes(max_q_len, Hq, hkv, d), torch.uint8, q.device)
-    check("tpa_paged_attn_fwd", lib().tpa_paged_attn_fwd(
-        cache, q.data_ptr(), sq, o.data_ptr(), lse.data_ptr(), Hq, max_q_len,
-        float(softmax_scale or 0.0), window, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-        st))
+    rest = (o.data_ptr(), lse.data_ptr(), Hq, max_q_len, float(softmax_scale or 0.0), window, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), st)
+    if masks is None:
+        check("tpa_paged_attn_fwd", lib().tpa_paged_attn_fwd(cache, q.data_ptr(), sq, *rest))
+    else:
+        check("tpa_paged_attn_tree_fwd", lib().tpa_paged_attn_tree_fwd(
+            cache, q.data_ptr(), sq, masks.data_ptr(), masks.shape[1], _ptr(positions), *rest))
     return o, lse
 
 
@@ -716,6 +750,219 @@ def verify_drafts(target_probs: torch.Tensor, draft_tokens: torch.Tensor, u_acce
         target_probs.data_ptr(), ts, _ptr(draft_probs) if K else None, ds, draft_tokens.data_ptr(), _ptr(n_drafts),
         u_accept.data_ptr(), u_next.data_ptr(), tokens.data_ptr(), n_accepted.data_ptr(), S, K, V, st))
     return tokens, n_accepted
+
+
+def _vector(name: str, t: torch.Tensor, n: int) -> int:
+    """The address of a contiguous int32 tensor [n]."""
+    if t.dtype is not torch.int32 or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor [{n}]")
+    return t.data_ptr()
+
+
+def _table(name: str, t: torch.Tensor, n: int, m: int) -> int:
+    """The address of a contiguous int32 tensor [n, m]."""
+    if t.dtype is not torch.int32 or t.shape != (n, m) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor [{n}, {m}]")
+    return t.data_ptr()
+
+
+def draft_masks(parents: torch.Tensor, offsets: torch.Tensor, kv_lens: torch.Tensor, max_q_len: int, window: int = 0,
+                out: tuple | None = None, stream=None):
+    """Positions [tokens] and masks [tokens, ceil(max_q_len / 32)], int32, of a
+    batch's drafted trees (tpa_draft_masks): for ``qk_norm_rope_fwd`` and
+    ``paged_attn_tree_fwd`` of a step's layers.
+
+    ``parents`` [tokens] int32 has each new token's parent, its number among its
+    sequence's new tokens (lower than its own), or -1 behind the last cached token;
+    ``offsets`` and ``kv_lens`` are ``paged_append``'s, ``max_q_len`` <= 1024 the most new tokens of any sequence."""
+    rows, n = parents.shape[0], kv_lens.shape[0]
+    at = _vector("parents", parents, rows), _vector("offsets", offsets, n + 1), _vector("kv_lens", kv_lens, n)
+    words, window = (int(max_q_len) + 31) // 32, int(window)
+    if not 1 <= words <= 32 or window < 0:
+        raise ValueError("max_q_len must be in [1, 1024] and window not negative")
+    if out is None:
+        st = _launch_stream(stream, parents, offsets, kv_lens)
+        dev = parents.device
+        positions, masks = _new(stream, (rows,), torch.int32, dev), _new(stream, (rows, words), torch.int32, dev)
+    else:
+        positions, masks = out
+        _vector("positions", positions, rows)
+        _table("masks", masks, rows, words)
+        st = _launch_stream(stream, parents, offsets, kv_lens, positions, masks)
+    check("tpa_draft_masks", lib().tpa_draft_masks(*at, n, rows, min(window, 2 ** 31 - 1), positions.data_ptr(),
+                                                   masks.data_ptr(), words, st))
+    return positions, masks
+
+
+def accept_drafts(parents: torch.Tensor, offsets: torch.Tensor, draft_tokens: torch.Tensor, sampled: torch.Tensor,
+                  max_path: int, out: tuple | None = None, stream=None):
+    """The path that sampled tokens follow through drafted trees (tpa_accept_drafts).
+
+    Row 0 of a sequence's new tokens is its last sampled token; behind a row that stands, its child stands whose
+    ``draft_tokens`` entry is the one ``sampled`` behind the row (both [tokens] int32).  Returns tokens [S, max_path]
+    (the sequences' next tokens, then -1), path [S, max_path] (the standing rows, then -1: for ``paged_compact``)
+    and the number of standing rows [S], int32."""
+    rows, n, most = parents.shape[0], offsets.shape[0] - 1, int(max_path)
+    if not 1 <= most <= 1024:
+        raise ValueError("max_path must be in [1, 1024]")
+    at = (_vector("parents", parents, rows), _vector("offsets", offsets, n + 1), _vector("draft_tokens", draft_tokens, rows),
+          _vector("sampled", sampled, rows))
+    if out is None:
+        st = _launch_stream(stream, parents, offsets, draft_tokens, sampled)
+        dev, i32 = parents.device, torch.int32
+        tokens, path, n_accepted = _new(stream, (n, most), i32, dev), _new(stream, (n, most), i32, dev), _new(stream, (n,), i32, dev)
+    else:
+        tokens, path, n_accepted = out
+        _table("tokens", tokens, n, most)
+        _table("path", path, n, most)
+        _vector("n_accepted", n_accepted, n)
+        st = _launch_stream(stream, parents, offsets, draft_tokens, sampled, tokens, path, n_accepted)
+    check("tpa_accept_drafts", lib().tpa_accept_drafts(*at, n, rows, tokens.data_ptr(), path.data_ptr(), n_accepted.data_ptr(),
+                                                       most, st))
+    return tokens, path, n_accepted
+
+
+def _layers(k_cache, v_cache) -> tuple:
+    """(layers, n_pages, Hkv, page_size, d) of bf16 caches of that shape, or of one layer's."""
+    shape = k_cache.shape
+    if (k_cache.dtype is not torch.bfloat16 or v_cache.dtype is not torch.bfloat16 or v_cache.shape != shape or
+            not k_cache.is_contiguous() or not v_cache.is_contiguous()):
+        raise ValueError("k_cache and v_cache must be contiguous bf16 tensors of one shape")
+    if len(shape) == 4:
+        return (1, *shape)
+    if len(shape) != 5 or shape[0] < 1:
+        raise ValueError("k_cache and v_cache must be [layers, n_pages, Hkv, page_size, d] or one layer's")
+    return tuple(shape)
+
+
+def _pages(pages) -> tuple[int, int, int, int]:
+    """(address, rows, width, row stride) of a page table."""
+    if pages.dtype is not torch.int32 or pages.dim() != 2 or pages.stride(1) != 1:
+        raise ValueError("pages must be an int32 tensor [n_seqs, max_pages] with unit column stride")
+    n, width = pages.shape
+    return pages.data_ptr(), n, width, pages.stride(0) if n > 1 else max(width, 1)
+
+
+def paged_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Tensor, offsets: torch.Tensor,
+                  kv_lens: torch.Tensor, path: torch.Tensor, n_accepted: torch.Tensor, out: torch.Tensor | None = None,
+                  stream=None) -> torch.Tensor:
+    """Move an accepted path's keys and values to where their sequences go on
+    (tpa_paged_compact), in all layers of caches [layers, n_pages, Hkv, page_size, d] (or one layer's); returns
+    the sequences' new lengths [S] int32, ``kv_lens`` without the new tokens that do not stand.
+
+    ``offsets`` and ``kv_lens`` are those of the step's ``paged_append``; ``path`` and ``n_accepted``
+    come from ``accept_drafts``."""
+    layers, n_pages, heads, page, d = _layers(k_cache, v_cache)
+    at, n, width, stride = _pages(pages)
+    if path.dim() != 2:
+        raise ValueError("path must be an int32 tensor [n_seqs, max_path]")
+    most = path.shape[1]
+    # (the rows of the step's tensors are told by the offsets alone: no call has more)
+    cache = PAGED_VIEW.pack(k_cache.data_ptr(), v_cache.data_ptr(), at, _vector("offsets", offsets, n + 1),
+                            _vector("kv_lens", kv_lens, n), n_pages, page, n, width, stride, heads, d, 2 ** 30 - 1 if n else 0)
+    at_path, at_n = _table("path", path, n, most), _vector("n_accepted", n_accepted, n)
+    st = _launch_stream(stream, k_cache, v_cache, pages, offsets, kv_lens, path, n_accepted, out)
+    if out is None:
+        out = _new(stream, (n,), torch.int32, kv_lens.device)
+    else:
+        _vector("out", out, n)
+    check("tpa_paged_compact", lib().tpa_paged_compact(cache, layers, at_path, at_n, most, out.data_ptr(), st))
+    return out
+
+
+def paged_resize(pages: torch.Tensor, kv_lens: torch.Tensor, refs: torch.Tensor, page_size: int,
+                 out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Give every sequence the pages that its length needs (tpa_paged_resize):
+    new ones for those that grow, none for those of length 0, whose pages go back.
+
+    ``pages`` [S, max_pages] int32 (-1 where a row has no page) and ``refs`` [n_pages] int32 (0: free), both changed
+    in place, are the state of a cache's pages: start with -1 and 0.  ``kv_lens`` [S] int32 are the lengths wanted.
+    Returns the number of free pages left [1] int32; negative, and no row has grown, where that many are missing."""
+    at, n, width, stride = _pages(pages)
+    n_pages = refs.shape[0]
+    pool = PAGED_POOL.pack(0, 0, at, _vector("kv_lens", kv_lens, n), _vector("refs", refs, n_pages), 0, n_pages,
+                           _int32("page_size", page_size), 0, 0, n, width, stride)
+    st = _launch_stream(stream, refs, pages, kv_lens, out)
+    if out is None:
+        out = _new(stream, (1,), torch.int32, refs.device)
+    else:
+        _vector("out", out, 1)
+    check("tpa_paged_resize", lib().tpa_paged_resize(pool, out.data_ptr(), st))
+    return out
+
+
+def paged_fork(k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Tensor, kv_lens: torch.Tensor,
+               refs: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, out: torch.Tensor | None = None,
+               stream=None) -> torch.Tensor:
+    """Make sequences copies of others (tpa_paged_fork), as the samples of a
+    prompt are: rows ``dst`` [F] of ``pages`` and ``kv_lens`` become those of rows ``src`` [F], with whole
+    pages shared and the last, partly filled one copied in all layers of the caches.
+
+    State, caches and result as for ``paged_resize`` and ``paged_compact``; what the dst rows held goes back first."""
+    layers, n_pages, heads, page, d = _layers(k_cache, v_cache)
+    at, n, width, stride = _pages(pages)
+    pool = PAGED_POOL.pack(k_cache.data_ptr(), v_cache.data_ptr(), at, _vector("kv_lens", kv_lens, n),
+                           _vector("refs", refs, n_pages), layers, n_pages, page, heads, d, n, width, stride)
+    forks = src.shape[0]
+    at_src, at_dst = _vector("src", src, forks), _vector("dst", dst, forks)
+    st = _launch_stream(stream, refs, k_cache, v_cache, pages, kv_lens, src, dst, out)
+    if out is None:
+        out = _new(stream, (1,), torch.int32, refs.device)
+    else:
+        _vector("out", out, 1)
+    check("tpa_paged_fork", lib().tpa_paged_fork(pool, at_src, at_dst, forks, out.data_ptr(), st))
+    return out
+
+
+def _row_parameter(name: str, value: torch.Tensor, rows: int, dtype: torch.dtype) -> int:
+    """The address of a parameter that is a tensor of one number a row."""
+    if value.dtype is not dtype or value.shape != (rows,) or not value.is_contiguous():
+        raise ValueError(f"{name} must be a number or a contiguous {dtype} tensor [rows]")
+    return value.data_ptr()
+
+
+def sample_tokens(logits: torch.Tensor, u: torch.Tensor, temperature: "float | torch.Tensor" = 1.0,
+                  top_k: "int | torch.Tensor" = 0, top_p: "float | torch.Tensor" = 1.0,
+                  min_p: "float | torch.Tensor" = 0.0, out: tuple | None = None, stream=None):
+    """Draw a token for each row of logits from given uniform numbers
+    (tpa_sample_tokens): temperature, then top-k, top-p and min-p.
+
+    logits [N, V] fp32 or bf16 with unit column stride, u [N] fp32 in [0, 1).  Each parameter is a number or a tensor
+    [N] (fp32, top_k int32): a temperature of 0 takes the largest logit; top_k <= 0, top_p = 1 and min_p = 0 keep all.
+    Returns tokens [N] int32 and their log-probabilities in the distribution that they were drawn from, [N] fp32."""
+    f32, i32, T = torch.float32, torch.int32, torch.Tensor
+    bf16 = logits.dtype is torch.bfloat16
+    if logits.dim() != 2 or not (bf16 or logits.dtype is f32) or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be fp32 or bf16 [rows, vocabulary] with unit column stride")
+    N, V = logits.shape
+    _int32("the number of rows", N)
+    _int32("the vocabulary", V)
+    if u.dtype is not f32 or u.shape != (N,) or not u.is_contiguous():
+        raise ValueError("u must be a contiguous fp32 tensor [rows]")
+    t = p = m = k = None  # the ones that are tensors
+    t_at = p_at = m_at = k_at = 0
+    if isinstance(temperature, T):
+        t, t_at, temperature = temperature, _row_parameter("temperature", temperature, N, f32), 1.0
+    if isinstance(top_k, T):
+        k, k_at, top_k = top_k, _row_parameter("top_k", top_k, N, i32), 0
+    if isinstance(top_p, T):
+        p, p_at, top_p = top_p, _row_parameter("top_p", top_p, N, f32), 1.0
+    if isinstance(min_p, T):
+        m, m_at, min_p = min_p, _row_parameter("min_p", min_p, N, f32), 0.0
+    params = SAMPLE_PARAMS.pack(t_at, p_at, m_at, k_at, temperature, top_p, min_p, _int32("top_k", top_k))
+    if out is None:
+        st = _launch_stream(stream, logits, u, t, p, m, k)
+        tokens, logp = _new(stream, (N,), i32, logits.device), _new(stream, (N,), f32, logits.device)
+    else:
+        tokens, logp = out
+        _vector("tokens", tokens, N)
+        if logp.dtype is not f32 or logp.shape != (N,) or not logp.is_contiguous():
+            raise ValueError("logp must be a contiguous fp32 tensor [rows]")
+        st = _launch_stream(stream, logits, u, t, p, m, k, tokens, logp)
+    check("tpa_sample_tokens", lib().tpa_sample_tokens(
+        logits.data_ptr(), LOGITS_BF16 if bf16 else LOGITS_F32, logits.stride(0) if N > 1 else V, N, V, params, u.data_ptr(),
+        tokens.data_ptr(), logp.data_ptr(), st))
+    return tokens, logp
 
 
 def sync_status(stream=None) -> None:

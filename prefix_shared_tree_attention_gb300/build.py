@@ -24,7 +24,7 @@ DEBUG_LIB_PATH = os.path.join(LIB_DIR, "libtpa_debug.so")
 
 CUDA_SOURCES = ["runtime.cu", "classify.cu", "logprobs.cu", "attn_fwd.cu", "attn_bwd.cu", "dense_mask.cu", "lm_head.cu",
                 "rope.cu", "verify.cu", "paged_attn.cu", "paged_tile.cu",
-                "paged_few.cu"]
+                "paged_few.cu", "sample.cu", "draft.cu", "pages.cu"]
 HOST_SOURCES = ["pack.cpp", "balance.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -34,6 +34,9 @@ unsigned int* tpa_internal_status_rope();
 unsigned int* tpa_internal_status_verify();
 unsigned int* tpa_internal_status_pfew();
 unsigned int* tpa_internal_status_ptile();
+unsigned int* tpa_internal_status_sample();
+unsigned int* tpa_internal_status_draft();
+unsigned int* tpa_internal_status_pages();
 
 // The per-sequence gather of the log-prob pass (logprobs.cu), shared with
 // the fused LM-head path: seq_entropy[t] = pos_entropy[position of token t],

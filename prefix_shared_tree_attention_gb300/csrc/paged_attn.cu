@@ -30,6 +30,7 @@ using namespace paged;
 // takes a row; with more (a long sequence by itself) the CTA's eight warps take
 // a share of one row's parts each.
 constexpr int kFewParts = 16;
+constexpr int kJoinCtas = 4;  // of an SM, all there at once
 
 template <int D>
 __device__ __forceinline__ void join_row_by_warp(const Params& p, const Split& s, int r, int lane) {
@@ -90,18 +91,49 @@ __global__ void __launch_bounds__(256, 4) paged_join_kernel(const Params p) {
   __shared__ float acc_s[8][D];
   __shared__ float scale_s[kMaxGrid];
   __shared__ float top_s[8], sum_s[8];
+  __shared__ Split split_s[kMaxGrid];
+  __shared__ int warp_units[8], tile_s, first_s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   tc::grid_launch_dependents();
   tc::grid_wait_prior();
-  const Split s = p.split[blockIdx.x];
-  if (!s.valid) return;
-  const int parts = s.c1 - s.c0 + 1;
-  if (parts <= kFewParts) {
-    for (int r = blockIdx.y * 8 + warp; r < s.n * p.b.group; r += gridDim.y * 8) join_row_by_warp<D>(p, s, r, lane);
-    return;
+  // The work of all split tiles in one line: eight rows with few parts, or one with many, at a time.  A CTA takes every
+  // gridDim.x-th piece, so that the rows of one long sequence's few tiles find as many CTAs as those of many tiles.
+  int units = 0;
+  if (int(threadIdx.x) < p.grid) {
+    const Split s = p.split[threadIdx.x];
+    split_s[threadIdx.x] = s;
+    const int rows = s.n * p.b.group;
+    if (s.valid) units = s.c1 - s.c0 < kFewParts ? (rows + 7) >> 3 : rows;
   }
-  auto slot = [&](int i) { return int64_t(2) * (s.c0 + i) + (i == 0 ? 1 : 0); };
-  for (int r = blockIdx.y; r < s.n * p.b.group; r += gridDim.y) {
+  int end = units;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, end, o);
+    if (lane >= o) end += t;
+  }
+  if (lane == 31) warp_units[warp] = end;
+  __syncthreads();
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    if (w < warp) end += warp_units[w];
+    total += warp_units[w];
+  }
+  for (int unit = blockIdx.x; unit < total; unit += gridDim.x) {
+    if (unit < end && unit >= end - units) {
+      tile_s = threadIdx.x;
+      first_s = unit - (end - units);
+    }
+    __syncthreads();
+    const Split s = split_s[tile_s];
+    const int piece = first_s, parts = s.c1 - s.c0 + 1;
+    auto slot = [&](int i) { return int64_t(2) * (s.c0 + i) + (i == 0 ? 1 : 0); };
+    if (parts <= kFewParts) {
+      if (piece * 8 + warp < s.n * p.b.group) join_row_by_warp<D>(p, s, piece * 8 + warp, lane);
+      __syncthreads();  // tile_s is read
+      continue;
+    }
+    const int r = piece;
     float2 ml = make_float2(-INFINITY, 0.f);  // thread i: part i
     if (int(threadIdx.x) < parts) ml = p.part_ml[slot(threadIdx.x) * p.rows + r];
     auto value = [&](int k) {
@@ -196,9 +228,64 @@ uint64_t part_bytes(int rows, int d) {
 }
 
 template <int D>
-int launch_join(const Params& p, int grid, int64_t rows, cudaStream_t st) {
-  return launch_overlapped(paged_join_kernel<D>, dim3(grid, unsigned(rows < 8 ? rows : 8)), 256, 0, st,
-                           static_cast<const Params>(p));
+int launch_join(const Params& p, cudaStream_t st) {
+  return launch_overlapped(paged_join_kernel<D>, dim3(kJoinCtas * p.grid), 256, 0, st, static_cast<const Params>(p));
+}
+
+// Both forms of the call; masks NULL: chains.
+int attend(const tpa_paged_view* cache, const void* q, int64_t q_stride, const int32_t* masks, int32_t mask_words,
+           const int32_t* positions, void* o, float* lse, int32_t n_heads_q, int32_t max_q_len, float softmax_scale,
+           int32_t window, void* workspace, uint64_t workspace_bytes, void* stream) {
+  const int rc = tpa_internal_check_paged(cache);
+  if (rc != TPA_OK) return rc;
+  const int d = cache->head_dim, hkv = cache->n_heads_kv;
+  if (n_heads_q < 1 || n_heads_q > 65535 || n_heads_q % hkv || n_heads_q / hkv > 64 || window < 0 ||
+      max_q_len < (cache->n_rows ? 1 : 0) || std::isnan(softmax_scale) || std::isinf(softmax_scale))
+    return TPA_ERR_INVALID_ARG;
+  if (cache->n_rows == 0) return TPA_OK;
+  auto al = [](const void* x, uintptr_t a) { return (reinterpret_cast<uintptr_t>(x) & (a - 1)) == 0; };
+  if (!q || !o || !lse || !workspace || !al(q, 16) || !al(o, 16) || !al(lse, 4) || !al(workspace, 256) ||
+      q_stride < int64_t(n_heads_q) * d || q_stride % 8 || q_stride >= (int64_t(1) << 40))
+    return TPA_ERR_INVALID_ARG;
+  const int group = n_heads_q / hkv, R = tile_rows(max_q_len, group);
+  if (workspace_bytes < part_bytes(R, d)) return TPA_ERR_BUFFER_TOO_SMALL;
+  Params p = {};
+  p.b.pages = cache->pages;
+  p.b.offsets = cache->offsets;
+  p.b.kv_lens = cache->kv_lens;
+  p.b.n_pages = cache->n_pages;
+  p.b.page_shift = cache->page_size == 16 ? 4 : cache->page_size == 32 ? 5 : cache->page_size == 64 ? 6 : 7;
+  p.b.n_seqs = cache->n_seqs;
+  p.b.max_pages = cache->max_pages;
+  p.b.page_stride = cache->page_stride;
+  p.b.hkv = hkv;
+  p.b.n_rows = cache->n_rows;
+  p.b.group = group;
+  // positions are below 2^30: a longer window reaches no further, and differences with this one stay in 32 bits
+  p.b.window = window < (1 << 30) ? window : 1 << 30;
+  p.b.masks = reinterpret_cast<const uint32_t*>(masks);
+  p.b.positions = positions;
+  p.b.mask_words = mask_words;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_stride = q_stride;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.hq = n_heads_q;
+  p.rows = R;
+  p.scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf(float(d))) * kLog2e;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.part_o = reinterpret_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(ws + uint64_t(2) * kMaxGrid * R * d * 4);
+  p.split = reinterpret_cast<Split*>(ws + uint64_t(2) * kMaxGrid * R * (uint64_t(d) * 4 + 8));
+  int sms = 0;
+  const int dv = device_sms(&sms);
+  if (dv != TPA_OK) return dv;
+  const int grid = sms < kMaxGrid ? sms : kMaxGrid;
+  p.grid = grid;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int rt = R == 256 ? tpa_internal_paged_tile(cache, p, grid, st) : tpa_internal_paged_few(cache, p, R, grid, st);
+  if (rt != TPA_OK) return rt;
+  return d == 128 ? launch_join<128>(p, st) : launch_join<64>(p, st);
 }
 
 }  // namespace
@@ -215,51 +302,21 @@ extern "C" int tpa_paged_attn_fwd(const tpa_paged_view* cache, const void* q, in
                                   int32_t n_heads_q, int32_t max_q_len, float softmax_scale, int32_t window,
                                   void* workspace, uint64_t workspace_bytes, void* stream) {
   TPA_NVTX_RANGE("tpa_paged_attn_fwd");
+  return attend(cache, q, q_stride, nullptr, 0, nullptr, o, lse, n_heads_q, max_q_len, softmax_scale, window, workspace,
+                workspace_bytes, stream);
+}
+
+extern "C" int tpa_paged_attn_tree_fwd(const tpa_paged_view* cache, const void* q, int64_t q_stride, const int32_t* masks,
+                                       int32_t mask_words, const int32_t* positions, void* o, float* lse, int32_t n_heads_q,
+                                       int32_t max_q_len, float softmax_scale, int32_t window, void* workspace,
+                                       uint64_t workspace_bytes, void* stream) {
+  TPA_NVTX_RANGE("tpa_paged_attn_tree_fwd");
   const int rc = tpa_internal_check_paged(cache);
   if (rc != TPA_OK) return rc;
-  const int d = cache->head_dim, hkv = cache->n_heads_kv;
-  if (n_heads_q < 1 || n_heads_q > 65535 || n_heads_q % hkv || n_heads_q / hkv > 64 || window < 0 ||
-      max_q_len < (cache->n_rows ? 1 : 0) || std::isnan(softmax_scale) || std::isinf(softmax_scale))
+  auto al4 = [](const void* x) { return (reinterpret_cast<uintptr_t>(x) & 3) == 0; };
+  if (mask_words < 1 || mask_words > 32 || !al4(masks) || !al4(positions) ||
+      (cache->n_rows > 0 && (!masks || (window > 0 && !positions))))
     return TPA_ERR_INVALID_ARG;
-  if (cache->n_rows == 0) return TPA_OK;
-  auto al = [](const void* x, uintptr_t a) { return (reinterpret_cast<uintptr_t>(x) & (a - 1)) == 0; };
-  if (!q || !o || !lse || !workspace || !al(q, 16) || !al(o, 16) || !al(lse, 4) || !al(workspace, 256) ||
-      q_stride < int64_t(n_heads_q) * d || q_stride % 8 || q_stride >= (int64_t(1) << 40))
-    return TPA_ERR_INVALID_ARG;
-  const int group = n_heads_q / hkv, R = tile_rows(max_q_len, group);
-  const int64_t rows = int64_t(max_q_len) * group;  // of the largest sequence
-  if (workspace_bytes < part_bytes(R, d)) return TPA_ERR_BUFFER_TOO_SMALL;
-  Params p = {};
-  p.b.pages = cache->pages;
-  p.b.offsets = cache->offsets;
-  p.b.kv_lens = cache->kv_lens;
-  p.b.n_pages = cache->n_pages;
-  p.b.page_shift = cache->page_size == 16 ? 4 : cache->page_size == 32 ? 5 : cache->page_size == 64 ? 6 : 7;
-  p.b.n_seqs = cache->n_seqs;
-  p.b.max_pages = cache->max_pages;
-  p.b.page_stride = cache->page_stride;
-  p.b.hkv = hkv;
-  p.b.n_rows = cache->n_rows;
-  p.b.group = group;
-  // positions are below 2^30: a longer window reaches no further, and differences with this one stay in 32 bits
-  p.b.window = window < (1 << 30) ? window : 1 << 30;
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.q_stride = q_stride;
-  p.o = static_cast<__nv_bfloat16*>(o);
-  p.lse = lse;
-  p.hq = n_heads_q;
-  p.rows = R;
-  p.scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf(float(d))) * kLog2e;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  p.part_o = reinterpret_cast<float*>(ws);
-  p.part_ml = reinterpret_cast<float2*>(ws + uint64_t(2) * kMaxGrid * R * d * 4);
-  p.split = reinterpret_cast<Split*>(ws + uint64_t(2) * kMaxGrid * R * (uint64_t(d) * 4 + 8));
-  int sms = 0;
-  const int dv = device_sms(&sms);
-  if (dv != TPA_OK) return dv;
-  const int grid = sms < kMaxGrid ? sms : kMaxGrid;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int rt = R == 256 ? tpa_internal_paged_tile(cache, p, grid, st) : tpa_internal_paged_few(cache, p, R, grid, st);
-  if (rt != TPA_OK) return rt;
-  return d == 128 ? launch_join<128>(p, grid, rows, st) : launch_join<64>(p, grid, rows, st);
+  return attend(cache, q, q_stride, masks, mask_words, positions, o, lse, n_heads_q, max_q_len, softmax_scale, window, workspace,
+                workspace_bytes, stream);
 }

@@ -39,6 +39,11 @@ struct Batch {
   int32_t group;     // query heads of a key/value head
   int32_t tile_tok;  // tokens of a tile
   int32_t window;    // 0: none
+  // Drafted trees (NULL: chains): which of a sequence's new tokens each of them sees, mask_words words of bits a row, and,
+  // read with a window, the rows' positions.
+  const uint32_t* masks;
+  const int32_t* positions;
+  int32_t mask_words;
 };
 
 struct Seq {
@@ -48,7 +53,8 @@ struct Seq {
 // A sequence whose numbers are out of range has no tokens (and is reported).
 __device__ __forceinline__ Seq load_seq(const Batch& b, int s, unsigned int* status) {
   const int o0 = __ldg(b.offsets + s), o1 = __ldg(b.offsets + s + 1), kv = __ldg(b.kv_lens + s);
-  if (o0 < 0 || o1 < o0 || o1 > b.n_rows || kv < 0 || kv > (int64_t(b.max_pages) << b.page_shift)) {
+  if (o0 < 0 || o1 < o0 || o1 > b.n_rows || kv < 0 || kv > (int64_t(b.max_pages) << b.page_shift) ||
+      (b.masks && o1 - o0 > 32 * b.mask_words)) {
     if (status) atomicOr(status, TPA_DEV_BAD_INPUT);
     return Seq{0, 0, 0};
   }
@@ -74,7 +80,8 @@ __device__ __forceinline__ Tile make_tile(const Batch& b, const Seq& q, int i) {
   t.pos0 = q.kv - q.n + t0;
   t.hi = max(t.pos0 + t.n, 0);
   t.end = q.kv;
-  t.lo = b.window > 0 ? max(t.pos0 - b.window + 1, 0) : 0;
+  // (in a tree, each token's position may be as low as the first one's)
+  t.lo = b.window > 0 ? max((b.masks ? q.kv - q.n : t.pos0) - b.window + 1, 0) : 0;
   t.step0 = t.lo >> kStepShift;
   t.steps = max(((t.hi + kStep - 1) >> kStepShift) - t.step0, 1);
   return t;
@@ -250,6 +257,7 @@ struct Params {
   Split* split;     // [grid]
   int64_t q_stride;
   int32_t hq, rows;  // rows: R, of a part
+  int32_t grid;      // CTAs of the attention kernel
   float scale_log2;
 };
 
@@ -262,11 +270,17 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* m, uin
       : "memory");
 }
 
+// The position of a drafted token, number i of its sequence: between the tree's first and the one that a chain would have.
+__device__ __forceinline__ int tree_position(const Batch& b, int row, int base, int i) {
+  return min(max(__ldg(b.positions + row), base), base + i);
+}
+
 // One CTA's part of a tile, as the producer hands it to the other roles.
 struct Segment {
   int32_t n_it;  // steps; -1: no more
   int32_t head, first, n, pos0, lo, hi, key0, whole, slot;
-  int32_t pad_[2];
+  int32_t at;  // number of the tile's first token among its sequence's new ones
+  int32_t pad_;
 };
 
 __device__ __forceinline__ float max3(float a, float b, float c) {

@@ -130,7 +130,7 @@ __device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[N]) {
   else tc::tmem_ld32(at, r);
 }
 
-template <int D, int NR>
+template <int D, int NR, bool TREE>
 __global__ void __launch_bounds__(512, 1)
     paged_few_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const Params p) {
@@ -248,6 +248,7 @@ __global__ void __launch_bounds__(512, 1)
           sg->lo = w.t.lo;
           sg->hi = w.t.hi;
           sg->key0 = key0;
+          if (TREE) sg->at = w.i * p.b.tile_tok;
           sg->whole = w.begin == 0 && w.end == w.t.steps;
           sg->slot = blockIdx.x * 2 + (w.begin == 0 ? 1 : 0);
           tc::mbar_arrive(seg_full + (k & 3));
@@ -395,11 +396,13 @@ __global__ void __launch_bounds__(512, 1)
       if (group_any(h, !fine)) break;
       const volatile Segment* sg = seg_ring + (k & 3);
       const int n_it = sg->n_it, n_tok = sg->n, lo = sg->lo, hi = sg->hi, key_first = sg->key0, pos_first = sg->pos0;
+      const int row_first = TREE ? sg->first : 0, at_first = TREE ? sg->at : 0;
       tc::mbar_arrive(seg_empty + (k & 3));
       if (n_it < 0) break;
       const uint32_t tO = tmem + lane_base + o_col(k, h);
       // every row in use sees the keys in [all_lo, all_hi)
-      const int all_hi = pos_first + 1;
+      const int base = pos_first - at_first;  // (TREE) the sequence's tokens before its tree
+      const int all_hi = TREE ? base : pos_first + 1;
       const int all_lo = p.b.window > 0 ? pos_first + n_tok - p.b.window : 0;
       // Rows behind the tile's own (the load brings the next sequence's queries, or padding) never pass an infinite
       // maximum, so they have no say in when the others' are moved, and no bit of those depends on what they hold.  Their
@@ -442,6 +445,25 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
         for (int i = 0; i < NR; ++i) x[i] = __uint_as_float(raw[i]) * p.scale_log2;
         if (key0 + kStep > all_hi || key0 < all_lo) {
+          if constexpr (TREE) {
+            // the rows that see this thread's key, a bit each
+            const int key = key0 + r, drafted = key - base;
+            const uint32_t heads = p.b.group < 32 ? (1u << p.b.group) - 1 : ~0u;
+            uint32_t rows = 0;
+            if (key < hi)
+              for (int t_ = 0; t_ < n_tok; ++t_) {
+                bool sees;
+                if (drafted < 0)
+                  sees = p.b.window == 0 || key > tree_position(p.b, row_first + t_, base, at_first + t_) - p.b.window;
+                else
+                  sees = drafted <= at_first + t_ &&
+                         (__ldg(p.b.masks + int64_t(row_first + t_) * p.b.mask_words + (drafted >> 5)) >> (drafted & 31) & 1);
+                if (sees) rows |= heads << (t_ * p.b.group);
+              }
+#pragma unroll
+            for (int i = 0; i < NR; ++i)
+              if (!(rows >> i & 1)) x[i] = -INFINITY;
+          } else {
           // rows [first_row, last_row) see this thread's key
           const int rel = key0 + r - pos_first;
           int first_row = max(rel, 0) * p.b.group, last_row = NR;
@@ -450,6 +472,7 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
           for (int i = 0; i < NR; ++i)
             if (i < first_row || i >= last_row) x[i] = -INFINITY;
+          }
         }
         bool grow = j == j0;
 #pragma unroll
@@ -616,7 +639,7 @@ __global__ void __launch_bounds__(512, 1)
   if (warp == W_MMA) tc::tmem_dealloc(tmem, C::TMEM_COLS);
 }
 
-template <int D, int NR>
+template <int D, int NR, bool TREE>
 int launch_few(const tpa_paged_view* c, Params& p, int grid, cudaStream_t st) {
   using C = FewCfg<D, NR>;
   CUtensorMap tq, tk, tv;
@@ -625,11 +648,11 @@ int launch_few(const tpa_paged_view* c, Params& p, int grid, cudaStream_t st) {
   if (!query_map(&tq, c, p, p.b.tile_tok) || !cache_map(&tk, c->k_cache, rows, D, c->page_size) ||
       !cache_map(&tv, c->v_cache, rows, D, c->page_size))
     return TPA_ERR_CUDA;
-  TPA_CUDA_TRY(cudaFuncSetAttribute(paged_few_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES));
+  TPA_CUDA_TRY(cudaFuncSetAttribute(paged_few_kernel<D, NR, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES));
   cudaFuncAttributes fa;
-  TPA_CUDA_TRY(cudaFuncGetAttributes(&fa, paged_few_kernel<D, NR>));
+  TPA_CUDA_TRY(cudaFuncGetAttributes(&fa, paged_few_kernel<D, NR, TREE>));
   if (fa.numRegs != C::REG_LAUNCH) return TPA_ERR_BAD_BUILD;  // the setmaxnreg split would not add up
-  return launch_overlapped(paged_few_kernel<D, NR>, dim3(grid), C::THREADS, C::BYTES, st, tq, tk, tv,
+  return launch_overlapped(paged_few_kernel<D, NR, TREE>, dim3(grid), C::THREADS, C::BYTES, st, tq, tk, tv,
                            static_cast<const Params>(p));
 }
 
@@ -638,6 +661,14 @@ int launch_few(const tpa_paged_view* c, Params& p, int grid, cudaStream_t st) {
 TPA_DEFINE_STATUS_READER(tpa_internal_status_pfew, g_status_pfew)
 
 int tpa_internal_paged_few(const tpa_paged_view* c, Params& p, int rows, int grid, cudaStream_t st) {
-  if (c->head_dim == 128) return rows == 16 ? launch_few<128, 16>(c, p, grid, st) : launch_few<128, 32>(c, p, grid, st);
-  return rows == 16 ? launch_few<64, 16>(c, p, grid, st) : launch_few<64, 32>(c, p, grid, st);
+  auto launch = [&](auto d, auto nr) {
+    constexpr int D = decltype(d)::value, NR = decltype(nr)::value;
+    return p.b.masks ? launch_few<D, NR, true>(c, p, grid, st) : launch_few<D, NR, false>(c, p, grid, st);
+  };
+  using std::integral_constant;
+  if (c->head_dim == 128)
+    return rows == 16 ? launch(integral_constant<int, 128>(), integral_constant<int, 16>())
+                      : launch(integral_constant<int, 128>(), integral_constant<int, 32>());
+  return rows == 16 ? launch(integral_constant<int, 64>(), integral_constant<int, 16>())
+                    : launch(integral_constant<int, 64>(), integral_constant<int, 32>());
 }

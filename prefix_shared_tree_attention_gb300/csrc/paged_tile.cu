@@ -82,7 +82,7 @@ struct TileCfg {
   static_assert(BYTES <= kSmemMax, "shared memory budget");
 };
 
-template <int D>
+template <int D, bool TREE>
 __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
     paged_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const Params p) {
@@ -180,6 +180,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             sg->lo = w.t.lo;
             sg->hi = w.t.end;
             sg->key0 = key0;
+            if (TREE) sg->at = w.i * p.b.tile_tok;
             sg->whole = w.begin == 0 && w.end == w.t.steps;
             sg->slot = blockIdx.x * 2 + (w.begin == 0 ? 1 : 0);
             tc::mbar_arrive(seg_full + (k & 1));
@@ -320,6 +321,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
       const volatile Segment* sg = seg_ring + (k & 1);
       const int n_it = sg->n_it, first = sg->first, n_tok = sg->n, lo = sg->lo, end = sg->hi, key_first = sg->key0;
       const int slot = sg->whole ? -1 : sg->slot, head = sg->head * p.b.group + gh, pos_first = sg->pos0;
+      const int at_first = TREE ? sg->at : 0;
       tc::mbar_arrive(seg_empty + (k & 1));
       if (n_it < 0) break;
       if (h * sub_tok >= n_tok) {  // nothing in this sub-tile
@@ -329,7 +331,8 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
       const bool live = r < sub_tok * p.b.group && tok < n_tok;
       const int pos = live ? pos_first + tok : -1;
       // every live row of the sub-tile sees the keys in [all_lo, all_hi)
-      const int all_hi = pos_first + h * sub_tok + 1;
+      const int base = pos_first - at_first;  // (TREE) the sequence's tokens before its tree
+      const int all_hi = TREE ? base : pos_first + h * sub_tok + 1;
       const int all_lo = p.b.window > 0 ? pos_first + min((h + 1) * sub_tok, n_tok) - p.b.window : 0;
       float m_run = -INFINITY, l_run = 0.f;
       for (int j = 0; j < n_it; ++j) {
@@ -362,10 +365,30 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
 #pragma unroll
           for (int c = 0; c < 128; ++c)
             if (c > last) sv[c] = 0xff800000u;  // -inf
+          if (TREE && live && key0 + kStep > base) {
+            // the row's bits for the step's columns: all before the tree, then those of its mask
+            const uint32_t* mask = p.b.masks + int64_t(first + tok) * p.b.mask_words;
+            auto word = [&](int i) { return i < p.b.mask_words ? __ldg(mask + i) : 0u; };
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const int rel = key0 + 32 * w - base;
+              uint32_t bits = ~0u;
+              if (rel >= 0) bits = __funnelshift_r(word(rel >> 5), word((rel >> 5) + 1), rel & 31);
+              else if (rel > -32) bits = word(0) << -rel | ((1u << -rel) - 1);
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (!(bits >> c & 1)) sv[32 * w + c] = 0xff800000u;
+            }
+          }
           if (p.b.window > 0) {
+            int below = last - p.b.window;
+            if (TREE) {  // of the tokens before the tree; its own are the mask's
+              const int mine = live ? tree_position(p.b, first + tok, base, at_first + tok) : -1;
+              below = min(mine - p.b.window, base - 1) - key0;
+            }
 #pragma unroll
             for (int c = 0; c < 128; ++c)
-              if (c <= last - p.b.window) sv[c] = 0xff800000u;
+              if (c <= below) sv[c] = 0xff800000u;
           }
         }
         // row max: 8 independent chains, then a short tree
@@ -505,7 +528,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
   if (warp == W_MMA) tc::tmem_dealloc(tmem, C::TMEM_COLS);
 }
 
-template <int D>
+template <int D, bool TREE>
 int launch_tile(const tpa_paged_view* c, Params& p, int grid, cudaStream_t st) {
   using C = TileCfg<D>;
   const int sub_tok = 128 / p.b.group;
@@ -515,13 +538,13 @@ int launch_tile(const tpa_paged_view* c, Params& p, int grid, cudaStream_t st) {
       !cache_map(&tv, c->v_cache, rows, D, c->page_size))
     return TPA_ERR_CUDA;
   p.b.tile_tok = NH * sub_tok;
-  TPA_CUDA_TRY(cudaFuncSetAttribute(paged_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES));
+  TPA_CUDA_TRY(cudaFuncSetAttribute(paged_tile_kernel<D, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES));
   {
     cudaFuncAttributes fa;
-    TPA_CUDA_TRY(cudaFuncGetAttributes(&fa, paged_tile_kernel<D>));
+    TPA_CUDA_TRY(cudaFuncGetAttributes(&fa, paged_tile_kernel<D, TREE>));
     if (fa.numRegs != C::REG_LAUNCH) return TPA_ERR_BAD_BUILD;  // the setmaxnreg split would not add up
   }
-  return launch_overlapped(paged_tile_kernel<D>, dim3(grid), C::THREADS, C::BYTES, st, tq, tk, tv,
+  return launch_overlapped(paged_tile_kernel<D, TREE>, dim3(grid), C::THREADS, C::BYTES, st, tq, tk, tv,
                            static_cast<const Params>(p));
 }
 
@@ -530,5 +553,6 @@ int launch_tile(const tpa_paged_view* c, Params& p, int grid, cudaStream_t st) {
 TPA_DEFINE_STATUS_READER(tpa_internal_status_ptile, g_status_ptile)
 
 int tpa_internal_paged_tile(const tpa_paged_view* c, Params& p, int grid, cudaStream_t st) {
-  return c->head_dim == 128 ? launch_tile<128>(c, p, grid, st) : launch_tile<64>(c, p, grid, st);
+  if (p.b.masks) return c->head_dim == 128 ? launch_tile<128, true>(c, p, grid, st) : launch_tile<64, true>(c, p, grid, st);
+  return c->head_dim == 128 ? launch_tile<128, false>(c, p, grid, st) : launch_tile<64, false>(c, p, grid, st);
 }

@@ -33,9 +33,9 @@ bool mask_layout(int32_t n_trees, int32_t t_pad, MaskLayout* L) {
   return true;
 }
 
-// The translation units' status words are brought together by a kernel and read by one copy: a copy for each of the
+// The translation units' status words are brought together by a kernel and read by one copy: a copy for each of
 // nine took 84 us a call.  Both run on the legacy default stream.
-constexpr int kStatusWords = 9;
+constexpr int kStatusWords = 12;
 struct StatusWords {
   unsigned int* at[kStatusWords];
 };
@@ -120,7 +120,8 @@ int tpa_sync_status(void* stream) {
   }
   StatusWords w = {{tpa_internal_status_classify(), tpa_internal_status_logprobs(), tpa_internal_status_fwd(),
                     tpa_internal_status_bwd(), tpa_internal_status_lmh(), tpa_internal_status_rope(),
-                    tpa_internal_status_verify(), tpa_internal_status_pfew(), tpa_internal_status_ptile()}};
+                    tpa_internal_status_verify(), tpa_internal_status_pfew(), tpa_internal_status_ptile(),
+                    tpa_internal_status_sample(), tpa_internal_status_draft(), tpa_internal_status_pages()}};
   for (unsigned int* at : w.at)
     if (!at) return TPA_ERR_CUDA;
   unsigned int v[kStatusWords] = {};

@@ -1,0 +1,1051 @@
+// The next token of each row of logits: temperature, top-k, top-p, min-p and a
+// draw from a given uniform number.  One cluster of 8 CTAs a row.
+//
+// Tokens stand in the order of their logits, highest first, equal ones by
+// index: the order of the 64-bit number (logit as an ordered 32-bit key, index
+// complemented), all of which differ.  Top-k and top-p each keep the tokens from
+// a cut on; the cuts are found by histograms, first over the distance to the row's
+// maximum in steps of T / 64, then over digits of that number, until 256
+// tokens or fewer are left, which are ranked against each other.
+//
+// A draw has to be the same whatever the order of summation, so weights
+// exp((x - max) / T) are whole numbers: 2^y, y = (x - max) log2(e) / T, with the
+// product formed as a pair of fp32, y = k / 32 + g, 2^(k / 32) from a table to 30 bits, 2^g - 1
+// by its series (|g| <= 1/64, four terms, off by 2^-39).  The product of the two is off by 2^-30 of
+// itself (the rounding of g and of the series' value), and below 2^-(62 - log2 vocab) of
+// the largest weight it is cut off.  Their sums are exact, so nothing depends on
+// the grouping, and a running sum is off by less than 2^-29 of the whole.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstddef>
+
+#include "device_common.cuh"
+#include "internal.h"
+#include "tc.cuh"
+
+namespace {
+
+__device__ unsigned int g_status_sample = 0;
+
+constexpr int kMostCtas = 8;  // of a row: a cluster
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMostParts = kMostCtas * kWarps;  // contiguous parts of a row, one a warp
+constexpr int kBins = 1024;
+constexpr int kBinsEach = kBins / kThreads;  // bins that a thread adds up, at most
+constexpr int kFew = kThreads;     // tokens that are ranked against each other, one a thread
+constexpr int kList = 512;         // candidates that a warp has room for
+constexpr float kBinsPerT = 32.f;  // bins of the first level in a distance of T
+constexpr int kMostLevels = 8;
+constexpr float kHead = 8.f, kWider = 10.5f;  // distances from the maximum, in T, within which top_p's cut is looked for first
+
+// round(2^(i / 32) * 2^30)
+__constant__ uint32_t kRoots[32] = {
+    1073741824u, 1097253708u, 1121280436u, 1145833280u, 1170923762u, 1196563654u, 1222764986u, 1249540052u,
+    1276901417u, 1304861917u, 1333434672u, 1362633090u, 1392470869u, 1422962010u, 1454120821u, 1485961921u,
+    1518500250u, 1551751076u, 1585730000u, 1620452965u, 1655936265u, 1692196547u, 1729250827u, 1767116489u,
+    1805811301u, 1845353420u, 1885761398u, 1927054196u, 1969251188u, 2012372174u, 2056437387u, 2101467502u};
+
+struct Params {
+  const void* logits;
+  int64_t row_stride;
+  const float* temperature;
+  const float* top_p;
+  const float* min_p;
+  const int32_t* top_k;
+  const float* u;
+  int32_t* tokens;
+  float* logp;
+  float temperature_all, top_p_all, min_p_all;
+  int32_t top_k_all;
+  int32_t vocab, shift;  // shift: 32 - log2 of the vocabulary, rounded up
+  int32_t ctas;          // of a row
+};
+
+constexpr float kLargest = 3.402823466e38f;  // finite number
+
+// A logit as it is compared: NaN as -inf, +inf as the largest finite number, one zero.
+__device__ __forceinline__ float clean(float x) { return fminf(fmaxf(x, -INFINITY), kLargest) + 0.f; }
+
+__device__ __forceinline__ uint32_t key_of(float x) {
+  const uint32_t b = __float_as_uint(x);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float of_key(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+__device__ __forceinline__ uint64_t number_of(float x, int i) { return uint64_t(key_of(x)) << 32 | (0xffffffffu - uint32_t(i)); }
+
+constexpr float kMagic = 1.5f * 262144.f;  // its last place is 1/32
+constexpr int kMagicBits = 0x48c00000;
+
+// What a row's weights are made with.  y = x c - M, c = log2(e) / T = ch + cl, and M the multiple of 1/32 next to (max x) c; `rest`
+// is M - (max x) c.  For a maximum so far from 0 that M does not fit beside kMagic's last place, x is
+// first taken from the maximum (FAR): d + e = x - max, M = rest = 0.
+struct Scale {
+  float m, ch, cl, base, rest;  // base = kMagic - M
+  float least;                  // logits from here down weigh 2^-64, which is cut off
+  int shift, s0;                // s0: 32 times the shift of a weight with y = 0, and kMagic's bits, and 31 to round up
+};
+
+// Weights of two logits, whole numbers; the maximum's is 2^(30 + shift).
+template <bool FAR>
+struct Weigher {
+  Scale k;
+  const uint32_t* roots;
+
+  // y = kMagic + k / 32, q = 2^32 (2^g - 1)
+  __device__ __forceinline__ uint64_t finish(float y, float q) const {
+    const int root = int(roots[__float_as_uint(y) & 31]);
+    const uint32_t w = uint32_t(root + __mulhi(root, __float2int_rn(q)));
+    uint64_t r;
+    asm("shr.b64 %0, %1, %2;" : "=l"(r) : "l"(uint64_t(w) << 32), "r"((k.s0 - __float_as_int(y)) >> 5));
+    return r;
+  }
+  __device__ __forceinline__ void operator()(float x0, float x1, uint64_t& w0, uint64_t& w1) const {
+    using tc::add2;
+    using tc::f2;
+    using tc::fma2;
+    const uint64_t ch = f2(k.ch, k.ch), cl = f2(k.cl, k.cl), base = f2(k.base, k.base);
+    const bool some0 = !FAR || x0 >= k.least, some1 = !FAR || x1 >= k.least;
+    x0 = fmaxf(x0, k.least);  // (NaN and -inf, too)
+    x1 = fmaxf(x1, k.least);
+    uint64_t x = f2(x0, x1), low;
+    if (FAR) {
+      const float v[2] = {fminf(x0, kLargest), fminf(x1, kLargest)};
+      float d[2], e[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        d[i] = __fsub_rn(v[i], k.m);
+        const float t = __fsub_rn(d[i], v[i]);
+        e[i] = __fadd_rn(__fsub_rn(v[i], __fsub_rn(d[i], t)), -__fadd_rn(k.m, t));
+      }
+      x = f2(d[0], d[1]);
+      low = fma2(f2(e[0], e[1]), ch, tc::mul2(x, cl));
+    } else {
+      low = fma2(x, cl, f2(k.rest, k.rest));
+    }
+    const uint64_t y = fma2(x, ch, base);
+    const uint64_t g = add2(fma2(x, ch, tc::sub2(base, y)), low);
+    // ln(2)^n / n!, times 2^32
+    constexpr float k32 = 4294967296.f, c1 = 0.693147181f * k32, c2 = 0.240226507f * k32, c3 = 0.0555041087f * k32,
+                    c4 = 0.00961812911f * k32;
+    uint64_t q = fma2(g, f2(c4, c4), f2(c3, c3));
+    q = fma2(g, q, f2(c2, c2));
+    q = fma2(g, q, f2(c1, c1));
+    q = tc::mul2(g, q);
+    float y0, y1, q0, q1;
+    tc::unf2(y, y0, y1);
+    tc::unf2(q, q0, q1);
+    w0 = finish(y0, q0);
+    w1 = finish(y1, q1);
+    if (FAR) {  // where `least` may be the maximum itself
+      w0 = some0 ? w0 : 0;
+      w1 = some1 ? w1 : 0;
+    }
+  }
+  __device__ __forceinline__ uint64_t operator()(float x) const {
+    uint64_t a, b;
+    (*this)(x, x, a, b);
+    return a;
+  }
+};
+
+__device__ __forceinline__ uint64_t shfl_xor64(uint64_t v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
+__device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += shfl_xor64(v, o);
+  return v;
+}
+
+__device__ __forceinline__ void st_cluster_u64(uint32_t at, uint64_t v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t at) {
+  uint64_t v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t add_cluster_u32(uint32_t at, uint32_t v) {
+  uint32_t r;
+  asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(r) : "r"(at), "r"(v) : "memory");
+  return r;
+}
+
+struct Shared {
+  uint64_t sums[kBins];    // weights of each bin: the sums of their lower 16 bits and of the others, 32 bits each, or one sum
+  uint32_t counts[kBins];  // tokens of each bin
+  uint64_t few[kFew];      // the last tokens of a search, in the cluster's first CTA
+  uint64_t few_w[kFew];
+  uint64_t totals[kMostCtas];
+  uint64_t part[kMostParts], whole[kMostParts], listed_w[kMostParts];
+  uint64_t warp_v[kWarps];
+  uint64_t found_above, cut;
+  uint32_t found_bin, found_count, few_n;
+  uint32_t roots[32];
+  uint32_t listed[kMostParts];       // candidates of each part; more than kList: they did not fit
+  float tops[kMostCtas], kth[2][kMostCtas];
+  alignas(16) uint32_t own[kThreads];  // read four at a time
+  float warp_top[kWarps];
+  Scale scale;
+  float list_x[kWarps][kList];       // a part's candidates in order
+  uint16_t list_i[kWarps][kList];    // and their places in it
+};
+static_assert(sizeof(Shared) <= 48 * 1024 && offsetof(Shared, own) % 16 == 0, "static shared memory");
+
+// The place of a CTA in its row's cluster.
+struct Place {
+  int ctas, rank;
+  __device__ __forceinline__ int parts() const { return ctas * kWarps; }
+  __device__ __forceinline__ int part() const { return rank * kWarps + (threadIdx.x >> 5); }
+};
+
+template <class T>
+struct Piece;  // 16 bytes of logits
+template <>
+struct Piece<float> {
+  static constexpr int N = 4;
+  static constexpr uint32_t kNone = 0xff800000u;  // -inf
+  static __device__ __forceinline__ float at(const uint4& v, int i) { return __uint_as_float(i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w); }
+  static __device__ __forceinline__ float top(const uint4& v) {
+    return fmaxf(fmaxf(at(v, 0), at(v, 1)), fmaxf(at(v, 2), at(v, 3)));
+  }
+};
+template <>
+struct Piece<__nv_bfloat16> {
+  static constexpr int N = 8;
+  static constexpr uint32_t kNone = 0xff80ff80u;
+  static __device__ __forceinline__ float at(const uint4& v, int i) {
+    const uint32_t w = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
+    return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+  }
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  static __device__ __forceinline__ float top(const uint4& v) {
+    const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
+    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  }
+};
+
+// A row's tokens, as this warp reads them: a contiguous part of the row in whole
+// 16-byte pieces of memory, wherever the row begins.  Pieces that pass an end of the row are read element by element.
+template <class T>
+struct Row {
+  using P = Piece<T>;
+  static constexpr int N = P::N;
+  const T* x;
+  int vocab, skew;  // skew: elements by which the row begins behind a 16-byte border
+  int pieces, per;  // 16-byte pieces that the row touches, and of a part
+
+  __device__ __forceinline__ Row(const T* x_, int vocab_, int parts) : x(x_), vocab(vocab_) {
+    skew = int((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
+    pieces = int((int64_t(vocab) + skew + N - 1) / N);
+    per = (pieces + parts - 1) / parts;
+  }
+  // first element of a part
+  __device__ __forceinline__ int begin(int part) const {
+    const int64_t i = int64_t(part) * per * N - skew;
+    return int(i < 0 ? 0 : i < vocab ? i : vocab);
+  }
+  // a piece; -inf outside of the row
+  __device__ __forceinline__ uint4 piece(int j) const {
+    const int i = j * N - skew;
+    if (i >= 0 && i <= vocab - N) return __ldg(reinterpret_cast<const uint4*>(x + i));
+    uint4 v = make_uint4(P::kNone, P::kNone, P::kNone, P::kNone);
+    T* e = reinterpret_cast<T*>(&v);
+#pragma unroll
+    for (int t = 0; t < N; ++t)
+      if (i + t >= 0 && i + t < vocab) e[t] = x[i + t];
+    return v;
+  }
+  // f(piece, index of its first element, which may be below 0) by all lanes together, in the order of the row; -inf outside of it
+  template <int kU, class F>
+  __device__ __forceinline__ void pieces_of(int part, int lane, F f) const {
+    const uint4 none = make_uint4(P::kNone, P::kNone, P::kNone, P::kNone);
+    const int a = int(min(int64_t(part) * per, int64_t(pieces))), b = min(a + per, pieces);
+    const bool first = a < b && a == 0 && skew, last = a < b && b == pieces && (vocab + skew) % N && !(first && b == 1);
+    auto end = [&](int j) { f(lane == 0 ? piece(j) : none, lane == 0 ? j * N - skew : 0); };
+    if (first) end(a);
+    const int whole = b - last;
+    const uint4* from = reinterpret_cast<const uint4*>(x - skew);
+    for (int base = a + first + lane; base - lane < whole; base += 32 * kU) {
+      uint4 v[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) v[u] = base + 32 * u < whole ? __ldg(from + base + 32 * u) : none;
+#pragma unroll
+      for (int u = 0; u < kU; ++u) f(v[u], (base + 32 * u) * N - skew);
+    }
+    if (last) end(b - 1);
+  }
+  // elements of a CTA's parts, at most
+  __device__ __forceinline__ int64_t most(const Place&) const { return int64_t(per) * N * kWarps; }
+  // f(logit, index, weight), by lanes apart, of the logits in [lo, hi] (finite ones), as they are compared; weights where
+  // they are asked for
+  template <bool kWeigh, class W, class F>
+  __device__ __forceinline__ void each(int part, int lane, const W& weigh, float lo, float hi, F f) const {
+    pieces_of<2>(part, lane, [&](const uint4& v, int i) {
+      if (!__any_sync(0xffffffffu, P::top(v) >= lo)) return;
+#pragma unroll
+      for (int t = 0; t < N; t += 2) {
+        float x[2] = {P::at(v, t), P::at(v, t + 1)};
+        uint64_t w[2] = {0, 0};
+        if (kWeigh) weigh(x[0], x[1], w[0], w[1]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          x[u] = (x[u] > kLargest ? kLargest : x[u]) + 0.f;  // (a NaN stays one, and fails)
+          if (x[u] >= lo && x[u] <= hi) f(x[u], i + t + u, w[u]);
+        }
+      }
+    });
+  }
+};
+
+// The same of the candidates: a warp's list stands for its part of the row.
+struct List {
+  const Shared& sh;
+  int begin, n;  // first element of the part, candidates
+  template <bool kWeigh, class W, class F>
+  __device__ __forceinline__ void each(int, int lane, const W& weigh, float lo, float hi, F f) const {
+    const int warp = threadIdx.x >> 5;
+    for (int i = lane; i < n; i += 32) {
+      const float x = sh.list_x[warp][i];
+      if (x >= lo && x <= hi) f(x, begin + sh.list_i[warp][i], kWeigh ? weigh(x) : 0);
+    }
+  }
+  __device__ __forceinline__ int64_t most(const Place&) const { return kWarps * kList; }
+};
+
+// The sum of a part's weights (a lane's share): of the tokens from `from` on that weigh `least` or more.  Loops over a row stand in
+// functions of their own, which have the registers to themselves.
+template <bool FAR, class T>
+__device__ __noinline__ uint64_t sum_of(const Row<T> row, int part, const Shared& sh) {
+  const Weigher<FAR> weigh{sh.scale, sh.roots};
+  uint64_t sum = 0;
+  row.template pieces_of<2>(part, threadIdx.x & 31, [&](const uint4& v, int) {
+#pragma unroll
+    for (int t = 0; t < Row<T>::N; t += 2) {
+      uint64_t a, b;
+      weigh(Piece<T>::at(v, t), Piece<T>::at(v, t + 1), a, b);
+      sum += a + b;
+    }
+  });
+  return sum;
+}
+template <bool FAR, class T>
+__device__ __noinline__ uint64_t sum_of(const Row<T> row, int part, uint64_t from, uint64_t least, const Shared& sh) {
+  using P = Piece<T>;
+  const Weigher<FAR> weigh{sh.scale, sh.roots};
+  uint64_t sum = 0;
+  const float last = from ? of_key(uint32_t(from >> 32)) : -INFINITY;  // of its equals, those up to an index
+  const int last_i = from ? int(0xffffffffu - uint32_t(from)) : 0x7fffffff;
+  row.template pieces_of<2>(part, threadIdx.x & 31, [&](const uint4& v, int i) {
+    if (!__any_sync(0xffffffffu, P::top(v) >= last)) return;
+#pragma unroll
+    for (int t = 0; t < Row<T>::N; t += 2) {
+      float x0 = P::at(v, t), x1 = P::at(v, t + 1);
+      uint64_t a, b;
+      weigh(x0, x1, a, b);
+      x0 = x0 > kLargest ? kLargest : x0;  // (a NaN stays one, and fails)
+      x1 = x1 > kLargest ? kLargest : x1;
+      if ((x0 > last || (x0 == last && i + t <= last_i)) && a >= least) sum += a;
+      if ((x1 > last || (x1 == last && i + t + 1 <= last_i)) && b >= least) sum += b;
+    }
+  });
+  return sum;
+}
+template <bool FAR, class T>
+__device__ __forceinline__ uint64_t sum_of(const Row<T>& row, const Row<T>&, int part, uint64_t from, uint64_t least, const Shared& sh) {
+  return from == 0 && least == 0 ? sum_of<FAR>(row, part, sh) : sum_of<FAR>(row, part, from, least, sh);
+}
+template <bool FAR, class T>
+__device__ __forceinline__ uint64_t sum_of(const Row<T>&, const List& list, int part, uint64_t from, uint64_t least, const Shared& sh) {
+  const Weigher<FAR> weigh{sh.scale, sh.roots};
+  uint64_t sum = 0;
+  list.each<true>(part, threadIdx.x & 31, weigh, -kLargest, kLargest, [&](float x, int i, uint64_t w) {
+    if (number_of(x, i) >= from && w >= least) sum += w;
+  });
+  return sum;
+}
+
+// What a search looks for at a level.
+struct Search {
+  uint64_t lo, hi;    // numbers that take part
+  int level, chosen;  // the first level's bin
+  int shift;          // of a number's distance from hi, to its bin, from the second level on
+  float steps;        // bins of the first level in a distance of 1
+  bool by_weight, halves;
+  __device__ __forceinline__ int bin0(float m, float x) const { return min(int(__fmul_rn(__fsub_rn(m, x), steps)), kBins - 1); }
+  // bits of a weight that are left out in a bin
+  static __device__ __forceinline__ int bits_off(int shift, int bin) {
+    return max(shift - int(float(bin) * (1.4426950f / kBinsPerT)), 0);
+  }
+  static __device__ __forceinline__ float value(uint64_t n) {  // the logit of a number, within those that there are
+    return of_key(min(max(uint32_t(n >> 32), key_of(-kLargest)), key_of(kLargest)));
+  }
+};
+
+// This warp's tokens into the CTA's histogram.
+template <bool FAR, bool kWeigh, class Source>
+__device__ __noinline__ void count_in(const Source src, int part, const Search q, Shared& sh) {
+  const Weigher<FAR> weigh{sh.scale, sh.roots};
+  src.template each<kWeigh>(part, threadIdx.x & 31, weigh, q.value(q.lo), q.value(q.hi), [&](float x, int i, uint64_t w) {
+    const uint64_t n = number_of(x, i);
+    if (n < q.lo || n > q.hi) return;
+    int b = q.bin0(weigh.k.m, x);
+    if (q.level > 0 && b != q.chosen) return;
+    if (q.by_weight && !kWeigh) w = weigh(x);
+    w >>= q.bits_off(weigh.k.shift, b);
+    if (q.level > 0) b = int((q.hi - n) >> q.shift);
+    atomicAdd(&sh.counts[b], 1u);
+    if (!q.by_weight) return;
+    if (q.halves) {
+      uint32_t* sums = reinterpret_cast<uint32_t*>(&sh.sums[b]);
+      atomicAdd(sums, uint32_t(w) & 0xffffu);
+      atomicAdd(sums + 1, uint32_t(w) >> 16);
+    } else {
+      atomicAdd(reinterpret_cast<unsigned long long*>(&sh.sums[b]), static_cast<unsigned long long>(w));
+    }
+  });
+}
+
+// The last tokens of a search, to the first CTA.
+template <bool FAR, class Source>
+__device__ __noinline__ void gather(const Source src, int part, const Search q, Shared& sh) {
+  const Weigher<FAR> weigh{sh.scale, sh.roots};
+  src.template each<false>(part, threadIdx.x & 31, weigh, q.value(q.lo), q.value(q.hi), [&](float x, int i, uint64_t) {
+    const uint64_t n = number_of(x, i);
+    if (n < q.lo || n > q.hi || q.bin0(weigh.k.m, x) != q.chosen) return;
+    const uint32_t at = add_cluster_u32(tc::peer_addr(&sh.few_n, 0), 1u);
+    if (at < kFew) st_cluster_u64(tc::peer_addr(&sh.few[at], 0), n);
+  });
+}
+
+// Sum over the CTA.
+__device__ __forceinline__ uint64_t cta_sum64(uint64_t v, Shared& sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  v = warp_sum64(v);
+  __syncthreads();
+  if (lane == 0) sh.warp_v[warp] = v;
+  __syncthreads();
+  uint64_t t = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) t += sh.warp_v[w];
+  return t;
+}
+// Running sum over the CTA, without the thread's own.
+__device__ __forceinline__ uint64_t cta_scan64(uint64_t v, Shared& sh, uint64_t& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint64_t incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t t = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += t;
+  }
+  __syncthreads();
+  if (lane == 31) sh.warp_v[warp] = incl;
+  __syncthreads();
+  uint64_t before = incl - v;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += sh.warp_v[w];
+    total += sh.warp_v[w];
+  }
+  return before;
+}
+
+// v f, f in [0, 1], rounded down or up: exactly, in whole numbers.  (fp64 has so few units here that an operation of a warp takes
+// 16 cycles; with this and the like in fp64, 64 rows took a third longer.)
+template <bool kUp>
+__device__ __forceinline__ uint64_t times(uint64_t v, float f) {
+  const uint32_t bits = __float_as_uint(f), exponent = bits >> 23;
+  const uint64_t m = exponent ? (bits & 0x7fffffu) | 0x800000u : bits & 0x7fffffu;
+  const int e = 150 - int(exponent ? exponent : 1);  // f = m 2^-e, e >= 23
+  const uint64_t lo = v * m, hi = __umul64hi(v, m);
+  uint64_t r = 0, rest = lo | hi;
+  if (e < 64) {
+    r = lo >> e | hi << (64 - e);
+    rest = lo << (64 - e);
+  } else if (e < 128) {
+    r = e == 64 ? hi : hi >> (e - 64);
+    rest = lo | (e == 64 ? 0 : hi << (128 - e));
+  }
+  return r + (kUp && rest != 0);
+}
+
+// What is asked of top_p: the sum that the run from the first on has to reach.
+__device__ __forceinline__ uint64_t target_of(float p, uint64_t whole) {
+  const uint64_t t = times<true>(whole, p);
+  return t ? t : 1;
+}
+// The draw is of the token at which the running sum passes this (the last one for u >= 1).
+__device__ __forceinline__ uint64_t limit_of(float u, uint64_t all) {
+  return u > 0.f ? min(times<false>(all, fminf(u, 1.f)), all - 1) : 0;
+}
+
+// The cut of top-k or top-p: the number of the last token kept.  With by_weight, the last
+// is the first at which the sum of the weights from the highest on reaches p of `whole` (0: of all that take part); otherwise the
+// count-th.  Only tokens from `from` on take part.
+template <bool FAR, class Source>
+__device__ __noinline__ uint64_t find_cut(const Source src, bool by_weight, uint64_t count, float p, uint64_t whole, float inv_t,
+                                          uint64_t from, const Place place, Shared& sh) {
+  const Weigher<FAR> weigh{sh.scale, sh.roots};
+  const int part = place.part();
+  const float m = weigh.k.m, steps = kBinsPerT * inv_t;
+  // A search leaves out the bits of a weight below 2^-30 of the largest that its bin can hold, 31 are left, and a sum of 65536
+  // of them fits in two halves of 32 bits (the hardware adds to no 64-bit number in shared memory: one sum in a
+  // loop took 90 us for a row of 32000).
+  Search q{from, ~uint64_t(0), 0, -1, 0, steps, by_weight, src.most(place) <= 65536};
+  uint64_t &lo = q.lo, &hi = q.hi, above = 0, target = count;
+  int &chosen = q.chosen, &shift = q.shift;
+  for (int level = 0;; ++level) {
+    for (int i = threadIdx.x; i < kBins; i += kThreads) {
+      sh.counts[i] = 0;
+      sh.sums[i] = 0;
+    }
+    __syncthreads();  // (and the level before is read)
+    if (threadIdx.x == 0) {
+      sh.few_n = 0;
+      sh.found_bin = kBins;
+      sh.cut = from;
+    }
+    q.level = level;
+    if (by_weight && level == 0) count_in<FAR, true>(src, part, q, sh);
+    else count_in<FAR, false>(src, part, q, sh);
+    tc::cluster_sync();  // the histograms are there
+    // each CTA adds up a share of the bins, a run of them a thread
+    const int each = kBins / place.ctas, run = (each + kThreads - 1) / kThreads;
+    const int first = place.rank * each + int(threadIdx.x) * run;
+    const bool mine = int(threadIdx.x) * run < each;
+    uint64_t v[kBinsEach], sum = 0;
+    uint32_t tokens[kBinsEach];
+#pragma unroll
+    for (int j = 0; j < kBinsEach; ++j) {
+      v[j] = 0;
+      tokens[j] = 0;
+      if (mine && j < run) {
+        for (int c0 = 0; c0 < place.ctas; c0 += 4) {
+          uint32_t n[4];  // under way together
+          uint64_t t[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (c0 + c < place.ctas) {
+              n[c] = ld_cluster_u32(tc::peer_addr(&sh.counts[first + j], c0 + c));
+              if (by_weight) t[c] = ld_cluster_u64(tc::peer_addr(&sh.sums[first + j], c0 + c));
+            }
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (c0 + c < place.ctas) {
+              tokens[j] += n[c];
+              if (by_weight) v[j] += q.halves ? ((t[c] >> 32) << 16) + uint32_t(t[c]) : t[c];
+            }
+        }
+        if (by_weight) v[j] <<= q.bits_off(weigh.k.shift, level > 0 ? chosen : first + j);
+        else v[j] = tokens[j];
+      }
+      sum += v[j];
+    }
+    uint64_t total;
+    const uint64_t here = cta_scan64(sum, sh, total);
+    if (int(threadIdx.x) < place.ctas) st_cluster_u64(tc::peer_addr(&sh.totals[place.rank], threadIdx.x), total);
+    tc::cluster_sync();
+    uint64_t before = above, all = 0;
+    for (int c = 0; c < place.ctas; ++c) {
+      if (c < place.rank) before += sh.totals[c];
+      all += sh.totals[c];
+    }
+    if (level == 0) {
+      if (by_weight) target = target_of(p, whole ? whole : all);
+      if (target > all) target = all;  // (fewer tokens than k have a finite logit; min_p has left less than top_p would)
+    }
+    // the thread that has it finds the first bin at which the running sum reaches the target
+    uint64_t at = before + here;
+#pragma unroll
+    for (int j = 0; j < kBinsEach; ++j) {
+      if (target > at && target <= at + v[j]) {
+        for (int c = 0; c < place.ctas; ++c) {
+          tc::st_cluster_u32(tc::peer_addr(&sh.found_bin, c), first + j);
+          tc::st_cluster_u32(tc::peer_addr(&sh.found_count, c), tokens[j]);
+          st_cluster_u64(tc::peer_addr(&sh.found_above, c), at);
+        }
+      }
+      at += v[j];
+    }
+    tc::cluster_sync();
+    const int b = int(sh.found_bin);
+    if (b == kBins || level > kMostLevels) {  // not reached: a bin holds the target, and a level takes 10 of 64 bits
+      if (threadIdx.x == 0) atomicOr(&g_status_sample, TPA_DEV_BAD_INPUT);
+      return from;
+    }
+    const uint32_t left = sh.found_count;
+    above = sh.found_above;
+    if (level == 0) {
+      chosen = b;
+      // the numbers that the bin can hold: its logits, and the roundings of their distances
+      const float far = float(b + 1) / steps, near = float(b) / steps;
+      const float slack = 1e-6f * (fabsf(m) + far) + 1e-37f;
+      const uint64_t low = uint64_t(key_of(clean(m - far - slack))) << 32;
+      const uint64_t high = uint64_t(key_of(clean(m - near + slack))) << 32 | 0xffffffffu;
+      if (b < kBins - 1 && low > lo) lo = low;
+      if (high < hi) hi = high;
+    } else {
+      const uint64_t top = hi - (uint64_t(b) << shift);
+      const uint64_t size = uint64_t(1) << shift;
+      hi = top;
+      if (top - lo >= size) lo = top - size + 1;
+    }
+    if (left <= kFew) break;
+    const int bits = 64 - __clzll(static_cast<long long>(hi - lo));
+    shift = bits > 10 ? bits - 10 : 0;
+  }
+  gather<FAR>(src, part, q, sh);
+  tc::cluster_sync();
+  if (place.rank == 0) {
+    const int n = min(int(sh.few_n), kFew), me = threadIdx.x;
+    uint64_t mine = 0, w = 0, before = above;
+    if (me < n) {
+      mine = sh.few[me];
+      const int off = q.bits_off(weigh.k.shift, chosen);
+      w = by_weight ? weigh(of_key(uint32_t(mine >> 32))) >> off << off : 1;
+      sh.few_w[me] = w;
+    }
+    __syncthreads();
+    if (me < n) {
+      for (int j = 0; j < n; ++j)
+        if (sh.few[j] > mine) before += sh.few_w[j];
+      if (before < target && before + w >= target)
+        for (int c = 0; c < place.ctas; ++c) st_cluster_u64(tc::peer_addr(&sh.cut, c), mine);
+    }
+  }
+  tc::cluster_sync();
+  return sh.cut;
+}
+
+struct Request {
+  float t, top_p, min_p;
+  int top_k;
+  float u;
+};
+
+__device__ __forceinline__ void write_token(const Params& p, int64_t r, int token, uint64_t w, uint64_t all) {
+  p.tokens[r] = token;
+  // The quotient's logarithm, with what its roundings lost added; next to 1 from what is missing, so that little is lost where one
+  // token has nearly all the weight.
+  const bool most = w > all - w;
+  const uint64_t num = most ? all - w : w;
+  const float a = float(num), b = float(all), x = a / b;
+  const float off = (fmaf(-x, b, a) + float(int64_t(num - uint64_t(a))) - x * float(int64_t(all - uint64_t(b)))) / b;
+  p.logp[r] = most ? log1pf(-(x + off)) : logf(x) + off / x;
+}
+
+// kFew candidates or fewer, in order in the first CTA's few (their numbers): a thread each.  `whole`: top_p is of it (0: of
+// those that top_k leaves).
+template <bool FAR>
+__device__ __noinline__ void finish_few(const Params& p, const int64_t r, const Request q, int n, uint64_t whole, uint64_t least,
+                                        Shared& sh) {
+  const Weigher<FAR> weigh{sh.scale, sh.roots};
+  const int me = threadIdx.x;
+  uint64_t mine = 0, w = 0, before = 0;
+  int rank = 0;
+  if (me < n) {
+    mine = sh.few[me];
+    w = weigh(of_key(uint32_t(mine >> 32)));
+    sh.few_w[me] = w;
+  }
+  __syncthreads();
+  const bool top_k = q.top_k > 0;
+  if (me < n && (top_k || q.top_p < 1.f)) {
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+      const bool higher = sh.few[j] > mine;
+      rank += higher;
+      before += higher ? sh.few_w[j] : 0;
+    }
+  }
+  bool kept = me < n && (!top_k || rank < q.top_k);
+  if (q.top_p < 1.f) {
+    if (whole == 0) whole = cta_sum64(kept ? w : 0, sh);
+    kept = kept && before < target_of(q.top_p, whole);
+  }
+  kept = kept && w >= least;
+  uint64_t all;
+  const uint64_t at = cta_scan64(kept ? w : 0, sh, all);
+  const uint64_t limit = limit_of(q.u, all);
+  if (kept && at <= limit && at + w > limit) write_token(p, r, int(0xffffffffu - uint32_t(mine)), w, all);
+}
+
+// Any number of tokens, of which those below `above` are not kept: the cuts, the sums of the parts, and the one in which the running sum passes u of the whole.
+template <bool FAR, class T, class Source>
+__device__ __noinline__ void finish_many(const Params& p, const int64_t r, const Request q, const Row<T> row, const Source src,
+                                         uint64_t whole, float above, uint64_t least, const Place place, Shared& sh) {
+  const Weigher<FAR> weigh{sh.scale, sh.roots};
+  const int lane = threadIdx.x & 31, part = place.part();
+  const float inv_t = 1.f / q.t;
+  uint64_t from = above > -INFINITY ? uint64_t(key_of(above)) << 32 : 0;
+  if (q.top_k > 0) from = find_cut<FAR>(src, false, uint64_t(q.top_k), 0.f, 0, inv_t, from, place, sh);
+  if (q.top_p < 1.f) from = find_cut<FAR>(src, true, 0, q.top_p, whole, inv_t, from, place, sh);
+  auto weight_of = [&](float x, int i) -> uint64_t {
+    if (number_of(x, i) < from) return 0;
+    const uint64_t w = weigh(x);
+    return w >= least ? w : 0;
+  };
+  const uint64_t sum = warp_sum64(sum_of<FAR>(row, src, part, from, least, sh));
+  if (lane < place.ctas) st_cluster_u64(tc::peer_addr(&sh.part[part], lane), sum);
+  tc::cluster_sync();
+  // two parts a lane, in every warp
+  uint64_t v[2], incl = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    v[i] = 2 * lane + i < place.parts() ? sh.part[2 * lane + i] : 0;
+    incl += v[i];
+  }
+  const uint64_t own = incl;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t t = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += t;
+  }
+  const uint64_t all = __shfl_sync(0xffffffffu, incl, 31), limit = limit_of(q.u, all);
+  if (all == 0) return;
+  // the first lane whose sum passes the limit
+  const int at_lane = __ffs(__ballot_sync(0xffffffffu, incl > limit)) - 1;
+  const uint64_t first = incl - own;
+  const bool second = first + v[0] <= limit;
+  const int owner = __shfl_sync(0xffffffffu, 2 * lane + second, at_lane);
+  const uint64_t before = __shfl_sync(0xffffffffu, first + (second ? v[0] : 0), at_lane);
+  if (owner / kWarps != place.rank) return;
+
+  // the token: a run of the part's pieces a thread
+  using P = Piece<T>;
+  const int a = min(owner * row.per, row.pieces), b = min(a + row.per, row.pieces), run = (b - a + kThreads - 1) / kThreads;
+  const int a0 = min(a + int(threadIdx.x) * run, b), b0 = min(a0 + run, b);
+  auto weights_of = [&](const uint4& piece, int i, int t, uint64_t (&w)[2]) {  // of elements t and t + 1
+    weigh(P::at(piece, t), P::at(piece, t + 1), w[0], w[1]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (w[k] < least || number_of(clean(P::at(piece, t + k)), i + t + k) < from) w[k] = 0;
+  };
+  uint64_t mine = 0;
+#pragma unroll 2
+  for (int j = a0; j < b0; ++j) {
+    const uint4 piece = row.piece(j);
+#pragma unroll
+    for (int t = 0; t < P::N; t += 2) {
+      uint64_t w[2];
+      weights_of(piece, j * P::N - row.skew, t, w);
+      mine += w[0] + w[1];
+    }
+  }
+  uint64_t total;
+  uint64_t at = before + cta_scan64(mine, sh, total);
+  if (at > limit || at + mine <= limit) return;
+  for (int j = a0; j < b0; ++j) {
+    const uint4 piece = row.piece(j);
+#pragma unroll
+    for (int t = 0; t < P::N; t += 2) {
+      uint64_t w[2];
+      weights_of(piece, j * P::N - row.skew, t, w);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (at <= limit && at + w[k] > limit) write_token(p, r, j * P::N - row.skew + t + k, w[k], all);
+        at += w[k];
+      }
+    }
+  }
+}
+
+// A part's tokens from `bound` on, in order, into the warp's list; their number, and the sum of all weights of the part (a lane's share).
+struct Collected {
+  uint64_t sum;
+  int n;  // more than kList: there was no room
+};
+template <bool FAR, bool kSums, class T>
+__device__ __noinline__ Collected collect(const Row<T> row, int part, float bound, Shared& sh) {
+  using P = Piece<T>;
+  constexpr int N = P::N;
+  const Weigher<FAR> weigh{sh.scale, sh.roots};
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, begin = row.begin(part);
+  uint64_t sum = 0;
+  int n = 0;
+  row.template pieces_of<kSums ? 2 : 4>(part, lane, [&](const uint4& v, int i) {
+    if (kSums) {
+#pragma unroll
+      for (int t = 0; t < N; t += 2) {
+        uint64_t a, b;
+        weigh(P::at(v, t), P::at(v, t + 1), a, b);
+        sum += a + b;
+      }
+    }
+    if (n > kList || !__any_sync(0xffffffffu, P::top(v) >= bound)) return;
+    uint32_t which = 0;
+#pragma unroll
+    for (int t = 0; t < N; ++t) which |= uint32_t(P::at(v, t) >= bound) << t;
+    int incl = __popc(which);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    int at = n + incl - __popc(which);
+    n += __shfl_sync(0xffffffffu, incl, 31);
+    while (which) {
+      const int t = __ffs(which) - 1;
+      which &= which - 1;
+      if (at < kList) {
+        sh.list_x[warp][at] = clean(P::at(v, t));
+        sh.list_i[warp][at] = uint16_t(i + t - begin);
+      }
+      ++at;
+    }
+  });
+  return Collected{sum, n};
+}
+
+// From the maximum on.  With a cut, the tokens that may be kept are first collected: those from `bound` on, which may be a guess.
+template <class T, bool FAR>
+__device__ void draw(const Params& p, int64_t r, const Request& q, const Row<T>& row, float bound, bool guess, const Place& place,
+                     Shared& sh) {
+  constexpr int N = Piece<T>::N;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = place.part();
+  const Weigher<FAR> weigh{sh.scale, sh.roots};
+  const uint64_t least = q.min_p > 0.f ? times<true>(weigh(weigh.k.m), q.min_p) : 0;
+  const bool of_all = q.top_p < 1.f && q.top_k <= 0;  // top_p of the whole row's weights
+  if (bound == -INFINITY || row.per * N > 65536) {
+    finish_many<FAR>(p, r, q, row, row, 0, -INFINITY, least, place, sh);
+    return;
+  }
+  const int begin = row.begin(part);
+  uint64_t whole = 0;
+  for (int attempt = 0;; ++attempt) {
+    const bool sums = of_all && whole == 0;
+    const Collected got = sums ? collect<FAR, true>(row, part, bound, sh) : collect<FAR, false>(row, part, bound, sh);
+    const int n = got.n;
+    uint64_t sum = got.sum;
+    __syncwarp();
+    const List list{sh, begin, min(n, kList)};
+    uint64_t in_list = 0;
+    if (sums) {
+      sum = warp_sum64(sum);
+    }
+    if (guess && attempt < 2) in_list = warp_sum64(sum_of<FAR>(row, list, part, 0, 0, sh));
+    if (lane < place.ctas) {
+      tc::st_cluster_u32(tc::peer_addr(&sh.listed[part], lane), uint32_t(n));
+      st_cluster_u64(tc::peer_addr(&sh.whole[part], lane), sum);
+      st_cluster_u64(tc::peer_addr(&sh.listed_w[part], lane), in_list);
+    }
+    tc::cluster_sync();
+    // two parts a lane, in every warp
+    int before = 0, all = 0;
+    bool fits = true;
+    uint64_t known = 0, listed = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int o = lane + 32 * i;
+      if (o < place.parts()) {
+        const int c = int(sh.listed[o]);
+        fits &= c <= kList;
+        all += min(c, kList);
+        if (o < part) before += min(c, kList);
+        known += sh.whole[o];
+        listed += sh.listed_w[o];
+      }
+    }
+    before = warp_sum(before);
+    all = warp_sum(all);
+    fits = __all_sync(0xffffffffu, fits);
+    if (sums) whole = warp_sum64(known);
+    // A guess holds when the candidates' weights reach top_p's target.  Tokens that each weigh less than (1 - top_p) / vocab of
+    // the whole are less than 1 - top_p of it together: none has the cut, so the last attempt needs no luck.
+    if (guess && attempt < 2 && warp_sum64(listed) < target_of(q.top_p, whole)) {
+      const float share = float(whole) / float(uint64_t(1) << 30 << weigh.k.shift) * (1.f - q.top_p) / float(p.vocab);
+      const float safe = weigh.k.m + q.t * logf(share) - 1e-5f * (fabsf(weigh.k.m) + 100.f * q.t);
+      const float next = attempt == 0 && fits ? fmaxf(weigh.k.m - kWider * q.t, safe) : safe;
+      bound = next < bound ? next : safe;
+      if (bound == safe) attempt = 1;
+      // (with an eighth of the room used, a wider guess will hardly fit)
+      if (bound > -kLargest && fits && all <= place.parts() * (kList / 8)) {
+        tc::cluster_sync();  // all have read what is written again
+        continue;
+      }
+      bound = safe > -kLargest ? safe : -INFINITY;
+      fits = false;
+    }
+    if (!fits) {
+      finish_many<FAR>(p, r, q, row, row, whole, bound, least, place, sh);
+    } else if (all > kFew) {
+      finish_many<FAR>(p, r, q, row, list, whole, -INFINITY, least, place, sh);
+    } else {
+      for (int i = lane; i < list.n; i += 32)
+        st_cluster_u64(tc::peer_addr(&sh.few[before + i], 0), number_of(sh.list_x[warp][i], begin + sh.list_i[warp][i]));
+      tc::cluster_sync();
+      if (place.rank == 0) finish_few<FAR>(p, r, q, all, whole, least, sh);
+    }
+    return;
+  }
+}
+
+template <class T>
+__global__ void __launch_bounds__(kThreads, 4) sample_kernel(const Params p) {
+  __shared__ Shared sh;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // this CTA runs
+  const Place place{p.ctas, int(tc::cta_rank())};
+  const int64_t r = blockIdx.x / p.ctas;
+  const Row<T> row(static_cast<const T*>(p.logits) + r * p.row_stride, p.vocab, place.parts());
+  Request q;
+  q.t = p.temperature ? __ldg(p.temperature + r) : p.temperature_all;
+  q.top_p = p.top_p ? __ldg(p.top_p + r) : p.top_p_all;
+  q.min_p = p.min_p ? __ldg(p.min_p + r) : p.min_p_all;
+  q.top_k = p.top_k ? __ldg(p.top_k + r) : p.top_k_all;
+  q.u = __ldg(p.u + r);
+  const bool fine = (q.t == 0.f || (q.t >= 1e-6f && q.t <= 1e6f)) && q.top_p >= 0.f && q.top_p <= 1.f && q.min_p >= 0.f &&
+                    q.min_p <= 1.f;
+  if (q.t == 0.f) {  // the first of the largest
+    q.t = 1.f;
+    q.top_k = 1;
+    q.top_p = 1.f;
+  }
+  if (q.top_k >= p.vocab) q.top_k = 0;
+  if (threadIdx.x < 32) sh.roots[threadIdx.x] = kRoots[threadIdx.x];
+
+  // log2(e) / T as a pair
+  const float ch = __fdiv_rn(1.44269502f, q.t), cl = __fdiv_rn(__fmaf_rn(-ch, q.t, 1.44269502f) + 1.92596299e-8f, q.t);
+
+  // the maximum
+  float own = -INFINITY;
+  row.template pieces_of<4>(place.part(), lane, [&](const uint4& v, int) { own = fmaxf(own, Piece<T>::top(v)); });
+  float top = warp_max_f(own);
+  if (lane == 0) sh.warp_top[warp] = top;
+  const uint32_t mine = (key_of(own) & ~uint32_t(kThreads - 1)) | (kThreads - 1 - threadIdx.x);
+  sh.own[threadIdx.x] = mine;
+  __syncthreads();
+  top = sh.warp_top[0];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sh.warp_top[w]);
+  auto own_value = [](uint32_t key) {
+    const float v = of_key(key & ~uint32_t(kThreads - 1));
+    return v > -INFINITY ? v : -INFINITY;  // (below -inf: a NaN's pattern)
+  };
+  // A logit that top_k does not leave out is at least the ceil(k / CTAs)-th largest of the threads' own maxima in the CTA where that
+  // is lowest, and the k-th largest in any: so many tokens are at least that.
+  const int share = (q.top_k + place.ctas - 1) / place.ctas;
+  float kth[2] = {-INFINITY, -INFINITY};
+  if (q.top_k > 0 && share <= kThreads) {
+    // (the low bits of a maximum make way for the thread's number, so that no two are equal: a bound that is lower by 2^-15 of itself)
+    int above = 0;
+#pragma unroll 8
+    for (int j = 0; j < kThreads; j += 4) {
+      const uint4 o = *reinterpret_cast<const uint4*>(&sh.own[j]);
+      above += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
+    }
+    if (above == share - 1) sh.warp_v[0] = mine;
+    if (above == q.top_k - 1) sh.warp_v[1] = mine;
+    __syncthreads();
+    kth[0] = own_value(uint32_t(sh.warp_v[0]));
+    if (q.top_k <= kThreads) kth[1] = own_value(uint32_t(sh.warp_v[1]));
+  }
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // the other CTAs run: their shared memory may be written
+  if (int(threadIdx.x) < place.ctas) {
+    tc::st_cluster_u32(tc::peer_addr(&sh.tops[place.rank], threadIdx.x), __float_as_uint(top));
+    tc::st_cluster_u32(tc::peer_addr(&sh.kth[0][place.rank], threadIdx.x), __float_as_uint(kth[0]));
+    tc::st_cluster_u32(tc::peer_addr(&sh.kth[1][place.rank], threadIdx.x), __float_as_uint(kth[1]));
+  }
+  tc::cluster_sync();
+  float low = INFINITY, bound = -INFINITY;
+  for (int c = 0; c < place.ctas; ++c) {
+    top = fmaxf(top, sh.tops[c]);
+    low = fminf(low, sh.kth[0][c]);
+    bound = fmaxf(bound, sh.kth[1][c]);
+  }
+  if (q.top_k > 0) bound = fminf(fmaxf(bound, low), kLargest);
+  if (!fine || top == -INFINITY) {  // nothing to draw from, or no way to
+    if (place.rank == 0 && threadIdx.x == 0) {
+      if (!fine) atomicOr(&g_status_sample, TPA_DEV_BAD_INPUT);
+      p.tokens[r] = -1;
+      p.logp[r] = __int_as_float(0x7fc00000);
+    }
+    return;
+  }
+  top = fminf(top, kLargest);
+  // (of the tokens that top_k leaves, top_p needs the weights of all)
+  if (q.min_p > 0.f && !(q.top_k > 0 && q.top_p < 1.f)) bound = fmaxf(bound, top + q.t * logf(q.min_p) - 1e-5f * (fabsf(top) + 100.f * q.t));
+  // top_p's cut is first looked for next to the maximum
+  const bool guess = q.top_p < 1.f && q.top_k <= 0 && top - kHead * q.t > bound;
+  if (guess) bound = top - kHead * q.t;
+  const bool far = !(fabsf(top) * ch < 65536.f);
+  if (threadIdx.x == 0) {
+    const float near = far ? 0.f : __fsub_rn(__fmaf_rn(top, ch, kMagic), kMagic);
+    Scale& k = sh.scale;
+    k.m = top;
+    k.ch = ch;
+    k.cl = cl;
+    k.base = kMagic - near;
+    k.rest = far ? 0.f : -__fmaf_rn(top, cl, __fmaf_rn(top, ch, -near));
+    k.least = fmaxf(top - 64.f / ch, -kLargest);
+    k.shift = p.shift;
+    k.s0 = 32 * (32 - p.shift) + kMagicBits + 31;
+  }
+  __syncthreads();
+  if (far) draw<T, true>(p, r, q, row, bound, guess, place, sh);
+  else draw<T, false>(p, r, q, row, bound, guess, place, sh);
+}
+
+template <class T>
+int launch(Params& p, int n_rows, cudaStream_t st) {
+  // CTAs of a row: as many as are at work together on the device, and not less than kLeast bytes for each
+  constexpr int kLeast = 8192;
+  p.ctas = kMostCtas;
+  while (p.ctas > 1 && (int64_t(n_rows) * p.ctas > 600 || int64_t(p.vocab) * int(sizeof(T)) < int64_t(kLeast) * p.ctas)) p.ctas /= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(n_rows) * p.ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  TPA_CUDA_TRY(cudaLaunchKernelEx(&cfg, sample_kernel<T>, static_cast<const Params>(p)));
+  return TPA_OK;
+}
+
+}  // namespace
+
+TPA_DEFINE_STATUS_READER(tpa_internal_status_sample, g_status_sample)
+
+extern "C" int tpa_sample_tokens(const void* logits, int32_t logits_type, int64_t row_stride, int32_t n_rows, int32_t vocab,
+                                 const tpa_sample_params* params, const float* u, int32_t* tokens, float* logp,
+                                 void* stream) {
+  TPA_NVTX_RANGE("tpa_sample_tokens");
+  if (n_rows < 0 || n_rows > 0x7fffffff / kMostCtas || vocab < 1 || vocab > (1 << 30) || !params ||
+      (logits_type != TPA_LOGITS_F32 && logits_type != TPA_LOGITS_BF16))
+    return TPA_ERR_INVALID_ARG;
+  auto in = [](float v, float lo, float hi) { return v >= lo && v <= hi; };
+  if ((!params->temperature && params->temperature_all != 0.f && !in(params->temperature_all, 1e-6f, 1e6f)) ||
+      (!params->top_p && !in(params->top_p_all, 0.f, 1.f)) || (!params->min_p && !in(params->min_p_all, 0.f, 1.f)))
+    return TPA_ERR_INVALID_ARG;
+  if (n_rows == 0) return TPA_OK;
+  if (!logits || !u || !tokens || !logp || row_stride < vocab || row_stride >= (int64_t(1) << 40)) return TPA_ERR_INVALID_ARG;
+  const uintptr_t al = reinterpret_cast<uintptr_t>(u) | reinterpret_cast<uintptr_t>(tokens) | reinterpret_cast<uintptr_t>(logp) |
+                       reinterpret_cast<uintptr_t>(params->temperature) | reinterpret_cast<uintptr_t>(params->top_p) |
+                       reinterpret_cast<uintptr_t>(params->min_p) | reinterpret_cast<uintptr_t>(params->top_k);
+  const bool f32 = logits_type == TPA_LOGITS_F32;
+  if ((al & 3) || (reinterpret_cast<uintptr_t>(logits) & (f32 ? 3 : 1))) return TPA_ERR_INVALID_ARG;
+  int bits = 0;
+  while ((int64_t(1) << bits) < vocab) ++bits;
+  Params p{logits, row_stride, params->temperature, params->top_p, params->min_p, params->top_k, u, tokens, logp,
+                 params->temperature_all, params->top_p_all, params->min_p_all, params->top_k_all, vocab, 32 - bits, 1};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return f32 ? launch<float>(p, n_rows, st) : launch<__nv_bfloat16>(p, n_rows, st);
+}
