@@ -19,7 +19,6 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
-#include <cstddef>
 
 #include "device_common.cuh"
 #include "internal.h"
@@ -37,9 +36,9 @@ constexpr int kBins = 1024;
 constexpr int kBinsEach = kBins / kThreads;  // bins that a thread adds up, at most
 constexpr int kFew = kThreads;     // tokens that are ranked against each other, one a thread
 constexpr int kList = 512;         // candidates that a warp has room for
-constexpr float kBinsPerT = 32.f;  // bins of the first level in a distance of T
+constexpr int kBinsPerBit = 32;    // bins of the first level in a factor of 2 of the weights
 constexpr int kMostLevels = 8;
-constexpr float kHead = 8.f, kWider = 10.5f;  // distances from the maximum, in T, within which top_p's cut is looked for first
+constexpr float kHead = 10.f, kWider = 12.f;  // distances from the maximum, in T, within which top_p's cut is looked for first
 
 // round(2^(i / 32) * 2^30)
 __constant__ uint32_t kRoots[32] = {
@@ -81,37 +80,46 @@ __device__ __forceinline__ uint64_t number_of(float x, int i) { return uint64_t(
 constexpr float kMagic = 1.5f * 262144.f;  // its last place is 1/32
 constexpr int kMagicBits = 0x48c00000;
 
-// What a row's weights are made with.  y = x c - M, c = log2(e) / T = ch + cl, and M the multiple of 1/32 next to (max x) c; `rest`
-// is M - (max x) c.  For a maximum so far from 0 that M does not fit beside kMagic's last place, x is
-// first taken from the maximum (FAR): d + e = x - max, M = rest = 0.
+// What a row's weights are made with.  y = x c - M, c = log2(e) / T = ch + cl, and M the multiple of 1/32 next to (max x) c, so that
+// the maximum's weight is 2^(30 + shift) but for a factor of 2^(1/64) (all have it).  For a maximum so far
+// from 0 that M does not fit beside kMagic's last place, x is first taken from the maximum (FAR): d + e = x - max, M = 0.
 struct Scale {
-  float m, ch, cl, base, rest;  // base = kMagic - M
-  float least;                  // logits from here down weigh 2^-64, which is cut off
-  int shift, s0;                // s0: 32 times the shift of a weight with y = 0, and kMagic's bits, and 31 to round up
+  float m, ch, cl, base;  // base = kMagic - M
+  float least;            // logits from here down weigh less than 2^-(30 + shift) of the largest: nothing
+  int shift, s0;          // s0: 32 times the shift of a weight with y = 0, and kMagic's bits, and 31 to round up
 };
 
-// Weights of two logits, whole numbers; the maximum's is 2^(30 + shift).
+// A weight, a whole number of at most 31 + shift bits: root (1 + q) shifted.
+struct Weight {
+  uint32_t w;
+  int by;
+  __device__ __forceinline__ uint64_t value() const {
+    uint64_t r;
+    asm("shr.b64 %0, %1, %2;" : "=l"(r) : "l"(uint64_t(w) << 32), "r"(by));
+    return r;
+  }
+};
+
 template <bool FAR>
 struct Weigher {
   Scale k;
   const uint32_t* roots;
+  uint32_t root;  // this lane's
 
-  // y = kMagic + k / 32, q = 2^32 (2^g - 1)
-  __device__ __forceinline__ uint64_t finish(float y, float q) const {
-    const int root = int(roots[__float_as_uint(y) & 31]);
-    const uint32_t w = uint32_t(root + __mulhi(root, __float2int_rn(q)));
-    uint64_t r;
-    asm("shr.b64 %0, %1, %2;" : "=l"(r) : "l"(uint64_t(w) << 32), "r"((k.s0 - __float_as_int(y)) >> 5));
-    return r;
-  }
-  __device__ __forceinline__ void operator()(float x0, float x1, uint64_t& w0, uint64_t& w1) const {
-    using tc::add2;
+  __device__ __forceinline__ Weigher(const Scale& k_, const uint32_t* roots_) : k(k_), roots(roots_), root(roots_[threadIdx.x & 31]) {}
+
+  // Of two logits; by all lanes of the warp together (the roots come from the lanes), or by some (kApart).  Logits are not below
+  // k.least, but in FAR and apart, where it is seen to here (NaN, too).
+  template <bool kApart>
+  __device__ __forceinline__ void pair(float x0, float x1, Weight (&w)[2]) const {
     using tc::f2;
     using tc::fma2;
     const uint64_t ch = f2(k.ch, k.ch), cl = f2(k.cl, k.cl), base = f2(k.base, k.base);
-    const bool some0 = !FAR || x0 >= k.least, some1 = !FAR || x1 >= k.least;
-    x0 = fmaxf(x0, k.least);  // (NaN and -inf, too)
-    x1 = fmaxf(x1, k.least);
+    const bool some[2] = {!FAR || x0 >= k.least, !FAR || x1 >= k.least};
+    if (FAR || kApart) {
+      x0 = fmaxf(x0, k.least);
+      x1 = fmaxf(x1, k.least);
+    }
     uint64_t x = f2(x0, x1), low;
     if (FAR) {
       const float v[2] = {fminf(x0, kLargest), fminf(x1, kLargest)};
@@ -124,32 +132,38 @@ struct Weigher {
       }
       x = f2(d[0], d[1]);
       low = fma2(f2(e[0], e[1]), ch, tc::mul2(x, cl));
-    } else {
-      low = fma2(x, cl, f2(k.rest, k.rest));
     }
-    const uint64_t y = fma2(x, ch, base);
-    const uint64_t g = add2(fma2(x, ch, tc::sub2(base, y)), low);
-    // ln(2)^n / n!, times 2^32
+    const uint64_t y = fma2(x, ch, base);  // kMagic + k / 32
+    uint64_t g = fma2(x, ch, tc::sub2(base, y));
+    g = FAR ? tc::add2(g, low) : fma2(x, cl, g);
+    // 2^g - 1, times 2^32: ln(2)^n / n!
     constexpr float k32 = 4294967296.f, c1 = 0.693147181f * k32, c2 = 0.240226507f * k32, c3 = 0.0555041087f * k32,
                     c4 = 0.00961812911f * k32;
     uint64_t q = fma2(g, f2(c4, c4), f2(c3, c3));
     q = fma2(g, q, f2(c2, c2));
     q = fma2(g, q, f2(c1, c1));
     q = tc::mul2(g, q);
-    float y0, y1, q0, q1;
-    tc::unf2(y, y0, y1);
-    tc::unf2(q, q0, q1);
-    w0 = finish(y0, q0);
-    w1 = finish(y1, q1);
-    if (FAR) {  // where `least` may be the maximum itself
-      w0 = some0 ? w0 : 0;
-      w1 = some1 ? w1 : 0;
+    float ys[2], qs[2];
+    tc::unf2(y, ys[0], ys[1]);
+    tc::unf2(q, qs[0], qs[1]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int bits = __float_as_int(ys[i]);
+      const int r = kApart ? int(roots[bits & 31]) : int(__shfl_sync(0xffffffffu, root, bits));  // the lane is a number mod 32
+      w[i].w = uint32_t(r + __mulhi(r, __float2int_rn(qs[i])));
+      w[i].by = (k.s0 - bits) >> 5;
+      if (FAR && !some[i]) w[i].by = 64;  // where `least` may be the maximum itself
     }
   }
+  // what logits are raised to before they are weighed together (FAR: nothing, pair sees to it)
+  template <class P>
+  __device__ __forceinline__ uint32_t floor_of() const {
+    return FAR ? P::kNone : P::floor_of(k.least);
+  }
   __device__ __forceinline__ uint64_t operator()(float x) const {
-    uint64_t a, b;
-    (*this)(x, x, a, b);
-    return a;
+    Weight w[2];
+    pair<true>(x, x, w);
+    return w[0].value();
   }
 };
 
@@ -191,14 +205,13 @@ struct Shared {
   uint32_t found_bin, found_count, few_n;
   uint32_t roots[32];
   uint32_t listed[kMostParts];       // candidates of each part; more than kList: they did not fit
-  float tops[kMostCtas], kth[2][kMostCtas];
-  alignas(16) uint32_t own[kThreads];  // read four at a time
+  float tops[kMostCtas], kth[kMostCtas];
   float warp_top[kWarps];
   Scale scale;
   float list_x[kWarps][kList];       // a part's candidates in order
   uint16_t list_i[kWarps][kList];    // and their places in it
 };
-static_assert(sizeof(Shared) <= 48 * 1024 && offsetof(Shared, own) % 16 == 0, "static shared memory");
+static_assert(sizeof(Shared) <= 48 * 1024, "static shared memory");
 
 // The place of a CTA in its row's cluster.
 struct Place {
@@ -217,6 +230,12 @@ struct Piece<float> {
   static __device__ __forceinline__ float top(const uint4& v) {
     return fmaxf(fmaxf(at(v, 0), at(v, 1)), fmaxf(at(v, 2), at(v, 3)));
   }
+  // no element below `least`, and no NaN (bf16: the next value down)
+  static __device__ __forceinline__ uint32_t floor_of(float least) { return __float_as_uint(least); }
+  static __device__ __forceinline__ uint4 raised(const uint4& v, uint32_t least) {
+    auto up = [least](uint32_t x) { return __float_as_uint(fmaxf(__uint_as_float(x), __uint_as_float(least))); };
+    return make_uint4(up(v.x), up(v.y), up(v.z), up(v.w));
+  }
 };
 template <>
 struct Piece<__nv_bfloat16> {
@@ -234,6 +253,12 @@ struct Piece<__nv_bfloat16> {
   static __device__ __forceinline__ float top(const uint4& v) {
     const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
     return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  }
+  static __device__ __forceinline__ uint32_t floor_of(float least) {
+    return uint32_t(__bfloat16_as_ushort(__float2bfloat16_rd(least))) * 0x10001u;
+  }
+  static __device__ __forceinline__ uint4 raised(const uint4& v, uint32_t least) {
+    return make_uint4(max2(v.x, least), max2(v.y, least), max2(v.z, least), max2(v.w, least));
   }
 };
 
@@ -293,17 +318,18 @@ struct Row {
   // they are asked for
   template <bool kWeigh, class W, class F>
   __device__ __forceinline__ void each(int part, int lane, const W& weigh, float lo, float hi, F f) const {
+    const uint32_t least = weigh.template floor_of<P>();
     pieces_of<2>(part, lane, [&](const uint4& v, int i) {
       if (!__any_sync(0xffffffffu, P::top(v) >= lo)) return;
+      const uint4 r = kWeigh ? P::raised(v, least) : v;
 #pragma unroll
       for (int t = 0; t < N; t += 2) {
-        float x[2] = {P::at(v, t), P::at(v, t + 1)};
-        uint64_t w[2] = {0, 0};
-        if (kWeigh) weigh(x[0], x[1], w[0], w[1]);
+        Weight w[2];
+        if (kWeigh) weigh.template pair<false>(P::at(r, t), P::at(r, t + 1), w);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          x[u] = (x[u] > kLargest ? kLargest : x[u]) + 0.f;  // (a NaN stays one, and fails)
-          if (x[u] >= lo && x[u] <= hi) f(x[u], i + t + u, w[u]);
+          const float e = P::at(v, t + u), x = (e > kLargest ? kLargest : e) + 0.f;  // (a NaN stays one, and fails)
+          if (x >= lo && x <= hi) f(x, i + t + u, w[u]);
         }
       }
     });
@@ -319,7 +345,9 @@ struct List {
     const int warp = threadIdx.x >> 5;
     for (int i = lane; i < n; i += 32) {
       const float x = sh.list_x[warp][i];
-      if (x >= lo && x <= hi) f(x, begin + sh.list_i[warp][i], kWeigh ? weigh(x) : 0);
+      Weight w[2];
+      if (kWeigh) weigh.template pair<true>(x, x, w);
+      if (x >= lo && x <= hi) f(x, begin + sh.list_i[warp][i], w[0]);
     }
   }
   __device__ __forceinline__ int64_t most(const Place&) const { return kWarps * kList; }
@@ -327,38 +355,46 @@ struct List {
 
 // The sum of a part's weights (a lane's share): of the tokens from `from` on that weigh `least` or more.  Loops over a row stand in
 // functions of their own, which have the registers to themselves.
+template <class T, class W>
+__device__ __forceinline__ uint64_t sum_piece(const W& weigh, const uint4& v, uint64_t sum) {
+#pragma unroll
+  for (int t = 0; t < Piece<T>::N; t += 2) {
+    Weight w[2];
+    weigh.template pair<false>(Piece<T>::at(v, t), Piece<T>::at(v, t + 1), w);
+    sum += w[0].value();
+    sum += w[1].value();
+  }
+  return sum;
+}
 template <bool FAR, class T>
 __device__ __noinline__ uint64_t sum_of(const Row<T> row, int part, const Shared& sh) {
-  const Weigher<FAR> weigh{sh.scale, sh.roots};
+  const Weigher<FAR> weigh(sh.scale, sh.roots);
+  const uint32_t least = weigh.template floor_of<Piece<T>>();
   uint64_t sum = 0;
-  row.template pieces_of<2>(part, threadIdx.x & 31, [&](const uint4& v, int) {
-#pragma unroll
-    for (int t = 0; t < Row<T>::N; t += 2) {
-      uint64_t a, b;
-      weigh(Piece<T>::at(v, t), Piece<T>::at(v, t + 1), a, b);
-      sum += a + b;
-    }
-  });
+  row.template pieces_of<2>(part, threadIdx.x & 31, [&](const uint4& v, int) { sum = sum_piece<T>(weigh, Piece<T>::raised(v, least), sum); });
   return sum;
 }
 template <bool FAR, class T>
 __device__ __noinline__ uint64_t sum_of(const Row<T> row, int part, uint64_t from, uint64_t least, const Shared& sh) {
   using P = Piece<T>;
-  const Weigher<FAR> weigh{sh.scale, sh.roots};
+  const Weigher<FAR> weigh(sh.scale, sh.roots);
+  const uint32_t floor = weigh.template floor_of<P>();
   uint64_t sum = 0;
   const float last = from ? of_key(uint32_t(from >> 32)) : -INFINITY;  // of its equals, those up to an index
   const int last_i = from ? int(0xffffffffu - uint32_t(from)) : 0x7fffffff;
   row.template pieces_of<2>(part, threadIdx.x & 31, [&](const uint4& v, int i) {
     if (!__any_sync(0xffffffffu, P::top(v) >= last)) return;
+    const uint4 r = P::raised(v, floor);
 #pragma unroll
     for (int t = 0; t < Row<T>::N; t += 2) {
-      float x0 = P::at(v, t), x1 = P::at(v, t + 1);
-      uint64_t a, b;
-      weigh(x0, x1, a, b);
-      x0 = x0 > kLargest ? kLargest : x0;  // (a NaN stays one, and fails)
-      x1 = x1 > kLargest ? kLargest : x1;
-      if ((x0 > last || (x0 == last && i + t <= last_i)) && a >= least) sum += a;
-      if ((x1 > last || (x1 == last && i + t + 1 <= last_i)) && b >= least) sum += b;
+      Weight w[2];
+      weigh.template pair<false>(P::at(r, t), P::at(r, t + 1), w);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float e = P::at(v, t + u), x = e > kLargest ? kLargest : e;  // (a NaN stays one, and fails)
+        const uint64_t a = w[u].value();
+        if ((x > last || (x == last && i + t + u <= last_i)) && a >= least) sum += a;
+      }
     }
   });
   return sum;
@@ -369,10 +405,11 @@ __device__ __forceinline__ uint64_t sum_of(const Row<T>& row, const Row<T>&, int
 }
 template <bool FAR, class T>
 __device__ __forceinline__ uint64_t sum_of(const Row<T>&, const List& list, int part, uint64_t from, uint64_t least, const Shared& sh) {
-  const Weigher<FAR> weigh{sh.scale, sh.roots};
+  const Weigher<FAR> weigh(sh.scale, sh.roots);
   uint64_t sum = 0;
-  list.each<true>(part, threadIdx.x & 31, weigh, -kLargest, kLargest, [&](float x, int i, uint64_t w) {
-    if (number_of(x, i) >= from && w >= least) sum += w;
+  list.each<true>(part, threadIdx.x & 31, weigh, -kLargest, kLargest, [&](float x, int i, const Weight& w) {
+    const uint64_t v = w.value();
+    if (number_of(x, i) >= from && v >= least) sum += v;
   });
   return sum;
 }
@@ -380,40 +417,47 @@ __device__ __forceinline__ uint64_t sum_of(const Row<T>&, const List& list, int 
 // What a search looks for at a level.
 struct Search {
   uint64_t lo, hi;    // numbers that take part
+  float lo_x, hi_x;   // their logits
   int level, chosen;  // the first level's bin
   int shift;          // of a number's distance from hi, to its bin, from the second level on
   float steps;        // bins of the first level in a distance of 1
   bool by_weight, halves;
   __device__ __forceinline__ int bin0(float m, float x) const { return min(int(__fmul_rn(__fsub_rn(m, x), steps)), kBins - 1); }
   // bits of a weight that are left out in a bin
-  static __device__ __forceinline__ int bits_off(int shift, int bin) {
-    return max(shift - int(float(bin) * (1.4426950f / kBinsPerT)), 0);
-  }
+  static __device__ __forceinline__ int bits_off(int shift, int bin) { return max(shift - bin / kBinsPerBit, 0); }
   static __device__ __forceinline__ float value(uint64_t n) {  // the logit of a number, within those that there are
     return of_key(min(max(uint32_t(n >> 32), key_of(-kLargest)), key_of(kLargest)));
+  }
+  // whether a token whose logit is in [lo_x, hi_x] takes part
+  __device__ __forceinline__ bool has(float x, int i) const {
+    return !((x == lo_x && number_of(x, i) < lo) || (x == hi_x && number_of(x, i) > hi));
   }
 };
 
 // This warp's tokens into the CTA's histogram.
 template <bool FAR, bool kWeigh, class Source>
 __device__ __noinline__ void count_in(const Source src, int part, const Search q, Shared& sh) {
-  const Weigher<FAR> weigh{sh.scale, sh.roots};
-  src.template each<kWeigh>(part, threadIdx.x & 31, weigh, q.value(q.lo), q.value(q.hi), [&](float x, int i, uint64_t w) {
-    const uint64_t n = number_of(x, i);
-    if (n < q.lo || n > q.hi) return;
-    int b = q.bin0(weigh.k.m, x);
-    if (q.level > 0 && b != q.chosen) return;
-    if (q.by_weight && !kWeigh) w = weigh(x);
-    w >>= q.bits_off(weigh.k.shift, b);
-    if (q.level > 0) b = int((q.hi - n) >> q.shift);
+  const Weigher<FAR> weigh(sh.scale, sh.roots);
+  src.template each<kWeigh>(part, threadIdx.x & 31, weigh, q.lo_x, q.hi_x, [&](float x, int i, const Weight& weight) {
+    if (!q.has(x, i)) return;
+    const int b0 = q.bin0(weigh.k.m, x), b = q.level > 0 ? int((q.hi - number_of(x, i)) >> q.shift) : b0;
+    if (q.level > 0 && b0 != q.chosen) return;
     atomicAdd(&sh.counts[b], 1u);
     if (!q.by_weight) return;
-    if (q.halves) {
+    Weight w = weight;
+    if (!kWeigh) {
+      Weight v[2];
+      weigh.template pair<true>(x, x, v);
+      w = v[0];
+    }
+    if (q.halves) {  // (by - (32 - shift) bits are off the weight: as many as the bin leaves out, or one more)
+      const uint32_t v = w.w >> min(max(w.by - 32 + weigh.k.shift - min(b0 / kBinsPerBit, weigh.k.shift), 0), 31);
       uint32_t* sums = reinterpret_cast<uint32_t*>(&sh.sums[b]);
-      atomicAdd(sums, uint32_t(w) & 0xffffu);
-      atomicAdd(sums + 1, uint32_t(w) >> 16);
+      atomicAdd(sums, v & 0xffffu);
+      atomicAdd(sums + 1, v >> 16);
     } else {
-      atomicAdd(reinterpret_cast<unsigned long long*>(&sh.sums[b]), static_cast<unsigned long long>(w));
+      atomicAdd(reinterpret_cast<unsigned long long*>(&sh.sums[b]),
+                static_cast<unsigned long long>(w.value() >> q.bits_off(weigh.k.shift, b0)));
     }
   });
 }
@@ -421,12 +465,11 @@ __device__ __noinline__ void count_in(const Source src, int part, const Search q
 // The last tokens of a search, to the first CTA.
 template <bool FAR, class Source>
 __device__ __noinline__ void gather(const Source src, int part, const Search q, Shared& sh) {
-  const Weigher<FAR> weigh{sh.scale, sh.roots};
-  src.template each<false>(part, threadIdx.x & 31, weigh, q.value(q.lo), q.value(q.hi), [&](float x, int i, uint64_t) {
-    const uint64_t n = number_of(x, i);
-    if (n < q.lo || n > q.hi || q.bin0(weigh.k.m, x) != q.chosen) return;
+  const Weigher<FAR> weigh(sh.scale, sh.roots);
+  src.template each<false>(part, threadIdx.x & 31, weigh, q.lo_x, q.hi_x, [&](float x, int i, const Weight&) {
+    if (!q.has(x, i) || q.bin0(weigh.k.m, x) != q.chosen) return;
     const uint32_t at = add_cluster_u32(tc::peer_addr(&sh.few_n, 0), 1u);
-    if (at < kFew) st_cluster_u64(tc::peer_addr(&sh.few[at], 0), n);
+    if (at < kFew) st_cluster_u64(tc::peer_addr(&sh.few[at], 0), number_of(x, i));
   });
 }
 
@@ -497,15 +540,15 @@ __device__ __forceinline__ uint64_t limit_of(float u, uint64_t all) {
 // is the first at which the sum of the weights from the highest on reaches p of `whole` (0: of all that take part); otherwise the
 // count-th.  Only tokens from `from` on take part.
 template <bool FAR, class Source>
-__device__ __noinline__ uint64_t find_cut(const Source src, bool by_weight, uint64_t count, float p, uint64_t whole, float inv_t,
-                                          uint64_t from, const Place place, Shared& sh) {
-  const Weigher<FAR> weigh{sh.scale, sh.roots};
+__device__ __noinline__ uint64_t find_cut(const Source src, bool by_weight, uint64_t count, float p, uint64_t whole, uint64_t from,
+                                          const Place place, Shared& sh) {
+  const Weigher<FAR> weigh(sh.scale, sh.roots);
   const int part = place.part();
-  const float m = weigh.k.m, steps = kBinsPerT * inv_t;
+  const float m = weigh.k.m, steps = float(kBinsPerBit) * weigh.k.ch;
   // A search leaves out the bits of a weight below 2^-30 of the largest that its bin can hold, 31 are left, and a sum of 65536
   // of them fits in two halves of 32 bits (the hardware adds to no 64-bit number in shared memory: one sum in a
   // loop took 90 us for a row of 32000).
-  Search q{from, ~uint64_t(0), 0, -1, 0, steps, by_weight, src.most(place) <= 65536};
+  Search q{from, ~uint64_t(0), 0.f, 0.f, 0, -1, 0, steps, by_weight, src.most(place) <= 65536};
   uint64_t &lo = q.lo, &hi = q.hi, above = 0, target = count;
   int &chosen = q.chosen, &shift = q.shift;
   for (int level = 0;; ++level) {
@@ -520,6 +563,8 @@ __device__ __noinline__ uint64_t find_cut(const Source src, bool by_weight, uint
       sh.cut = from;
     }
     q.level = level;
+    q.lo_x = q.value(lo);
+    q.hi_x = q.value(hi);
     if (by_weight && level == 0) count_in<FAR, true>(src, part, q, sh);
     else count_in<FAR, false>(src, part, q, sh);
     tc::cluster_sync();  // the histograms are there
@@ -533,7 +578,11 @@ __device__ __noinline__ uint64_t find_cut(const Source src, bool by_weight, uint
     for (int j = 0; j < kBinsEach; ++j) {
       v[j] = 0;
       tokens[j] = 0;
-      if (mine && j < run) {
+      if (mine && j < run && place.ctas == 1) {
+        tokens[j] = sh.counts[first + j];
+        const uint64_t t = sh.sums[first + j];
+        if (by_weight) v[j] = q.halves ? ((t >> 32) << 16) + uint32_t(t) : t;
+      } else if (mine && j < run) {
         for (int c0 = 0; c0 < place.ctas; c0 += 4) {
           uint32_t n[4];  // under way together
           uint64_t t[4];
@@ -550,9 +599,9 @@ __device__ __noinline__ uint64_t find_cut(const Source src, bool by_weight, uint
               if (by_weight) v[j] += q.halves ? ((t[c] >> 32) << 16) + uint32_t(t[c]) : t[c];
             }
         }
-        if (by_weight) v[j] <<= q.bits_off(weigh.k.shift, level > 0 ? chosen : first + j);
-        else v[j] = tokens[j];
       }
+      if (by_weight) v[j] <<= q.bits_off(weigh.k.shift, level > 0 ? chosen : first + j);
+      else v[j] = tokens[j];
       sum += v[j];
     }
     uint64_t total;
@@ -608,6 +657,8 @@ __device__ __noinline__ uint64_t find_cut(const Source src, bool by_weight, uint
     const int bits = 64 - __clzll(static_cast<long long>(hi - lo));
     shift = bits > 10 ? bits - 10 : 0;
   }
+  q.lo_x = q.value(lo);
+  q.hi_x = q.value(hi);
   gather<FAR>(src, part, q, sh);
   tc::cluster_sync();
   if (place.rank == 0) {
@@ -653,7 +704,7 @@ __device__ __forceinline__ void write_token(const Params& p, int64_t r, int toke
 template <bool FAR>
 __device__ __noinline__ void finish_few(const Params& p, const int64_t r, const Request q, int n, uint64_t whole, uint64_t least,
                                         Shared& sh) {
-  const Weigher<FAR> weigh{sh.scale, sh.roots};
+  const Weigher<FAR> weigh(sh.scale, sh.roots);
   const int me = threadIdx.x;
   uint64_t mine = 0, w = 0, before = 0;
   int rank = 0;
@@ -688,17 +739,11 @@ __device__ __noinline__ void finish_few(const Params& p, const int64_t r, const 
 template <bool FAR, class T, class Source>
 __device__ __noinline__ void finish_many(const Params& p, const int64_t r, const Request q, const Row<T> row, const Source src,
                                          uint64_t whole, float above, uint64_t least, const Place place, Shared& sh) {
-  const Weigher<FAR> weigh{sh.scale, sh.roots};
+  const Weigher<FAR> weigh(sh.scale, sh.roots);
   const int lane = threadIdx.x & 31, part = place.part();
-  const float inv_t = 1.f / q.t;
   uint64_t from = above > -INFINITY ? uint64_t(key_of(above)) << 32 : 0;
-  if (q.top_k > 0) from = find_cut<FAR>(src, false, uint64_t(q.top_k), 0.f, 0, inv_t, from, place, sh);
-  if (q.top_p < 1.f) from = find_cut<FAR>(src, true, 0, q.top_p, whole, inv_t, from, place, sh);
-  auto weight_of = [&](float x, int i) -> uint64_t {
-    if (number_of(x, i) < from) return 0;
-    const uint64_t w = weigh(x);
-    return w >= least ? w : 0;
-  };
+  if (q.top_k > 0) from = find_cut<FAR>(src, false, uint64_t(q.top_k), 0.f, 0, from, place, sh);
+  if (q.top_p < 1.f) from = find_cut<FAR>(src, true, 0, q.top_p, whole, from, place, sh);
   const uint64_t sum = warp_sum64(sum_of<FAR>(row, src, part, from, least, sh));
   if (lane < place.ctas) st_cluster_u64(tc::peer_addr(&sh.part[part], lane), sum);
   tc::cluster_sync();
@@ -725,41 +770,27 @@ __device__ __noinline__ void finish_many(const Params& p, const int64_t r, const
   const uint64_t before = __shfl_sync(0xffffffffu, first + (second ? v[0] : 0), at_lane);
   if (owner / kWarps != place.rank) return;
 
-  // the token: a run of the part's pieces a thread
-  using P = Piece<T>;
-  const int a = min(owner * row.per, row.pieces), b = min(a + row.per, row.pieces), run = (b - a + kThreads - 1) / kThreads;
-  const int a0 = min(a + int(threadIdx.x) * run, b), b0 = min(a0 + run, b);
-  auto weights_of = [&](const uint4& piece, int i, int t, uint64_t (&w)[2]) {  // of elements t and t + 1
-    weigh(P::at(piece, t), P::at(piece, t + 1), w[0], w[1]);
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      if (w[k] < least || number_of(clean(P::at(piece, t + k)), i + t + k) < from) w[k] = 0;
+  // the token: a run of the part's entries a thread
+  const int i0 = row.begin(owner), i1 = row.begin(owner + 1), run = (i1 - i0 + kThreads - 1) / kThreads;
+  const int a = min(i0 + int(threadIdx.x) * run, i1), b = min(a + run, i1);
+  auto weight_of = [&](int i) -> uint64_t {
+    const float x = clean(float(row.x[i]));
+    const uint64_t w = weigh(x);
+    return number_of(x, i) >= from && w >= least ? w : 0;
   };
   uint64_t mine = 0;
-#pragma unroll 2
-  for (int j = a0; j < b0; ++j) {
-    const uint4 piece = row.piece(j);
-#pragma unroll
-    for (int t = 0; t < P::N; t += 2) {
-      uint64_t w[2];
-      weights_of(piece, j * P::N - row.skew, t, w);
-      mine += w[0] + w[1];
-    }
-  }
+#pragma unroll 4
+  for (int i = a; i < b; ++i) mine += weight_of(i);
   uint64_t total;
   uint64_t at = before + cta_scan64(mine, sh, total);
   if (at > limit || at + mine <= limit) return;
-  for (int j = a0; j < b0; ++j) {
-    const uint4 piece = row.piece(j);
-#pragma unroll
-    for (int t = 0; t < P::N; t += 2) {
-      uint64_t w[2];
-      weights_of(piece, j * P::N - row.skew, t, w);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        if (at <= limit && at + w[k] > limit) write_token(p, r, j * P::N - row.skew + t + k, w[k], all);
-        at += w[k];
-      }
+#pragma unroll 1
+  for (int i = a; i < b; ++i) {
+    const uint64_t w = weight_of(i);
+    at += w;
+    if (at > limit) {
+      write_token(p, r, i, w, all);
+      return;
     }
   }
 }
@@ -773,31 +804,30 @@ template <bool FAR, bool kSums, class T>
 __device__ __noinline__ Collected collect(const Row<T> row, int part, float bound, Shared& sh) {
   using P = Piece<T>;
   constexpr int N = P::N;
-  const Weigher<FAR> weigh{sh.scale, sh.roots};
+  const Weigher<FAR> weigh(sh.scale, sh.roots);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, begin = row.begin(part);
+  const uint32_t least = weigh.template floor_of<P>();
   uint64_t sum = 0;
   int n = 0;
   row.template pieces_of<kSums ? 2 : 4>(part, lane, [&](const uint4& v, int i) {
-    if (kSums) {
-#pragma unroll
-      for (int t = 0; t < N; t += 2) {
-        uint64_t a, b;
-        weigh(P::at(v, t), P::at(v, t + 1), a, b);
-        sum += a + b;
-      }
-    }
-    if (n > kList || !__any_sync(0xffffffffu, P::top(v) >= bound)) return;
+    if (kSums) sum = sum_piece<T>(weigh, P::raised(v, least), sum);
+    if (n > kList || !__any_sync(0xffffffffu, P::top(v) >= bound)) return;  // (more than there is room for)
     uint32_t which = 0;
 #pragma unroll
     for (int t = 0; t < N; ++t) which |= uint32_t(P::at(v, t) >= bound) << t;
-    int incl = __popc(which);
+    // candidates of the lanes before, and of all
+    const unsigned before = (1u << lane) - 1, lanes = __ballot_sync(0xffffffffu, which != 0);
+    int at = n + __popc(lanes & before);
+    n += __popc(lanes);
+    if (__any_sync(0xffffffffu, which & (which - 1))) {  // more than one of a lane: the counts' higher parts, less one
+      const int more = which ? __popc(which) - 1 : 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += t;
+      for (int bit = 0; bit < 3; ++bit) {
+        const unsigned m = __ballot_sync(0xffffffffu, more >> bit & 1);
+        at += __popc(m & before) << bit;
+        n += __popc(m) << bit;
+      }
     }
-    int at = n + incl - __popc(which);
-    n += __shfl_sync(0xffffffffu, incl, 31);
     while (which) {
       const int t = __ffs(which) - 1;
       which &= which - 1;
@@ -817,7 +847,7 @@ __device__ void draw(const Params& p, int64_t r, const Request& q, const Row<T>&
                      Shared& sh) {
   constexpr int N = Piece<T>::N;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = place.part();
-  const Weigher<FAR> weigh{sh.scale, sh.roots};
+  const Weigher<FAR> weigh(sh.scale, sh.roots);
   const uint64_t least = q.min_p > 0.f ? times<true>(weigh(weigh.k.m), q.min_p) : 0;
   const bool of_all = q.top_p < 1.f && q.top_k <= 0;  // top_p of the whole row's weights
   if (bound == -INFINITY || row.per * N > 65536) {
@@ -867,7 +897,7 @@ __device__ void draw(const Params& p, int64_t r, const Request& q, const Row<T>&
     // A guess holds when the candidates' weights reach top_p's target.  Tokens that each weigh less than (1 - top_p) / vocab of
     // the whole are less than 1 - top_p of it together: none has the cut, so the last attempt needs no luck.
     if (guess && attempt < 2 && warp_sum64(listed) < target_of(q.top_p, whole)) {
-      const float share = float(whole) / float(uint64_t(1) << 30 << weigh.k.shift) * (1.f - q.top_p) / float(p.vocab);
+      const float share = 0.98f * float(whole) / float(uint64_t(1) << 30 << weigh.k.shift) * (1.f - q.top_p) / float(p.vocab);
       const float safe = weigh.k.m + q.t * logf(share) - 1e-5f * (fabsf(weigh.k.m) + 100.f * q.t);
       const float next = attempt == 0 && fits ? fmaxf(weigh.k.m - kWider * q.t, safe) : safe;
       bound = next < bound ? next : safe;
@@ -926,48 +956,38 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const Params p) {
   row.template pieces_of<4>(place.part(), lane, [&](const uint4& v, int) { own = fmaxf(own, Piece<T>::top(v)); });
   float top = warp_max_f(own);
   if (lane == 0) sh.warp_top[warp] = top;
-  const uint32_t mine = (key_of(own) & ~uint32_t(kThreads - 1)) | (kThreads - 1 - threadIdx.x);
-  sh.own[threadIdx.x] = mine;
   __syncthreads();
   top = sh.warp_top[0];
 #pragma unroll
   for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sh.warp_top[w]);
-  auto own_value = [](uint32_t key) {
-    const float v = of_key(key & ~uint32_t(kThreads - 1));
-    return v > -INFINITY ? v : -INFINITY;  // (below -inf: a NaN's pattern)
-  };
   // A logit that top_k does not leave out is at least the ceil(k / CTAs)-th largest of the threads' own maxima in the CTA where that
-  // is lowest, and the k-th largest in any: so many tokens are at least that.
+  // is lowest: k of the maxima are.  Bisection finds it to 2^-9 of itself, which is near enough for a bound.
   const int share = (q.top_k + place.ctas - 1) / place.ctas;
-  float kth[2] = {-INFINITY, -INFINITY};
+  float kth = -INFINITY;
   if (q.top_k > 0 && share <= kThreads) {
-    // (the low bits of a maximum make way for the thread's number, so that no two are equal: a bound that is lower by 2^-15 of itself)
-    int above = 0;
-#pragma unroll 8
-    for (int j = 0; j < kThreads; j += 4) {
-      const uint4 o = *reinterpret_cast<const uint4*>(&sh.own[j]);
-      above += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
+    const uint32_t mine = key_of(own);
+    uint32_t lo = key_of(-kLargest), hi = key_of(top);  // lo: so many are at least that
+    if (__syncthreads_count(mine >= lo) >= share) {
+      for (int i = 0; i < 18 && lo < hi; ++i) {
+        const uint32_t mid = lo + (hi - lo + 1) / 2;
+        if (__syncthreads_count(mine >= mid) >= share) lo = mid;
+        else hi = mid - 1;
+      }
+      kth = of_key(lo);
     }
-    if (above == share - 1) sh.warp_v[0] = mine;
-    if (above == q.top_k - 1) sh.warp_v[1] = mine;
-    __syncthreads();
-    kth[0] = own_value(uint32_t(sh.warp_v[0]));
-    if (q.top_k <= kThreads) kth[1] = own_value(uint32_t(sh.warp_v[1]));
   }
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // the other CTAs run: their shared memory may be written
   if (int(threadIdx.x) < place.ctas) {
     tc::st_cluster_u32(tc::peer_addr(&sh.tops[place.rank], threadIdx.x), __float_as_uint(top));
-    tc::st_cluster_u32(tc::peer_addr(&sh.kth[0][place.rank], threadIdx.x), __float_as_uint(kth[0]));
-    tc::st_cluster_u32(tc::peer_addr(&sh.kth[1][place.rank], threadIdx.x), __float_as_uint(kth[1]));
+    tc::st_cluster_u32(tc::peer_addr(&sh.kth[place.rank], threadIdx.x), __float_as_uint(kth));
   }
   tc::cluster_sync();
   float low = INFINITY, bound = -INFINITY;
   for (int c = 0; c < place.ctas; ++c) {
     top = fmaxf(top, sh.tops[c]);
-    low = fminf(low, sh.kth[0][c]);
-    bound = fmaxf(bound, sh.kth[1][c]);
+    low = fminf(low, sh.kth[c]);
   }
-  if (q.top_k > 0) bound = fminf(fmaxf(bound, low), kLargest);
+  if (q.top_k > 0) bound = fminf(low, kLargest);
   if (!fine || top == -INFINITY) {  // nothing to draw from, or no way to
     if (place.rank == 0 && threadIdx.x == 0) {
       if (!fine) atomicOr(&g_status_sample, TPA_DEV_BAD_INPUT);
@@ -990,8 +1010,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const Params p) {
     k.ch = ch;
     k.cl = cl;
     k.base = kMagic - near;
-    k.rest = far ? 0.f : -__fmaf_rn(top, cl, __fmaf_rn(top, ch, -near));
-    k.least = fmaxf(top - 64.f / ch, -kLargest);
+    k.least = fmaxf(top - float(31 + p.shift) / ch, -kLargest);
     k.shift = p.shift;
     k.s0 = 32 * (32 - p.shift) + kMagicBits + 31;
   }
