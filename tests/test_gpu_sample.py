@@ -256,3 +256,28 @@ def test_streams_and_graphs(tpa):
 def test_no_rows(tpa):
     t, l = tpa.sample_tokens(torch.zeros((0, 10), device="cuda"), torch.zeros(0, device="cuda"))
     assert t.shape == (0,) and l.shape == (0,)
+
+
+@pytest.mark.parametrize("n,v", [(3, 151936), (70, 20000), (200, 7000)])
+@pytest.mark.parametrize("form", [dict(temperature=5.0, top_p=0.97), dict(temperature=1.5, top_p=0.5), dict(temperature=3.0, top_p=0.9, min_p=0.01)])
+def test_cuts_among_very_many_tokens(tpa, n, v, form):
+    """top_p keeps far more tokens than the ones next to the maximum; every second row has its own, narrow cut."""
+    for dtype in (torch.float32, torch.bfloat16):
+        x, u = _logits(n, v, 23, dtype)
+        t = torch.full((n,), form["temperature"])
+        t[1::2] = 0.5
+        _check(tpa, x, u, t, 0, form["top_p"], form.get("min_p", 0.0))
+    tpa.sync_status()
+
+
+def test_equal_logits_with_top_p_of_many(tpa):
+    x = torch.zeros((5, 30011))
+    x[1, ::3] = -2.0
+    x[2] = torch.arange(30011) % 7
+    x[3, 20000:] = math.inf
+    x[4] = -1e38
+    u = torch.tensor([0.0, 0.3, 0.6, 0.9, 1 - 2.0 ** -24])
+    for p in (0.1, 0.5, 0.999):
+        _check(tpa, x, u, top_p=p)
+        _check(tpa, x, u, top_k=torch.tensor([0, 29000, 0, 5000, 20], dtype=torch.int32), top_p=p)
+    tpa.sync_status()
