@@ -75,7 +75,16 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 __device__ __forceinline__ float of_key(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
-__device__ __forceinline__ uint64_t number_of(float x, int i) { return uint64_t(key_of(x)) << 32 | (0xffffffffu - uint32_t(i)); }
+// A token's number: the key of its logit, and below it `bits` bits of its index, complemented (bits: as many as indexes have, so that a
+// histogram's bins over a range of numbers hold equal logits apart).
+__device__ __forceinline__ uint64_t number_of(float x, int i, int bits) {
+  return uint64_t(key_of(x)) << bits | (((1u << bits) - 1) - uint32_t(i));
+}
+__device__ __forceinline__ float logit_of(uint64_t n, int bits) { return of_key(uint32_t(n >> bits)); }
+__device__ __forceinline__ int index_of(uint64_t n, int bits) {
+  const uint32_t most = (1u << bits) - 1;
+  return int(most - (uint32_t(n) & most));
+}
 
 constexpr float kMagic = 1.5f * 262144.f;  // its last place is 1/32
 constexpr int kMagicBits = 0x48c00000;
@@ -404,8 +413,9 @@ __device__ __noinline__ uint64_t sum_of(const Row<T> row, int part, uint64_t fro
   const Weigher<FAR> weigh(sh.scale, sh.roots);
   const uint32_t floor = weigh.template floor_of<P>();
   uint64_t sum = 0;
-  const float last = from ? of_key(uint32_t(from >> 32)) : -INFINITY;  // of its equals, those up to an index
-  const int last_i = from ? int(0xffffffffu - uint32_t(from)) : 0x7fffffff;
+  const int bits = 32 - weigh.k.shift;
+  const float last = from ? logit_of(from, bits) : -INFINITY;  // of its equals, those up to an index
+  const int last_i = from ? index_of(from, bits) : 0x7fffffff;
   row.template pieces_of<2>(part, threadIdx.x & 31, [&](const uint4& v, int i) {
     if (!__any_sync(0xffffffffu, P::top(v) >= last)) return;
     const uint4 r = P::raised(v, floor);
@@ -416,8 +426,9 @@ __device__ __noinline__ uint64_t sum_of(const Row<T> row, int part, uint64_t fro
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const float e = P::at(v, t + u), x = e > kLargest ? kLargest : e;  // (a NaN stays one, and fails)
+        const bool kept = x > last || (x == last && i + t + u <= last_i);
         const uint64_t a = w[u].value();
-        if ((x > last || (x == last && i + t + u <= last_i)) && a >= least) sum += a;
+        sum += kept && a >= least ? a : 0;
       }
     }
   });
@@ -433,7 +444,7 @@ __device__ __forceinline__ uint64_t sum_of(const Row<T>&, const List& list, int 
   uint64_t sum = 0;
   list.all<true>(part, threadIdx.x & 31, weigh, -kLargest, [&](float x, int i, const Weight& w, bool) {
     const uint64_t v = w.value();
-    sum += number_of(x, i) >= from && v >= least ? v : 0;
+    sum += number_of(x, i, 32 - weigh.k.shift) >= from && v >= least ? v : 0;
   });
   return sum;
 }
@@ -446,23 +457,25 @@ struct Search {
   int shift;          // of a number's distance from hi, to its bin, from the second level on
   float steps;        // bins of the first level in a distance of 1
   bool by_weight, halves;
+  int bits;           // of an index, in a number
   __device__ __forceinline__ int bin0(float m, float x) const { return min(int(__fmul_rn(__fsub_rn(m, x), steps)), kBins - 1); }
   // bits of a weight that are left out in a bin
   static __device__ __forceinline__ int bits_off(int shift, int bin) { return max(shift - bin / kBinsPerBit, 0); }
-  static __device__ __forceinline__ float value(uint64_t n) {  // the logit of a number, within those that there are
-    return of_key(min(max(uint32_t(n >> 32), key_of(-kLargest)), key_of(kLargest)));
+  __device__ __forceinline__ float value(uint64_t n) const {  // the logit of a number, within those that there are
+    return of_key(min(max(uint32_t(n >> bits), key_of(-kLargest)), key_of(kLargest)));
   }
   // whether a token whose logit is in [lo_x, hi_x] takes part
   __device__ __forceinline__ bool has(float x, int i) const {
-    return !((x == lo_x && number_of(x, i) < lo) || (x == hi_x && number_of(x, i) > hi));
+    return !((x == lo_x && number_of(x, i, bits) < lo) || (x == hi_x && number_of(x, i, bits) > hi));
   }
 };
 
 // Into a bin: a token, and of a weight the bits that are not left out.
+template <bool kHalves>
 __device__ __forceinline__ void add_to(Shared& sh, int bin, bool ok, const Weight& w, int b0, const Search& q, int shift) {
   if (ok) atomicAdd(&sh.counts[bin], 1u);
   if (!q.by_weight) return;
-  if (q.halves) {  // (by - (32 - shift) bits are off the weight: as many as the bin leaves out, or one more)
+  if (kHalves) {  // (by - (32 - shift) bits are off the weight: as many as the bin leaves out, or one more)
     const uint32_t v = w.w >> min(max(w.by - 32 + shift - min(b0 / kBinsPerBit, shift), 0), 31);
     uint32_t* sums = reinterpret_cast<uint32_t*>(&sh.sums[bin]);
     if (ok) atomicAdd(sums, v & 0xffffu);
@@ -473,26 +486,26 @@ __device__ __forceinline__ void add_to(Shared& sh, int bin, bool ok, const Weigh
 }
 
 // This warp's tokens into the CTA's histogram: all from q.lo on at the first level (kWeigh: with their weights), then those of the bin.
-template <bool FAR, bool kWeigh, class Source>
+template <bool FAR, bool kWeigh, bool kHalves, class Source>
 __device__ __noinline__ void count_first(const Source src, int part, const Search q, Shared& sh) {
   const Weigher<FAR> weigh(sh.scale, sh.roots);
-  const int last_i = int(0xffffffffu - uint32_t(q.lo)), shift = weigh.k.shift;
+  const int last_i = index_of(q.lo, q.bits), shift = weigh.k.shift;
   const float m = weigh.k.m;
   src.template all<kWeigh>(part, threadIdx.x & 31, weigh, q.lo_x, [&](float x, int i, const Weight& w, bool ok) {
     // (q.lo as a number has no token below it among those of its logit where it is a bound's: its lower half is 0)
     const bool in = ok && (x > q.lo_x || uint32_t(i) <= uint32_t(last_i));
     const int b = q.bin0(m, x);
-    add_to(sh, in ? b : 0, in, w, b, q, shift);
+    add_to<kHalves>(sh, in ? b : 0, in, w, b, q, shift);
   });
 }
-template <bool FAR, class Source>
+template <bool FAR, bool kHalves, class Source>
 __device__ __noinline__ void count_more(const Source src, int part, const Search q, Shared& sh) {
   const Weigher<FAR> weigh(sh.scale, sh.roots);
   src.some(part, threadIdx.x & 31, q.lo_x, q.hi_x, [&](float x, int i) {
     if (!q.has(x, i) || q.bin0(weigh.k.m, x) != q.chosen) return;
     Weight w[2];
     if (q.by_weight) weigh.template pair<true>(x, x, w);
-    add_to(sh, int((q.hi - number_of(x, i)) >> q.shift), true, w[0], q.chosen, q, weigh.k.shift);
+    add_to<kHalves>(sh, int((q.hi - number_of(x, i, q.bits)) >> q.shift), true, w[0], q.chosen, q, weigh.k.shift);
   });
 }
 
@@ -503,7 +516,7 @@ __device__ __noinline__ void gather(const Source src, int part, const Search q, 
   src.some(part, threadIdx.x & 31, q.lo_x, q.hi_x, [&](float x, int i) {
     if (!q.has(x, i) || q.bin0(m, x) != q.chosen) return;
     const uint32_t at = atomicAdd(&sh.here_n, 1u);
-    if (at < kFew) sh.few_w[at] = number_of(x, i);
+    if (at < kFew) sh.few_w[at] = number_of(x, i, q.bits);
   });
   __syncthreads();
   const uint32_t n = min(sh.here_n, uint32_t(kFew));
@@ -588,7 +601,8 @@ __device__ __noinline__ uint64_t find_cut(const Source src, bool by_weight, uint
   // A search leaves out the bits of a weight below 2^-30 of the largest that its bin can hold, 31 are left, and a sum of 65536
   // of them fits in two halves of 32 bits (the hardware adds to no 64-bit number in shared memory: one sum in a
   // loop took 90 us for a row of 32000).
-  Search q{from, ~uint64_t(0), 0.f, 0.f, 0, -1, 0, steps, by_weight, src.most(place) <= 65536};
+  const int ib = 32 - weigh.k.shift;
+  Search q{from, ((uint64_t(key_of(kLargest)) + 1) << ib) - 1, 0.f, 0.f, 0, -1, 0, steps, by_weight, src.most(place) <= 65536, ib};
   uint64_t &lo = q.lo, &hi = q.hi, above = 0, target = count;
   int &chosen = q.chosen, &shift = q.shift;
   for (int level = 0;; ++level) {
@@ -605,9 +619,15 @@ __device__ __noinline__ uint64_t find_cut(const Source src, bool by_weight, uint
     q.level = level;
     q.lo_x = q.value(lo);
     q.hi_x = q.value(hi);
-    if (level > 0) count_more<FAR>(src, part, q, sh);
-    else if (by_weight) count_first<FAR, true>(src, part, q, sh);
-    else count_first<FAR, false>(src, part, q, sh);
+    if (level > 0) {
+      if (q.halves) count_more<FAR, true>(src, part, q, sh);
+      else count_more<FAR, false>(src, part, q, sh);
+    } else if (by_weight) {
+      if (q.halves) count_first<FAR, true, true>(src, part, q, sh);
+      else count_first<FAR, true, false>(src, part, q, sh);
+    } else {
+      count_first<FAR, false, true>(src, part, q, sh);
+    }
     tc::cluster_sync();  // the histograms are there
     // each CTA adds up a share of the bins, a run of them a thread
     const int each = kBins / place.ctas, run = (each + kThreads - 1) / kThreads;
@@ -624,21 +644,18 @@ __device__ __noinline__ uint64_t find_cut(const Source src, bool by_weight, uint
         const uint64_t t = sh.sums[first + j];
         if (by_weight) v[j] = q.halves ? ((t >> 32) << 16) + uint32_t(t) : t;
       } else if (mine && j < run) {
-        for (int c0 = 0; c0 < place.ctas; c0 += 4) {
-          uint32_t n[4];  // under way together
-          uint64_t t[4];
+        uint32_t n[kMostCtas];  // under way together (of CTAs that are not there, this one's, which do not count)
+        uint64_t t[kMostCtas];
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (c0 + c < place.ctas) {
-              n[c] = ld_cluster_u32(tc::peer_addr(&sh.counts[first + j], c0 + c));
-              if (by_weight) t[c] = ld_cluster_u64(tc::peer_addr(&sh.sums[first + j], c0 + c));
-            }
+        for (int c = 0; c < kMostCtas; ++c) {
+          const int from_cta = c < place.ctas ? c : place.rank;
+          n[c] = ld_cluster_u32(tc::peer_addr(&sh.counts[first + j], from_cta));
+          t[c] = ld_cluster_u64(tc::peer_addr(&sh.sums[first + j], from_cta));
+        }
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (c0 + c < place.ctas) {
-              tokens[j] += n[c];
-              if (by_weight) v[j] += q.halves ? ((t[c] >> 32) << 16) + uint32_t(t[c]) : t[c];
-            }
+        for (int c = 0; c < kMostCtas; ++c) {
+          tokens[j] += c < place.ctas ? n[c] : 0;
+          v[j] += c < place.ctas ? (q.halves ? ((t[c] >> 32) << 16) + uint32_t(t[c]) : t[c]) : 0;
         }
       }
       if (by_weight) v[j] <<= q.bits_off(weigh.k.shift, level > 0 ? chosen : first + j);
@@ -684,8 +701,8 @@ __device__ __noinline__ uint64_t find_cut(const Source src, bool by_weight, uint
       // the numbers that the bin can hold: its logits, and the roundings of their distances
       const float far = float(b + 1) / steps, near = float(b) / steps;
       const float slack = 1e-6f * (fabsf(m) + far) + 1e-37f;
-      const uint64_t low = uint64_t(key_of(clean(m - far - slack))) << 32;
-      const uint64_t high = uint64_t(key_of(clean(m - near + slack))) << 32 | 0xffffffffu;
+      const uint64_t low = uint64_t(key_of(clean(m - far - slack))) << q.bits;
+      const uint64_t high = ((uint64_t(key_of(clean(m - near + slack))) + 1) << q.bits) - 1;
       if (b < kBins - 1 && low > lo) lo = low;
       if (high < hi) hi = high;
     } else {
@@ -708,13 +725,16 @@ __device__ __noinline__ uint64_t find_cut(const Source src, bool by_weight, uint
     if (me < n) {
       mine = sh.few[me];
       const int off = q.bits_off(weigh.k.shift, chosen);
-      w = by_weight ? weigh(of_key(uint32_t(mine >> 32))) >> off << off : 1;
+      w = by_weight ? weigh(logit_of(mine, q.bits)) >> off << off : 1;
       sh.few_w[me] = w;
     }
     __syncthreads();
     if (me < n) {
-      for (int j = 0; j < n; ++j)
-        if (sh.few[j] > mine) before += sh.few_w[j];
+#pragma unroll 8
+      for (int j = 0; j < n; ++j) {
+        const uint64_t v = sh.few_w[j];
+        before += sh.few[j] > mine ? v : 0;
+      }
       if (before < target && before + w >= target)
         for (int c = 0; c < place.ctas; ++c) st_cluster_u64(tc::peer_addr(&sh.cut, c), mine);
     }
@@ -759,17 +779,18 @@ __device__ __noinline__ void finish_few(const Result out, const Request q, int n
   int rank = 0;
   if (me < n) {
     mine = sh.few[me];
-    w = weigh(of_key(uint32_t(mine >> 32)));
+    w = weigh(logit_of(mine, 32 - weigh.k.shift));
     sh.few_w[me] = w;
   }
   __syncthreads();
   const bool top_k = q.top_k > 0;
   if (me < n && (top_k || q.top_p < 1.f)) {
-#pragma unroll 4
+#pragma unroll 8
     for (int j = 0; j < n; ++j) {
+      const uint64_t v = sh.few_w[j];
       const bool higher = sh.few[j] > mine;
       rank += higher;
-      before += higher ? sh.few_w[j] : 0;
+      before += higher ? v : 0;
     }
   }
   bool kept = me < n && (!top_k || rank < q.top_k);
@@ -781,7 +802,7 @@ __device__ __noinline__ void finish_few(const Result out, const Request q, int n
   uint64_t all;
   const uint64_t at = cta_scan64(kept ? w : 0, sh, all);
   const uint64_t limit = limit_of(q.u, all);
-  if (kept && at <= limit && at + w > limit) write_token(out, int(0xffffffffu - uint32_t(mine)), w, 0, all);
+  if (kept && at <= limit && at + w > limit) write_token(out, index_of(mine, 32 - weigh.k.shift), w, 0, all);
 }
 
 // The token of a part at which its running sum passes `limit`, among those from `from` on that weigh `least` or more; their weights are
@@ -795,7 +816,7 @@ __device__ __noinline__ void find_in_part(const Result out, const Row<T> row, in
   auto weight_of = [&](int i) -> uint64_t {
     const float x = clean(float(row.x[i]));
     const uint64_t w = weigh(x);
-    return number_of(x, i) >= from && w >= least ? w : 0;
+    return number_of(x, i, 32 - weigh.k.shift) >= from && w >= least ? w : 0;
   };
   uint64_t mine = 0;
 #pragma unroll 4
@@ -820,7 +841,7 @@ __device__ __noinline__ void finish_many(const Result out, const Request q, cons
                                          uint64_t whole, float above, uint64_t least, const Place place, Shared& sh) {
   const Weigher<FAR> weigh(sh.scale, sh.roots);
   const int lane = threadIdx.x & 31, part = place.part();
-  uint64_t from = above > -INFINITY ? uint64_t(key_of(above)) << 32 : 0;
+  uint64_t from = above > -INFINITY ? uint64_t(key_of(above)) << (32 - weigh.k.shift) : 0;
   if (q.top_k > 0) from = find_cut<FAR>(src, false, uint64_t(q.top_k), 0.f, 0, from, place, sh);
   if (q.top_p < 1.f) from = find_cut<FAR>(src, true, 0, q.top_p, whole, from, place, sh);
   const uint64_t sum = warp_sum64(sum_of<FAR>(row, src, part, from, least, sh));
@@ -1077,7 +1098,7 @@ __device__ void draw(const Result& out, const Request& q, const Row<T>& row, flo
       finish_many<FAR>(out, q, row, list, whole, -INFINITY, least, place, sh);
     } else {
       for (int i = lane; i < list.n; i += 32)
-        st_cluster_u64(tc::peer_addr(&sh.few[before + i], 0), number_of(sh.list_x[warp][i], begin + sh.list_i[warp][i]));
+        st_cluster_u64(tc::peer_addr(&sh.few[before + i], 0), number_of(sh.list_x[warp][i], begin + sh.list_i[warp][i], 32 - weigh.k.shift));
       tc::cluster_sync();
       if (place.rank == 0) finish_few<FAR>(out, q, all, whole, least, sh);
     }
