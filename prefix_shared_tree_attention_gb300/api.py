@@ -752,18 +752,21 @@ def verify_drafts(target_probs: torch.Tensor, draft_tokens: torch.Tensor, u_acce
     return tokens, n_accepted
 
 
+_I32 = torch.int32
+
+
 def _vector(name: str, t: torch.Tensor, n: int) -> int:
     """The address of a contiguous int32 tensor [n]."""
-    if t.dtype is not torch.int32 or t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor [{n}]")
-    return t.data_ptr()
+    if t.dtype is _I32 and t.shape == (n,) and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous int32 tensor [{n}]")
 
 
 def _table(name: str, t: torch.Tensor, n: int, m: int) -> int:
     """The address of a contiguous int32 tensor [n, m]."""
-    if t.dtype is not torch.int32 or t.shape != (n, m) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor [{n}, {m}]")
-    return t.data_ptr()
+    if t.dtype is _I32 and t.shape == (n, m) and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous int32 tensor [{n}, {m}]")
 
 
 def draft_masks(parents: torch.Tensor, offsets: torch.Tensor, kv_lens: torch.Tensor, max_q_len: int, window: int = 0,
@@ -783,7 +786,7 @@ def draft_masks(parents: torch.Tensor, offsets: torch.Tensor, kv_lens: torch.Ten
     if out is None:
         st = _launch_stream(stream, parents, offsets, kv_lens)
         dev = parents.device
-        positions, masks = _new(stream, (rows,), torch.int32, dev), _new(stream, (rows, words), torch.int32, dev)
+        positions, masks = _new(stream, (rows,), _I32, dev), _new(stream, (rows, words), _I32, dev)
     else:
         positions, masks = out
         _vector("positions", positions, rows)
@@ -809,8 +812,8 @@ def accept_drafts(parents: torch.Tensor, offsets: torch.Tensor, draft_tokens: to
           _vector("sampled", sampled, rows))
     if out is None:
         st = _launch_stream(stream, parents, offsets, draft_tokens, sampled)
-        dev, i32 = parents.device, torch.int32
-        tokens, path, n_accepted = _new(stream, (n, most), i32, dev), _new(stream, (n, most), i32, dev), _new(stream, (n,), i32, dev)
+        dev = parents.device
+        tokens, path, n_accepted = _new(stream, (n, most), _I32, dev), _new(stream, (n, most), _I32, dev), _new(stream, (n,), _I32, dev)
     else:
         tokens, path, n_accepted = out
         _table("tokens", tokens, n, most)
@@ -863,7 +866,7 @@ def paged_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Ten
     at_path, at_n = _table("path", path, n, most), _vector("n_accepted", n_accepted, n)
     st = _launch_stream(stream, k_cache, v_cache, pages, offsets, kv_lens, path, n_accepted, out)
     if out is None:
-        out = _new(stream, (n,), torch.int32, kv_lens.device)
+        out = _new(stream, (n,), _I32, kv_lens.device)
     else:
         _vector("out", out, n)
     check("tpa_paged_compact", lib().tpa_paged_compact(cache, layers, at_path, at_n, most, out.data_ptr(), st))
@@ -884,7 +887,7 @@ def paged_resize(pages: torch.Tensor, kv_lens: torch.Tensor, refs: torch.Tensor,
                            _int32("page_size", page_size), 0, 0, n, width, stride)
     st = _launch_stream(stream, refs, pages, kv_lens, out)
     if out is None:
-        out = _new(stream, (1,), torch.int32, refs.device)
+        out = _new(stream, (1,), _I32, refs.device)
     else:
         _vector("out", out, 1)
     check("tpa_paged_resize", lib().tpa_paged_resize(pool, out.data_ptr(), st))
@@ -907,7 +910,7 @@ def paged_fork(k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Tensor
     at_src, at_dst = _vector("src", src, forks), _vector("dst", dst, forks)
     st = _launch_stream(stream, refs, k_cache, v_cache, pages, kv_lens, src, dst, out)
     if out is None:
-        out = _new(stream, (1,), torch.int32, refs.device)
+        out = _new(stream, (1,), _I32, refs.device)
     else:
         _vector("out", out, 1)
     check("tpa_paged_fork", lib().tpa_paged_fork(pool, at_src, at_dst, forks, out.data_ptr(), st))
