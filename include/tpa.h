@@ -671,10 +671,11 @@ int tpa_paged_attn_tree_fwd(const tpa_paged_view* cache, const void* q, int64_t 
  * tpa_paged_compact — keep an accepted path: for each sequence the keys and
  * values in slots base + path[s][i], i < n_accepted[s], move to slots base + i (base as
  * above), and new_lens[s] = base + n_accepted[s].  What is behind is left as it was.
+ * The pages that hold a sequence's new tokens must be its own: it writes there.
  *   cache: as above; k_cache and v_cache hold n_layers caches one behind another,
  *     [n_layers, n_pages, Hkv, page_size, d], of the same pages
  *   path [n_seqs, max_path] int32, rising, path[s][i] >= i; n_accepted [n_seqs] int32
- *   new_lens [n_seqs] int32 (written; not kv_lens itself)
+ *   new_lens [n_seqs] int32 (written; neither kv_lens nor n_accepted itself)
  * A sequence whose path is none (not rising, beyond its new tokens, n_accepted
  * out of range) or whose lengths are out of range is left as it was, new_lens[s] = kv_lens[s], and is
  * reported.  One kernel.  Errors: TPA_ERR_INVALID_ARG, TPA_ERR_CUDA.
@@ -757,11 +758,12 @@ typedef struct {            /* each: an array of one entry a row (device), or NU
  *     number.  -inf (a masked token) is never drawn; a row of nothing else gives -1 and NaN.
  *   u [n_rows] fp32 in [0, 1);  tokens [n_rows] int32, logp [n_rows] fp32 (written)
  *   vocab <= 2^30
- * Weights are within 2^-29 of themselves and cut off below 2^-43 of the largest one for a vocabulary of 2^18 (2^-(61 - log2
- * vocab)), and their sums are exact: borders of top_p, min_p and the draw are those of the formulas to within
- * that.  Deterministic; a row's result does not depend on the others.  Parameters in arrays that are out of range
- * give -1 and NaN in their rows and are reported; a single value out of range is refused.  One kernel, one cluster of
- * CTAs a row.  Errors: TPA_ERR_INVALID_ARG, TPA_ERR_CUDA.
+ * Weights are within 2^-29 of themselves and cut off below 2^-(61 - log2 vocab) of the largest one (2^-43 for a
+ * vocabulary of 2^18), and their sums are exact: borders of top_p, min_p and the draw are those of the formulas to within
+ * that.  Deterministic; a row's result does not depend on what the others hold (where nothing is cut off, calls of different
+ * numbers of rows may have borders that differ by 2^-(61 - log2 vocab) of the sum).  Parameters in arrays that are out of
+ * range give -1 and NaN in their rows and are reported; a single value out of range is refused.  One kernel, one cluster
+ * of CTAs a row.  Errors: TPA_ERR_INVALID_ARG, TPA_ERR_CUDA.
  */
 int tpa_sample_tokens(const void* logits, int32_t logits_type, int64_t row_stride, int32_t n_rows, int32_t vocab,
                       const tpa_sample_params* params, const float* u, int32_t* tokens, float* logp, void* stream);
@@ -818,7 +820,7 @@ int tpa_draft_masks(const int32_t* parents, const int32_t* offsets, const int32_
 /*
  * tpa_accept_drafts — the path that the sampled tokens follow through each drafted tree.  Row 0 of a sequence is its last
  * sampled token and stands; behind a standing row r stands its first child whose drafted token is
- * the one sampled behind r.  With every row's token drawn from the policy (tpa_sample_tokens), the tokens
+ * the one sampled behind r (a negative one, padding or a row with nothing to draw, is nobody's).  With every row's token drawn from the policy (tpa_sample_tokens), the tokens
  * along the path are distributed as the policy's own, whatever was drafted.
  *   draft_tokens [n_rows] int32: each row's own token; sampled [n_rows] int32: the token drawn behind it
  *   path [n_seqs, max_path] int32 (written): the standing rows (numbers among the sequence's new tokens), then -1

@@ -22,6 +22,10 @@ method computes, written from the AReaL "树训练" (tree training) page:
 * ``balance``   — FFD and KK allocation of weighted items (trees or
                   sequences) to micro-batches / ranks and the packing metrics,
                   from the blog post "AReaL 序列打包算法 FFD 与 KK".
+* ``rope``, ``paged``, ``verify`` — the policy's rotation, paged attention and
+  draft verification; ``sample``, ``draft``, ``pages`` — tokens from logits,
+  drafted trees and a cache's pages.  In 64 bits or whole numbers, from the
+  formulas in ``include/tpa.h``.
 
 Only ``tests/``, ``__graft_entry__.smoke()`` and ``bench.py``'s CPU-baseline
 leg may import this package. It shares no code with the CUDA library and

@@ -25,12 +25,12 @@ def masks(parents, base: int, words: int, window: int = 0):
 
 
 def accept(parents, drafted, sampled, most: int):
-    """The rows that stand, at most `most`, and the tokens sampled behind them."""
+    """The rows that stand, at most `most`, and the tokens sampled behind them.  A negative token is nobody's."""
     if not parents or most < 1:
         return [], []
     path = [0]
     while len(path) < most:
-        below = [j for j, p in enumerate(parents) if p == path[-1] and drafted[j] == sampled[path[-1]]]
+        below = [j for j, p in enumerate(parents) if p == path[-1] and drafted[j] == sampled[path[-1]] >= 0]
         if not below:
             break
         path.append(below[0])

@@ -24,11 +24,12 @@ constexpr int kThreads = 128;
 __device__ __forceinline__ void report() { atomicOr(&g_status_draft, TPA_DEV_BAD_INPUT); }
 
 // First row and number of a sequence's new tokens; none (and reported) where its numbers are out of range.
+// (Inputs are read by plain loads, here and below: the kernel before, which may still run when this one starts, may write them.)
 struct Rows {
   int first, n;
 };
 __device__ __forceinline__ Rows load_rows(const int32_t* offsets, int s, int n_rows, int most) {
-  const int o0 = __ldg(offsets + s), o1 = __ldg(offsets + s + 1);
+  const int o0 = offsets[s], o1 = offsets[s + 1];
   if (o0 < 0 || o1 < o0 || o1 > n_rows || o1 - o0 > most || (s == 0 && o0 != 0)) {
     if (threadIdx.x == 0) report();
     return Rows{0, 0};
@@ -45,9 +46,9 @@ __global__ void __launch_bounds__(kThreads) masks_kernel(const int32_t* parents,
   const int s = blockIdx.x;
   const Rows q = load_rows(offsets, s, n_rows, 32 * words);
   if (q.n == 0) return;
-  const int base = __ldg(kv_lens + s) - q.n;
+  const int base = kv_lens[s] - q.n;
   for (int i = threadIdx.x; i < q.n; i += kThreads) {
-    int p = __ldg(parents + q.first + i);
+    int p = parents[q.first + i];
     if (p < -1 || p >= i) {
       report();
       p = -1;
@@ -77,7 +78,7 @@ __global__ void __launch_bounds__(kThreads) masks_kernel(const int32_t* parents,
 }
 
 // Every token that is the first of its parent's children with the token sampled behind the parent becomes that one's
-// next; then one thread follows the path from row 0.
+// next (a negative token, padding of a tree or a row with nothing to draw, is nobody's); then one thread follows the path from row 0.
 __global__ void __launch_bounds__(kThreads) accept_kernel(const int32_t* parents, const int32_t* offsets, const int32_t* drafted,
                                                           const int32_t* sampled, int n_rows, int32_t* tokens, int32_t* path,
                                                           int32_t* n_accepted, int most) {
@@ -90,13 +91,13 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const int32_t* parents
   const Rows q = load_rows(offsets, s, n_rows, kMostDrafted);
   for (int i = threadIdx.x; i < q.n; i += kThreads) {
     next_s[i] = q.n;
-    sampled_s[i] = __ldg(sampled + q.first + i);
+    sampled_s[i] = sampled[q.first + i];
   }
   __syncthreads();
   for (int i = threadIdx.x; i < q.n; i += kThreads) {
-    const int p = __ldg(parents + q.first + i), x = __ldg(drafted + q.first + i);
+    const int p = parents[q.first + i], x = drafted[q.first + i];
     if (p < -1 || p >= i) report();
-    else if (p >= 0 && sampled_s[p] == x) atomicMin(next_s + p, i);
+    else if (p >= 0 && x >= 0 && sampled_s[p] == x) atomicMin(next_s + p, i);
   }
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -136,15 +137,15 @@ __global__ void __launch_bounds__(256) compact_kernel(const CompactParams p) {
   tc::grid_wait_prior();
   const int s = blockIdx.x, layer = blockIdx.y >> 1;
   const Rows q = load_rows(p.offsets, s, p.n_rows, 1 << 30);
-  const int kv = __ldg(p.kv_lens + s), base = kv - q.n;
+  const int kv = p.kv_lens[s], base = kv - q.n;
   const int32_t* path = p.path + int64_t(s) * p.most;
-  int n = __ldcg(p.n_accepted + s);
+  int n = p.n_accepted[s];
   bool bad = n < 0 || n > p.most || n > q.n || base < 0 || kv > (int64_t(p.max_pages) << p.page_shift);
   if (!bad) {
     int wrong = 0;
     for (int i = threadIdx.x; i < n; i += blockDim.x) {
-      const int at = __ldcg(path + i);
-      wrong |= at < i || at >= q.n || (i > 0 && at <= __ldcg(path + i - 1));
+      const int at = path[i];
+      wrong |= at < i || at >= q.n || (i > 0 && at <= path[i - 1]);
     }
     bad = __syncthreads_or(wrong);
   }
@@ -156,7 +157,7 @@ __global__ void __launch_bounds__(256) compact_kernel(const CompactParams p) {
   uint4* cache = (blockIdx.y & 1 ? p.v_cache : p.k_cache) + layer * p.layer_pieces;
   const int32_t* row = p.pages + int64_t(s) * p.page_stride;
   auto piece_of = [&](int slot, int head, int c) -> int64_t {  // -1: no such page
-    const int page = __ldg(row + (slot >> p.page_shift));
+    const int page = row[slot >> p.page_shift];
     if (uint32_t(page) >= uint32_t(p.n_pages)) {
       report();
       return -1;
@@ -171,7 +172,7 @@ __global__ void __launch_bounds__(256) compact_kernel(const CompactParams p) {
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
         to[u] = -1;
-        const int i = i0 + u, at = i < n ? __ldcg(path + i) : i;
+        const int i = i0 + u, at = i < n ? path[i] : i;
         if (at == i) continue;  // it is there (or there is none)
         const int64_t from = piece_of(base + at, head, c);
         if (from < 0) continue;
@@ -229,7 +230,7 @@ extern "C" int tpa_paged_compact(const tpa_paged_view* cache, int32_t n_layers, 
   if (rc != TPA_OK) return rc;
   if (n_layers < 1 || n_layers > 32767 || max_path < 1) return TPA_ERR_INVALID_ARG;
   if (cache->n_seqs == 0) return TPA_OK;
-  if (!path || !n_accepted || !new_lens || new_lens == cache->kv_lens || !aligned4({path, n_accepted, new_lens}))
+  if (!path || !n_accepted || !new_lens || new_lens == cache->kv_lens || new_lens == n_accepted || !aligned4({path, n_accepted, new_lens}))
     return TPA_ERR_INVALID_ARG;
   CompactParams p = {};
   p.k_cache = static_cast<uint4*>(cache->k_cache);

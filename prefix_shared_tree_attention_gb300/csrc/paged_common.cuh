@@ -272,7 +272,7 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* m, uin
 
 // The position of a drafted token, number i of its sequence: between the tree's first and the one that a chain would have.
 __device__ __forceinline__ int tree_position(const Batch& b, int row, int base, int i) {
-  return min(max(__ldg(b.positions + row), base), base + i);
+  return min(max(b.positions[row], base), base + i);
 }
 
 // One CTA's part of a tile, as the producer hands it to the other roles.

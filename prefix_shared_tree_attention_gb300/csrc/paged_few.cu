@@ -20,6 +20,10 @@
 // 2950 cycles, what HBM gives an SM; the start (lengths, first pages, first
 // keys: 7 us) and the joining of cut tiles (3 us) come on top: 64 sequences of 300
 // to 3000 tokens, 440 MB, 78 us; 256 of 50 to 600, where a tile has three steps, 80.4 us for 342 MB.
+//
+// Drafted trees (TREE, an instance of its own: chains keep their code) differ in steps that hold new tokens, or a window's
+// border: a thread builds, for its key, the word of rows that see it, from the tokens' masks and positions, which few
+// steps of a sequence do.  64 sequences of 300 to 3000 tokens, 8 drafted each, 499 MB: 95 us, as chains of that length.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -457,7 +461,7 @@ __global__ void __launch_bounds__(512, 1)
                   sees = p.b.window == 0 || key > tree_position(p.b, row_first + t_, base, at_first + t_) - p.b.window;
                 else
                   sees = drafted <= at_first + t_ &&
-                         (__ldg(p.b.masks + int64_t(row_first + t_) * p.b.mask_words + (drafted >> 5)) >> (drafted & 31) & 1);
+                         (p.b.masks[int64_t(row_first + t_) * p.b.mask_words + (drafted >> 5)] >> (drafted & 31) & 1);
                 if (sees) rows |= heads << (t_ * p.b.group);
               }
 #pragma unroll

@@ -24,6 +24,13 @@
 // thread, gave nothing or lost 2 %.
 // Few rows cost no more here than in the kernel made for them: one chunk of 512 tokens
 // beside 63 single ones of other sequences takes 114 us, the two by themselves 32 and 79.
+//
+// Drafted trees (TREE, an instance of its own: chains keep their code): a row's thread has its mask's words beside its 128
+// columns of a step, shifted to where the tree begins, so that a step with drafted tokens costs 128 selects more.  Trees
+// of 20 to 64 tokens are one sub-tile or two of few rows: bound by the reads of the cache (16 sequences
+// of 1000 to 8000 tokens, 280 MB: 78 us, as chains 75) or, where one sequence's rows are more than a tile's (48 tokens of 8 heads, 130001
+// cached: 62 us), by reading it once for each tile.  The masks are read by plain loads: the kernel that writes them may
+// end after this one starts.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -368,7 +375,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
           if (TREE && live && key0 + kStep > base) {
             // the row's bits for the step's columns: all before the tree, then those of its mask
             const uint32_t* mask = p.b.masks + int64_t(first + tok) * p.b.mask_words;
-            auto word = [&](int i) { return i < p.b.mask_words ? __ldg(mask + i) : 0u; };
+            auto word = [&](int i) { return i < p.b.mask_words ? mask[i] : 0u; };
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
               const int rel = key0 + 32 * w - base;

@@ -34,6 +34,7 @@ constexpr int kU = 4;                       // entries of a row that a lane has 
 
 __device__ __forceinline__ void report() { atomicOr(&g_status_pages, TPA_DEV_BAD_INPUT); }
 
+// (Inputs are read by plain loads: the kernel before, which may still run when this one starts, may write them.)
 struct Params {
   int32_t* pages;
   int32_t* kv_lens;
@@ -49,8 +50,8 @@ struct Params {
 // Shared memory: what each row wants (and one more), the entry of the row that the first of them goes to, the free
 // pages of this CTA's shares as bits, and in a fork a bit for each row that is a dst.
 struct Shared {
+  int64_t warp_v[kWarps];
   int32_t share[kShares + 1];  // free pages of each share; then their running sums
-  int32_t warp_v[kWarps];
   int32_t bad;
 };
 struct View {
@@ -104,26 +105,27 @@ __device__ __forceinline__ void tell_all(int32_t* at, int32_t v) {
   for (int c = 0; c < kCluster; ++c) tc::st_cluster_u32(tc::peer_addr(at, c), uint32_t(v));
 }
 
-// Running sums of v over the CTA's threads; the whole in `total`.
-__device__ __forceinline__ int cta_scan(int v, Shared& sh, int& total) {  // (by all threads)
+// Running sums of v >= 0 over the CTA's threads, modulo 2^32; the whole in `total`, exactly.
+__device__ __forceinline__ int cta_scan(int v, Shared& sh, int64_t& total) {  // (by all threads)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int incl = v;
+  uint32_t incl = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int t = __shfl_up_sync(0xffffffffu, incl, o);
+    const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += t;
   }
+  const uint32_t high = __reduce_add_sync(0xffffffffu, uint32_t(v) >> 16), low = __reduce_add_sync(0xffffffffu, uint32_t(v) & 0xffffu);
   __syncthreads();
-  if (lane == 31) sh.warp_v[warp] = incl;
+  if (lane == 31) sh.warp_v[warp] = (int64_t(high) << 16) + low;
   __syncthreads();
-  int before = 0;
+  uint32_t before = 0;
   total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += sh.warp_v[w];
+    if (w < warp) before += uint32_t(sh.warp_v[w]);
     total += sh.warp_v[w];
   }
-  return before + incl - v;
+  return int(before + incl - uint32_t(v));
 }
 
 // This CTA's rows of n, dealt out in turn: f(row) by a thread each.
@@ -162,26 +164,28 @@ __device__ int hand_out(const Params& p, int n, int rank, const View& v, RowOf r
     }
     if (lane < kCluster) tc::st_cluster_u32(tc::peer_addr(&v.sh.share[share], lane), uint32_t(mine));
   }
-  // running sums of what the rows want, a run of rows a thread
+  // running sums of what the rows want, a run of rows a thread (8 rows of less than 2^26 pages; the whole may pass 32
+  // bits, and `room` with them: then the sums are not looked at)
   const int each = (n + kThreads - 1) / kThreads;
   const int a = min(int(threadIdx.x) * each, n), b = min(a + each, n);
-  int sum = 0, all;
+  int sum = 0;
+  int64_t all;
   for (int i = a; i < b; ++i) sum += v.want[i];
   int at = cta_scan(sum, v.sh, all);
   for (int i = a; i < b; ++i) {
     const int w = v.want[i];
     v.want[i] = at;
-    at += w;
+    at = int(uint32_t(at) + uint32_t(w));
   }
   tc::cluster_sync();
   const int mine = int(threadIdx.x) < kShares ? v.sh.share[threadIdx.x] : 0;
-  int room;
+  int64_t room;
   at = cta_scan(mine, v.sh, room);
   if (int(threadIdx.x) < kShares) v.sh.share[threadIdx.x] = at;
   __syncthreads();
   if (all <= room) {
     // ranks [r0, r1) among the free pages are this warp's
-    const int r0 = int(int64_t(all) * share / kShares), r1 = int(int64_t(all) * (share + 1) / kShares);
+    const int r0 = int(all * share / kShares), r1 = int(all * (share + 1) / kShares);
     int s = 0;  // the last share that begins at r0 or before
     for (int step = kShares / 2; step > 0; step >>= 1)
       if (v.sh.share[s + step] <= r0) s += step;
@@ -223,7 +227,7 @@ __device__ int hand_out(const Params& p, int n, int rank, const View& v, RowOf r
     }
   }
   tc::cluster_sync();  // the others' bits are read no more
-  return room - all;
+  return int(max(room - all, int64_t(INT32_MIN) + 1));
 }
 
 // Rows get the pages that their lengths need: what is behind them goes back, what is missing is handed out.
@@ -236,7 +240,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1) 
   const int rank = int(tc::cta_rank()), lane = threadIdx.x & 31;
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   each_row(p.n_rows, rank, [&](int r) {
-    const int len = __ldg(p.kv_lens + r);
+    const int len = p.kv_lens[r];
     const int have = held(p.pages + int64_t(r) * p.page_stride, p.max_pages);
     int need = have;
     if (len < 0 || len > (int64_t(p.max_pages) << p.page_shift)) report();
@@ -279,16 +283,16 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1) 
   __syncthreads();
   // a call with a row out of range, named twice, or both copied and written is not done at all
   for (int f = threadIdx.x; f < p.n_forks; f += kThreads) {
-    const int d = __ldg(p.dst + f);
+    const int d = p.dst[f];
     if (uint32_t(d) >= uint32_t(p.n_rows) || (atomicOr(v.named + (d >> 5), 1u << (d & 31)) >> (d & 31) & 1)) v.sh.bad = 1;
   }
   __syncthreads();
   for (int f = threadIdx.x; f < p.n_forks; f += kThreads) {
-    const int s = __ldg(p.src + f);
+    const int s = p.src[f];
     if (uint32_t(s) >= uint32_t(p.n_rows) || (v.named[s >> 5] >> (s & 31) & 1)) {
       v.sh.bad = 1;
     } else {
-      const int len = __ldg(p.kv_lens + s);
+      const int len = p.kv_lens[s];
       if (len < 0 || len > (int64_t(p.max_pages) << p.page_shift)) v.sh.bad = 1;
     }
   }
@@ -297,8 +301,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1) 
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   const int n = bad ? 0 : p.n_forks;
   each_row_warp(n, rank, [&](int f) {
-    const int s = __ldg(p.src + f), d = __ldg(p.dst + f);
-    const int len = __ldg(p.kv_lens + s), whole = len >> p.page_shift, part = len & ((1 << p.page_shift) - 1);
+    const int s = p.src[f], d = p.dst[f];
+    const int len = p.kv_lens[s], whole = len >> p.page_shift, part = len & ((1 << p.page_shift) - 1);
     const int32_t* from = p.pages + int64_t(s) * p.page_stride;
     int32_t* to = p.pages + int64_t(d) * p.page_stride;
     for (int j0 = lane; j0 - lane < p.max_pages; j0 += 32 * kU) {
@@ -333,14 +337,14 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1) 
     }
   });
   tc::cluster_sync();
-  const int left = hand_out(p, n, rank, v, [&](int f) { return __ldg(p.dst + f); });
+  const int left = hand_out(p, n, rank, v, [&](int f) { return p.dst[f]; });
   if (rank == 0 && threadIdx.x == 0) {
     *p.n_free = bad ? INT32_MIN : left;
     if (bad) report();
   }
   if (left < 0) {  // too few: the rows are left empty
     each_row_warp(n, rank, [&](int f) {
-      const int d = __ldg(p.dst + f);
+      const int d = p.dst[f];
       int32_t* to = p.pages + int64_t(d) * p.page_stride;
       for (int j = lane; j < v.have[f]; j += 32) {
         give_back(p, to[j]);
@@ -368,9 +372,9 @@ __global__ void __launch_bounds__(256) copy_kernel(const CopyParams p) {
   tc::grid_launch_dependents();
   tc::grid_wait_prior();
   const int f = blockIdx.x, layer = blockIdx.y >> 1;
-  const int s = __ldg(p.src + f), d = __ldg(p.dst + f);
+  const int s = p.src[f], d = p.dst[f];
   if (__ldcg(p.n_free) < 0 || uint32_t(s) >= uint32_t(p.n_rows) || uint32_t(d) >= uint32_t(p.n_rows)) return;
-  const int len = __ldcg(p.kv_lens + s), whole = len >> p.page_shift, part = len & ((1 << p.page_shift) - 1);
+  const int len = p.kv_lens[s], whole = len >> p.page_shift, part = len & ((1 << p.page_shift) - 1);
   if (part == 0 || len < 0 || whole >= p.max_pages) return;
   const int from = __ldcg(p.pages + int64_t(s) * p.page_stride + whole), to = __ldcg(p.pages + int64_t(d) * p.page_stride + whole);
   if (uint32_t(from) >= uint32_t(p.n_pages) || uint32_t(to) >= uint32_t(p.n_pages)) {
@@ -430,7 +434,9 @@ Params make_params(const tpa_paged_pool* c, int32_t* n_free) {
 // rows: of the call; table: rows of the table in a fork, else 0
 int launch(void (*kernel)(Params), const Params& p, int rows, int table, cudaStream_t st) {
   const uint32_t smem = shared_bytes(rows, p.words, table);
-  if (smem > 48 * 1024) TPA_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
+  // (always the same limit: calls from several threads set it beside one another)
+  const int most = int(shared_bytes(kMostRows, kMostPages / 32 / kShares, kMostTable));
+  if (smem > 48 * 1024) TPA_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
   return paged::launch_overlapped(kernel, dim3(kCluster), kThreads, smem, st, Params(p));
 }
 

@@ -1,20 +1,35 @@
 // The next token of each row of logits: temperature, top-k, top-p, min-p and a
-// draw from a given uniform number.  One cluster of 8 CTAs a row.
+// draw from a given uniform number.
 //
 // Tokens stand in the order of their logits, highest first, equal ones by
-// index: the order of the 64-bit number (logit as an ordered 32-bit key, index
-// complemented), all of which differ.  Top-k and top-p each keep the tokens from
-// a cut on; the cuts are found by histograms, first over the distance to the row's
-// maximum in steps of T / 64, then over digits of that number, until 256
-// tokens or fewer are left, which are ranked against each other.
+// index: the order of a 64-bit number (the logit as an ordered 32-bit key, below it the index
+// complemented), all of which differ.  Top-k and top-p each keep the tokens from a cut on.
 //
-// A draw has to be the same whatever the order of summation, so weights
-// exp((x - max) / T) are whole numbers: 2^y, y = (x - max) log2(e) / T, with the
-// product formed as a pair of fp32, y = k / 32 + g, 2^(k / 32) from a table to 30 bits, 2^g - 1
-// by its series (|g| <= 1/64, four terms, off by 2^-39).  The product of the two is off by 2^-30 of
-// itself (the rounding of g and of the series' value), and below 2^-(62 - log2 vocab) of
-// the largest weight it is cut off.  Their sums are exact, so nothing depends on
-// the grouping, and a running sum is off by less than 2^-29 of the whole.
+// Weights.  A draw has to be the same whatever the order of summation, so weights exp((x - max) / T) are
+// whole numbers: 2^y, y = x c - M with c = log2(e) / T as a pair of fp32 and M a multiple of 1/32,
+// y = k / 32 + g, 2^(k / 32) from a table to 30 bits, 2^g - 1 by its series (|g| <= 1/64, four terms, off by
+// 2^-39).  The product of the two is off by 2^-29 of itself (the rounding of g and of the series' value),
+// shifted to 31 + s bits at most, s = 32 - log2 vocabulary, and what is below 1 there is nothing.  A row's sum fits in 64
+// bits, is exact, and nothing depends on the grouping: borders are off by 2^-29 of the whole from the weights.
+//
+// A row's way (sample_kernel; a cluster of 1 to 8 CTAs of 8 warps, each warp a contiguous part of the row):
+//   1. the maximum, and for top-k a bound below which nothing is kept (the warp's threads' own maxima);
+//   2. the tokens from a bound on are collected, each warp's in its list of 512 in shared memory, and the whole row's weights are
+//      summed where top-p is of them.  Top-p's bound is a guess, max - 9 T (of a model's logits that is
+//      nearly all the weight), which the listed weights confirm; else a wider one, max - 11 T, and then
+//      one that no token below can pass (each weighs less than (1 - p) / vocabulary of the whole);
+//   3. up to 256 candidates, one a thread of the first CTA, are ranked against each other; more, or a list that was too
+//      short, have their cuts found by histograms (in shared memory, joined over the cluster): 1024 bins of 1/32 of a factor of 2
+//      of the weights, then of the numbers within the bin, until 256 tokens are left; then each part's sum, and the
+//      part in which the running sum passes u of the whole.
+// Rows without any cut go through once (plain_kernel): each warp moves its sum when it meets a larger maximum.
+//
+// What it has to do is to read the row: 64 rows of 151936 in bf16, 19 MB, 2.9 us at the copy's rate.  Without a cut it is bound by
+// the weights' instructions, 28 a token of which 7.5 us of issue slots are made here, and by a start and an end as long: 17.4 us.
+// With cuts it is bound by passes over a row that follow one another, with a cluster barrier after each, in which a warp has
+// little to overlap: 64 rows of 151936 in fp32, each with its own parameters, 42 us; with rows among them whose
+// top-p keeps thousands of tokens, which then have the device to themselves, 78; 64 such rows (T = 1.3, p = 0.97) 128;
+// 499 rows of 32000 45 us; one row of 32000 9.3 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -599,8 +614,8 @@ __device__ __noinline__ uint64_t find_cut(const Source src, bool by_weight, uint
   const int part = place.part();
   const float m = weigh.k.m, steps = float(kBinsPerBit) * weigh.k.ch;
   // A search leaves out the bits of a weight below 2^-30 of the largest that its bin can hold, 31 are left, and a sum of 65536
-  // of them fits in two halves of 32 bits (the hardware adds to no 64-bit number in shared memory: one sum in a
-  // loop took 90 us for a row of 32000).
+  // of them fits in two halves of 32 bits (the hardware adds to no 64-bit number in shared memory but in a loop of
+  // compare and swap, far slower where many meet in a bin).
   const int ib = 32 - weigh.k.shift;
   Search q{from, ((uint64_t(key_of(kLargest)) + 1) << ib) - 1, 0.f, 0.f, 0, -1, 0, steps, by_weight, src.most(place) <= 65536, ib};
   uint64_t &lo = q.lo, &hi = q.hi, above = 0, target = count;
@@ -1234,7 +1249,9 @@ __global__ void __launch_bounds__(kThreads, 4) plain_kernel(const Params p) {
 
 template <class T>
 int launch(Params& p, int n_rows, cudaStream_t st) {
-  // CTAs of a row: as many as are at work together on the device, and not less than kLeast bytes for each
+  // CTAs of a row: as many as are at work together on the device (4 an SM), and not less than kLeast bytes for each.  64 rows of
+  // 151936 with their own parameters take 42 us with 8, 59 with 4; 200 rows of 32000 13.2 with 2, 20.5 with 4; 499 rows
+  // 45.1 with 1, 47.5 with 2; one row of 32000 9.0 with 8, 10.4 with 4.
   constexpr int kLeast = 8192;
   p.ctas = kMostCtas;
   while (p.ctas > 1 && (int64_t(n_rows) * p.ctas > 600 || int64_t(p.vocab) * int(sizeof(T)) < int64_t(kLeast) * p.ctas)) p.ctas /= 2;

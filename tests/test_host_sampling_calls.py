@@ -203,3 +203,7 @@ def test_pool_arguments(tpa):
                                      dst=_i32(1)), **bad})
     with pytest.raises(ValueError, match="CUDA"):
         tpa.paged_resize(pages, lens, refs, 16)
+
+
+def test_compact_lengths_are_not_the_accepted_numbers(tpa):
+    assert tpa.lib().tpa_paged_compact(C.byref(_view()), 1, 3 * P, 4 * P, 3, 4 * P, None) == INVALID
