@@ -770,9 +770,17 @@ struct Request {
   float u;
 };
 
-// The token, and the logarithm of w 2^-down over `all`.
-__device__ __forceinline__ void write_token(const Result& out, int token, uint64_t w, int down, uint64_t all) {
+// The token, whose logit is x, and the logarithm of its weight w 2^-down over `all`.
+template <bool FAR>
+__device__ __forceinline__ void write_token(const Result& out, const Scale& k, float x_, int token, uint64_t w, int down, uint64_t all) {
   *out.token = token;
+  // A weight of few bits is off by the part of a unit that was cut off: of those, 2^(30 + shift + y), the logarithm is taken by y
+  // itself (u next to 0 draws such a token).
+  if (w < (1 << 25)) {
+    const float y = FAR ? __fsub_rn(x_, k.m) * k.ch : fmaf(x_, k.ch, k.base - kMagic) + x_ * k.cl;
+    *out.logp = (float(30 + k.shift - down) + y) * 0.693147181f - logf(float(all));
+    return;
+  }
   // The quotient's logarithm, with what its roundings lost added; next to 1 from what is missing, so that little is lost where one
   // token has nearly all the weight.
   const uint64_t part = down < 64 ? w >> down : 0;
@@ -817,7 +825,7 @@ __device__ __noinline__ void finish_few(const Result out, const Request q, int n
   uint64_t all;
   const uint64_t at = cta_scan64(kept ? w : 0, sh, all);
   const uint64_t limit = limit_of(q.u, all);
-  if (kept && at <= limit && at + w > limit) write_token(out, index_of(mine, 32 - weigh.k.shift), w, 0, all);
+  if (kept && at <= limit && at + w > limit) write_token<FAR>(out, weigh.k, logit_of(mine, 32 - weigh.k.shift), index_of(mine, 32 - weigh.k.shift), w, 0, all);
 }
 
 // The token of a part at which its running sum passes `limit`, among those from `from` on that weigh `least` or more; their weights are
@@ -844,7 +852,7 @@ __device__ __noinline__ void find_in_part(const Result out, const Row<T> row, in
     const uint64_t w = weight_of(i);
     at += w;
     if (at > limit) {
-      write_token(out, i, w, down, all);
+      write_token<FAR>(out, weigh.k, clean(float(row.x[i])), i, w, down, all);
       return;
     }
   }

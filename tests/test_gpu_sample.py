@@ -281,3 +281,21 @@ def test_equal_logits_with_top_p_of_many(tpa):
         _check(tpa, x, u, top_p=p)
         _check(tpa, x, u, top_k=torch.tensor([0, 29000, 0, 5000, 20], dtype=torch.int32), top_p=p)
     tpa.sync_status()
+
+
+@pytest.mark.parametrize("offset", [0.0, 300000.0])   # (the second: too far from 0 to be weighed without its maximum)
+@pytest.mark.parametrize("kw", [dict(), dict(top_k=900), dict(min_p=1e-25), dict(top_k=torch.full((8,), 990, dtype=torch.int32))])
+def test_log_probabilities_next_to_the_cut_off(tpa, offset, kw):
+    # u = 0 draws the first token with any weight, here of 2^-14 to 2^-50 of the largest: as whole numbers, down to a few bits
+    x = torch.zeros((8, 1000)) + offset
+    x[:, 100:] -= 60 if "top_k" in kw else 0
+    down = torch.arange(8) * 3.5 + 10
+    x[:, 0] = offset - down
+    kw = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in kw.items()}
+    t, l = tpa.sample_tokens(x.cuda(), torch.zeros(8, device="cuda"), **kw)
+    d = x[:, 0].double() - offset
+    whole = (x.double() - offset).exp().sum(1)
+    # y of up to 64 as two products and a sum, the sum's logarithm of up to 44: 2^-24 of each, thrice at most
+    assert (t == 0).all()
+    assert (l.cpu().double() - (d - whole.log())).abs().max() <= 3 * 2.0 ** -24 * (64 + 44)
+    tpa.sync_status()
