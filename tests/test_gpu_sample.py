@@ -299,3 +299,14 @@ def test_log_probabilities_next_to_the_cut_off(tpa, offset, kw):
     assert (t == 0).all()
     assert (l.cpu().double() - (d - whole.log())).abs().max() <= 3 * 2.0 ** -24 * (64 + 44)
     tpa.sync_status()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n,v,k", [(700, 700, 129), (310, 3000, 700), (301, 9001, 1030), (2, 40000, 3000), (5, 2100, 2049), (301, 2500, 2048)])
+def test_top_k_of_many(tpa, n, v, k, dtype):
+    # a bound from the threads' maxima, taken apart, and where there are too few of them
+    x, u = _logits(n, v, 31, dtype)
+    x[1, v // 3:] = -math.inf          # fewer than k are left of a row
+    x[0] = (x[0] * 2).round() / 2      # and of another many are equal
+    _check(tpa, x, u, 1.0, k, 0.999)
+    tpa.sync_status()
