@@ -757,9 +757,9 @@ typedef struct {            /* each: an array of one entry a row (device), or NU
  *     element (16-byte aligned rows are not needed).  NaN counts as -inf, +inf as the largest finite
  *     number.  -inf (a masked token) is never drawn; a row of nothing else gives -1 and NaN.
  *   u [n_rows] fp32 in [0, 1);  tokens [n_rows] int32, logp [n_rows] fp32 (written)
- *   vocab <= 2^30
- * Weights are within 2^-29 of themselves and cut off below 2^-(61 - log2 vocab) of the largest one (2^-43 for a
- * vocabulary of 2^18), and their sums are exact: borders of top_p, min_p and the draw are those of the formulas to within
+ *   vocab <= 2^24
+ * A weight is off by at most 2^-29 of itself and by one unit of 2^-(61 - log2 vocab) of the largest one (2^-43 for a
+ * vocabulary of 2^18; below a unit it is none), and their sums are exact: borders of top_p, min_p and the draw are those of the formulas to within
  * that.  Deterministic; a row's result does not depend on what the others hold (where nothing is cut off, calls of different
  * numbers of rows may have borders that differ by 2^-(61 - log2 vocab) of the sum).  Parameters in arrays that are out of
  * range give -1 and NaN in their rows and are reported; a single value out of range is refused.  One kernel, one cluster

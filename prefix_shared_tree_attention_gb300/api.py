@@ -930,7 +930,7 @@ def sample_tokens(logits: torch.Tensor, u: torch.Tensor, temperature: "float | t
     """Draw a token for each row of logits from given uniform numbers
     (tpa_sample_tokens): temperature, then top-k, top-p and min-p.
 
-    logits [N, V] fp32 or bf16 with unit column stride, u [N] fp32 in [0, 1).  Each parameter is a number or a tensor
+    logits [N, V] fp32 or bf16 with unit column stride, V <= 2^24, u [N] fp32 in [0, 1).  Each parameter is a number or a tensor
     [N] (fp32, top_k int32): a temperature of 0 takes the largest logit; top_k <= 0, top_p = 1 and min_p = 0 keep all.
     Returns tokens [N] int32 and their log-probabilities in the distribution that they were drawn from, [N] fp32."""
     f32, i32, T = torch.float32, torch.int32, torch.Tensor

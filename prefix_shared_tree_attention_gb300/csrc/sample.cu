@@ -9,8 +9,9 @@
 // whole numbers: 2^y, y = x c - M with c = log2(e) / T as a pair of fp32 and M a multiple of 1/32,
 // y = k / 32 + g, 2^(k / 32) from a table to 30 bits, 2^g - 1 by its series (|g| <= 1/64, four terms, off by
 // 2^-39).  The product of the two is off by 2^-29 of itself (the rounding of g and of the series' value),
-// shifted to 31 + s bits at most, s = 32 - log2 vocabulary, and what is below 1 there is nothing.  A row's sum fits in 64
-// bits, is exact, and nothing depends on the grouping: borders are off by 2^-29 of the whole from the weights.
+// shifted to 31 + s bits at most, s = 32 - log2 vocabulary, and the part below 1 is cut off there.  A row's sum fits in 64
+// bits, is exact, and nothing depends on the grouping: borders are off by what the weights are, 2^-29 of the whole, and by
+// the units cut off, vocabulary 2^-(30 + s) of the largest weight at most (2^-26 for a vocabulary of 2^18).
 //
 // A row's way (sample_kernel; a cluster of 1 to 8 CTAs of 8 warps, each warp a contiguous part of the row):
 //   1. the maximum, and for top-k a bound below which nothing is kept (the warp's threads' own maxima);
@@ -44,6 +45,7 @@ namespace {
 __device__ unsigned int g_status_sample = 0;
 
 constexpr int kMostCtas = 8;  // of a row: a cluster
+constexpr int kMostVocab = 1 << 24;  // beyond, a weight's unit times the vocabulary is no longer small
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMostParts = kMostCtas * kWarps;  // contiguous parts of a row, one a warp
@@ -1317,7 +1319,7 @@ extern "C" int tpa_sample_tokens(const void* logits, int32_t logits_type, int64_
                                  const tpa_sample_params* params, const float* u, int32_t* tokens, float* logp,
                                  void* stream) {
   TPA_NVTX_RANGE("tpa_sample_tokens");
-  if (n_rows < 0 || n_rows > 0x7fffffff / kMostCtas || vocab < 1 || vocab > (1 << 30) || !params ||
+  if (n_rows < 0 || n_rows > 0x7fffffff / kMostCtas || vocab < 1 || vocab > kMostVocab || !params ||
       (logits_type != TPA_LOGITS_F32 && logits_type != TPA_LOGITS_BF16))
     return TPA_ERR_INVALID_ARG;
   auto in = [](float v, float lo, float hi) { return v >= lo && v <= hi; };

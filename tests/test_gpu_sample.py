@@ -310,3 +310,32 @@ def test_top_k_of_many(tpa, n, v, k, dtype):
     x[0] = (x[0] * 2).round() / 2      # and of another many are equal
     _check(tpa, x, u, 1.0, k, 0.999)
     tpa.sync_status()
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(top_p=0.9), dict(top_p=0.5, min_p=1e-4), dict(top_k=5000, top_p=0.99), dict(top_k=100000)])
+@pytest.mark.parametrize("v", [1 << 24, 3000017])
+def test_largest_vocabularies(tpa, v, kw):
+    # (against sorted fp64 sums on the device: no border is nearer than they are off, 2^-12 of the whole at the most)
+    g = torch.Generator(device="cuda").manual_seed(v)
+    x = 2 * torch.randn((2, v), generator=g, device="cuda")
+    x[:, 12345] = 24.0                  # half of the weight or so, which u = 0.1 and 0.95 pass by
+    x[1] = x[1].flip(0)
+    u = torch.tensor([0.95, 0.1], device="cuda")
+    t, l = tpa.sample_tokens(x, u, 1.0, **kw)
+    for r in range(2):
+        w = (x[r].double() - x[r].max()).exp()
+        order = torch.sort(x[r], descending=True, stable=True).indices
+        k, p, m = kw.get("top_k", v), kw.get("top_p", 1.0), kw.get("min_p", 0.0)
+        run = w[order[:k]].cumsum(0)
+        n = k if p == 1 else int((run - w[order[:k]] < np.float32(p) * run[-1]).sum())
+        kept = torch.zeros_like(w)
+        kept[order[:n]] = w[order[:n]]
+        kept[kept < np.float32(m)] = 0
+        sums = kept.cumsum(0)
+        share = sums[int(t[r])] / sums[-1], (sums[int(t[r])] - kept[int(t[r])]) / sums[-1]
+        assert kept[int(t[r])] > 0
+        assert share[1] - 2.0 ** -12 <= float(u[r]) <= share[0] + 2.0 ** -12
+        # the kept sum: as many as top_p keeps to within its own border's distance
+        want = (w[int(t[r])] / sums[-1]).log()
+        assert abs(float(l[r]) - float(want)) <= 2.0 ** -11 + 2.0 ** -22 * abs(float(want))
+    tpa.sync_status()

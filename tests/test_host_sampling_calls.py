@@ -207,3 +207,8 @@ def test_pool_arguments(tpa):
 
 def test_compact_lengths_are_not_the_accepted_numbers(tpa):
     assert tpa.lib().tpa_paged_compact(C.byref(_view()), 1, 3 * P, 4 * P, 3, 4 * P, None) == INVALID
+
+
+def test_vocabularies_have_a_limit(tpa):
+    assert _sample(tpa.lib(), vocab=2 ** 24 + 1, stride=2 ** 25) == INVALID
+    assert _sample(tpa.lib(), vocab=2 ** 24, stride=2 ** 25, rows=0) == 0
