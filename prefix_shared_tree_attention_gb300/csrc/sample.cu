@@ -29,7 +29,7 @@
 // the weights' instructions, 28 a token of which 7.5 us of issue slots are made here, and by a start and an end as long: 17.4 us.
 // With cuts it is bound by passes over a row that follow one another, with a cluster barrier after each, in which a warp has
 // little to overlap: 64 rows of 151936 in fp32, each with its own parameters, 42 us; with rows among them whose
-// top-p keeps thousands of tokens, which then have the device to themselves, 78; 64 such rows (T = 1.3, p = 0.97) 128;
+// top-p keeps thousands of tokens, which then have the device to themselves, 72 to 79; 64 such rows (T = 1.3, p = 0.97) 112;
 // 499 rows of 32000 45 us; one row of 32000 9.3 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -1108,11 +1108,14 @@ __device__ void draw(const Result& out, const Request& q, const Row<T>& row, flo
     if (guess && attempt < 2 && warp_sum64(listed) < target_of(q.top_p, whole)) {
       const float share = 0.98f * float(whole) / float(uint64_t(1) << 30 << weigh.k.shift) * (1.f - q.top_p) / float(row.vocab);
       const float safe = weigh.k.m + q.t * logf(share) - 1e-5f * (fabsf(weigh.k.m) + 100.f * q.t);
-      const float next = attempt == 0 && fits ? fmaxf(weigh.k.m - kWider * q.t, safe) : safe;
+      // (where the first guess misses more than 0.15 of the whole, the wider one hardly ever holds: without it 64 rows of 151936
+      // at T = 1.3 with p = 0.97 take 112 us, not 127)
+      const bool near = target_of(q.top_p, whole) - warp_sum64(listed) < times<false>(whole, 0.15f);
+      const float next = attempt == 0 && fits && near ? fmaxf(weigh.k.m - kWider * q.t, safe) : safe;
       bound = next < bound ? next : safe;
       if (bound == safe) attempt = 1;
-      // (with a quarter of the room used, a wider guess will hardly fit)
-      if (bound > -kLargest && fits && all <= place.parts() * (kList / 4)) {
+      // (with a quarter of the room used, a wider guess will hardly fit; nor will the last bound's, but in a short row)
+      if (bound > -kLargest && fits && all <= place.parts() * (kList / 4) && (bound != safe || row.per * N <= 2 * kList)) {
         tc::cluster_sync();  // all have read what is written again
         continue;
       }
