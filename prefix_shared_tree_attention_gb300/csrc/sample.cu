@@ -834,6 +834,8 @@ __device__ __noinline__ void finish_few(const Result out, const Request q, int n
 
 // The token of a part at which its running sum passes `limit`, among those from `from` on that weigh `least` or more; their weights are
 // 2^down of those that `all` is made of.  By the CTA, a run of the part's entries a thread.
+// Where the part was summed beside a moving maximum (sum_online), that sum holds parts of units that are cut off here: `limit` may pass what
+// is there, by a unit a token, and then it is the last token with a weight (the part's largest has one: there always is one).
 template <bool FAR, class T>
 __device__ __noinline__ void find_in_part(const Result out, const Row<T> row, int part, uint64_t limit, uint64_t from,
                                           uint64_t least, int down, uint64_t all, Shared& sh) {
@@ -850,6 +852,7 @@ __device__ __noinline__ void find_in_part(const Result out, const Row<T> row, in
   for (int i = a; i < b; ++i) mine += weight_of(i);
   uint64_t total;
   uint64_t at = cta_scan64(mine, sh, total);
+  limit = min(limit, total - 1);
   if (at > limit || at + mine <= limit) return;
 #pragma unroll 1
   for (int i = a; i < b; ++i) {
