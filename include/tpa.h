@@ -759,9 +759,12 @@ typedef struct {            /* each: an array of one entry a row (device), or NU
  *   u [n_rows] fp32 in [0, 1);  tokens [n_rows] int32, logp [n_rows] fp32 (written)
  *   vocab <= 2^24
  * A weight is off by at most 2^-29 of itself and by one unit of 2^-(61 - log2 vocab) of the largest one (2^-43 for a
- * vocabulary of 2^18; below a unit it is none), and their sums are exact: borders of top_p, min_p and the draw are those of the formulas to within
- * that.  Deterministic; a row's result does not depend on what the others hold (where nothing is cut off, calls of different
- * numbers of rows may have borders that differ by 2^-(61 - log2 vocab) of the sum).  Parameters in arrays that are out of
+ * vocabulary of 2^18; below a unit it is none).  Borders of top_p, min_p and the draw are those of the formulas to within
+ * what that makes of their sums, which are exact and in any order the same, but for two: a top_p border among more than 256 tokens is
+ * found by sums that leave out up to 2^-28 of each weight; and where nothing at all is cut off, by single values, not arrays, the draw's sums are kept in
+ * units of the largest weight met so far.  Those hold parts of units too, and depend, by three units a token at most, on the order of the row and on
+ * the number of rows of the call, by which a row is split.  Deterministic; a row's result does not depend on
+ * what the others hold.  Parameters in arrays that are out of
  * range give -1 and NaN in their rows and are reported; a single value out of range is refused.  One kernel, one cluster
  * of CTAs a row.  Errors: TPA_ERR_INVALID_ARG, TPA_ERR_CUDA.
  */
