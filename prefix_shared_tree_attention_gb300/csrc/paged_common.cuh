@@ -50,9 +50,10 @@ struct Seq {
   int first, n, kv;  // first row, new tokens, cached tokens
 };
 
-// A sequence whose numbers are out of range has no tokens (and is reported).
+// A sequence whose numbers are out of range has no tokens (and is reported).  (Lengths, offsets and page tables are read by plain loads, here and
+// below, not by the read-only path: kernels that write them, which hand out pages or move sequences on, may still run when this one starts.)
 __device__ __forceinline__ Seq load_seq(const Batch& b, int s, unsigned int* status) {
-  const int o0 = __ldg(b.offsets + s), o1 = __ldg(b.offsets + s + 1), kv = __ldg(b.kv_lens + s);
+  const int o0 = b.offsets[s], o1 = b.offsets[s + 1], kv = b.kv_lens[s];
   if (o0 < 0 || o1 < o0 || o1 > b.n_rows || kv < 0 || kv > (int64_t(b.max_pages) << b.page_shift) ||
       (b.masks && o1 - o0 > 32 * b.mask_words)) {
     if (status) atomicOr(status, TPA_DEV_BAD_INPUT);
@@ -303,7 +304,7 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
 // Writes the record of the tile that this CTA's first segment is a part of: one thread of each CTA, behind its first
 // loads.  Rows before the first sequence are reported here, where nothing waits for it.
 __device__ __forceinline__ void write_split(const Params& p, const Scan* sc, const Shares& sh, unsigned int* status) {
-  if (blockIdx.x == 0 && __ldg(p.b.offsets) != 0) atomicOr(status, TPA_DEV_BAD_INPUT);
+  if (blockIdx.x == 0 && p.b.offsets[0] != 0) atomicOr(status, TPA_DEV_BAD_INPUT);
   Split s = {};
   if (int(blockIdx.x) < sh.n && sc->begin > 0) {  // the tile began in an earlier CTA
     const Tile t = sc->t;
@@ -337,7 +338,7 @@ __device__ __forceinline__ bool load_steps(const Batch& b, LoadRing& ring, const
     for (int i = 0; i < N; ++i) {
       const int ki = key0 + j * kStep + i * (kStep / N);
       const bool need = ki < hi && ki + kStep / N > lo;
-      at[i] = need ? __ldg(row + first_page + i) : 0;
+      at[i] = need ? row[first_page + i] : 0;
       needed |= uint32_t(need) << i;
     }
 #pragma unroll
