@@ -28,10 +28,12 @@ using namespace paged;
 // values, maxima and sums are loaded together; parts are added in a fixed order.
 // With 16 parts or fewer (the usual case: a tile on two or three CTAs) a warp
 // takes a row; with more (a long sequence by itself) the CTA's eight warps take
-// a share of one row's parts each.  The rows are dealt out to the CTAs evenly: with a CTA column for each
-// tile, a drafted tree of 48 tokens over 130001 keys, two tiles of many parts, took 91 us altogether, now 62.
+// a share of one row's parts each.  A CTA of the attention has a column of CTAs here, and a tile's rows are dealt out over the columns of
+// all that took it up from an earlier one: a tile has the more CTAs the more parts it was cut into, and none has to look at another's
+// record.  48 tokens of 16/2 heads over 130001 keys, four tiles of 38 parts, take 58 us altogether, with a column for each tile 88; with
+// the rows of all tiles dealt out evenly, for which each CTA read all records, 60, and every other call 1 to 2 us more (one
+// token over 700 keys 7.8 -> 8.7, 64 sequences by one 84 -> 85, eight chunks of 512 133 -> 137.5).
 constexpr int kFewParts = 16;
-constexpr int kJoinCtas = 4;  // of an SM, all there at once
 
 template <int D>
 __device__ __forceinline__ void join_row_by_warp(const Params& p, const Split& s, int r, int lane) {
@@ -92,49 +94,20 @@ __global__ void __launch_bounds__(256, 4) paged_join_kernel(const Params p) {
   __shared__ float acc_s[8][D];
   __shared__ float scale_s[kMaxGrid];
   __shared__ float top_s[8], sum_s[8];
-  __shared__ Split split_s[kMaxGrid];
-  __shared__ int warp_units[8], tile_s, first_s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   tc::grid_launch_dependents();
   tc::grid_wait_prior();
-  // The work of all split tiles in one line: eight rows with few parts, or one with many, at a time.  A CTA takes every
-  // gridDim.x-th piece, so that the rows of one long sequence's few tiles find as many CTAs as those of many tiles.
-  int units = 0;
-  if (int(threadIdx.x) < p.grid) {
-    const Split s = p.split[threadIdx.x];
-    split_s[threadIdx.x] = s;
-    const int rows = s.n * p.b.group;
-    if (s.valid) units = s.c1 - s.c0 < kFewParts ? (rows + 7) >> 3 : rows;
+  const Split s = p.split[blockIdx.x];
+  if (!s.valid) return;
+  const int parts = s.c1 - s.c0 + 1;
+  // this CTA among those of the tile: of a tile of few rows the first column's
+  const int me = (int(blockIdx.x) - s.c0 - 1) * int(gridDim.y) + int(blockIdx.y), ctas = (s.c1 - s.c0) * int(gridDim.y);
+  if (parts <= kFewParts) {
+    for (int r = me * 8 + warp; r < s.n * p.b.group; r += ctas * 8) join_row_by_warp<D>(p, s, r, lane);
+    return;
   }
-  int end = units;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int t = __shfl_up_sync(0xffffffffu, end, o);
-    if (lane >= o) end += t;
-  }
-  if (lane == 31) warp_units[warp] = end;
-  __syncthreads();
-  int total = 0;
-#pragma unroll
-  for (int w = 0; w < 8; ++w) {
-    if (w < warp) end += warp_units[w];
-    total += warp_units[w];
-  }
-  for (int unit = blockIdx.x; unit < total; unit += gridDim.x) {
-    if (unit < end && unit >= end - units) {
-      tile_s = threadIdx.x;
-      first_s = unit - (end - units);
-    }
-    __syncthreads();
-    const Split s = split_s[tile_s];
-    const int piece = first_s, parts = s.c1 - s.c0 + 1;
-    auto slot = [&](int i) { return int64_t(2) * (s.c0 + i) + (i == 0 ? 1 : 0); };
-    if (parts <= kFewParts) {
-      if (piece * 8 + warp < s.n * p.b.group) join_row_by_warp<D>(p, s, piece * 8 + warp, lane);
-      __syncthreads();  // tile_s is read
-      continue;
-    }
-    const int r = piece;
+  auto slot = [&](int i) { return int64_t(2) * (s.c0 + i) + (i == 0 ? 1 : 0); };
+  for (int r = me; r < s.n * p.b.group; r += ctas) {
     float2 ml = make_float2(-INFINITY, 0.f);  // thread i: part i
     if (int(threadIdx.x) < parts) ml = p.part_ml[slot(threadIdx.x) * p.rows + r];
     auto value = [&](int k) {
@@ -229,8 +202,9 @@ uint64_t part_bytes(int rows, int d) {
 }
 
 template <int D>
-int launch_join(const Params& p, cudaStream_t st) {
-  return launch_overlapped(paged_join_kernel<D>, dim3(kJoinCtas * p.grid), 256, 0, st, static_cast<const Params>(p));
+int launch_join(const Params& p, int grid, int64_t rows, cudaStream_t st) {
+  return launch_overlapped(paged_join_kernel<D>, dim3(grid, unsigned(rows < 8 ? rows : 8)), 256, 0, st,
+                           static_cast<const Params>(p));
 }
 
 // Both forms of the call; masks NULL: chains.
@@ -249,6 +223,7 @@ int attend(const tpa_paged_view* cache, const void* q, int64_t q_stride, const i
       q_stride < int64_t(n_heads_q) * d || q_stride % 8 || q_stride >= (int64_t(1) << 40))
     return TPA_ERR_INVALID_ARG;
   const int group = n_heads_q / hkv, R = tile_rows(max_q_len, group);
+  const int64_t rows = int64_t(max_q_len) * group;  // of the largest sequence
   if (workspace_bytes < part_bytes(R, d)) return TPA_ERR_BUFFER_TOO_SMALL;
   Params p = {};
   p.b.pages = cache->pages;
@@ -282,11 +257,10 @@ int attend(const tpa_paged_view* cache, const void* q, int64_t q_stride, const i
   const int dv = device_sms(&sms);
   if (dv != TPA_OK) return dv;
   const int grid = sms < kMaxGrid ? sms : kMaxGrid;
-  p.grid = grid;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int rt = R == 256 ? tpa_internal_paged_tile(cache, p, grid, st) : tpa_internal_paged_few(cache, p, R, grid, st);
   if (rt != TPA_OK) return rt;
-  return d == 128 ? launch_join<128>(p, st) : launch_join<64>(p, st);
+  return d == 128 ? launch_join<128>(p, grid, rows, st) : launch_join<64>(p, grid, rows, st);
 }
 
 }  // namespace

@@ -242,7 +242,7 @@ struct Walk {
   }
 };
 
-// A tile whose steps went to the CTAs c0 .. c1, written by CTA c0 + 1.  Its
+// A tile whose steps went to the CTAs c0 .. c1, as each of them but c0 writes it down.  Its
 // part from CTA c0 is in that CTA's slot 1, the others' parts in their slot 0.
 struct Split {
   int32_t valid, head, first, n, c0, c1, pad_[2];
@@ -258,7 +258,6 @@ struct Params {
   Split* split;     // [grid]
   int64_t q_stride;
   int32_t hq, rows;  // rows: R, of a part
-  int32_t grid;      // CTAs of the attention kernel
   float scale_log2;
 };
 
@@ -309,7 +308,7 @@ __device__ __forceinline__ void write_split(const Params& p, const Scan* sc, con
   if (int(blockIdx.x) < sh.n && sc->begin > 0) {  // the tile began in an earlier CTA
     const Tile t = sc->t;
     const int c0 = sh.of(sc->item), c1 = sh.of(sc->item + t.steps - 1);
-    if (c0 + 1 == int(blockIdx.x)) s = Split{1, sc->head, t.first, t.n, c0, c1, {0, 0}};
+    s = Split{1, sc->head, t.first, t.n, c0, c1, {0, 0}};
   }
   p.split[blockIdx.x] = s;
 }
