@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(512, 1)
   // From here on memory is read and written that the kernel before may write and read.
   tc::grid_wait_prior();
   tc::grid_launch_dependents();  // the joining kernel waits for this one's end by itself
-  const Shares shares = scan_batch(p.b, sc, &g_status_pfew);
+  const Shares shares = scan_batch<TREE>(p.b, sc, &g_status_pfew);
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;  // columns: S^T of the two warpgroups, then two sets of their O^T
   auto o_col = [](int k, int h) { return uint32_t(2 * NR + ((k & 1) * 2 + h) * NR); };  // of segment k
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(512, 1)
       const CUtensorMap* tm = keys ? &tm_k : &tm_v;
       auto wait1 = [&](uint64_t* b_, uint32_t par) { return tc::mbar_wait(b_, par, abort_flag, &g_status_pfew); };
       LoadRing ring{keys ? k_full : v_full, keys ? k_empty : v_empty, keys ? sK : sV};
-      Walk w;
+      Walk<TREE> w;
       w.start(p.b, sc, shares);
       bool ok = true, more = w.end > w.begin;
       for (int k = 0; ok; ++k) {
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(512, 1)
     // thread for the keys would stop at them until the segment before is done)
     if (tc::elect_one()) {
       const uint32_t q_bytes = uint32_t(NCH) * p.b.tile_tok * p.b.group * 128;
-      Walk w;
+      Walk<TREE> w;
       w.start(p.b, sc, shares);
       int nq = 0;
       bool more = w.end > w.begin;

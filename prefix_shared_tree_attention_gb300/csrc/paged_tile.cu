@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
   // From here on memory is read and written that the kernel before may write and read.
   tc::grid_wait_prior();
   tc::grid_launch_dependents();  // the joining kernel waits for this one's end by itself
-  const Shares shares = scan_batch(p.b, sc, &g_status_ptile);
+  const Shares shares = scan_batch<TREE>(p.b, sc, &g_status_ptile);
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         tc::tma_prefetch_desc(tm);
         auto wait1 = [&](uint64_t* b_, uint32_t par) { return tc::mbar_wait(b_, par, abort_flag, &g_status_ptile); };
         LoadRing ring{keys ? k_full : v_full, keys ? k_empty : v_empty, keys ? sK : sV};
-        Walk w;
+        Walk<TREE> w;
         w.start(p.b, sc, shares);
         bool ok = true, more = w.end > w.begin;
         for (int k = 0; ok; ++k) {
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
       if (tc::elect_one()) {
         tc::tma_prefetch_desc(&tm_q);
         const uint32_t q_bytes = uint32_t(NCH) * sub_tok * p.b.group * 128;  // of a sub-tile
-        Walk w;
+        Walk<TREE> w;
         w.start(p.b, sc, shares);
         int nq = 0;
         bool more = w.end > w.begin;
