@@ -806,12 +806,13 @@ int tpa_verify_drafts(const float* target, int64_t target_stride, const float* d
  * Drafted trees.  A batch's new tokens are described by offsets as for a paged
  * cache (offsets [n_seqs + 1], n_rows rows); parents [n_rows] int32 gives for each the
  * number of its parent among its sequence's new tokens, below its own, or -1 for one whose parent is the last
- * cached token before them.  A tree has at most 1024 tokens.  Parents and offsets out of
- * range are reported by tpa_sync_status (TPA_ERR_INVALID_ARG): the token counts as without parent (masks) or is not
- * accepted, the sequence is passed over.
+ * cached token before them.  A tree has at most 1024 tokens.  Parents, offsets and (masks) negative kv_lens
+ * are reported by tpa_sync_status (TPA_ERR_INVALID_ARG): a token with such a parent counts as without one (masks) or is not
+ * accepted, a sequence with such offsets or length is passed over, its rows left as they were.
  *
  * tpa_draft_masks — what tpa_paged_attn_tree_fwd reads, and the positions at which a tree's tokens are rotated:
- *   positions [n_rows] int32 (written): kv_lens[s] - (new tokens of s) + the token's ancestors among them
+ *   positions [n_rows] int32 (written): kv_lens[s] - (new tokens of s) + the token's ancestors among them (negative
+ *     for tokens without a slot, where kv_lens[s] is less than the new tokens)
  *   masks [n_rows, mask_words] int32 (written): bit j % 32 of word j / 32 for the token itself and each of its
  *     ancestors j among the new tokens, with window > 0 those less than window positions before it
  *   mask_words in [1, 32], 32 mask_words >= the new tokens of any sequence

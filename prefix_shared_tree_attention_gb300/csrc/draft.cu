@@ -44,9 +44,11 @@ __global__ void __launch_bounds__(kThreads) masks_kernel(const int32_t* parents,
   tc::grid_launch_dependents();
   tc::grid_wait_prior();
   const int s = blockIdx.x;
+  const int kv = kv_lens[s];  // under way beside the offsets
   const Rows q = load_rows(offsets, s, n_rows, 32 * words);
-  if (q.n == 0) return;
-  const int base = kv_lens[s] - q.n;
+  if (kv < 0 && threadIdx.x == 0) report();
+  if (q.n == 0 || kv < 0) return;
+  const int base = kv - q.n;
   for (int i = threadIdx.x; i < q.n; i += kThreads) {
     int p = parents[q.first + i];
     if (p < -1 || p >= i) {
