@@ -35,3 +35,21 @@ def test_negative_lengths_are_reported(tpa, at, bad):
         assert positions[row:row + len(t)].tolist() == want[0] and masks[row:row + len(t)].tolist() == want[1]
         row += len(t)
     tpa.sync_status()
+
+
+@pytest.mark.parametrize("at,bad", [(0, 0), (1, 1), (2, 3), (5, -2), (3, 2 ** 31 - 1), (7, -2 ** 31), (4, 4), (6, 6)])
+def test_tokens_with_broken_parents_are_not_accepted(tpa, at, bad):
+    # every token fits; the broken one is nobody's child (a sequence's row 0 stands whatever its parent)
+    trees = [[-1, 0, 1, 2], [-1, 0, 1, 2]]
+    parents = trees[0] + trees[1]
+    parents[at] = bad
+    x = torch.zeros(8, dtype=torch.int32, device="cuda")
+    tokens, path, count = tpa.accept_drafts(_i32(parents), _i32([0, 4, 8]), x, x, 4)
+    with pytest.raises(tpa.TpaError, match="INVALID_ARG"):
+        tpa.sync_status()
+    trees[at // 4][at % 4] = -1
+    for s, t in enumerate(trees):
+        rows, out = accept(t, [0] * 4, [0] * 4, 4)
+        assert count[s] == len(rows) and path[s].tolist() == rows + [-1] * (4 - len(rows))
+        assert tokens[s].tolist() == out + [-1] * (4 - len(rows))
+    tpa.sync_status()
