@@ -907,7 +907,8 @@ __device__ __noinline__ void finish_many(const Result out, const Request q, cons
 // Rows without a cut, gone through once: each warp's weights are made for the largest logit that it has met, M a whole number of powers of 2
 // above it, and its sum is moved down when a larger one comes: up to a unit of each token is cut off as it is added, and two of a lane's sum
 // by all its moves (each leaves less than one, which the next ones halve at least).  (With the maximum found first, 64 rows
-// of 151936 in bf16 took 22 us, now 18.)
+// of 151936 in bf16 took 22 us, now 18.)  A row of which a warp's first step is all masked by a large finite number (-1e9) counts as too far
+// from 0 and goes the way of the rows with cuts: 64 rows with their first third at -1e9 take 31 us, at -inf 17.5.
 struct Online {
   uint64_t sum;  // a lane's share
   int top;       // M; kNothing: no logit that can be drawn; kFar: too far from 0 for this
