@@ -28,7 +28,7 @@
 // Drafted trees (TREE, an instance of its own: chains keep their code): a row's thread has its mask's words beside its 128
 // columns of a step, shifted to where the tree begins, so that a step with drafted tokens costs 128 selects more.  Trees
 // of 20 to 64 tokens are one sub-tile or two of few rows: bound by the reads of the cache (16 sequences
-// of 1000 to 8000 tokens, 280 MB: 78 us, as chains 75) or, where one sequence's rows are more than a tile's (48 tokens of 8 heads, 130001
+// of 1000 to 8000 tokens, 280 MB: 77 us, as chains 73) or, where one sequence's rows are more than a tile's (48 tokens of 8 heads, 130001
 // cached: 62 us), by reading it once for each tile.  The masks are read by plain loads: the kernel that writes them may
 // end after this one starts.
 #include <cuda.h>
